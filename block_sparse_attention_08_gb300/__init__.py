@@ -12,11 +12,16 @@ from .binding import (  # noqa: F401
     library_path,
     load,
     make_config,
+    msa_attend_chunk,
+    msa_attend_chunk_fp8kv,
     msa_check_bounded_wait,
     msa_index_produce_decode,
     msa_index_produce_prefill,
+    msa_map_slots,
     msa_pack,
     msa_pack_metadata,
+    msa_rotary,
+    msa_rotary_insert,
     msa_select_blocks_decode,
     msa_select_blocks_prefill,
     msa_sparse_attend_decode,
@@ -25,6 +30,7 @@ from .binding import (  # noqa: F401
     msa_sparse_attend_prefill,
     msa_sparse_attend_prefill_backward,
     msa_unpack,
+    rotary,
     sparse_attention,
     workspace_size,
 )

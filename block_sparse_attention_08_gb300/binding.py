@@ -9,6 +9,7 @@ tensors are allocated with torch when the caller does not pass them.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -19,11 +20,12 @@ from . import _build
 
 H, G, D, DI, BLOCK = 64, 4, 128, 128, 128
 MSA_ERR_CUDA = 6  # msa_status for a failed CUDA call
-MODE_DECODE, MODE_PREFILL, MODE_PACK, MODE_PREFILL_BWD = 0, 1, 2, 3
+MODE_DECODE, MODE_PREFILL, MODE_PACK, MODE_PREFILL_BWD, MODE_CHUNK = 0, 1, 2, 3, 4
 INDEX_DTYPES = {"bf16": 0, "e4m3": 1}
 DEVICE_ERRORS = {0: "none", 1: "page id outside the pool", 2: "block id outside the query's range",
                  3: "sequence length out of range", 4: "bounded on-chip wait gave up",
-                 5: "prefill attention score outside the fixed-reference range"}
+                 5: "prefill attention score outside the fixed-reference range",
+                 6: "no free page, or no room in the token buffers"}
 
 
 class MsaError(RuntimeError):
@@ -39,10 +41,16 @@ class msa_config(ctypes.Structure):
         "topk", "init_blocks", "local_blocks", "index_dtype")]
 
 
+class msa_rotary_config(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("num_axes", ctypes.c_int),
+                ("axis", ctypes.c_uint8 * 64)]
+
+
 _lib = None
 _lock = threading.Lock()
 P, I, I64, SZ, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 CFG = ctypes.POINTER(msa_config)
+ROT = ctypes.POINTER(msa_rotary_config)
 _SIGS = {
     "msa_config_default": [CFG],
     "msa_config_check": [CFG],
@@ -64,6 +72,11 @@ _SIGS = {
     "msa_check_bounded_wait": [P, P, ctypes.POINTER(I64)],
     "msa_index_produce_prefill": [CFG, P, P, P, I, I64, P, P, P, P, I, I64, P, SZ, P],
     "msa_index_produce_decode": [CFG, P, P, P, P, P, I, I, I64, P, P, P, SZ, P],
+    "msa_map_slots": [P, P, I, P, I, P, I64, P, I64, I64, P, P, P, P, P, SZ, P],
+    "msa_rotary": [ROT, P, I64, I, P, I64, I, P, P, I64, I, P, P, P],
+    "msa_rotary_insert": [ROT, P, I64, P, I64, P, I64, P, P, P, I64, P, P, P, P, I, F, F, I64, P, SZ, P],
+    "msa_attend_chunk": [CFG, P, P, P, P, P, P, I, I, I64, I64, F, P, P, P, SZ, P],
+    "msa_attend_chunk_fp8kv": [CFG, P, P, P, F, F, P, P, P, I, I, I64, I64, F, P, P, P, SZ, P],
 }
 EXPORTS = tuple(_SIGS) + ("msa_status_string", "msa_last_cuda_error", "msa_cuda_error_string")
 
@@ -496,6 +509,248 @@ def msa_index_produce_decode(index_q, index_k, index_k_cache, seq_lens, page_tab
           _ptr(page_table), _ptr(cu_seqlens_k if page_table is None else None), B, mb, index_k_cache.shape[0],
           _ptr(q_out), _ptr(index_k_cache), _ptr(ws.buf), ws.nbytes, _stream(dev))
     return q_out
+
+
+# ---- chunked serving over the paged cache ------------------------------------------
+# These calls keep no workspace between calls: without ``workspace`` each call takes its
+# scratch from the caching allocator, so calls on several streams or threads and several
+# captured graphs never share one (and a device error is then not kept: pass a
+# ``Workspace`` to read it).  They run on the device of their tensors, whatever the
+# current one is.
+
+def _scratch(nbytes, device, workspace):
+    """(pointer, size) of a call's workspace, and what keeps it alive during the call."""
+    if workspace is None:
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return buf.data_ptr(), nbytes, buf
+    if workspace.buf.device != device:
+        raise ValueError(f"workspace is on {workspace.buf.device}, the tensors are on {device}")
+    if workspace.nbytes < nbytes:
+        raise ValueError(f"workspace too small: {workspace.nbytes} < {nbytes}")
+    return workspace.buf.data_ptr(), workspace.nbytes, workspace
+
+
+def _call_on(device, name, *args):
+    """The call ``name(*args, stream)`` on ``device`` and its current stream."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        return _call(name, *args, stream)
+    with torch.cuda.device(device):
+        return _call(name, *args, stream)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def msa_map_slots(seq_lens, new_lens, page_table, free_pages, num_free, *, num_slots, capacity, cu_seqlens_q=None,
+                  slots=None, positions=None, num_free_out=None, workspace=None):
+    """Opens the pages of each request's new tokens (written into ``page_table``) and maps the
+    tokens to slots (C: msa_map_slots): returns (cu_seqlens_q int32 [batch + 1], slots int64
+    [capacity], positions int32 [capacity], num_free_out int32 [1])."""
+    B = seq_lens.shape[0]
+    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    _need(new_lens, "new_lens", torch.int32, (B,))
+    _need(page_table, "page_table", torch.int32, (B, None))
+    _need(free_pages, "free_pages", torch.int32, (None,))
+    _need(num_free, "num_free", torch.int32, (1,))
+    dev = seq_lens.device
+    capacity = int(capacity)
+    if cu_seqlens_q is None:
+        cu_seqlens_q = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty(capacity, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(capacity, dtype=torch.int32, device=dev)
+    if num_free_out is None:
+        num_free_out = torch.empty(1, dtype=torch.int32, device=dev)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
+    _need(slots, "slots", torch.int64, (capacity,))
+    _need(positions, "positions", torch.int32, (capacity,))
+    _need(num_free_out, "num_free_out", torch.int32, (1,))
+    _same_device(dev, new_lens=new_lens, page_table=page_table, free_pages=free_pages, num_free=num_free,
+                 cu_seqlens_q=cu_seqlens_q, slots=slots, positions=positions, num_free_out=num_free_out)
+    ws, wn, _keep = _scratch(256, dev, workspace)
+    _call_on(dev, "msa_map_slots", seq_lens.data_ptr(), new_lens.data_ptr(), B, page_table.data_ptr(),
+             page_table.shape[1], free_pages.data_ptr() or None, free_pages.shape[0], num_free.data_ptr(),
+             int(num_slots), capacity, cu_seqlens_q.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+             num_free_out.data_ptr(), ws, wn)
+    return cu_seqlens_q, slots, positions, num_free_out
+
+
+@functools.lru_cache(maxsize=64)
+def _rotary_config(pairs, num_axes, axes, interleaved):
+    axes = (0,) * pairs if axes is None else tuple(int(a) for a in axes)
+    if len(axes) != pairs:
+        raise ValueError(f"axes has {len(axes)} entries, inv_freq has {pairs}")
+    if any(a < 0 or a >= num_axes for a in axes):
+        raise ValueError(f"axes must lie in [0, {num_axes}), the rows of positions")
+    cfg = msa_rotary_config(2 * pairs, int(bool(interleaved)), num_axes)
+    for j, a in enumerate(axes[:64]):
+        cfg.axis[j] = a
+    return cfg
+
+
+def _rotary_args(positions, inv_freq, axes, interleaved, tokens):
+    _need(inv_freq, "inv_freq", torch.float32, (None,))
+    if positions.dim() == 1:
+        positions = positions[None]
+    _need(positions, "positions", torch.int32, (None, tokens))
+    axes = axes if axes is None or isinstance(axes, tuple) else tuple(axes)
+    return positions, _rotary_config(inv_freq.shape[0], positions.shape[0], axes, bool(interleaved))
+
+
+def _token_rows(t, name, tokens, heads):
+    """Stride between the tokens of a bf16 [tokens, heads, 128] tensor whose heads are dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must have dtype {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != tokens or (heads is not None and t.shape[1] != heads) or t.shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, D)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and t.shape[1] > 1):
+        raise ValueError(f"{name} must have dense heads, got strides {t.stride()}")
+    if tokens == 1:
+        return t.shape[1] * D  # a single token's stride says nothing
+    if s0 < t.shape[1] * D or s0 % 8:
+        raise ValueError(f"{name} must have tokens a multiple of 8 elements apart that do not overlap, got {s0}")
+    return s0
+
+
+def msa_rotary(q, k, positions, inv_freq, *, axes=None, interleaved=False, inverse=False, q_out=None, k_out=None):
+    """Rotary positions on q [tokens, heads, 128] and k (or None): returns (q_out, k_out)
+    (C: msa_rotary).  ``positions`` int32 [tokens] or [axes, tokens], ``inv_freq`` fp32 [pairs],
+    ``axes`` the axis of each pair (default: all 0), ``inverse`` turns back (the gradient)."""
+    T = q.shape[0]
+    qs = _token_rows(q, "q", T, None)
+    dev = q.device
+    positions, rot = _rotary_args(positions, inv_freq, axes, interleaved, T)
+    q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
+    _need(q_out, "q_out", torch.bfloat16, tuple(q.shape))
+    kp, ks, kh, ko = None, 0, 0, None
+    if k is not None:
+        ks, kh, kp = _token_rows(k, "k", T, None), k.shape[1], k.data_ptr()
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
+        _need(k_out, "k_out", torch.bfloat16, tuple(k.shape))
+        ko = k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _same_device(dev, k=k, positions=positions, inv_freq=inv_freq, q_out=q_out, k_out=k_out)
+    _call_on(dev, "msa_rotary", ctypes.byref(rot), q.data_ptr(), qs, q.shape[1], kp, ks, kh, positions.data_ptr(),
+             inv_freq.data_ptr(), T, int(bool(inverse)), q_out.data_ptr(), ko)
+    return q_out, k_out
+
+
+def msa_rotary_insert(q, k, v, positions, inv_freq, slots, k_cache, v_cache, *, axes=None, interleaved=False,
+                      k_scale=1.0, v_scale=1.0, q_out=None, k_out=None, workspace=None):
+    """Rotary positions on q [tokens, 64, 128] and k [tokens, 4, 128], with the rotated k and v
+    written at ``slots`` (int64 [tokens], -1: not inserted) of the paged caches, bf16 or E4M3
+    standing for scale * value; returns q_out (C: msa_rotary_insert).  ``k_out`` (optional)
+    receives the rotated k as well."""
+    T = q.shape[0]
+    qs, ks, vs = _token_rows(q, "q", T, H), _token_rows(k, "k", T, G), _token_rows(v, "v", T, G)
+    dev = q.device
+    positions, rot = _rotary_args(positions, inv_freq, axes, interleaved, T)
+    _need(slots, "slots", torch.int64, (T,))
+    _need(k_cache, "k_cache", (torch.bfloat16, torch.float8_e4m3fn, torch.uint8), (None, G, D))
+    _need(v_cache, "v_cache", k_cache.dtype, tuple(k_cache.shape))
+    q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev) if q_out is None else q_out
+    _need(q_out, "q_out", torch.bfloat16, (T, H, D))
+    if k_out is not None:
+        _need(k_out, "k_out", torch.bfloat16, (T, G, D))
+    _same_device(dev, k=k, v=v, positions=positions, inv_freq=inv_freq, slots=slots, k_cache=k_cache,
+                 v_cache=v_cache, q_out=q_out, k_out=k_out)
+    ws, wn, _keep = _scratch(256, dev, workspace)
+    _call_on(dev, "msa_rotary_insert", ctypes.byref(rot), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+             positions.data_ptr(), inv_freq.data_ptr(), slots.data_ptr(), T, q_out.data_ptr(),
+             None if k_out is None else k_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+             int(k_cache.dtype != torch.bfloat16), float(k_scale), float(v_scale), k_cache.shape[0], ws, wn)
+    return q_out
+
+
+class _Rotary(torch.autograd.Function):
+    """The rotation as an autograd function: the gradient turns back."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, axes, interleaved):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.axes, ctx.interleaved = axes, interleaved
+        return msa_rotary(q, k, positions, inv_freq, axes=axes, interleaved=interleaved)
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        positions, inv_freq = ctx.saved_tensors
+        dq, dk = msa_rotary(gq.contiguous(), gk.contiguous(), positions, inv_freq, axes=ctx.axes,
+                            interleaved=ctx.interleaved, inverse=True)
+        return dq, dk, None, None, None, None
+
+
+def rotary(q, k, positions, inv_freq, *, axes=None, interleaved=False):
+    """Differentiable rotary positions: (q, k) rotated as by :func:`msa_rotary`; q and k receive
+    gradients through the same kernel turning back."""
+    axes = axes if axes is None or isinstance(axes, tuple) else tuple(axes)
+    return _Rotary.apply(q, k, positions, inv_freq, axes, bool(interleaved))
+
+
+@functools.lru_cache(maxsize=1)
+def _chunk_config():
+    return make_config()
+
+
+@functools.lru_cache(maxsize=1024)
+def _chunk_bytes(tokens, max_blocks):
+    return workspace_size(_chunk_config(), MODE_CHUNK, tokens, max_blocks)
+
+
+def _attend_chunk(name, kv_dtypes, kv_scales, q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, scale, out,
+                  lse, workspace):
+    T = q.shape[0]
+    _need(q, "q", torch.bfloat16, (T, H, D))
+    _need(k_cache, "k_cache", kv_dtypes, (None, G, D))
+    _need(v_cache, "v_cache", k_cache.dtype, tuple(k_cache.shape))
+    _need(seq_lens, "seq_lens", torch.int32, (None,))
+    B = seq_lens.shape[0]
+    _need(page_table, "page_table", torch.int32, (B, None))
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
+    dev = q.device
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, (T, H, D))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, H))
+    _same_device(dev, k_cache=k_cache, v_cache=v_cache, seq_lens=seq_lens, page_table=page_table,
+                 cu_seqlens_q=cu_seqlens_q, out=out, lse=lse)
+    mb = page_table.shape[1]
+    ws, wn, _keep = _scratch(_chunk_bytes(T, mb), dev, workspace)
+    _call_on(dev, name, ctypes.byref(_chunk_config()), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+             *kv_scales, seq_lens.data_ptr(), page_table.data_ptr(), cu_seqlens_q.data_ptr(), B, mb, T,
+             k_cache.shape[0], 1.0 / math.sqrt(D) if scale is None else float(scale), out.data_ptr(),
+             None if lse is None else lse.data_ptr(), ws, wn)
+    return out
+
+
+def msa_attend_chunk(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, *, scale=None, out=None, lse=None,
+                     workspace=None):
+    """bf16 out [tokens, 64, 128]: each request's new tokens (rows cu_seqlens_q[r] ..) attend to all
+    their keys in the paged cache (C: msa_attend_chunk).  ``lse`` (fp32 [tokens, 64], optional)
+    receives the log2 of the softmax denominators.  Rows from cu_seqlens_q[-1] on are left as they
+    are."""
+    return _attend_chunk("msa_attend_chunk", torch.bfloat16, (), q, k_cache, v_cache, seq_lens, page_table,
+                         cu_seqlens_q, scale, out, lse, workspace)
+
+
+def msa_attend_chunk_fp8kv(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, *, k_scale=1.0, v_scale=1.0,
+                           scale=None, out=None, lse=None, workspace=None):
+    """:func:`msa_attend_chunk` over E4M3 caches standing for k_scale * k and v_scale * v
+    (C: msa_attend_chunk_fp8kv)."""
+    return _attend_chunk("msa_attend_chunk_fp8kv", (torch.float8_e4m3fn, torch.uint8),
+                         (float(k_scale), float(v_scale)), q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q,
+                         scale, out, lse, workspace)
 
 
 # ---- packing ----------------------------------------------------------------------

@@ -100,6 +100,10 @@ msa_status msa_workspace_size(const msa_config* cfg, int mode, int64_t n, int ma
     *bytes = kHeaderBytes + pack_workspace_bytes(max_blocks, static_cast<int>(n / max_blocks));
     return MSA_OK;
   }
+  if (mode == MSA_MODE_CHUNK) {
+    *bytes = kHeaderBytes + attend_chunk_bytes(n, max_blocks);
+    return MSA_OK;
+  }
   if (mode != MSA_MODE_DECODE && mode != MSA_MODE_PREFILL && mode != MSA_MODE_PREFILL_BWD) return MSA_ERR_SHAPE;
   if (mode != MSA_MODE_DECODE && !prefill_attend_fits(n, max_blocks * kBlock, cfg->topk)) return MSA_ERR_SHAPE;
   *bytes = layout(mode, n, max_blocks, cfg->topk).total;
@@ -438,6 +442,167 @@ msa_status msa_unpack(const void* packed, const int64_t* token_rows, int64_t tot
   if (const cudaError_t ce = cudaMemsetAsync(external, 0, static_cast<size_t>(batch_seq) * row_bytes, s); ce != cudaSuccess)
     return cuda_fail(ce);
   return run_gather(packed, token_rows, total_tokens, row_bytes, external, s, true);
+}
+
+msa_status msa_map_slots(const int32_t* seq_lens, const int32_t* new_lens, int batch, int32_t* page_table,
+                         int max_blocks, const int32_t* free_pages, int64_t free_capacity, const int32_t* num_free,
+                         int64_t num_slots, int64_t capacity, int32_t* cu_seqlens_q, int64_t* slots,
+                         int32_t* positions, int32_t* num_free_out, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  if (!seq_lens || !new_lens || !page_table || !num_free || !cu_seqlens_q || !slots || !positions || !num_free_out)
+    return MSA_ERR_NULL;
+  if (free_capacity < 0 || free_capacity >= (1LL << 31)) return MSA_ERR_SHAPE;
+  if (!free_pages && free_capacity) return MSA_ERR_NULL;
+  if (batch < 1 || max_blocks < 1 || num_slots < 1 || num_slots >= (1LL << 31) || num_slots % kBlock ||
+      capacity < 1 || capacity >= (1LL << 31) || num_free == num_free_out)
+    return MSA_ERR_SHAPE;
+  msa_status st = check_ws(workspace, workspace_bytes, kHeaderBytes);
+  if (st != MSA_OK) return st;
+  const SlotsLaunch L{seq_lens, new_lens, batch,        page_table, max_blocks, free_pages, free_capacity, num_free,
+                      num_slots / kBlock, capacity, cu_seqlens_q, slots, positions, num_free_out,
+                      static_cast<DevError*>(workspace)};
+  return cuda_result(launch_map_slots(L, static_cast<cudaStream_t>(stream)));
+}
+
+// The checks that both rotary calls share.
+static msa_status check_rotary(const msa_rotary_config* rot, const void* q, int64_t q_stride, int q_heads,
+                               const int32_t* positions, const float* inv_freq, int64_t tokens, const void* q_out) {
+  if (!rot || !q || !positions || !inv_freq || !q_out) return MSA_ERR_NULL;
+  if (rot->rot_dim < 16 || rot->rot_dim > kDim || rot->rot_dim % 16 || rot->num_axes < 1 || rot->num_axes > 4 ||
+      (rot->interleaved != 0 && rot->interleaved != 1))
+    return MSA_ERR_SHAPE;
+  for (int j = 0; j < rot->rot_dim / 2; ++j)
+    if (rot->axis[j] >= rot->num_axes) return MSA_ERR_SHAPE;
+  if (tokens < 1 || tokens >= (1LL << 31) || q_heads < 1 || q_heads > kHeads || q_stride % 8 ||
+      q_stride < static_cast<int64_t>(q_heads) * kDim)
+    return MSA_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(q_out)) return MSA_ERR_ALIGN;
+  return MSA_OK;
+}
+
+msa_status msa_rotary(const msa_rotary_config* rot, const void* q, int64_t q_stride, int q_heads, const void* k,
+                      int64_t k_stride, int k_heads, const int32_t* positions, const float* inv_freq, int64_t tokens,
+                      int inverse, void* q_out, void* k_out, void* stream) {
+  msa_status st = check_rotary(rot, q, q_stride, q_heads, positions, inv_freq, tokens, q_out);
+  if (st != MSA_OK) return st;
+  if (!k != !k_out) return MSA_ERR_NULL;
+  if (k && (k_heads < 1 || k_heads > kHeads || k_stride % 8 || k_stride < static_cast<int64_t>(k_heads) * kDim))
+    return MSA_ERR_SHAPE;
+  if (k && (!aligned16(k) || !aligned16(k_out))) return MSA_ERR_ALIGN;
+  RotaryLaunch L{};
+  L.rot = *rot;
+  L.q = q;
+  L.k = k;
+  L.q_stride = q_stride;
+  L.k_stride = k_stride;
+  L.q_heads = q_heads;
+  L.k_heads = k ? k_heads : 0;
+  L.positions = positions;
+  L.inv_freq = inv_freq;
+  L.tokens = tokens;
+  L.inverse = inverse != 0;
+  L.q_out = q_out;
+  L.k_out = k_out;
+  return cuda_result(launch_rotary(L, static_cast<cudaStream_t>(stream)));
+}
+
+msa_status msa_rotary_insert(const msa_rotary_config* rot, const void* q, int64_t q_stride, const void* k,
+                             int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                             const float* inv_freq, const int64_t* slots, int64_t tokens, void* q_out, void* k_out,
+                             void* k_cache, void* v_cache, int kv_fp8, float k_scale, float v_scale,
+                             int64_t num_slots, void* workspace, size_t workspace_bytes, void* stream) {
+  msa_status st = check_rotary(rot, q, q_stride, kHeads, positions, inv_freq, tokens, q_out);
+  if (st != MSA_OK) return st;
+  if (!k || !v || !slots || !k_cache || !v_cache) return MSA_ERR_NULL;
+  if (k_stride % 8 || k_stride < kKvHeads * kDim || v_stride % 8 || v_stride < kKvHeads * kDim || num_slots < 1 ||
+      num_slots >= (1LL << 31))
+    return MSA_ERR_SHAPE;
+  if (kv_fp8 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale)))
+    return MSA_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || (k_out && !aligned16(k_out)))
+    return MSA_ERR_ALIGN;
+  if ((st = check_ws(workspace, workspace_bytes, kHeaderBytes)) != MSA_OK) return st;
+  RotaryLaunch L{};
+  L.rot = *rot;
+  L.q = q;
+  L.k = k;
+  L.v = v;
+  L.q_stride = q_stride;
+  L.k_stride = k_stride;
+  L.v_stride = v_stride;
+  L.q_heads = kHeads;
+  L.k_heads = kKvHeads;
+  L.positions = positions;
+  L.inv_freq = inv_freq;
+  L.tokens = tokens;
+  L.q_out = q_out;
+  L.k_out = k_out;
+  L.slots = slots;
+  L.k_cache = k_cache;
+  L.v_cache = v_cache;
+  L.kv_fp8 = kv_fp8 != 0;
+  L.k_scale = k_scale;
+  L.v_scale = v_scale;
+  L.num_slots = num_slots;
+  L.err = static_cast<DevError*>(workspace);
+  return cuda_result(launch_rotary(L, static_cast<cudaStream_t>(stream)));
+}
+
+static msa_status attend_chunk(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
+                               int kv_fp8, float k_scale, float v_scale, const int32_t* seq_lens,
+                               const int32_t* page_table, const int32_t* cu_seqlens_q, int batch, int max_blocks,
+                               int64_t total_tokens, int64_t num_slots, float scale, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  msa_status st = msa_config_check(cfg);
+  if (st != MSA_OK) return st;
+  if (!q || !k_cache || !v_cache || !seq_lens || !page_table || !cu_seqlens_q || !out) return MSA_ERR_NULL;
+  if (batch < 1 || max_blocks < 1 || max_blocks > 0x7fffffff / kBlock || total_tokens < 1 ||
+      total_tokens >= (1LL << 31) || num_slots < 1 || num_slots >= (1LL << 31) || num_slots % kBlock)
+    return MSA_ERR_SHAPE;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return MSA_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return MSA_ERR_ALIGN;
+  if ((st = check_ws(workspace, workspace_bytes, kHeaderBytes + attend_chunk_bytes(total_tokens, max_blocks))) !=
+      MSA_OK)
+    return st;
+  ChunkLaunch L{};
+  L.q = q;
+  L.k = k_cache;
+  L.v = v_cache;
+  L.kv_fp8 = kv_fp8;
+  L.k_scale = k_scale;
+  L.v_scale = v_scale;
+  L.seq_lens = seq_lens;
+  L.page_table = page_table;
+  L.cu = cu_seqlens_q;
+  L.batch = batch;
+  L.max_blocks = max_blocks;
+  L.tokens = total_tokens;
+  L.num_slots = num_slots;
+  L.scale = scale;
+  L.out = out;
+  L.lse = lse;
+  L.scratch = static_cast<uint8_t*>(workspace) + kHeaderBytes;
+  L.err = static_cast<DevError*>(workspace);
+  return cuda_result(launch_attend_chunk(L, static_cast<cudaStream_t>(stream)));
+}
+
+msa_status msa_attend_chunk(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* seq_lens, const int32_t* page_table, const int32_t* cu_seqlens_q,
+                            int batch, int max_blocks, int64_t total_tokens, int64_t num_slots, float scale,
+                            void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return attend_chunk(cfg, q, k_cache, v_cache, 0, 1.f, 1.f, seq_lens, page_table, cu_seqlens_q, batch, max_blocks,
+                      total_tokens, num_slots, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_attend_chunk_fp8kv(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
+                                  float k_scale, float v_scale, const int32_t* seq_lens, const int32_t* page_table,
+                                  const int32_t* cu_seqlens_q, int batch, int max_blocks, int64_t total_tokens,
+                                  int64_t num_slots, float scale, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+    return MSA_ERR_SHAPE;
+  return attend_chunk(cfg, q, k_cache, v_cache, 1, k_scale, v_scale, seq_lens, page_table, cu_seqlens_q, batch,
+                      max_blocks, total_tokens, num_slots, scale, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -72,6 +72,62 @@ struct IpLaunch {
   DevError* err;
 };
 cudaError_t launch_index_produce(const IpLaunch& L, cudaStream_t stream);
+// One msa_map_slots call (arguments as declared in msa.h).
+struct SlotsLaunch {
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int batch;
+  int32_t* page_table;
+  int max_blocks;
+  const int32_t* free_pages;
+  long long free_capacity;
+  const int32_t* num_free;
+  long long num_pages;
+  long long capacity;
+  int32_t* cu;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* num_free_out;
+  DevError* err;
+};
+cudaError_t launch_map_slots(const SlotsLaunch& L, cudaStream_t stream);
+// One rotary call; cache rows are written where k_cache is given.
+struct RotaryLaunch {
+  msa_rotary_config rot;
+  const void *q, *k, *v;            // bf16; k, v may be null
+  long long q_stride, k_stride, v_stride;
+  int q_heads, k_heads;
+  const int32_t* positions;
+  const float* inv_freq;
+  long long tokens;
+  int inverse;
+  void *q_out, *k_out;              // k_out may be null
+  const int64_t* slots;
+  void *k_cache, *v_cache;          // null without insertion
+  int kv_fp8;
+  float k_scale, v_scale;
+  long long num_slots;
+  DevError* err;
+};
+cudaError_t launch_rotary(const RotaryLaunch& L, cudaStream_t stream);
+// One chunk attention call.
+struct ChunkLaunch {
+  const void *q, *k, *v;
+  int kv_fp8;
+  float k_scale, v_scale;
+  const int32_t* seq_lens;
+  const int32_t* page_table;
+  const int32_t* cu;
+  int batch, max_blocks;
+  long long tokens, num_slots;
+  float scale;
+  void* out;
+  float* lse;
+  uint8_t* scratch;
+  DevError* err;
+};
+cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream);
+size_t attend_chunk_bytes(long long tokens, int max_blocks);
 // First step of every launcher.  Clears the calling thread's last CUDA error
 // (the launches are checked with cudaGetLastError, which reports the calling
 // thread's error) and makes the current device's primary context current on

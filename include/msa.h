@@ -65,7 +65,13 @@ typedef enum {
 enum { MSA_INDEX_BF16 = 0, MSA_INDEX_E4M3 = 1 };
 
 /* Workspace modes for msa_workspace_size. */
-enum { MSA_MODE_DECODE = 0, MSA_MODE_PREFILL = 1, MSA_MODE_PACK = 2, MSA_MODE_PREFILL_BWD = 3 };
+enum {
+  MSA_MODE_DECODE = 0,
+  MSA_MODE_PREFILL = 1,
+  MSA_MODE_PACK = 2,
+  MSA_MODE_PREFILL_BWD = 3,
+  MSA_MODE_CHUNK = 4
+};
 
 /* Device error codes reported by msa_read_device_error. */
 enum {
@@ -74,8 +80,10 @@ enum {
   MSA_DEVERR_BLOCK = 2,    /* q2k id outside [0, blocks of the query) */
   MSA_DEVERR_LENGTH = 3,   /* seq_len < 1, or above max_blocks * 128 */
   MSA_DEVERR_TIMEOUT = 4,  /* a bounded on-chip wait gave up */
-  MSA_DEVERR_RANGE = 5     /* prefill attention: a score outside the fixed-reference range (see
+  MSA_DEVERR_RANGE = 5,    /* prefill attention: a score outside the fixed-reference range (see
                               msa_sparse_attend_prefill); detail = the flat q2k index */
+  MSA_DEVERR_FULL = 6      /* msa_map_slots: no free page, or no room in the token buffers, for
+                              request `detail` */
 };
 
 /* Layer configuration (TensorRT-LLM MiniMaxM3SparseAttentionConfig fields:
@@ -110,6 +118,8 @@ msa_status msa_config_check(const msa_config* cfg);
  *   MSA_MODE_PREFILL: n = total compact tokens, max_blocks = ceil(max_seqlen/128).
  *   MSA_MODE_PACK   : n = batch * seq of the document map, max_blocks = batch.
  *   MSA_MODE_PREFILL_BWD: as MSA_MODE_PREFILL, for msa_sparse_attend_prefill_backward.
+ *   MSA_MODE_CHUNK  : n = total new tokens, max_blocks = blocks per row of the page table,
+ *                     for msa_attend_chunk; only its first 256 bytes need the zero-fill.
  * The workspace must be zero-filled once before its first use (see
  * msa_workspace_init), which clears the device error word and the decode
  * scorer's page-claim counter in its first 256 bytes, and the completion
@@ -446,6 +456,150 @@ msa_status msa_pack(const void* external, const int64_t* token_rows, int64_t tot
  * every other row of external dev [batch_seq, row_bytes] zero-filled. */
 msa_status msa_unpack(const void* packed, const int64_t* token_rows, int64_t total_tokens,
                       int64_t batch_seq, int64_t row_bytes, void* external, void* stream);
+
+/* ---- chunked serving over the paged cache -----------------------------------
+ * The step of a serving batch in which request r brings new_lens[r] new tokens
+ * (one when it decodes, a chunk of its prompt otherwise) at the end of a
+ * context of seq_lens[r] tokens, the new ones included:
+ *   msa_map_slots      opens their pages and gives each new token its slot,
+ *   msa_rotary_insert  rotates Q and K and writes K and V at those slots,
+ *   msa_attend_chunk   attends each new token to all its keys in the cache.
+ * Pages are the 128-slot pages of the decode calls, so the cache that these
+ * calls fill is the one that msa_select_blocks_decode and
+ * msa_sparse_attend_decode read (those give the slots behind a request's last
+ * key the weight zero, so a cache for them has to be finite there: zero-fill it
+ * once; msa_attend_chunk reads past NaN). */
+
+/* Page-table rows and slot maps from the requests' lengths, on the device.
+ * With old = seq_lens[r] - new_lens[r], request r holds its first
+ * ceil(old / 128) pages already; the pages up to ceil(seq_lens[r] / 128) are
+ * taken from the top of a stack of free page ids, in request order.
+ *   seq_lens, new_lens dev int32 [batch]; 0 <= new_lens[r] <= seq_lens[r] <= max_blocks * 128
+ *   page_table   dev int32 [batch, max_blocks]; the entries of the opened pages
+ *                are written, every other entry is left as it is
+ *   free_pages   dev int32 [free_capacity]: the stack, its top at num_free[0] - 1
+ *                (NULL with free_capacity 0)
+ *   num_free     dev int32 [1]
+ *   num_slots    slots of the cache, a multiple of 128
+ *   capacity     rows of slots and positions (>= the new tokens; a larger one
+ *                lets a captured graph serve batches of several sizes)
+ *   cu_seqlens_q dev int32 [batch + 1]: offsets of the requests' new tokens
+ *   slots        dev int64 [capacity]: new token i of request r sits at position
+ *                p = old + i, row cu_seqlens_q[r] + i, slot
+ *                page_table[r, p / 128] * 128 + p % 128; -1 in the rows behind the
+ *                last token
+ *   positions    dev int32 [capacity]: p; 0 behind the last token
+ *   num_free_out dev int32 [1]: num_free less the opened pages (not num_free itself:
+ *                a repeated call with the same inputs gives the same result)
+ * A request with bad lengths maps nothing (MSA_DEVERR_LENGTH, detail r).  The
+ * first request that the free pages or the capacity do not hold maps nothing,
+ * and neither does any after it (MSA_DEVERR_FULL, detail r); a num_free outside
+ * [0, free_capacity] counts as 0.  A page id outside the pool gives slot -1, and
+ * -1 in the table if it came from the stack (MSA_DEVERR_PAGE, detail = row).
+ *   workspace    >= 256 bytes (only its device error word is used)
+ * Errors: MSA_ERR_NULL, MSA_ERR_SHAPE (sizes out of range, num_slots not a
+ * multiple of 128, num_free_out the same as num_free), MSA_ERR_WORKSPACE,
+ * MSA_ERR_CUDA. */
+msa_status msa_map_slots(const int32_t* seq_lens, const int32_t* new_lens, int batch,
+                         int32_t* page_table, int max_blocks, const int32_t* free_pages,
+                         int64_t free_capacity, const int32_t* num_free, int64_t num_slots,
+                         int64_t capacity, int32_t* cu_seqlens_q, int64_t* slots,
+                         int32_t* positions, int32_t* num_free_out, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Rotary positions with several axes.  The first rot_dim dims of a head form
+ * rot_dim / 2 pairs: (x[j], x[j + rot_dim / 2]), or (x[2j], x[2j + 1]) when
+ * interleaved.  Pair j turns by positions[axis[j]][t] * inv_freq[j]:
+ *   a' = a cos - b sin, b' = a sin + b cos;
+ * the dims from rot_dim on pass unchanged.  The angle is taken from the exact
+ * product (reduced in binary64, so a position of a million keeps its fraction),
+ * the rotation is computed in fp32 and rounded once.
+ * rot_dim: a multiple of 16 in [16, 128]; 1 <= num_axes <= 4; axis[j] < num_axes
+ * for j < rot_dim / 2. */
+typedef struct {
+  int rot_dim;
+  int interleaved;
+  int num_axes;
+  uint8_t axis[64];
+} msa_rotary_config;
+
+/* Rotates q and k (k may be NULL, with k_out NULL):
+ *   q         dev bf16 [tokens, q_heads, 128], consecutive tokens q_stride elements
+ *             apart (a multiple of 8, >= q_heads * 128: q may be a slice of a fused
+ *             projection's output); k with k_heads and k_stride likewise; 1 to 64 heads
+ *   positions dev int32 [num_axes, tokens];  inv_freq dev fp32 [rot_dim / 2]
+ *   inverse   1 turns by the negative angle: the backward, dq from q_out's gradient
+ *   q_out     dev bf16 [tokens, q_heads, 128] dense; may be q itself where q is dense
+ *             (no other overlap); k_out likewise
+ * Errors: MSA_ERR_NULL, MSA_ERR_SHAPE, MSA_ERR_ALIGN, MSA_ERR_CUDA. */
+msa_status msa_rotary(const msa_rotary_config* rot, const void* q, int64_t q_stride, int q_heads,
+                      const void* k, int64_t k_stride, int k_heads, const int32_t* positions,
+                      const float* inv_freq, int64_t tokens, int inverse, void* q_out, void* k_out,
+                      void* stream);
+
+/* The same rotation of q (64 heads) and k (4 heads), with the rotated k and v
+ * written at slots[t] of the paged caches; a row with a negative slot is not
+ * inserted, and no other slot is touched.  Two rows with the same slot leave
+ * one of the two there.
+ *   v         dev bf16 [tokens, 4, 128], v_stride as q_stride
+ *   slots     dev int64 [tokens]; one outside the cache is skipped and recorded
+ *             (MSA_DEVERR_PAGE, detail = the row)
+ *   k_cache, v_cache dev [num_slots, 4, 128]: bf16, or with kv_fp8 E4M3 bytes
+ *             standing for k_scale * k and v_scale * v (as
+ *             msa_sparse_attend_decode_fp8kv reads them): x / scale rounded once to
+ *             nearest even, saturating at +-448
+ *   k_scale, v_scale finite and > 0 (unused for a bf16 cache)
+ *   k_out     dev bf16 [tokens, 4, 128] or NULL: the rotated k, packed as well
+ *   workspace >= 256 bytes (only its device error word is used)
+ * Errors: MSA_ERR_NULL, MSA_ERR_SHAPE, MSA_ERR_ALIGN, MSA_ERR_WORKSPACE, MSA_ERR_CUDA. */
+msa_status msa_rotary_insert(const msa_rotary_config* rot, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const int32_t* positions, const float* inv_freq, const int64_t* slots,
+                             int64_t tokens, void* q_out, void* k_out, void* k_cache, void* v_cache,
+                             int kv_fp8, float k_scale, float v_scale, int64_t num_slots,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention of the new tokens over all their keys in the paged cache:
+ *   out[t, h, :] = softmax_j(scale * <q[t,h,:], k[j, h/16, :]>) v[j, h/16, :]
+ * for row t = cu_seqlens_q[r] + i over the keys j <= p of request r, where
+ * p = seq_lens[r] - new + i, new = cu_seqlens_q[r+1] - cu_seqlens_q[r].
+ *   q            dev bf16 [total_tokens, 64, 128]
+ *   k_cache, v_cache dev bf16 [num_slots, 4, 128]
+ *   seq_lens     dev int32 [batch], the new tokens included and already in the cache
+ *   page_table   dev int32 [batch, max_blocks]
+ *   cu_seqlens_q dev int32 [batch + 1], cu_seqlens_q[0] = 0, not decreasing; rows from
+ *                cu_seqlens_q[batch] on are not read, and their out and lse not written
+ *   scale        finite and > 0
+ *   out          dev bf16 [total_tokens, 64, 128]
+ *   lse          dev fp32 [total_tokens, 64] or NULL: log2 of the softmax denominator
+ *                in the base-2 domain of the scaled scores
+ *   workspace    >= msa_workspace_size(cfg, MSA_MODE_CHUNK, total_tokens, max_blocks)
+ * Slots behind a request's last key do not reach its rows, whatever they hold.
+ * A request with bad lengths (new > seq_lens[r], or seq_lens[r] > max_blocks *
+ * 128) gets out 0 and lse -inf (MSA_DEVERR_LENGTH, detail r); the keys of a page
+ * whose id is outside the pool are left out (MSA_DEVERR_PAGE, detail = the flat
+ * page-table index); a row left without a key gets 0 and -inf.  fp32 accumulation;
+ * the softmax weights enter the product with V in bf16, their sum is fp32 over
+ * the unrounded weights.  The result is bitwise reproducible.
+ * Errors: MSA_ERR_NULL, MSA_ERR_SHAPE, MSA_ERR_ALIGN, MSA_ERR_WORKSPACE, MSA_ERR_CUDA. */
+msa_status msa_attend_chunk(const msa_config* cfg, const void* q, const void* k_cache,
+                            const void* v_cache, const int32_t* seq_lens,
+                            const int32_t* page_table, const int32_t* cu_seqlens_q, int batch,
+                            int max_blocks, int64_t total_tokens, int64_t num_slots, float scale,
+                            void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* The same over an FP8 cache: k_cache, v_cache dev uint8 [num_slots, 4, 128],
+ * E4M3 bytes standing for k_scale * k and v_scale * v (finite, > 0), as
+ * msa_sparse_attend_decode_fp8kv: the E4M3 values and q enter fp16 products (q
+ * is exact for |q| in 2^-14 .. 65504), the softmax weights in fp16. */
+msa_status msa_attend_chunk_fp8kv(const msa_config* cfg, const void* q, const void* k_cache,
+                                  const void* v_cache, float k_scale, float v_scale,
+                                  const int32_t* seq_lens, const int32_t* page_table,
+                                  const int32_t* cu_seqlens_q, int batch, int max_blocks,
+                                  int64_t total_tokens, int64_t num_slots, float scale, void* out,
+                                  float* lse, void* workspace, size_t workspace_bytes,
+                                  void* stream);
 
 #ifdef __cplusplus
 }
