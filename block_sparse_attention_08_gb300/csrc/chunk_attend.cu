@@ -2,94 +2,887 @@
 // keys in the paged cache (bf16 or E4M3).
 //
 // out[t, h] = sum_j p_j v_j / sum_j p_j, p_j = 2^(x_j - m), x_j = scale log2(e)
-// <q, k_j>, over the keys j <= the token's position; the running maximum m and
-// the sums are kept in one pass over the keys (when m grows, the sums so far
-// are multiplied by 2^(m_old - m_new)).
+// <q, k_j>, over the keys j <= the token's position.  One pass over the keys, a
+// block of 128 at a time: the sums are taken against a reference m, and when a
+// block's maximum passes it by more than kCaSlack (the weights would grow past
+// 2^kCaSlack) m is raised and the sums so far are multiplied by
+// 2^(m_old - m_new).
 //
-// This form: one warp per (token, query head), four dims per lane, one key at
-// a time.
-#include <cuda_fp8.h>
+// An item is 16 consecutive new tokens of a request and one KV head: 256 rows
+// (token, query head) that share their keys, as two tiles of 128 rows.  Its work
+// is counted in units of one 128-key block, and every CTA takes an equal
+// contiguous share of all units of the batch, wherever that cuts an item: a long
+// context with one new token is spread over the GPU like a long chunk is.  The
+// pieces of a cut item leave (m, sum of p, sum of p v) in scratch, and a second
+// kernel joins them.  Each CTA finds its share itself from the lengths (no
+// planning launch, nothing kept between calls).
+//
+// Roles: a producer warp walks the share and copies Q rows and K and V pages by
+// TMA; an MMA thread issues S = Q K^T and O += P V on the tensor cores (S, P and
+// O in tensor memory, P over the S it came from); two warpgroups turn S into P,
+// one row per thread.  With more than 8 tokens each warpgroup owns a tile, and
+// all blocks pass both; with 8 or fewer there is one tile, and the warpgroups
+// take its blocks in turn, each into sums of its own, joined at the end: the
+// tensor cores work on one block while the other's softmax runs.  An E4M3 cache
+// has a third warpgroup that widens each page to fp16 (exactly) in shared memory.
+#include <cuda_fp16.h>
 
 #include "launch.h"
 
 namespace msa {
 
-constexpr int kCaWarps = 8;
+constexpr int kCaTok = 16;            // new tokens per item
+constexpr int kCaTile = 128 * 256;    // 128 rows x 128 dims of 16 bits
+constexpr int kCaHalf = kCaTile / 2;  // one 64-dim half
+constexpr int kCaQEntry = 4096;       // one token's 16 heads x 128 dims
+constexpr int kCaInfo = 4;            // item descriptors in flight
+constexpr int kCaBad = 8;             // block flags in flight (at most 5 blocks are)
+constexpr int kCaMmaWarp = 9, kCaProducerWarp = 8, kCaWidenWarp = 10;
+constexpr float kCaSlack = 8.f;
+// tensor memory: S of warpgroup w (and P over its first half) at 128 w, O at 256 + 128 w
+constexpr uint32_t kCaOCol = 256;
 
-size_t attend_chunk_bytes(long long, int) { return 0; }
+// A piece of an item: blocks b0 .. b0 + nb - 1.  nb = 0 ends the list.
+struct CaItem {
+  int t0, ntok, g;  // first row of q, tokens, KV head
+  int pos0, len;    // position of the first token, keys of the request
+  int b0, nb;
+  int slot;         // partial slot, or -1: the piece is the whole item
+};
+// For the joining kernel: an item that begins in CTA c and ends in CTA `last`.
+struct CaCut {
+  int t0, ntok, g, last;
+};
+
+struct CaArgs {
+  const int32_t* seq_lens;
+  const int32_t* page_table;
+  const int32_t* cu;
+  int batch, max_blocks, num_pages;
+  long long tokens;
+  float scale_log2, v_scale;
+  __nv_bfloat16* out;
+  float* lse;
+  CaCut* cuts;      // [kNumSMs]
+  float* part_o;    // [2 kNumSMs][rows][128]
+  float2* part_ml;  // [2 kNumSMs][rows]
+  int rows;         // rows of a partial slot
+  DevError* err;
+};
 
 template <bool kFp8>
-__device__ __forceinline__ float4 ca_load(const void* cache, long long at, int lane) {
-  if (kFp8) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(cache) + at)[lane];
-    const __nv_fp8_e4m3* b = reinterpret_cast<const __nv_fp8_e4m3*>(&w);
-    return make_float4(float(b[0]), float(b[1]), float(b[2]), float(b[3]));
+struct CaShape {
+  static constexpr int kTiles = kFp8 ? 3 : 5;  // 16-bit K / V tiles
+  static constexpr int kRaw = kFp8 ? 4 : 0;    // E4M3 tiles as copied
+  static constexpr int kThreads = kFp8 ? 448 : 320;
+  // fp16 weights are kept near the top of their range (at most 2^(kLift + kCaSlack) = 2^15), so that small ones
+  // stay normal down to 2^-21 of the largest
+  static constexpr float kLift = kFp8 ? 7.f : 0.f;
+};
+
+template <bool kFp8>
+struct CaSmem {
+  uint8_t q[2][kCaTile];
+  uint8_t kv[CaShape<kFp8>::kTiles][kCaTile];
+  uint8_t raw[CaShape<kFp8>::kRaw ? CaShape<kFp8>::kRaw : 1][kFp8 ? kCaHalf : 16];
+  float2 ml[2][128];
+  uint64_t q_full[2], q_ready[2], q_empty[2];  // q_ready: as fp16 (E4M3 cache)
+  uint64_t kv_full[CaShape<kFp8>::kTiles], kv_empty[CaShape<kFp8>::kTiles];
+  uint64_t raw_full[4], raw_empty[4];
+  uint64_t s_full[2], p_full[2], o_full[2], x_full, x_done, done;
+  uint64_t info_full[kCaInfo], info_empty[kCaInfo];
+  CaItem info[kCaInfo];
+  int bad[kCaBad];
+  long long wsum[16];
+  long long start_unit;
+  int start_r;
+  uint32_t tmem_base;
+};
+
+// ---- the units of a request --------------------------------------------------------
+
+// sum of floor(y / 8) over 0 <= y < x
+__device__ __forceinline__ long long ca_eighths(long long x) {
+  const long long q = x >> 3;
+  return 4 * q * (q - 1) + q * (x & 7);
+}
+// A request's n new tokens at positions len - n .. len - 1, as ceil(n / 16) items per KV head; item i sees the
+// blocks up to its last token's.
+struct CaReq {
+  int t0, n, len;
+  __device__ __forceinline__ int items() const { return (n + kCaTok - 1) / kCaTok; }
+  __device__ __forceinline__ int blocks(int i) const {
+    return (len - n + min(n, kCaTok * (i + 1)) - 1) / kBlock + 1;
   }
-  const uint2 w = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(cache) + at)[lane];
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
+  // blocks of the items before item i
+  __device__ __forceinline__ long long before(int i) const {
+    const long long a = (static_cast<long long>(len) - n + kCaTok - 1) / kCaTok;
+    long long s = ca_eighths(a + i) - ca_eighths(a) + i;
+    // the last item may end short of 16 tokens
+    if (i == items() && i > 0) s += blocks(i - 1) - ((len - n + static_cast<long long>(kCaTok) * i - 1) / kBlock + 1);
+    return s;
+  }
+  __device__ __forceinline__ long long per_head() const { return n > 0 ? before(items()) : 0; }
+};
+__device__ __forceinline__ bool ca_good(const CaArgs& a, long long c0, long long c1, int len) {
+  return c0 >= 0 && c0 <= c1 && c1 <= a.tokens && c1 - c0 <= len && (len + kBlock - 1LL) / kBlock <= a.max_blocks;
+}
+// Request r; one with bad lengths has no tokens.
+__device__ __forceinline__ CaReq ca_req(const CaArgs& a, int r) {
+  const int c0 = a.cu[r], c1 = a.cu[r + 1], len = a.seq_lens[r];
+  return ca_good(a, c0, c1, len) ? CaReq{c0, c1 - c0, len} : CaReq{0, 0, 0};
+}
+// Zeros for the rows of a request with bad lengths (the whole warp).
+__device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
+  if (lane == 0) record_error(a.err, MSA_DEVERR_LENGTH, r);
+  const long long c0 = max(0, a.cu[r]), c1 = min(a.tokens, static_cast<long long>(a.cu[r + 1]));
+  uint4* out = reinterpret_cast<uint4*>(a.out);
+  for (long long i = c0 * (kHeads * kDim / 8) + lane; i < c1 * (kHeads * kDim / 8); i += 32)
+    out[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (a.lse)
+    for (long long i = c0 * kHeads + lane; i < c1 * kHeads; i += 32) a.lse[i] = -INFINITY;
+}
+
+// Instruction descriptors: fp32 accumulation, A and B bf16 (or fp16), M = N = 128; B (V) MN-major for O.
+__host__ __device__ constexpr uint32_t ca_idesc(bool fp16) {
+  return fp16 ? tc::idesc_bf16_f32(128, 128) & ~((1u << 7) | (1u << 10)) : tc::idesc_bf16_f32(128, 128);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ bool ca_wait(uint64_t* bar, uint32_t parity, DevError* err, int where) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, where));
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kCaWarps * 32) chunk_attend_kernel(ChunkLaunch a, float scale_log2) {
-  const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * kCaWarps + (threadIdx.x >> 5);
-  const long long t = w / kHeads;
-  const int h = static_cast<int>(w - t * kHeads), g = h / kGroup;
-  if (t >= a.tokens || t >= a.cu[a.batch]) return;
-  int lo = 0, hi = a.batch - 1;  // the request r with cu[r] <= t < cu[r + 1]
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.cu[mid] <= t) lo = mid;
-    else hi = mid - 1;
+__global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kernel(
+    const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CaArgs a) {
+  using Shape = CaShape<kFp8>;
+  constexpr int kTiles = Shape::kTiles, kThreads = Shape::kThreads;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  CaSmem<kFp8>& sm = *reinterpret_cast<CaSmem<kFp8>*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  DevError* err = a.err;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (smem_u32(smem_raw) & 1023) {  // the swizzled tiles need it; with no static shared memory it holds
+    if (tid == 0) record_error(err, MSA_DEVERR_TIMEOUT, 899);
+    return;
   }
-  const int len = a.seq_lens[lo], fresh = a.cu[lo + 1] - a.cu[lo];
-  long long keys = min(static_cast<long long>(len), len - fresh + (t - a.cu[lo]) + 1);
-  if (fresh > len || len > a.max_blocks * static_cast<long long>(kBlock)) {
-    if (lane == 0) record_error(a.err, MSA_DEVERR_LENGTH, lo);
-    keys = 0;
-  }
-  const float4 q = ca_load<false>(a.q, (t * kHeads + h) * kDim, lane);
-  float m = -INFINITY, l = 0.f, c = 0.f;  // c: what the additions to l have rounded away
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (long long j = 0; j < keys; ++j) {
-    const long long e = lo * static_cast<long long>(a.max_blocks) + j / kBlock;
-    const int page = a.page_table[e];
-    if (page < 0 || (page + 1LL) * kBlock > a.num_slots) {
-      if (lane == 0) record_error(a.err, MSA_DEVERR_PAGE, e);
-      j |= kBlock - 1;
-      continue;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_ready[i], 4);
+      mbar_init(&sm.q_empty[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.o_full[i], 1);
     }
-    const long long at = ((static_cast<long long>(page) * kBlock + j % kBlock) * kKvHeads + g) * kDim;
-    const float4 k = ca_load<kFp8>(a.k, at, lane), v = ca_load<kFp8>(a.v, at, lane);
-    float x = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x *= scale_log2;
-    const float mn = fmaxf(m, x), f = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(x - mn);
-    const float lf = l * f, y = fmaf(-c, f, p), sum = lf + y;
-    c = (sum - lf) - y;
-    l = sum;
-    o.x = o.x * f + p * v.x;
-    o.y = o.y * f + p * v.y;
-    o.z = o.z * f + p * v.z;
-    o.w = o.w * f + p * v.w;
-    m = mn;
+    for (int i = 0; i < kTiles; ++i) {
+      mbar_init(&sm.kv_full[i], kFp8 ? 4 : 1);
+      mbar_init(&sm.kv_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.raw_full[i], 1);
+      mbar_init(&sm.raw_empty[i], 4);
+    }
+    mbar_init(&sm.x_full, 8);
+    mbar_init(&sm.x_done, 8);
+    mbar_init(&sm.done, 1);
+    for (int i = 0; i < kCaInfo; ++i) {
+      mbar_init(&sm.info_full[i], 1);
+      mbar_init(&sm.info_empty[i], kFp8 ? 13 : 9);  // the softmax warps, the MMA warp, the widening warps
+    }
+    fence_mbar_init();
+    sm.start_r = -1;
   }
-  const float inv = l > 0.f ? a.v_scale / l : 0.f;
-  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (t * kHeads + h) * kDim)[lane] =
-      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (a.lse && lane == 0) a.lse[t * kHeads + h] = l > 0.f ? m + log2f(l) : -INFINITY;
+  if (warp == kCaMmaWarp) {
+    tc::alloc(&sm.tmem_base, 512);
+    tc::relinquish();
+  }
+
+  // ---- this CTA's share of the units ----
+  // pass 1: all units; pass 2: the request that holds the first unit of the share
+  auto warp_incl = [&](long long x) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    return x;
+  };
+  long long total = 0, first_units = 0;
+  for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
+    const int r = r0 + tid;
+    long long u = 0;
+    bool bad = false;
+    if (r < a.batch) {
+      const int c0 = a.cu[r], c1 = a.cu[r + 1], len = a.seq_lens[r];
+      bad = !ca_good(a, c0, c1, len);
+      if (!bad) u = kKvHeads * CaReq{c0, c1 - c0, len}.per_head();
+    }
+    if (r0 == 0) first_units = u;
+    for (unsigned m = __ballot_sync(0xffffffffu, bad && r % gridDim.x == blockIdx.x); m; m &= m - 1)
+      ca_refuse(a, r0 + warp * 32 + __ffs(m) - 1, lane);
+    const long long incl = warp_incl(u);
+    if (lane == 31) sm.wsum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) total += sm.wsum[w];
+    __syncthreads();
+  }
+  const long long ctas = min(static_cast<long long>(gridDim.x), max(total, 1LL));
+  const long long u0 = min(total, total * blockIdx.x / ctas), u1 = min(total, total * (blockIdx.x + 1) / ctas);
+  if (u0 < u1) {
+    long long base = 0;
+    for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
+      const int r = r0 + tid;
+      long long u = first_units;
+      if (r0) u = r < a.batch ? kKvHeads * ca_req(a, r).per_head() : 0;
+      const long long incl = warp_incl(u);
+      if (lane == 31) sm.wsum[warp] = incl;
+      __syncthreads();
+      long long before = base;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sm.wsum[w];
+        base += sm.wsum[w];
+      }
+      before += incl - u;
+      if (before <= u0 && u0 < before + u) {
+        sm.start_r = r;
+        sm.start_unit = u0 - before;
+      }
+      __syncthreads();
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  // A wait that gives up (recorded in the error word) ends its role, so a broken pipeline ends after one bounded wait
+  // per role.
+  if (warp == kCaProducerWarp) {
+    // ---------------- the share's items, and their copies ----------------
+    if (lane == 0) {
+      prefetch_tmap(&qmap);
+      prefetch_tmap(&kmap);
+      prefetch_tmap(&vmap);
+    }
+    CaCut cut{0, 0, 0, 0};
+    int nitem = 0, nq = 0, nload = 0, nblk = 0;  // descriptors, Q tiles, K / V tiles and blocks issued
+    bool ok = true;
+    if (u0 < u1) {
+      int r = sm.start_r;
+      CaReq rq = ca_req(a, r);
+      long long per = rq.per_head();
+      int g = static_cast<int>(sm.start_unit / per);
+      const long long rem = sm.start_unit - g * per;
+      int i = 0;  // the last item that begins at or before unit rem of the head
+      for (int lo = 0, hi = rq.items() - 1; lo <= hi;) {
+        const int mid = (lo + hi) >> 1;
+        if (rq.before(mid) <= rem) {
+          i = mid;
+          lo = mid + 1;
+        } else {
+          hi = mid - 1;
+        }
+      }
+      int b = static_cast<int>(rem - rq.before(i));
+      long long at = u0;
+      while (ok) {
+        const int blocks = rq.blocks(i);
+        CaItem it;
+        it.t0 = rq.t0 + kCaTok * i;
+        it.ntok = min(kCaTok, rq.n - kCaTok * i);
+        it.g = g;
+        it.pos0 = rq.len - rq.n + kCaTok * i;
+        it.len = rq.len;
+        it.b0 = b;
+        it.nb = static_cast<int>(min(static_cast<long long>(blocks - b), u1 - at));
+        const bool to_end = b + it.nb == blocks;
+        it.slot = b == 0 && to_end ? -1 : static_cast<int>(2 * blockIdx.x + (b == 0));
+        at += it.nb;
+        if (b == 0 && !to_end) {
+          const long long last_unit = at + blocks - b - it.nb - 1;
+          cut = CaCut{it.t0, it.ntok, g, static_cast<int>(((last_unit + 1) * ctas + total - 1) / total - 1)};
+        }
+        // publish
+        const int is = nitem % kCaInfo;
+        if (!(ok = ca_wait(&sm.info_empty[is], ((nitem / kCaInfo) & 1) ^ 1, err, 800))) break;
+        if (lane == 0) {
+          sm.info[is] = it;
+          mbar_arrive(&sm.info_full[is]);
+        }
+        ++nitem;
+        const int tiles = it.ntok > 8 ? 2 : 1;
+        const int32_t* row = a.page_table + static_cast<long long>(r) * a.max_blocks;
+        int ids = 0, ids_next = lane < it.nb ? row[b + lane] : 0;
+        for (int k = 0; k < it.nb && ok; ++k) {
+          if ((k & 31) == 0) {
+            ids = ids_next;
+            ids_next = k + 32 + lane < it.nb ? row[b + k + 32 + lane] : 0;
+          }
+          int page = __shfl_sync(0xffffffffu, ids, k & 31);
+          const bool bad = page < 0 || page >= a.num_pages;
+          if (bad) {
+            if (lane == 0) record_error(err, MSA_DEVERR_PAGE, static_cast<long long>(r) * a.max_blocks + b + k);
+            page = 0;
+          }
+          if (lane == 0) sm.bad[nblk % kCaBad] = bad;
+          ++nblk;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const CUtensorMap* map = kv ? &vmap : &kmap;
+            if (kFp8) {
+              const int s = nload % 4;
+              if (!(ok = ca_wait(&sm.raw_empty[s], ((nload / 4) & 1) ^ 1, err, 801))) break;
+              if (lane == 0) {
+                mbar_expect_tx(&sm.raw_full[s], kCaHalf);
+                tma_load_3d(sm.raw[kFp8 ? s : 0], map, 0, g, page * kBlock, &sm.raw_full[s]);
+              }
+            } else {
+              const int s = nload % kTiles;
+              if (!(ok = ca_wait(&sm.kv_empty[s], ((nload / kTiles) & 1) ^ 1, err, 802))) break;
+              if (lane == 0) {
+                mbar_expect_tx(&sm.kv_full[s], kCaTile);
+                tma_load_3d(sm.kv[s], map, 0, g, page * kBlock, &sm.kv_full[s]);
+                tma_load_3d(sm.kv[s] + kCaHalf, map, 64, g, page * kBlock, &sm.kv_full[s]);
+              }
+            }
+            ++nload;
+            // The item's Q follows its first K tile: that tile's place was freed by the items before, but Q's
+            // may have to wait for their last S products.
+            if (k == 0 && kv == 0) {
+              for (int q = 0; q < tiles && ok; ++q) {
+                const int s = nq & 1, n = min(8, it.ntok - 8 * q);
+                if (!(ok = ca_wait(&sm.q_empty[s], ((nq >> 1) & 1) ^ 1, err, 803))) break;
+                if (lane == 0) mbar_expect_tx(&sm.q_full[s], n * kCaQEntry);
+                __syncwarp();
+                if (lane < n)
+                  tma_load_5d(sm.q[s] + lane * kCaQEntry, &qmap, 0, 0, 0, 2 * g, it.t0 + 8 * q + lane, &sm.q_full[s]);
+                ++nq;
+              }
+              if (!ok) break;
+            }
+          }
+        }
+        if (!ok || at >= u1) break;
+        // the next item (the share goes on, so there is one)
+        b = 0;
+        if (++i == rq.items()) {
+          i = 0;
+          if (++g == kKvHeads) {
+            g = 0;
+            do {
+              rq = ca_req(a, ++r);
+            } while (rq.n == 0);
+          }
+        }
+      }
+    }
+    if (lane == 0) a.cuts[blockIdx.x] = cut;
+    if (ok && ca_wait(&sm.info_empty[nitem % kCaInfo], ((nitem / kCaInfo) & 1) ^ 1, err, 804) && lane == 0) {
+      sm.info[nitem % kCaInfo] = CaItem{0, 0, 0, 0, 0, 0, 0, 0};
+      mbar_arrive(&sm.info_full[nitem % kCaInfo]);
+    }
+    // no copy may still be landing when the CTA exits: wait for the last fill of every place
+    __syncwarp();
+    if (lane == 0) {
+      for (int s = 0; s < (kFp8 ? 4 : kTiles); ++s) {
+        const int ring = kFp8 ? 4 : kTiles, fills = (nload - s + ring - 1) / ring;
+        if (fills > 0) mbar_wait(kFp8 ? &sm.raw_full[s] : &sm.kv_full[s], (fills - 1) & 1, err, 805);
+      }
+      for (int s = 0; s < 2; ++s) {
+        const int fills = (nq - s + 1) / 2;
+        if (fills > 0) mbar_wait(&sm.q_full[s], (fills - 1) & 1, err, 806);
+      }
+    }
+  } else if (warp == kCaMmaWarp) {
+    // ---------------- S and O products ----------------
+    // Products execute in the order in which they are issued: an S product that overwrites P follows the O product
+    // that reads it.
+    constexpr uint32_t idesc_s = ca_idesc(kFp8), idesc_o = ca_idesc(kFp8) | (1u << 16);
+    int base = 0, nq = 0;       // blocks and Q tiles of the items before
+    uint32_t pcount[2] = {0, 0};  // P tiles taken
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int is = n % kCaInfo;
+      if (!(ok = ca_wait(&sm.info_full[is], (n / kCaInfo) & 1, err, 810))) break;
+      const int nb = sm.info[is].nb, b0 = sm.info[is].b0, len = sm.info[is].len;
+      const bool dual = sm.info[is].ntok > 8;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.info_empty[is]);
+      if (nb == 0) break;
+      const int steps[2] = {dual ? nb : (nb + 1) / 2, dual ? nb : nb / 2};
+      bool acc[2] = {false, false};
+      auto issue_s = [&](int w, int s) {
+        const int blk = dual ? s : 2 * s + w, load = 2 * (base + blk), st = load % kTiles;
+        const int qt = dual ? nq + w : nq, qs = qt & 1;
+        if (s == 0 && (dual || w == 0)) {
+          uint64_t* bar = kFp8 ? &sm.q_ready[qs] : &sm.q_full[qs];
+          if (!(ok = ok && ca_wait(bar, (qt >> 1) & 1, err, 811))) return;
+        }
+        if (!dual || w == 0) {
+          if (!(ok = ok && ca_wait(&sm.kv_full[st], (load / kTiles) & 1, err, 812))) return;
+        }
+        tc::fence_after();
+        if (lane == 0) {
+          const uint32_t qa = smem_u32(sm.q[qs]), ka = smem_u32(sm.kv[st]);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_bf16(tmem + 128 * w, tc::desc_k_sw128_sbo(qa + (kk >> 2) * 1024 + (kk & 3) * 32, 2048),
+                         tc::desc_k_sw128(ka + (kk >> 2) * kCaHalf + (kk & 3) * 32), idesc_s, kk > 0);
+          tc::commit(&sm.s_full[w]);
+          if (!dual || w == 1) tc::commit(&sm.kv_empty[st]);
+          if (dual ? s == nb - 1 : blk == nb - 1) tc::commit(&sm.q_empty[qs]);
+        }
+        __syncwarp();
+      };
+      auto issue_o = [&](int w, int s) {
+        const int blk = dual ? s : 2 * s + w, load = 2 * (base + blk) + 1, st = load % kTiles;
+        const int keys = sm.bad[(base + blk) % kCaBad] ? 0 : min(kBlock, len - (b0 + blk) * kBlock);
+        if (!dual || w == 0) {
+          if (!(ok = ok && ca_wait(&sm.kv_full[st], (load / kTiles) & 1, err, 813))) return;
+          if (!kFp8 && (keys & 15)) {
+            // V rows behind the last key, up to the end of their 16-row step: their weight is zero, but they may hold
+            // anything, so they become zero too
+            const uint32_t va = smem_u32(sm.kv[st]);
+            for (int j = lane; j < (16 - (keys & 15)) * 16; j += 32) {
+              const int vr = keys + (j >> 4);
+              sts128(va + ((j >> 3) & 1) * kCaHalf + vr * 128 + (j & 7) * 16, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (!(ok = ok && ca_wait(&sm.p_full[w], pcount[w] & 1, err, 814))) return;
+        ++pcount[w];
+        tc::fence_after();
+        if (lane == 0) {
+          const uint32_t va = smem_u32(sm.kv[st]);
+          const int ks = (keys + 15) / 16;  // the 16-key steps behind the last key are left out
+          for (int kk = 0; kk < ks; ++kk)
+            tc::mma_bf16_ts(tmem + kCaOCol + 128 * w, tmem + 128 * w + kk * 8, tc::desc_v_mn_sw128(va + kk * 2048),
+                            idesc_o, acc[w] || kk > 0);
+          if (!dual || w == 1) tc::commit(&sm.kv_empty[st]);
+          if (s == steps[w] - 1) tc::commit(&sm.o_full[w]);
+        }
+        acc[w] = acc[w] || keys > 0;
+        __syncwarp();
+      };
+      for (int w = 0; w < 2 && ok; ++w)
+        if (steps[w] > 0) issue_s(w, 0);
+      for (int s = 0; s < steps[0] && ok; ++s)
+        for (int w = 0; w < 2 && ok; ++w)
+          if (s < steps[w]) {
+            issue_o(w, s);
+            if (ok && s + 1 < steps[w]) issue_s(w, s + 1);
+          }
+      base += nb;
+      nq += dual ? 2 : 1;
+    }
+    // every product has finished before tensor memory is released
+    if (lane == 0) {
+      tc::commit(&sm.done);
+      mbar_wait(&sm.done, 0, err, 815);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---------------- softmax, one row per thread; the end of an item ----------------
+    const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t scol = lanes + 128 * wg, ocol = lanes + kCaOCol + 128 * wg;
+    int base = 0;
+    uint32_t scount = 0, ocount = 0, xcount = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int is = n % kCaInfo;
+      if (!(ok = ca_wait(&sm.info_full[is], (n / kCaInfo) & 1, err, 820))) break;
+      const CaItem it = sm.info[is];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.info_empty[is]);
+      if (it.nb == 0) break;
+      const bool dual = it.ntok > 8;
+      const int steps = dual ? it.nb : (it.nb + 1 - wg) / 2;
+      const int tok = (dual ? 8 * wg : 0) + (row >> 4);
+      const bool valid = tok < it.ntok;
+      const bool active = __any_sync(0xffffffffu, valid);  // a warp without a row only keeps the barriers
+      float m = -INFINITY, l = 0.f;  // reference (lowered by kLift), sum of the weights
+      for (int s = 0; s < steps; ++s) {
+        const int blk = dual ? s : 2 * s + wg;
+        if (!(ok = ca_wait(&sm.s_full[wg], scount & 1, err, 821))) break;
+        ++scount;
+        tc::fence_after();
+        if (active) {
+          const int keys = !valid ? kBlock
+                                  : sm.bad[(base + blk) % kCaBad]
+                                        ? 0
+                                        : min(kBlock, it.pos0 + tok + 1 - (it.b0 + blk) * kBlock);
+          const bool masked = !__all_sync(0xffffffffu, keys >= kBlock);
+          auto block = [&](auto mask_tag) {
+            constexpr bool kMask = decltype(mask_tag)::value;
+            float m8[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m8[q] = -INFINITY;
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t v[32];
+              tc::ld_32x32b_x32(scol + ch * 32, v);
+              tc::wait_ld();
+#pragma unroll
+              for (int q = 0; q < 16; ++q) {
+                float xa = __uint_as_float(v[2 * q]), xb = __uint_as_float(v[2 * q + 1]);
+                if (kMask) {
+                  xa = ch * 32 + 2 * q < keys ? xa : -INFINITY;
+                  xb = ch * 32 + 2 * q + 1 < keys ? xb : -INFINITY;
+                }
+                m8[q & 7] = fmax3(m8[q & 7], xa, xb);
+              }
+            }
+            const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                                   fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) *
+                             a.scale_log2 - Shape::kLift;
+            const bool raise = mx > m + kCaSlack;  // (true for the first key: m is -inf)
+            if (__any_sync(0xffffffffu, raise)) {
+              // what the sums are multiplied by; where there was no key yet they are zero (or, before the item's
+              // first O product, not there)
+              const float f = raise && m != -INFINITY ? ex2(m - mx) : 1.f;
+              if (raise) m = mx;
+              l *= f;
+              if (s > 0) {
+#pragma unroll 1
+                for (int ch = 0; ch < 8; ++ch) {
+                  uint32_t v[16];
+                  tc::ld_32x32b_x16(ocol + ch * 16, v);
+                  tc::wait_ld();
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * f);
+                  tc::st_32x32b_x16(ocol + ch * 16, v);
+                }
+              }
+            }
+            const float mu = m == -INFINITY ? 0.f : m;
+            float2 l4[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) l4[q] = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t v[32];
+              tc::ld_32x32b_x32(scol + ch * 32, v);
+              tc::wait_ld();
+              uint32_t pk[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) {
+                const int kc = ch * 32 + 2 * q;
+                float2 x = fma2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]), a.scale_log2, a.scale_log2,
+                                -mu, -mu);
+                if (kMask) {
+                  x.x = kc < keys ? x.x : -INFINITY;
+                  x.y = kc + 1 < keys ? x.y : -INFINITY;
+                }
+                const float pa = ex2(x.x), pb = ex2(x.y);
+                pk[q] = kFp8 ? pack_f16(pa, pb) : pack_bf16(pa, pb);
+                l4[q & 3] = add2(l4[q & 3].x, l4[q & 3].y, pa, pb);
+              }
+              // over S columns that this pass has read
+              tc::st_32x32b_x16(scol + ch * 16, pk);
+            }
+            l += ((l4[0].x + l4[0].y) + (l4[1].x + l4[1].y)) + ((l4[2].x + l4[2].y) + (l4[3].x + l4[3].y));
+          };
+          if (masked) block(std::true_type{});
+          else block(std::false_type{});
+          tc::wait_st();
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[wg]);
+      }
+      if (!ok) break;
+      base += it.nb;
+
+      // ---- the end of the item: its rows, or its partial ----
+      if (steps > 0 && !(ok = ca_wait(&sm.o_full[wg], ocount & 1, err, 822))) break;
+      ocount += steps > 0;
+      const int h = it.g * kGroup + (row & 15);
+      const long long orow = (static_cast<long long>(it.t0) + tok) * kHeads + h;
+      const long long prow = static_cast<long long>(it.slot) * a.rows + tok * kGroup + (row & 15);
+      // f0, f1: what the two warpgroups' sums are multiplied by; l: the row's denominator; dims d0 ..
+      float f0 = 1.f, f1 = 0.f;
+      uint32_t c0 = ocol, c1 = ocol;
+      int d0 = 0, nd = kDim;
+      if (!dual) {
+        // both warpgroups hold sums of the same rows: each writes half of their dims
+        sm.ml[wg][row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.x_full);
+        if (!(ok = ca_wait(&sm.x_full, xcount & 1, err, 823))) break;
+        const float2 x0 = sm.ml[0][row], x1 = sm.ml[1][row];
+        m = fmaxf(x0.x, x1.x);
+        f0 = x0.x == -INFINITY ? 0.f : ex2(x0.x - m);
+        f1 = x1.x == -INFINITY ? 0.f : ex2(x1.x - m);
+        l = f0 * x0.y + f1 * x1.y;
+        c0 = lanes + kCaOCol;
+        c1 = lanes + kCaOCol + 128;
+        d0 = 64 * wg;
+        nd = 64;
+      } else if (m == -INFINITY) {
+        f0 = 0.f;
+      }
+      tc::fence_after();
+      if (active) {
+        const float inv = it.slot >= 0 ? 1.f : l == 0.f ? 0.f : a.v_scale / l;
+        f0 *= inv;
+        f1 *= inv;
+#pragma unroll 1
+        for (int d = d0; d < d0 + nd; d += 16) {
+          uint32_t u[16], v[16];
+          tc::ld_32x32b_x16(c0 + d, u);
+          if (!dual) tc::ld_32x32b_x16(c1 + d, v);
+          tc::wait_ld();
+          float o[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            // a factor of zero stands for sums that hold nothing: they are not read as numbers
+            o[q] = f0 != 0.f ? __uint_as_float(u[q]) * f0 : 0.f;
+            if (!dual && f1 != 0.f) o[q] = fmaf(__uint_as_float(v[q]), f1, o[q]);
+          }
+          if (valid && it.slot >= 0) {
+            float4* p = reinterpret_cast<float4*>(a.part_o + prow * kDim + d);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) p[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          } else if (valid) {
+            uint4* p = reinterpret_cast<uint4*>(a.out + orow * kDim + d);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              p[q] = make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]), pack_bf16(o[8 * q + 2], o[8 * q + 3]),
+                                pack_bf16(o[8 * q + 4], o[8 * q + 5]), pack_bf16(o[8 * q + 6], o[8 * q + 7]));
+          }
+          __syncwarp();
+        }
+        if (valid && d0 == 0) {
+          if (it.slot >= 0) a.part_ml[prow] = make_float2(m, l);
+          else if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : m + log2f(l);
+        }
+      }
+      if (!dual) {
+        // neither goes on to its next O while the other still reads it
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.x_done);
+        if (!(ok = ca_wait(&sm.x_done, xcount & 1, err, 824))) break;
+        ++xcount;
+      }
+    }
+  } else if (kFp8) {
+    // ---------------- E4M3 pages and bf16 queries to fp16 ----------------
+    const int wt = tid - kCaWidenWarp * 32;  // 0 .. 127
+    int base = 0, nq = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const int is = n % kCaInfo;
+      if (!(ok = ca_wait(&sm.info_full[is], (n / kCaInfo) & 1, err, 830))) break;
+      const int nb = sm.info[is].nb, b0 = sm.info[is].b0, len = sm.info[is].len, ntok = sm.info[is].ntok;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.info_empty[is]);
+      if (nb == 0) break;
+      for (int k = 0; k < nb && ok; ++k) {
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          const int load = 2 * (base + k) + kv, rs = load % 4, st = load % kTiles;
+          if (!(ok = ca_wait(&sm.raw_full[rs], (load / 4) & 1, err, 831))) break;
+          if (!(ok = ca_wait(&sm.kv_empty[st], ((load / kTiles) & 1) ^ 1, err, 832))) break;
+          // rows behind the last key become zero: their weight is zero, but they may hold anything
+          const int keys = kv == 0 ? kBlock : sm.bad[(base + k) % kCaBad] ? 0 : min(kBlock, len - (b0 + k) * kBlock);
+          const uint32_t src = smem_u32(sm.raw[kFp8 ? rs : 0]), dst = smem_u32(sm.kv[st]);
+#pragma unroll 4
+          for (int j = 0; j < 8; ++j) {
+            const int c = wt + 128 * j, r = c >> 3, p = c & 7;  // 16 bytes: row r, dims 16 p ..
+            const uint4 x = lds128(src + c * 16);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n"
+                  " cvt.rn.f16x2.e4m3x2 %1, hi;\n}"
+                  : "=r"(y[2 * q]), "=r"(y[2 * q + 1])
+                  : "r"(w[q]));
+            }
+            if (r >= keys)
+#pragma unroll
+              for (int q = 0; q < 8; ++q) y[q] = 0u;
+            const uint32_t half = dst + (p >> 2) * kCaHalf;
+            sts128(half + sw128(r, 2 * (p & 3)), y[0], y[1], y[2], y[3]);
+            sts128(half + sw128(r, 2 * (p & 3) + 1), y[4], y[5], y[6], y[7]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm.raw_empty[rs]);
+            mbar_arrive(&sm.kv_full[st]);
+          }
+          if (k == 0 && kv == 0) {
+            for (int q = 0; q < (ntok > 8 ? 2 : 1) && ok; ++q, ++nq) {
+              const int s = nq & 1, bytes = min(8, ntok - 8 * q) * kCaQEntry;
+              if (!(ok = ca_wait(&sm.q_full[s], (nq >> 1) & 1, err, 833))) break;
+              const uint32_t at = smem_u32(sm.q[s]);
+              for (int j = wt * 16; j < bytes; j += 128 * 16) {
+                const uint4 x = lds128(at + j);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  y[i] = pack_f16(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+                sts128(at + j, y[0], y[1], y[2], y[3]);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.q_ready[s]);
+            }
+          }
+        }
+      }
+      base += nb;
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kCaMmaWarp) {
+    tc::fence_after();
+    tc::dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of the items that were cut: CTA c those of the item that begins in share c, a warp per row, four
+// dims per lane.
+constexpr int kCaJoinWarps = 16;
+__global__ void __launch_bounds__(kCaJoinWarps * 32) chunk_join_kernel(const __grid_constant__ CaArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, c = blockIdx.x;
+  const CaCut cut = a.cuts[c];
+  const int parts = cut.last - c + 1;
+  for (int r = threadIdx.x >> 5; r < cut.ntok * kGroup; r += kCaJoinWarps) {
+    auto at = [&](int s) { return static_cast<long long>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * a.rows + r; };
+    float m = -INFINITY;
+    for (int s = lane; s < parts; s += 32) m = fmaxf(m, a.part_ml[at(s)].x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+      const float2 ml = a.part_ml[at(s)];
+      const float4 x = reinterpret_cast<const float4*>(a.part_o + at(s) * kDim)[lane];
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+      l = fmaf(f, ml.y, l);
+      o.x = fmaf(f, x.x, o.x);
+      o.y = fmaf(f, x.y, o.y);
+      o.z = fmaf(f, x.z, o.z);
+      o.w = fmaf(f, x.w, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : a.v_scale / l;
+    const long long row =
+        (static_cast<long long>(cut.t0) + r / kGroup) * kHeads + cut.g * kGroup + r % kGroup;
+    reinterpret_cast<uint2*>(a.out + row * kDim)[lane] =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m + log2f(l);
+  }
+}
+
+// ---- host side ----------------------------------------------------------------------
+
+static size_t ca_up(size_t x) { return (x + 255) / 256 * 256; }
+static int ca_rows(long long tokens) { return kGroup * static_cast<int>(tokens < kCaTok ? tokens : kCaTok); }
+
+// Scratch of a call: the cuts, then the two partials of every CTA.
+size_t attend_chunk_bytes(long long tokens, int) {
+  const size_t rows = 2 * static_cast<size_t>(kNumSMs) * ca_rows(tokens);
+  return ca_up(kNumSMs * sizeof(CaCut)) + ca_up(rows * sizeof(float2)) + rows * kDim * sizeof(float);
+}
+
+// q [T, 64, 128] bf16 as (dims 0-63, head % 8, dims / 64, head / 8, token): a token's 16 heads of a KV head in one box of
+// four 8-row swizzle atoms.
+static bool ca_encode_q(CUtensorMap* map, const void* base, cuuint64_t T) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[5] = {64, 8, 2, kHeads / 8, T};
+  const cuuint64_t strides[4] = {kDim * 2, 128, 8 * kDim * 2, kHeads * kDim * 2};
+  const cuuint32_t box[5] = {64, 8, 2, 2, 1}, step[5] = {1, 1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// A cache [slots, 4, 128]: boxes of one head's 128 slots, 64 dims of bf16 (swizzled) or all 128 of E4M3 (plain).
+static bool ca_encode_kv(CUtensorMap* map, const void* base, cuuint64_t slots, bool fp8) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t size = fp8 ? 1 : 2;
+  const cuuint64_t dims[3] = {kDim, kKvHeads, slots}, strides[2] = {kDim * size, kKvHeads * kDim * size};
+  const cuuint32_t box[3] = {fp8 ? 128u : 64u, 1, kBlock}, step[3] = {1, 1, 1};
+  return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+             dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kFp8>
+static cudaError_t ca_launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, const CaArgs& a,
+                             cudaStream_t stream) {
+  constexpr size_t bytes = sizeof(CaSmem<kFp8>);
+  static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+  if (const cudaError_t e = cudaFuncSetAttribute(chunk_attend_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(bytes));
+      e != cudaSuccess)
+    return e;
+  chunk_attend_kernel<kFp8><<<kNumSMs, CaShape<kFp8>::kThreads, bytes, stream>>>(qmap, kmap, vmap, a);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream) {
   if (const cudaError_t e0 = launch_prologue(); e0 != cudaSuccess) return e0;
-  const long long grid = (L.tokens * kHeads + kCaWarps - 1) / kCaWarps;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const float scale_log2 = L.scale * 1.4426950408889634f * L.k_scale;
-  if (L.kv_fp8) chunk_attend_kernel<true><<<static_cast<unsigned>(grid), kCaWarps * 32, 0, stream>>>(L, scale_log2);
-  else chunk_attend_kernel<false><<<static_cast<unsigned>(grid), kCaWarps * 32, 0, stream>>>(L, scale_log2);
-  return cudaGetLastError();
+  CUtensorMap qmap, kmap, vmap;
+  if (!ca_encode_q(&qmap, L.q, L.tokens) || !ca_encode_kv(&kmap, L.k, L.num_slots, L.kv_fp8) ||
+      !ca_encode_kv(&vmap, L.v, L.num_slots, L.kv_fp8))
+    return cudaErrorInvalidValue;
+  CaArgs a{};
+  a.seq_lens = L.seq_lens;
+  a.page_table = L.page_table;
+  a.cu = L.cu;
+  a.batch = L.batch;
+  a.max_blocks = L.max_blocks;
+  a.num_pages = static_cast<int>(L.num_slots / kBlock);
+  a.tokens = L.tokens;
+  a.scale_log2 = L.scale * 1.4426950408889634f * L.k_scale;
+  a.v_scale = L.v_scale;
+  a.out = static_cast<__nv_bfloat16*>(L.out);
+  a.lse = L.lse;
+  a.rows = ca_rows(L.tokens);
+  const size_t rows = 2 * static_cast<size_t>(kNumSMs) * a.rows;
+  uint8_t* p = L.scratch;
+  a.cuts = reinterpret_cast<CaCut*>(p);
+  p += ca_up(kNumSMs * sizeof(CaCut));
+  a.part_ml = reinterpret_cast<float2*>(p);
+  p += ca_up(rows * sizeof(float2));
+  a.part_o = reinterpret_cast<float*>(p);
+  a.err = L.err;
+  if (const cudaError_t e = L.kv_fp8 ? ca_launch<true>(qmap, kmap, vmap, a, stream)
+                                     : ca_launch<false>(qmap, kmap, vmap, a, stream);
+      e != cudaSuccess)
+    return e;
+  // launched as a programmatic dependent: its launch overlaps the main kernel's end, and it reads nothing before that
+  // has completed
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kNumSMs);
+  cfg.blockDim = dim3(kCaJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel, a);
 }
 
 }  // namespace msa

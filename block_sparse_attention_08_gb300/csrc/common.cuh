@@ -323,6 +323,26 @@ __device__ __forceinline__ uint32_t sw128(int row, int chunk) {
   return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Single MUFU base-2 exponential (ex2.approx.ftz: relative error about 2^-22;
+// exp2(-inf) = +0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void stg128(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 // Orderable key for a float: larger float -> larger unsigned key.
 __device__ __forceinline__ uint32_t float_key(float f) {
   uint32_t u = __float_as_uint(f);
@@ -349,6 +369,20 @@ __device__ __forceinline__ uint64_t desc_k_sw128(uint32_t saddr) {
 // The same with another distance between 8-row groups (a multiple of 1024).
 __device__ __forceinline__ uint64_t desc_k_sw128_sbo(uint32_t saddr, uint32_t sbo) {
   return (desc_k_sw128(saddr) & ~(static_cast<uint64_t>(0x3FFF) << 32)) | (static_cast<uint64_t>(sbo >> 4) << 32);
+}
+
+// Shared-memory descriptor of V read MN-major (N = head dims contiguous inside a
+// 128-byte swizzled row, K = keys along rows) of a 128-key tile: 64-dim atoms
+// 16 KB apart (LBO),
+// 8-key groups 1024 bytes apart (SBO).
+__device__ __forceinline__ uint64_t desc_v_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFF);
+  d |= static_cast<uint64_t>(16384 >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
 }
 
 // Instruction descriptor, kind::f16: bf16 A and B (both K-major), fp32 D.

@@ -439,27 +439,6 @@ __global__ void __launch_bounds__(256) bm_scatter_kernel(long long entries, long
 
 // ---- the tensor-core kernel ---------------------------------------------------------
 
-// Shared-memory descriptor of V read MN-major (N = head dims contiguous inside a
-// 128-byte swizzled row, K = keys along rows): 64-dim atoms 16 KB apart (LBO),
-// 8-key groups 1024 bytes apart (SBO).
-__device__ __forceinline__ uint64_t desc_v_mn_sw128(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFF);
-  d |= static_cast<uint64_t>(kBmHalf >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
@@ -473,18 +452,6 @@ __device__ __forceinline__ int local_tiles(int n_tiles) {
   int n = 0;
   for (int k = blockIdx.x; k * kBmChunk < n_tiles; k += gridDim.x) n += min(kBmChunk, n_tiles - k * kBmChunk);
   return n;
-}
-
-// Single MUFU base-2 exponential (ex2.approx.ftz: relative error about 2^-22;
-// exp2(-inf) = +0).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ void stg128(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 __global__ void __launch_bounds__(kBmThreads, 1) bm_attend_kernel(
@@ -697,7 +664,7 @@ __global__ void __launch_bounds__(kBmThreads, 1) bm_attend_kernel(
         const uint32_t dt = tmem + kBmOCol;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          tc::mma_bf16_ts(dt, pt + kk * 8, desc_v_mn_sw128(va + kk * 2048), kBmIdescO, kk > 0);
+          tc::mma_bf16_ts(dt, pt + kk * 8, tc::desc_v_mn_sw128(va + kk * 2048), kBmIdescO, kk > 0);
         tc::commit(&sm.o_full);
         tc::commit(&sm.p_free[b]);
       }
@@ -1283,18 +1250,18 @@ __global__ void __maxnreg__(kBwMaxRegs) bw_attend_kernel(
         tc::fence_after();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          tc::mma_bf16(tmem + 384, desc_v_mn_sw128(dsa + kk * 2048), desc_v_mn_sw128(qa + kk * 2048), kIdescMM,
+          tc::mma_bf16(tmem + 384, tc::desc_v_mn_sw128(dsa + kk * 2048), tc::desc_v_mn_sw128(qa + kk * 2048), kIdescMM,
                        kk > 0 || !fresh);
         tc::commit(&sm.qd_empty[sq]);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          tc::mma_bf16(tmem + 256, desc_v_mn_sw128(pa + kk * 2048), desc_v_mn_sw128(oa + kk * 2048), kIdescMM,
+          tc::mma_bf16(tmem + 256, tc::desc_v_mn_sw128(pa + kk * 2048), tc::desc_v_mn_sw128(oa + kk * 2048), kIdescMM,
                        kk > 0 || !fresh);
         tc::commit(&sm.qd_empty[so]);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint32_t off = (kk >> 2) * kBmHalf + (kk & 3) * 32;
-          tc::mma_bf16(tmem + 128, tc::desc_k_sw128(dsa + off), desc_v_mn_sw128(ka + kk * 2048), kIdescKM, kk > 0);
+          tc::mma_bf16(tmem + 128, tc::desc_k_sw128(dsa + off), tc::desc_v_mn_sw128(ka + kk * 2048), kIdescKM, kk > 0);
         }
         tc::commit(&sm.dq_full);
         if (last) {

@@ -580,7 +580,9 @@ msa_status msa_rotary_insert(const msa_rotary_config* rot, const void* q, int64_
  * whose id is outside the pool are left out (MSA_DEVERR_PAGE, detail = the flat
  * page-table index); a row left without a key gets 0 and -inf.  fp32 accumulation;
  * the softmax weights enter the product with V in bf16, their sum is fp32 over
- * the unrounded weights.  The result is bitwise reproducible.
+ * the unrounded weights.  A repeated call gives the same bits (where a request's
+ * keys are split follows the lengths of the whole batch, so another batch may
+ * round its rows differently).
  * Errors: MSA_ERR_NULL, MSA_ERR_SHAPE, MSA_ERR_ALIGN, MSA_ERR_WORKSPACE, MSA_ERR_CUDA. */
 msa_status msa_attend_chunk(const msa_config* cfg, const void* q, const void* k_cache,
                             const void* v_cache, const int32_t* seq_lens,
