@@ -27,6 +27,8 @@
 // has a third warpgroup that widens each page to fp16 (exactly) in shared memory.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "launch.h"
 
 namespace msa {
@@ -37,10 +39,19 @@ constexpr int kCaHalf = kCaTile / 2;  // one 64-dim half
 constexpr int kCaQEntry = 4096;       // one token's 16 heads x 128 dims
 constexpr int kCaInfo = 4;            // item descriptors in flight
 constexpr int kCaBad = 8;             // block flags in flight (at most 5 blocks are)
-constexpr int kCaMmaWarp = 9, kCaProducerWarp = 8, kCaWidenWarp = 10;
+// warps 0-7 softmax, 8 producer, 9 MMA (10 and 11 fill their warpgroup), 12-15 widening
+constexpr int kCaProducerWarp = 8, kCaMmaWarp = 9, kCaWidenWarp = 12;
 constexpr float kCaSlack = 8.f;
-// tensor memory: S of warpgroup w (and P over its first half) at 128 w, O at 256 + 128 w
+// tensor memory: S of warpgroup w at 128 w, P over its first half, O at 256 + 128 w
 constexpr uint32_t kCaOCol = 256;
+
+// The K and V tiles of a piece of nb blocks are loaded in the order K0 K1 V0 K2 V1 ... V(nb-2) V(nb-1): V is needed a
+// softmax later than its K, so the next block's K goes before it.  Tile number of K or V of block b:
+__device__ __forceinline__ int ca_load_k(int b) { return b == 0 ? 0 : 2 * b - 1; }
+__device__ __forceinline__ int ca_load_v(int b, int nb) { return b == nb - 1 ? 2 * nb - 1 : 2 * b + 2; }
+// and the other way round (tile j that is not a V tile is K of block (j + 1) / 2)
+__device__ __forceinline__ bool ca_is_v(int j, int nb) { return j > 0 && ((j & 1) == 0 || j == 2 * nb - 1); }
+__device__ __forceinline__ int ca_block_v(int j, int nb) { return j == 2 * nb - 1 ? nb - 1 : (j - 2) >> 1; }
 
 // A piece of an item: blocks b0 .. b0 + nb - 1.  nb = 0 ends the list.
 struct CaItem {
@@ -74,7 +85,11 @@ template <bool kFp8>
 struct CaShape {
   static constexpr int kTiles = kFp8 ? 3 : 5;  // 16-bit K / V tiles
   static constexpr int kRaw = kFp8 ? 4 : 0;    // E4M3 tiles as copied
-  static constexpr int kThreads = kFp8 ? 448 : 320;
+  static constexpr int kWiden = kFp8 ? 4 : 0;  // widening warps
+  static constexpr int kThreads = 32 * (kCaWidenWarp + kWiden);
+  // registers per thread of the roles, out of the launch's 168 (384 threads) or 128 (512 threads) a thread:
+  // 256 * 216 + 128 * 72 = 384 * 168, and 256 * 184 + 128 * 64 + 128 * 80 = 512 * 128
+  static constexpr int kRegsSoftmax = kFp8 ? 184 : 216, kRegsIssue = kFp8 ? 64 : 72, kRegsWiden = 80;
   // fp16 weights are kept near the top of their range (at most 2^(kLift + kCaSlack) = 2^15), so that small ones
   // stay normal down to 2^-21 of the largest
   static constexpr float kLift = kFp8 ? 7.f : 0.f;
@@ -157,6 +172,22 @@ __device__ __forceinline__ bool ca_wait(uint64_t* bar, uint32_t parity, DevError
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, where));
 }
 
+// One thread of the (whole) warp, always the same: the products' operands are then known to be those of one thread, and
+// go straight to the uniform registers that the instruction takes.
+__device__ __forceinline__ bool ca_elect() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
+}
+template <int kRegs>
+__device__ __forceinline__ void ca_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void ca_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 template <bool kFp8>
 __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kernel(
     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -165,7 +196,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   constexpr int kTiles = Shape::kTiles, kThreads = Shape::kThreads;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   CaSmem<kFp8>& sm = *reinterpret_cast<CaSmem<kFp8>*>(smem_raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   DevError* err = a.err;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -195,7 +226,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     mbar_init(&sm.done, 1);
     for (int i = 0; i < kCaInfo; ++i) {
       mbar_init(&sm.info_full[i], 1);
-      mbar_init(&sm.info_empty[i], kFp8 ? 13 : 9);  // the softmax warps, the MMA warp, the widening warps
+      mbar_init(&sm.info_empty[i], 9 + Shape::kWiden);  // the softmax, MMA and widening warps
     }
     fence_mbar_init();
     sm.start_r = -1;
@@ -261,10 +292,11 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
 
   // A wait that gives up (recorded in the error word) ends its role, so a broken pipeline ends after one bounded wait
   // per role.
+  if (warp >= 8 && warp < kCaWidenWarp) ca_regs_down<Shape::kRegsIssue>();
   if (warp == kCaProducerWarp) {
     // ---------------- the share's items, and their copies ----------------
     if (lane == 0) {
@@ -320,53 +352,57 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         ++nitem;
         const int tiles = it.ntok > 8 ? 2 : 1;
         const int32_t* row = a.page_table + static_cast<long long>(r) * a.max_blocks;
-        int ids = 0, ids_next = lane < it.nb ? row[b + lane] : 0;
-        for (int k = 0; k < it.nb && ok; ++k) {
-          if ((k & 31) == 0) {
-            ids = ids_next;
-            ids_next = k + 32 + lane < it.nb ? row[b + k + 32 + lane] : 0;
-          }
-          int page = __shfl_sync(0xffffffffu, ids, k & 31);
-          const bool bad = page < 0 || page >= a.num_pages;
-          if (bad) {
-            if (lane == 0) record_error(err, MSA_DEVERR_PAGE, static_cast<long long>(r) * a.max_blocks + b + k);
-            page = 0;
-          }
-          if (lane == 0) sm.bad[nblk % kCaBad] = bad;
-          ++nblk;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const CUtensorMap* map = kv ? &vmap : &kmap;
-            if (kFp8) {
-              const int s = nload % 4;
-              if (!(ok = ca_wait(&sm.raw_empty[s], ((nload / 4) & 1) ^ 1, err, 801))) break;
-              if (lane == 0) {
-                mbar_expect_tx(&sm.raw_full[s], kCaHalf);
-                tma_load_3d(sm.raw[kFp8 ? s : 0], map, 0, g, page * kBlock, &sm.raw_full[s]);
-              }
-            } else {
-              const int s = nload % kTiles;
-              if (!(ok = ca_wait(&sm.kv_empty[s], ((nload / kTiles) & 1) ^ 1, err, 802))) break;
-              if (lane == 0) {
-                mbar_expect_tx(&sm.kv_full[s], kCaTile);
-                tma_load_3d(sm.kv[s], map, 0, g, page * kBlock, &sm.kv_full[s]);
-                tma_load_3d(sm.kv[s] + kCaHalf, map, 64, g, page * kBlock, &sm.kv_full[s]);
-              }
+        int ids = 0, ids_next = lane < it.nb ? row[b + lane] : 0;  // 32 page ids, and the next 32
+        int last = 0, before = 0;  // pages of the last block that K was loaded of, and of the one before
+        for (int j = 0; j < 2 * it.nb && ok; ++j) {  // tile j: K of block (j + 1) / 2 and V in turn
+          const bool is_v = ca_is_v(j, it.nb);
+          int page;
+          if (!is_v) {
+            const int k = (j + 1) >> 1;
+            if ((k & 31) == 0) {
+              ids = ids_next;
+              ids_next = k + 32 + lane < it.nb ? row[b + k + 32 + lane] : 0;
             }
-            ++nload;
-            // The item's Q follows its first K tile: that tile's place was freed by the items before, but Q's
-            // may have to wait for their last S products.
-            if (k == 0 && kv == 0) {
-              for (int q = 0; q < tiles && ok; ++q) {
-                const int s = nq & 1, n = min(8, it.ntok - 8 * q);
-                if (!(ok = ca_wait(&sm.q_empty[s], ((nq >> 1) & 1) ^ 1, err, 803))) break;
-                if (lane == 0) mbar_expect_tx(&sm.q_full[s], n * kCaQEntry);
-                __syncwarp();
-                if (lane < n)
-                  tma_load_5d(sm.q[s] + lane * kCaQEntry, &qmap, 0, 0, 0, 2 * g, it.t0 + 8 * q + lane, &sm.q_full[s]);
-                ++nq;
-              }
-              if (!ok) break;
+            page = __shfl_sync(0xffffffffu, ids, k & 31);
+            const bool bad = page < 0 || page >= a.num_pages;
+            if (bad) {
+              if (lane == 0) record_error(err, MSA_DEVERR_PAGE, static_cast<long long>(r) * a.max_blocks + b + k);
+              page = 0;
+            }
+            if (lane == 0) sm.bad[nblk % kCaBad] = bad;
+            ++nblk;
+          }
+          // V of the block before the last K (the last tile: V of the last block itself)
+          const int from = is_v && j < 2 * it.nb - 1 ? before : is_v ? last : page;
+          if (!is_v) {
+            before = last;
+            last = page;
+          }
+          const CUtensorMap* map = is_v ? &vmap : &kmap;
+          const int s = nload % (kFp8 ? 4 : kTiles), turn = nload / (kFp8 ? 4 : kTiles);
+          if (!(ok = ca_wait(kFp8 ? &sm.raw_empty[s] : &sm.kv_empty[s], (turn & 1) ^ 1, err, 801))) break;
+          if (lane == 0) {
+            if (kFp8) {
+              mbar_expect_tx(&sm.raw_full[s], kCaHalf);
+              tma_load_3d(sm.raw[kFp8 ? s : 0], map, 0, g, from * kBlock, &sm.raw_full[s]);
+            } else {
+              mbar_expect_tx(&sm.kv_full[s], kCaTile);
+              tma_load_3d(sm.kv[s], map, 0, g, from * kBlock, &sm.kv_full[s]);
+              tma_load_3d(sm.kv[s] + kCaHalf, map, 64, g, from * kBlock, &sm.kv_full[s]);
+            }
+          }
+          ++nload;
+          // The item's Q follows its first K tile: that tile's place was freed by the items before, but Q's may have to
+          // wait for their last S products.
+          if (j == 0) {
+            for (int q = 0; q < tiles; ++q) {
+              const int qs = nq & 1, n = min(8, it.ntok - 8 * q);
+              if (!(ok = ca_wait(&sm.q_empty[qs], ((nq >> 1) & 1) ^ 1, err, 803))) break;
+              if (lane == 0) mbar_expect_tx(&sm.q_full[qs], n * kCaQEntry);
+              __syncwarp();
+              if (lane < n)
+                tma_load_5d(sm.q[qs] + lane * kCaQEntry, &qmap, 0, 0, 0, 2 * g, it.t0 + 8 * q + lane, &sm.q_full[qs]);
+              ++nq;
             }
           }
         }
@@ -403,10 +439,14 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     }
   } else if (warp == kCaMmaWarp) {
     // ---------------- S and O products ----------------
-    // Products execute in the order in which they are issued: an S product that overwrites P follows the O product
-    // that reads it.
+    // One thread issues them all, and they execute in the order in which they are issued: an S product that overwrites P
+    // follows the O product that reads it, and the two warpgroups' products alternate, so that one's softmax runs beside
+    // the other's products.  (With a thread for each warpgroup's they fell into step, both softmaxes and then both
+    // products at once: 1.59 ms instead of 1.34 ms for 2048 tokens over 32k keys.)  The thread holds few products
+    // ahead of the tensor cores, so it looks for what the next ones need before it issues a group, not between groups.
     constexpr uint32_t idesc_s = ca_idesc(kFp8), idesc_o = ca_idesc(kFp8) | (1u << 16);
-    int base = 0, nq = 0;       // blocks and Q tiles of the items before
+    const bool leader = ca_elect();
+    int base = 0, nq = 0;         // blocks and Q tiles of the items before
     uint32_t pcount[2] = {0, 0};  // P tiles taken
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -417,82 +457,109 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.info_empty[is]);
       if (nb == 0) break;
-      const int steps[2] = {dual ? nb : (nb + 1) / 2, dual ? nb : nb / 2};
-      bool acc[2] = {false, false};
-      auto issue_s = [&](int w, int s) {
-        const int blk = dual ? s : 2 * s + w, load = 2 * (base + blk), st = load % kTiles;
-        const int qt = dual ? nq + w : nq, qs = qt & 1;
-        if (s == 0 && (dual || w == 0)) {
-          uint64_t* bar = kFp8 ? &sm.q_ready[qs] : &sm.q_full[qs];
-          if (!(ok = ok && ca_wait(bar, (qt >> 1) & 1, err, 811))) return;
+      bool more[2] = {false, false};  // O holds sums of this item
+      // keys of a block that count for the last token: all, but in the request's last block and in a bad page
+      auto keys_of = [&](int blk) {
+        return sm.bad[(base + blk) % kCaBad] ? 0 : min(kBlock, len - (b0 + blk) * kBlock);
+      };
+      // O += P V of block `bo` (-1: none), then S of block `bs` (-1: none), for warpgroup w; one thread.  The tiles of
+      // a block that both warpgroups read are waited for by the first and given back by the second.
+      auto issue = [&](auto w_tag, int bo, int bs) {
+        constexpr int w = decltype(w_tag)::value;
+        const uint32_t s_col = tmem + 128 * w, o_col = tmem + kCaOCol + 128 * w;
+        const bool first = !dual || w == 0, last = !dual || w == 1;
+        const int lk = 2 * base + ca_load_k(max(bs, 0)), sk = lk % kTiles;
+        bool k_here = bs < 0 || !first;
+        if (!k_here) k_here = mbar_try_wait(&sm.kv_full[sk], (lk / kTiles) & 1);
+        if (bo >= 0) {
+          const int lv = 2 * base + ca_load_v(bo, nb), sv = lv % kTiles;
+          if (first && !mbar_wait(&sm.kv_full[sv], (lv / kTiles) & 1, err, 813)) return false;
+          const int ks = (keys_of(bo) + 15) / 16;  // the 16-key steps behind the last key are left out
+          const uint64_t vd = tc::desc_v_mn_sw128(smem_u32(sm.kv[sv]));
+          if (!mbar_wait(&sm.p_full[w], pcount[w] & 1, err, 814)) return false;
+          ++pcount[w];
+          tc::fence_after();
+          if (ks == 8) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)  // (descriptor addresses count 16 bytes)
+              tc::mma_bf16_ts(o_col, s_col + kk * 8, vd + kk * (2048 / 16), idesc_o, more[w] || kk > 0);
+          } else {
+            for (int kk = 0; kk < ks; ++kk)
+              tc::mma_bf16_ts(o_col, s_col + kk * 8, vd + kk * (2048 / 16), idesc_o, more[w] || kk > 0);
+          }
+          more[w] = more[w] || ks > 0;
+          if (last) tc::commit(&sm.kv_empty[sv]);
+          if (bs < 0) tc::commit(&sm.o_full[w]);  // the item's last of this warpgroup
         }
-        if (!dual || w == 0) {
-          if (!(ok = ok && ca_wait(&sm.kv_full[st], (load / kTiles) & 1, err, 812))) return;
-        }
-        tc::fence_after();
-        if (lane == 0) {
-          const uint32_t qa = smem_u32(sm.q[qs]), ka = smem_u32(sm.kv[st]);
+        if (bs >= 0) {
+          const int qs = (dual ? nq + w : nq) & 1;
+          const uint64_t qd = tc::desc_k_sw128_sbo(smem_u32(sm.q[qs]), 2048),
+                         kd = tc::desc_k_sw128(smem_u32(sm.kv[sk]));
+          if (!k_here) {
+            if (!mbar_wait(&sm.kv_full[sk], (lk / kTiles) & 1, err, 812)) return false;
+            tc::fence_after();
+          }
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc::mma_bf16(tmem + 128 * w, tc::desc_k_sw128_sbo(qa + (kk >> 2) * 1024 + (kk & 3) * 32, 2048),
-                         tc::desc_k_sw128(ka + (kk >> 2) * kCaHalf + (kk & 3) * 32), idesc_s, kk > 0);
+            tc::mma_bf16(s_col, qd + (kk >> 2) * (1024 / 16) + (kk & 3) * 2,
+                         kd + (kk >> 2) * (kCaHalf / 16) + (kk & 3) * 2, idesc_s, kk > 0);
           tc::commit(&sm.s_full[w]);
-          if (!dual || w == 1) tc::commit(&sm.kv_empty[st]);
-          if (dual ? s == nb - 1 : blk == nb - 1) tc::commit(&sm.q_empty[qs]);
+          if (last) tc::commit(&sm.kv_empty[sk]);
+          if (bs == nb - 1) tc::commit(&sm.q_empty[qs]);
         }
-        __syncwarp();
+        return true;
       };
-      auto issue_o = [&](int w, int s) {
-        const int blk = dual ? s : 2 * s + w, load = 2 * (base + blk) + 1, st = load % kTiles;
-        const int keys = sm.bad[(base + blk) % kCaBad] ? 0 : min(kBlock, len - (b0 + blk) * kBlock);
-        if (!dual || w == 0) {
-          if (!(ok = ok && ca_wait(&sm.kv_full[st], (load / kTiles) & 1, err, 813))) return;
-          if (!kFp8 && (keys & 15)) {
-            // V rows behind the last key, up to the end of their 16-row step: their weight is zero, but they may hold
-            // anything, so they become zero too
-            const uint32_t va = smem_u32(sm.kv[st]);
-            for (int j = lane; j < (16 - (keys & 15)) * 16; j += 32) {
-              const int vr = keys + (j >> 4);
-              sts128(va + ((j >> 3) & 1) * kCaHalf + vr * 128 + (j & 7) * 16, 0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+      const std::integral_constant<int, 0> w0;
+      const std::integral_constant<int, 1> w1;
+      if (leader) {
+        // everything but the O products of the last block
+        for (int q = 0; q < (dual ? 2 : 1) && ok; ++q) {
+          const int t = nq + q;
+          ok = mbar_wait(kFp8 ? &sm.q_ready[t & 1] : &sm.q_full[t & 1], (t >> 1) & 1, err, 811);
         }
-        if (!(ok = ok && ca_wait(&sm.p_full[w], pcount[w] & 1, err, 814))) return;
-        ++pcount[w];
         tc::fence_after();
-        if (lane == 0) {
-          const uint32_t va = smem_u32(sm.kv[st]);
-          const int ks = (keys + 15) / 16;  // the 16-key steps behind the last key are left out
-          for (int kk = 0; kk < ks; ++kk)
-            tc::mma_bf16_ts(tmem + kCaOCol + 128 * w, tmem + 128 * w + kk * 8, tc::desc_v_mn_sw128(va + kk * 2048),
-                            idesc_o, acc[w] || kk > 0);
-          if (!dual || w == 1) tc::commit(&sm.kv_empty[st]);
-          if (s == steps[w] - 1) tc::commit(&sm.o_full[w]);
-        }
-        acc[w] = acc[w] || keys > 0;
-        __syncwarp();
-      };
-      for (int w = 0; w < 2 && ok; ++w)
-        if (steps[w] > 0) issue_s(w, 0);
-      for (int s = 0; s < steps[0] && ok; ++s)
-        for (int w = 0; w < 2 && ok; ++w)
-          if (s < steps[w]) {
-            issue_o(w, s);
-            if (ok && s + 1 < steps[w]) issue_s(w, s + 1);
+        if (dual) {
+          ok = ok && issue(w0, -1, 0) && issue(w1, -1, 0);
+          for (int b = 0; b < nb - 1 && ok; ++b) ok = issue(w0, b, b + 1) && issue(w1, b, b + 1);
+        } else {
+          ok = ok && issue(w0, -1, 0) && (nb == 1 || issue(w1, -1, 1));
+          for (int b = 0; b < nb - 1 && ok; b += 2) {
+            ok = issue(w0, b, b + 2 < nb ? b + 2 : -1);
+            if (ok && b + 1 < nb - 1) ok = issue(w1, b + 1, b + 3 < nb ? b + 3 : -1);
           }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      const int lv = 2 * base + 2 * nb - 1, sv = lv % kTiles, keys = keys_of(nb - 1);
+      ok = ok && ca_wait(&sm.kv_full[sv], (lv / kTiles) & 1, err, 816);
+      if (!kFp8 && ok && (keys & 15)) {
+        // V rows behind the last key, up to the end of their 16-row step: their weight is zero, but they may hold
+        // anything, so they become zero too (the whole warp)
+        const uint32_t va = smem_u32(sm.kv[sv]);
+        for (int j = lane; j < (16 - (keys & 15)) * 16; j += 32) {
+          const int vr = keys + (j >> 4);
+          sts128(va + ((j >> 3) & 1) * kCaHalf + vr * 128 + (j & 7) * 16, 0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (leader && ok) {
+        if (dual) ok = issue(w0, nb - 1, -1) && issue(w1, nb - 1, -1);
+        else ok = (nb & 1) ? issue(w0, nb - 1, -1) : issue(w1, nb - 1, -1);
+      }
+      ok = __all_sync(0xffffffffu, ok);
       base += nb;
       nq += dual ? 2 : 1;
     }
     // every product has finished before tensor memory is released
-    if (lane == 0) {
+    if (leader) {
       tc::commit(&sm.done);
       mbar_wait(&sm.done, 0, err, 815);
     }
     __syncwarp();
   } else if (warp < 8) {
     // ---------------- softmax, one row per thread; the end of an item ----------------
+    ca_regs_up<Shape::kRegsSoftmax>();
     const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t scol = lanes + 128 * wg, ocol = lanes + kCaOCol + 128 * wg;
@@ -525,73 +592,75 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           const bool masked = !__all_sync(0xffffffffu, keys >= kBlock);
           auto block = [&](auto mask_tag) {
             constexpr bool kMask = decltype(mask_tag)::value;
-            float m8[8];
+            uint32_t x[4][32];  // the row of S, in four chunks
+            auto score = [&](int ch, int i) {
+              const float v = __uint_as_float(x[ch][i]);
+              return kMask && ch * 32 + i >= keys ? -INFINITY : v;
+            };
+            // P of the row against m, and in l the weights' sum; returns the row's maximum.  P's chunk goes over S columns
+            // that are in registers by then.
+            auto weights = [&](auto load_tag, float& sum) {
+              constexpr bool kLoad = decltype(load_tag)::value;
+              const float mu = m == -INFINITY ? 0.f : m;
+              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+              if (kLoad) tc::ld_32x32b_x32(scol, x[0]);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) m8[q] = -INFINITY;
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-              uint32_t v[32];
-              tc::ld_32x32b_x32(scol + ch * 32, v);
+              for (int ch = 0; ch < 4; ++ch) {
+                if (kLoad) {
+                  tc::wait_ld();
+                  if (ch < 3) tc::ld_32x32b_x32(scol + (ch + 1) * 32, x[ch + 1]);
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                  const float xa = score(ch, 2 * q), xb = score(ch, 2 * q + 1);
+                  top[q & 3] = fmax3(top[q & 3], xa, xb);
+                  const float2 y = fma2(xa, xb, a.scale_log2, a.scale_log2, -mu, -mu);
+                  const float pa = ex2(y.x), pb = ex2(y.y);
+                  pk[q] = kFp8 ? pack_f16(pa, pb) : pack_bf16(pa, pb);
+                  add[q & 1] = add2(add[q & 1].x, add[q & 1].y, pa, pb);
+                }
+                tc::st_32x32b_x16(scol + ch * 16, pk);
+              }
+              sum = (add[0].x + add[0].y) + (add[1].x + add[1].y);
+              return fmaxf(fmax3(top[0], top[1], top[2]), top[3]);
+            };
+            float sum;
+            if (s == 0) {
+              // the item's first block: its maximum is the reference
+              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int ch = 0; ch < 4; ++ch) tc::ld_32x32b_x32(scol + ch * 32, x[ch]);
               tc::wait_ld();
 #pragma unroll
-              for (int q = 0; q < 16; ++q) {
-                float xa = __uint_as_float(v[2 * q]), xb = __uint_as_float(v[2 * q + 1]);
-                if (kMask) {
-                  xa = ch * 32 + 2 * q < keys ? xa : -INFINITY;
-                  xb = ch * 32 + 2 * q + 1 < keys ? xb : -INFINITY;
-                }
-                m8[q & 7] = fmax3(m8[q & 7], xa, xb);
-              }
-            }
-            const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                   fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) *
-                             a.scale_log2 - Shape::kLift;
-            const bool raise = mx > m + kCaSlack;  // (true for the first key: m is -inf)
-            if (__any_sync(0xffffffffu, raise)) {
-              // what the sums are multiplied by; where there was no key yet they are zero (or, before the item's
-              // first O product, not there)
-              const float f = raise && m != -INFINITY ? ex2(m - mx) : 1.f;
-              if (raise) m = mx;
-              l *= f;
-              if (s > 0) {
+              for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) top[q & 3] = fmax3(top[q & 3], score(ch, 2 * q), score(ch, 2 * q + 1));
+              m = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * a.scale_log2 - Shape::kLift;
+              weights(std::false_type{}, sum);
+            } else {
+              // the weights against the reference so far; only where the block's maximum turns out to pass it by
+              // kCaSlack is it raised, and the weights are taken again
+              const float mx = weights(std::true_type{}, sum) * a.scale_log2 - Shape::kLift;
+              const bool raise = mx > m + kCaSlack;
+              if (__any_sync(0xffffffffu, raise)) {
+                const float f = raise && m != -INFINITY ? ex2(m - mx) : 1.f;  // (no key yet: the sums are zero)
+                if (raise) m = mx;
+                l *= f;
 #pragma unroll 1
                 for (int ch = 0; ch < 8; ++ch) {
-                  uint32_t v[16];
-                  tc::ld_32x32b_x16(ocol + ch * 16, v);
+                  uint32_t o[16];
+                  tc::ld_32x32b_x16(ocol + ch * 16, o);
                   tc::wait_ld();
 #pragma unroll
-                  for (int q = 0; q < 16; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * f);
-                  tc::st_32x32b_x16(ocol + ch * 16, v);
+                  for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+                  tc::st_32x32b_x16(ocol + ch * 16, o);
                 }
+                weights(std::false_type{}, sum);
               }
             }
-            const float mu = m == -INFINITY ? 0.f : m;
-            float2 l4[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) l4[q] = make_float2(0.f, 0.f);
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-              uint32_t v[32];
-              tc::ld_32x32b_x32(scol + ch * 32, v);
-              tc::wait_ld();
-              uint32_t pk[16];
-#pragma unroll
-              for (int q = 0; q < 16; ++q) {
-                const int kc = ch * 32 + 2 * q;
-                float2 x = fma2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]), a.scale_log2, a.scale_log2,
-                                -mu, -mu);
-                if (kMask) {
-                  x.x = kc < keys ? x.x : -INFINITY;
-                  x.y = kc + 1 < keys ? x.y : -INFINITY;
-                }
-                const float pa = ex2(x.x), pb = ex2(x.y);
-                pk[q] = kFp8 ? pack_f16(pa, pb) : pack_bf16(pa, pb);
-                l4[q & 3] = add2(l4[q & 3].x, l4[q & 3].y, pa, pb);
-              }
-              // over S columns that this pass has read
-              tc::st_32x32b_x16(scol + ch * 16, pk);
-            }
-            l += ((l4[0].x + l4[0].y) + (l4[1].x + l4[1].y)) + ((l4[2].x + l4[2].y) + (l4[3].x + l4[3].y));
+            l += sum;
           };
           if (masked) block(std::true_type{});
           else block(std::false_type{});
@@ -677,9 +746,13 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         ++xcount;
       }
     }
-  } else if (kFp8) {
+  } else if (kFp8 && warp >= kCaWidenWarp) {
     // ---------------- E4M3 pages and bf16 queries to fp16 ----------------
+    ca_regs_down<Shape::kRegsWiden>();
     const int wt = tid - kCaWidenWarp * 32;  // 0 .. 127
+    // Eight lanes take 16-byte pieces of two neighbouring rows, the odd row's from the other half: they read 128
+    // different bytes' banks, and write to eight different banks of the swizzled tile.
+    const int i8 = wt & 7, odd = i8 >> 2, piece = (i8 & 3) + 4 * (((wt >> 3) & 1) ^ odd), row0 = 2 * (wt >> 4) + odd;
     int base = 0, nq = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -689,58 +762,62 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.info_empty[is]);
       if (nb == 0) break;
-      for (int k = 0; k < nb && ok; ++k) {
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const int load = 2 * (base + k) + kv, rs = load % 4, st = load % kTiles;
-          if (!(ok = ca_wait(&sm.raw_full[rs], (load / 4) & 1, err, 831))) break;
-          if (!(ok = ca_wait(&sm.kv_empty[st], ((load / kTiles) & 1) ^ 1, err, 832))) break;
-          // rows behind the last key become zero: their weight is zero, but they may hold anything
-          const int keys = kv == 0 ? kBlock : sm.bad[(base + k) % kCaBad] ? 0 : min(kBlock, len - (b0 + k) * kBlock);
-          const uint32_t src = smem_u32(sm.raw[kFp8 ? rs : 0]), dst = smem_u32(sm.kv[st]);
-#pragma unroll 4
-          for (int j = 0; j < 8; ++j) {
-            const int c = wt + 128 * j, r = c >> 3, p = c & 7;  // 16 bytes: row r, dims 16 p ..
-            const uint4 x = lds128(src + c * 16);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t y[8];
+      for (int j = 0; j < 2 * nb && ok; ++j) {
+        const int load = 2 * base + j, rs = load % 4, st = load % kTiles;
+        const bool is_v = ca_is_v(j, nb);
+        if (!(ok = ca_wait(&sm.raw_full[rs], (load / 4) & 1, err, 831))) break;
+        if (!(ok = ca_wait(&sm.kv_empty[st], ((load / kTiles) & 1) ^ 1, err, 832))) break;
+        // V rows behind the last key become zero: their weight is zero, but they may hold anything
+        int keys = kBlock;
+        if (is_v) {
+          const int k = ca_block_v(j, nb);
+          keys = sm.bad[(base + k) % kCaBad] ? 0 : min(kBlock, len - (b0 + k) * kBlock);
+        }
+        const uint32_t src = smem_u32(sm.raw[kFp8 ? rs : 0]) + row0 * 128 + piece * 16;
+        const uint32_t dst = smem_u32(sm.kv[st]) + (piece >> 2) * kCaHalf;
+        uint4 x[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n"
-                  " cvt.rn.f16x2.e4m3x2 %1, hi;\n}"
-                  : "=r"(y[2 * q]), "=r"(y[2 * q + 1])
-                  : "r"(w[q]));
+        for (int q = 0; q < 8; ++q) x[q] = lds128(src + q * 16 * 128);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int r = row0 + 16 * q;
+          const uint32_t w[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+          uint32_t y[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n"
+                " cvt.rn.f16x2.e4m3x2 %1, hi;\n}"
+                : "=r"(y[2 * i]), "=r"(y[2 * i + 1])
+                : "r"(w[i]));
+          if (r >= keys)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = 0u;
+          sts128(dst + sw128(r, 2 * (piece & 3)), y[0], y[1], y[2], y[3]);
+          sts128(dst + sw128(r, 2 * (piece & 3) + 1), y[4], y[5], y[6], y[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.raw_empty[rs]);
+          mbar_arrive(&sm.kv_full[st]);
+        }
+        if (j == 0) {
+          for (int q = 0; q < (ntok > 8 ? 2 : 1); ++q, ++nq) {
+            const int s = nq & 1, bytes = min(8, ntok - 8 * q) * kCaQEntry;
+            if (!(ok = ca_wait(&sm.q_full[s], (nq >> 1) & 1, err, 833))) break;
+            const uint32_t at = smem_u32(sm.q[s]);
+            for (int o = wt * 16; o < bytes; o += 128 * 16) {
+              const uint4 v = lds128(at + o);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              uint32_t y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[i] = pack_f16(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+              sts128(at + o, y[0], y[1], y[2], y[3]);
             }
-            if (r >= keys)
-#pragma unroll
-              for (int q = 0; q < 8; ++q) y[q] = 0u;
-            const uint32_t half = dst + (p >> 2) * kCaHalf;
-            sts128(half + sw128(r, 2 * (p & 3)), y[0], y[1], y[2], y[3]);
-            sts128(half + sw128(r, 2 * (p & 3) + 1), y[4], y[5], y[6], y[7]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sm.raw_empty[rs]);
-            mbar_arrive(&sm.kv_full[st]);
-          }
-          if (k == 0 && kv == 0) {
-            for (int q = 0; q < (ntok > 8 ? 2 : 1) && ok; ++q, ++nq) {
-              const int s = nq & 1, bytes = min(8, ntok - 8 * q) * kCaQEntry;
-              if (!(ok = ca_wait(&sm.q_full[s], (nq >> 1) & 1, err, 833))) break;
-              const uint32_t at = smem_u32(sm.q[s]);
-              for (int j = wt * 16; j < bytes; j += 128 * 16) {
-                const uint4 x = lds128(at + j);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                uint32_t y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  y[i] = pack_f16(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-                sts128(at + j, y[0], y[1], y[2], y[3]);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sm.q_ready[s]);
-            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_ready[s]);
           }
         }
       }

@@ -94,7 +94,7 @@ def test_the_binding_refuses_other_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         msa.msa_map_slots(*[torch.zeros(1, dtype=torch.int32)] * 5, num_slots=128, capacity=1)
     with pytest.raises(TypeError):
-        _token_rows(None, "q", 1, 64)
+        _token_rows(None, "q", 1, 64, 0)
     with pytest.raises(ValueError, match="axes has 3"):
         _rotary_config(64, 1, (0, 0, 0), False)
     with pytest.raises(ValueError, match="axes must lie"):
