@@ -10,9 +10,10 @@
 //
 // An item is 16 consecutive new tokens of a request and one KV head: 256 rows
 // (token, query head) that share their keys, as two tiles of 128 rows.  Its work
-// is counted in units of one 128-key block, and every CTA takes an equal
-// contiguous share of all units of the batch, wherever that cuts an item: a long
-// context with one new token is spread over the GPU like a long chunk is.  The
+// is counted in units of one 128-key block and tile, and every CTA takes an
+// equal contiguous share of all units of the batch, wherever that cuts an item
+// (a block belongs to the share that holds its first unit): a long context with
+// one new token is spread over the GPU like a long chunk is.  The
 // pieces of a cut item leave (m, sum of p, sum of p v) in scratch, and a second
 // kernel joins them.  Each CTA finds its share itself from the lengths (no
 // planning launch, nothing kept between calls).
@@ -42,6 +43,7 @@ constexpr int kCaBad = 8;             // block flags in flight (at most 5 blocks
 // warps 0-7 softmax, 8 producer, 9 MMA (10 and 11 fill their warpgroup), 12-15 widening
 constexpr int kCaProducerWarp = 8, kCaMmaWarp = 9, kCaWidenWarp = 12;
 constexpr float kCaSlack = 8.f;
+constexpr int kCaShare = 2;           // least units of a share (so that it holds a block's first unit)
 // tensor memory: S of warpgroup w at 128 w, P over its first half, O at 256 + 128 w
 constexpr uint32_t kCaOCol = 256;
 
@@ -75,7 +77,7 @@ struct CaArgs {
   __nv_bfloat16* out;
   float* lse;
   CaCut* cuts;      // [kNumSMs]
-  float* part_o;    // [2 kNumSMs][rows][128]
+  float4* part_o;   // [2 kNumSMs][32][rows]: four dims of each row
   float2* part_ml;  // [2 kNumSMs][rows]
   int rows;         // rows of a partial slot
   DevError* err;
@@ -129,15 +131,18 @@ struct CaReq {
   __device__ __forceinline__ int blocks(int i) const {
     return (len - n + min(n, kCaTok * (i + 1)) - 1) / kBlock + 1;
   }
-  // blocks of the items before item i
+  // tensor-core work of one block of item i, in units: both tiles, or one
+  __device__ __forceinline__ int weight(int i) const { return n - kCaTok * i > kCaTok / 2 ? 2 : 1; }
+  // units of the items before item i (all of 16 tokens)
   __device__ __forceinline__ long long before(int i) const {
     const long long a = (static_cast<long long>(len) - n + kCaTok - 1) / kCaTok;
-    long long s = ca_eighths(a + i) - ca_eighths(a) + i;
-    // the last item may end short of 16 tokens
-    if (i == items() && i > 0) s += blocks(i - 1) - ((len - n + static_cast<long long>(kCaTok) * i - 1) / kBlock + 1);
-    return s;
+    return 2 * (ca_eighths(a + i) - ca_eighths(a) + i);
   }
-  __device__ __forceinline__ long long per_head() const { return n > 0 ? before(items()) : 0; }
+  __device__ __forceinline__ long long per_head() const {
+    if (n <= 0) return 0;
+    const int i = items() - 1;
+    return before(i) + static_cast<long long>(weight(i)) * blocks(i);
+  }
 };
 __device__ __forceinline__ bool ca_good(const CaArgs& a, long long c0, long long c1, int len) {
   return c0 >= 0 && c0 <= c1 && c1 <= a.tokens && c1 - c0 <= len && (len + kBlock - 1LL) / kBlock <= a.max_blocks;
@@ -168,6 +173,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 32 bytes in one store: a whole sector of the row
+__device__ __forceinline__ void ca_store32(void* p, const uint32_t (&y)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+               "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+               : "memory");
+}
 __device__ __forceinline__ bool ca_wait(uint64_t* bar, uint32_t parity, DevError* err, int where) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, where));
 }
@@ -199,8 +210,8 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   DevError* err = a.err;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (smem_u32(smem_raw) & 1023) {  // the swizzled tiles need it; with no static shared memory it holds
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) record_error(err, MSA_DEVERR_TIMEOUT, 899);
     return;
   }
@@ -235,6 +246,9 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     tc::alloc(&sm.tmem_base, 512);
     tc::relinquish();
   }
+  // the kernel before has completed; the joining kernel may be launched behind this one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- this CTA's share of the units ----
   // pass 1: all units; pass 2: the request that holds the first unit of the share
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     for (int w = 0; w < kThreads / 32; ++w) total += sm.wsum[w];
     __syncthreads();
   }
-  const long long ctas = min(static_cast<long long>(gridDim.x), max(total, 1LL));
+  const long long ctas = min(static_cast<long long>(gridDim.x), (total + kCaShare - 1) / kCaShare + (total == 0));
   const long long u0 = min(total, total * blockIdx.x / ctas), u1 = min(total, total * (blockIdx.x + 1) / ctas);
   if (u0 < u1) {
     long long base = 0;
@@ -311,7 +325,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       int r = sm.start_r;
       CaReq rq = ca_req(a, r);
       long long per = rq.per_head();
-      int g = static_cast<int>(sm.start_unit / per);
+      int g = (sm.start_unit >= per) + (sm.start_unit >= 2 * per) + (sm.start_unit >= 3 * per);
       const long long rem = sm.start_unit - g * per;
       int i = 0;  // the last item that begins at or before unit rem of the head
       for (int lo = 0, hi = rq.items() - 1; lo <= hi;) {
@@ -323,25 +337,26 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           hi = mid - 1;
         }
       }
-      int b = static_cast<int>(rem - rq.before(i));
-      long long at = u0;
+      long long at = u0, item0 = u0 - (rem - rq.before(i));  // where the share goes on, where the item begins
       while (ok) {
-        const int blocks = rq.blocks(i);
+        const int blocks = rq.blocks(i), weight = rq.weight(i);
+        const long long end = item0 + static_cast<long long>(blocks) * weight;
         CaItem it;
         it.t0 = rq.t0 + kCaTok * i;
         it.ntok = min(kCaTok, rq.n - kCaTok * i);
         it.g = g;
         it.pos0 = rq.len - rq.n + kCaTok * i;
         it.len = rq.len;
-        it.b0 = b;
-        it.nb = static_cast<int>(min(static_cast<long long>(blocks - b), u1 - at));
+        it.b0 = static_cast<int>((at - item0 + weight - 1) >> (weight - 1));
+        it.nb = static_cast<int>((min(end, u1) - item0 + weight - 1) >> (weight - 1)) - it.b0;
+        const int b = it.b0;
         const bool to_end = b + it.nb == blocks;
         it.slot = b == 0 && to_end ? -1 : static_cast<int>(2 * blockIdx.x + (b == 0));
-        at += it.nb;
-        if (b == 0 && !to_end) {
-          const long long last_unit = at + blocks - b - it.nb - 1;
-          cut = CaCut{it.t0, it.ntok, g, static_cast<int>(((last_unit + 1) * ctas + total - 1) / total - 1)};
-        }
+        // the share that holds the first unit of the item's last block
+        if (b == 0 && !to_end) cut = CaCut{it.t0, it.ntok, g, static_cast<int>(((end - weight + 1) * ctas - 1) / total)};
+        at = end;
+        item0 = end;
+        if (it.nb > 0) {
         // publish
         const int is = nitem % kCaInfo;
         if (!(ok = ca_wait(&sm.info_empty[is], ((nitem / kCaInfo) & 1) ^ 1, err, 800))) break;
@@ -406,9 +421,9 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
             }
           }
         }
+        }
         if (!ok || at >= u1) break;
         // the next item (the share goes on, so there is one)
-        b = 0;
         if (++i == rq.items()) {
           i = 0;
           if (++g == kKvHeads) {
@@ -678,7 +693,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       ocount += steps > 0;
       const int h = it.g * kGroup + (row & 15);
       const long long orow = (static_cast<long long>(it.t0) + tok) * kHeads + h;
-      const long long prow = static_cast<long long>(it.slot) * a.rows + tok * kGroup + (row & 15);
+      const long long prow = tok * kGroup + (row & 15);
       // f0, f1: what the two warpgroups' sums are multiplied by; l: the row's denominator; dims d0 ..
       float f0 = 1.f, f1 = 0.f;
       uint32_t c0 = ocol, c1 = ocol;
@@ -720,20 +735,19 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
             if (!dual && f1 != 0.f) o[q] = fmaf(__uint_as_float(v[q]), f1, o[q]);
           }
           if (valid && it.slot >= 0) {
-            float4* p = reinterpret_cast<float4*>(a.part_o + prow * kDim + d);
+            float4* p = a.part_o + (static_cast<long long>(it.slot) * (kDim / 4) + d / 4) * a.rows + prow;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) p[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) p[q * a.rows] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           } else if (valid) {
-            uint4* p = reinterpret_cast<uint4*>(a.out + orow * kDim + d);
+            uint32_t y[8];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-              p[q] = make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]), pack_bf16(o[8 * q + 2], o[8 * q + 3]),
-                                pack_bf16(o[8 * q + 4], o[8 * q + 5]), pack_bf16(o[8 * q + 6], o[8 * q + 7]));
+            for (int q = 0; q < 8; ++q) y[q] = pack_bf16(o[2 * q], o[2 * q + 1]);
+            ca_store32(a.out + orow * kDim + d, y);
           }
           __syncwarp();
         }
         if (valid && d0 == 0) {
-          if (it.slot >= 0) a.part_ml[prow] = make_float2(m, l);
+          if (it.slot >= 0) a.part_ml[static_cast<long long>(it.slot) * a.rows + prow] = make_float2(m, l);
           else if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : m + log2f(l);
         }
       }
@@ -832,40 +846,62 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   }
 }
 
-// Joins the pieces of the items that were cut: CTA c those of the item that begins in share c, a warp per row, four
-// dims per lane.
-constexpr int kCaJoinWarps = 16;
-__global__ void __launch_bounds__(kCaJoinWarps * 32) chunk_join_kernel(const __grid_constant__ CaArgs a) {
+// Joins the pieces of the items that were cut: CTA (c, e) token e of the item that begins in share c, 16 rows (the
+// token's heads).  The pieces' (m, l) go to shared memory; a warp per row turns them into factors; then thread (four
+// dims, row) adds up its values, the loads of eight pieces in flight at once.  Bound by the latency of those three
+// rounds, so the rows are spread over as many CTAs as there are tokens.
+constexpr int kCaJoinThreads = kGroup * kDim / 4;
+__global__ void __launch_bounds__(kCaJoinThreads) chunk_join_kernel(const __grid_constant__ CaArgs a) {
+  __shared__ float factor[kNumSMs][kGroup];
+  __shared__ float2 ml[kNumSMs][kGroup];
+  __shared__ float inv[kGroup];
+  __shared__ __align__(16) uint2 out[kGroup][kDim / 4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x, e = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, c = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const CaCut cut = a.cuts[c];
+  if (e >= cut.ntok) return;
   const int parts = cut.last - c + 1;
-  for (int r = threadIdx.x >> 5; r < cut.ntok * kGroup; r += kCaJoinWarps) {
-    auto at = [&](int s) { return static_cast<long long>(s == 0 ? 2 * c + 1 : 2 * (c + s)) * a.rows + r; };
-    float m = -INFINITY;
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, a.part_ml[at(s)].x);
+  auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
+  for (int i = tid; i < parts * kGroup; i += kCaJoinThreads)
+    ml[i / kGroup][i % kGroup] =
+        a.part_ml[static_cast<long long>(slot(i / kGroup)) * a.rows + e * kGroup + i % kGroup];
+  __syncthreads();
+  const long long row0 = (static_cast<long long>(cut.t0) + e) * kHeads + cut.g * kGroup;  // the token's first row
+  {
+    float m = -INFINITY, l = 0.f;
+    for (int s = lane; s < parts; s += 32) m = fmaxf(m, ml[s][warp].x);
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-      const float2 ml = a.part_ml[at(s)];
-      const float4 x = reinterpret_cast<const float4*>(a.part_o + at(s) * kDim)[lane];
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-      l = fmaf(f, ml.y, l);
-      o.x = fmaf(f, x.x, o.x);
-      o.y = fmaf(f, x.y, o.y);
-      o.z = fmaf(f, x.z, o.z);
-      o.w = fmaf(f, x.w, o.w);
+    for (int s = lane; s < parts; s += 32) {
+      const float f = ml[s][warp].x == -INFINITY ? 0.f : ex2(ml[s][warp].x - m);
+      factor[s][warp] = f;
+      l = fmaf(f, ml[s][warp].y, l);
     }
-    const float inv = l == 0.f ? 0.f : a.v_scale / l;
-    const long long row =
-        (static_cast<long long>(cut.t0) + r / kGroup) * kHeads + cut.g * kGroup + r % kGroup;
-    reinterpret_cast<uint2*>(a.out + row * kDim)[lane] =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m + log2f(l);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (lane == 0) {
+      inv[warp] = l == 0.f ? 0.f : a.v_scale / l;
+      if (a.lse) a.lse[row0 + warp] = l == 0.f ? -INFINITY : m + log2f(l);
+    }
   }
+  __syncthreads();
+  const int row = tid % kGroup, d4 = tid / kGroup;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = 0; s < parts; ++s) {
+    const float4 x = a.part_o[(static_cast<long long>(slot(s)) * (kDim / 4) + d4) * a.rows + e * kGroup + row];
+    const float f = factor[s][row];
+    o.x = fmaf(f, x.x, o.x);
+    o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z);
+    o.w = fmaf(f, x.w, o.w);
+  }
+  const float r = inv[row];
+  out[row][d4] = make_uint2(pack_bf16(o.x * r, o.y * r), pack_bf16(o.z * r, o.w * r));
+  __syncthreads();
+  if (tid < kGroup * kDim / 8)
+    reinterpret_cast<uint4*>(a.out + row0 * kDim)[tid] = reinterpret_cast<const uint4*>(&out[0][0])[tid];
 }
 
 // ---- host side ----------------------------------------------------------------------
@@ -904,6 +940,24 @@ static bool ca_encode_kv(CUtensorMap* map, const void* base, cuuint64_t slots, b
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch as a programmatic dependent of the kernel before it on the stream: the launch overlaps that kernel's end, and
+// nothing is read or written before it has completed (griddepcontrol.wait).
+template <class... Params, class... Args>
+static cudaError_t ca_launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t bytes,
+                                       cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <bool kFp8>
 static cudaError_t ca_launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, const CaArgs& a,
                              cudaStream_t stream) {
@@ -913,8 +967,8 @@ static cudaError_t ca_launch(const CUtensorMap& qmap, const CUtensorMap& kmap, c
                                                  static_cast<int>(bytes));
       e != cudaSuccess)
     return e;
-  chunk_attend_kernel<kFp8><<<kNumSMs, CaShape<kFp8>::kThreads, bytes, stream>>>(qmap, kmap, vmap, a);
-  return cudaGetLastError();
+  return ca_launch_dependent(chunk_attend_kernel<kFp8>, dim3(kNumSMs), CaShape<kFp8>::kThreads, bytes, stream, qmap, kmap,
+                             vmap, a);
 }
 
 cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream) {
@@ -942,24 +996,13 @@ cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream) {
   p += ca_up(kNumSMs * sizeof(CaCut));
   a.part_ml = reinterpret_cast<float2*>(p);
   p += ca_up(rows * sizeof(float2));
-  a.part_o = reinterpret_cast<float*>(p);
+  a.part_o = reinterpret_cast<float4*>(p);
   a.err = L.err;
   if (const cudaError_t e = L.kv_fp8 ? ca_launch<true>(qmap, kmap, vmap, a, stream)
                                      : ca_launch<false>(qmap, kmap, vmap, a, stream);
       e != cudaSuccess)
     return e;
-  // launched as a programmatic dependent: its launch overlaps the main kernel's end, and it reads nothing before that
-  // has completed
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kNumSMs);
-  cfg.blockDim = dim3(kCaJoinWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_join_kernel, a);
+  return ca_launch_dependent(chunk_join_kernel, dim3(kNumSMs, a.rows / kGroup), kCaJoinThreads, 0, stream, a);
 }
 
 }  // namespace msa
