@@ -5,26 +5,53 @@
 // a' = a cos - b sin, b' = a sin + b cos.  The turn is orthogonal, so its
 // gradient is the turn by the negative angle: the backward is the same kernel.
 //
-// The product of a 31-bit position and a 24-bit frequency has 55 bits, of
-// which fp32 would keep none of the fraction of a far position's angle; so
-// each angle is formed and reduced to a fraction of a turn in binary64 (once
-// per token and pair, shared by all heads) and sine and cosine are taken of
-// that fraction in fp32.  The rotation is fp32, rounded once to the output
-// type.
+// The angle of a far position keeps nothing of its fraction in fp32, so it is
+// reduced to a fraction of a turn before it is rounded: with u = inv_freq /
+// (2 pi) as a sum of two floats (exact products by fused multiply-adds), the
+// position times u loses less than 2^-25 of a turn as long as the position is
+// a float; one from 2^24 on takes the product in binary64.  Sine and cosine are
+// those of that fraction, once per token and pair, shared by all heads; the
+// rotation is fp32, rounded once to the output type.
 //
-// Each row is read once and written once: bound by HBM.  A CTA takes
-// kRoTokens tokens; its threads first fill a table of their (cos, sin) in
-// shared memory, then take the heads' rows, eight lanes to a row, two 16-byte
-// pieces to a lane, chosen so that a lane holds both members of its pairs.
-#include <cuda_fp8.h>
+// Each row is read once and written once: bound by HBM.  A CTA takes every
+// gridDim-th token through a ring of stages in shared memory: a producer warp
+// fills the stage's table of (cos, sin) and copies the token's rows in with the
+// bulk-copy engine; nine warps turn them where they are, eight lanes to a row of
+// 128 dims, two 16-byte pieces to a lane, chosen so that a lane holds both
+// members of its pairs; the producer copies the stage out, to q_out and (as they
+// lie there, or from the E4M3 bytes that the warps leave beside them) to the
+// caches' slots.  So no thread holds data that is on its way, and an SM has
+// kRoStages tokens of each of its CTAs in flight, 18 KB each.
+#include <algorithm>
 
 #include "launch.h"
 
 namespace msa {
 
-constexpr int kRoThreads = 256;
-constexpr int kRoTokens = 4;
-constexpr int kRoLanes = 8;  // lanes per row of 128 dims
+constexpr int kRoLanes = 8;    // lanes per row of 128 dims
+constexpr int kRoWarps = 9;    // turning warps: four rows each at a time, so 72 rows in two passes
+constexpr int kRoStages = 4;
+constexpr int kRoThreads = 32 * (kRoWarps + 1);
+constexpr int kRoRow = kDim * 2;
+
+// (cos, sin) of position * inv_freq.
+__device__ __forceinline__ float2 ro_turn(int position, float inv_freq) {
+  // 1 / (2 pi) as the sum of two floats
+  constexpr float kHi = 0.15915494f, kLo = static_cast<float>(0.15915494309189535 - static_cast<double>(kHi));
+  float turns;
+  if (abs(position) < (1 << 24)) {
+    const float p = static_cast<float>(position);
+    const float u = inv_freq * kHi, u_lo = fmaf(inv_freq, kLo, fmaf(inv_freq, kHi, -u));
+    const float t = p * u, t_lo = fmaf(p, u_lo, fmaf(p, u, -t));
+    turns = (t - rintf(t)) + t_lo;
+  } else {
+    const double t = static_cast<double>(position) * inv_freq * 0.15915494309189535;
+    turns = static_cast<float>(t - rint(t));
+  }
+  float s, c;
+  sincospif(2.f * turns, &s, &c);
+  return make_float2(c, s);
+}
 
 __device__ __forceinline__ void ro_unpack(const uint4& x, float (&f)[8]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -46,101 +73,202 @@ __device__ __forceinline__ uint2 ro_pack_e4m3(const float (&f)[8], float scale) 
   return make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
 }
 
-__global__ void __launch_bounds__(kRoThreads) rotary_kernel(RotaryLaunch a) {
-  __shared__ float2 turn[kRoTokens][kDim / 2];
-  const int tid = threadIdx.x;
-  const long long t0 = static_cast<long long>(blockIdx.x) * kRoTokens;
-  const int nt = static_cast<int>(min(static_cast<long long>(kRoTokens), a.tokens - t0));
-  const int pairs = a.rot.rot_dim / 2;
+// Copy shared -> global by the bulk-copy engine (16-byte aligned, bytes % 16 == 0; bulk group).
+__device__ __forceinline__ void ro_copy_out(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+// A bounded wait; the error word may be missing.
+__device__ __forceinline__ bool ro_wait(uint64_t* bar, uint32_t parity, DevError* err, int where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  do {
+    if (mbar_try_wait_suspend(bar, parity)) return true;
+  } while (global_ns() - t0 < kWaitNs);
+  if (err) record_error(err, MSA_DEVERR_TIMEOUT, where);
+  return false;
+}
 
-  for (int i = tid; i < nt * pairs; i += kRoThreads) {
-    const int tt = i / pairs, j = i - tt * pairs;
-    const int p = a.positions[a.rot.axis[j] * a.tokens + t0 + tt];
-    constexpr double kTurnsPerRadian = 0.15915494309189535;  // 1 / (2 pi)
-    const double turns = static_cast<double>(p) * static_cast<double>(a.inv_freq[j]) * kTurnsPerRadian;
-    float s, c;
-    sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
-    turn[tt][j] = make_float2(c, a.inverse ? -s : s);
+// A stage: the token's q, k and v rows, then (E4M3 caches) 1 KB of K and V bytes.
+struct RoGeom {
+  int q_bytes, k_bytes, v_bytes, stage;
+};
+
+__global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constant__ RotaryLaunch a, RoGeom geo) {
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ __align__(16) float2 turn[kRoStages][kDim / 2];
+  __shared__ uint64_t full[kRoStages], done[kRoStages];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kRoStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&done[i], kRoWarps);
+    }
+    fence_mbar_init();
   }
   __syncthreads();
+  const long long t0 = blockIdx.x;
+  const int n = static_cast<int>((a.tokens - t0 + gridDim.x - 1) / gridDim.x);  // tokens of this CTA
+  auto token = [&](int i) { return t0 + static_cast<long long>(i) * gridDim.x; };
+  const int pairs = a.rot.rot_dim / 2;
 
-  const int kv = a.v ? kKvHeads : 0;
-  const int rows = a.q_heads + a.k_heads + kv;  // per token: q, k, v
-  const int turned = a.rot.rot_dim / 16;        // lanes of a row that turn their 16 dims
-  const bool cross = !a.rot.interleaved;        // a lane's pieces hold the pairs' two members
-  for (int u = tid; u < nt * rows * kRoLanes; u += kRoThreads) {
-    const int lane = u % kRoLanes, row = u / kRoLanes;
-    const int tt = row / rows, h = row - tt * rows;
-    const long long t = t0 + tt;
-    const bool is_q = h < a.q_heads, is_k = !is_q && h < a.q_heads + a.k_heads;
-    const int head = is_q ? h : is_k ? h - a.q_heads : h - a.q_heads - a.k_heads;
-    const __nv_bfloat16* src =
-        is_q ? static_cast<const __nv_bfloat16*>(a.q) + t * a.q_stride
-             : is_k ? static_cast<const __nv_bfloat16*>(a.k) + t * a.k_stride
-                    : static_cast<const __nv_bfloat16*>(a.v) + t * a.v_stride;
-    // pieces of 8 dims: a turned lane of the split form takes piece l and the one
-    // rot_dim / 2 further on; every other lane takes 2 l and 2 l + 1
-    const bool rot = lane < turned && (is_q || is_k);
-    const bool split = cross && lane < turned;
-    const int pa = split ? lane : 2 * lane, pb = split ? lane + turned : 2 * lane + 1;
-    const uint4* s4 = reinterpret_cast<const uint4*>(src + head * kDim);
-    float x[8], y[8];
-    ro_unpack(s4[pa], x);
-    ro_unpack(s4[pb], y);
-    if (rot) {
-      if (cross) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 cs = turn[tt][8 * lane + i];
-          const float u0 = x[i], u1 = y[i];
-          x[i] = u0 * cs.x - u1 * cs.y;
-          y[i] = u0 * cs.y + u1 * cs.x;
+  if (warp == kRoWarps) {
+    // ---------------- producer ----------------
+    // each lane turns two pairs of a token; positions and slot are asked for one token ahead
+    const float f0 = lane < pairs ? a.inv_freq[lane] : 0.f, f1 = lane + 32 < pairs ? a.inv_freq[lane + 32] : 0.f;
+    const int32_t* at0 = a.positions + (lane < pairs ? a.rot.axis[lane] : 0) * a.tokens;
+    const int32_t* at1 = a.positions + (lane + 32 < pairs ? a.rot.axis[lane + 32] : 0) * a.tokens;
+    int p0 = at0[t0], p1 = at1[t0];
+    long long slots[kRoStages];  // of the tokens in flight
+    const bool insert = a.k_cache != nullptr;
+    // copies token i's stage out
+    auto copy_out = [&](int i, long long slot) {
+      const int s = i % kRoStages;
+      if (!__all_sync(0xffffffffu, ro_wait(&done[s], (i / kRoStages) & 1, a.err, 850))) return false;
+      if (lane == 0) {
+        const long long t = token(i);
+        const uint8_t* st = stages + s * geo.stage;
+        ro_copy_out(static_cast<uint8_t*>(a.q_out) + t * geo.q_bytes, st, geo.q_bytes);
+        if (a.k_out) ro_copy_out(static_cast<uint8_t*>(a.k_out) + t * geo.k_bytes, st + geo.q_bytes, geo.k_bytes);
+        if (slot >= a.num_slots) {
+          record_error(a.err, MSA_DEVERR_PAGE, t);
+        } else if (slot >= 0) {
+          const int bytes = kKvHeads * kDim * (a.kv_fp8 ? 1 : 2);
+          const uint8_t* kv = st + geo.q_bytes + (a.kv_fp8 ? geo.k_bytes + geo.v_bytes : 0);
+          ro_copy_out(static_cast<uint8_t*>(a.k_cache) + slot * bytes, kv, bytes);
+          ro_copy_out(static_cast<uint8_t*>(a.v_cache) + slot * bytes, kv + bytes, bytes);
         }
-      } else {
+        bulk_commit();
+      }
+      return true;
+    };
+    bool ok = true;
+    int i = 0;
+    for (int base = 0; base < n + kRoStages && ok; base += kRoStages) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 ca = turn[tt][8 * lane + i], cb = turn[tt][8 * lane + 4 + i];
-          const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
-          x[2 * i] = x0 * ca.x - x1 * ca.y;
-          x[2 * i + 1] = x0 * ca.y + x1 * ca.x;
-          y[2 * i] = y0 * cb.x - y1 * cb.y;
-          y[2 * i + 1] = y0 * cb.y + y1 * cb.x;
+      for (int s = 0; s < kRoStages; ++s) {
+        i = base + s;
+        if (i >= n + kRoStages || !ok) break;
+        if (i >= kRoStages && i - kRoStages < n) ok = copy_out(i - kRoStages, slots[s]);
+        if (!ok || i >= n) continue;
+        const int c0 = p0, c1 = p1;
+        slots[s] = insert ? a.slots[token(i)] : -1;
+        if (i + 1 < n) {
+          p0 = at0[token(i + 1)];
+          p1 = at1[token(i + 1)];
         }
+        if (lane < pairs) {
+          const float2 cs = ro_turn(c0, f0);
+          turn[s][lane] = make_float2(cs.x, a.inverse ? -cs.y : cs.y);
+        }
+        if (lane + 32 < pairs) {
+          const float2 cs = ro_turn(c1, f1);
+          turn[s][lane + 32] = make_float2(cs.x, a.inverse ? -cs.y : cs.y);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          bulk_wait_read_all();  // the stage has been copied out
+          const long long t = token(i);
+          uint8_t* st = stages + s * geo.stage;
+          mbar_expect_tx(&full[s], geo.q_bytes + geo.k_bytes + geo.v_bytes);
+          tma_bulk_g2s(st, static_cast<const __nv_bfloat16*>(a.q) + t * a.q_stride, geo.q_bytes, &full[s]);
+          if (geo.k_bytes)
+            tma_bulk_g2s(st + geo.q_bytes, static_cast<const __nv_bfloat16*>(a.k) + t * a.k_stride, geo.k_bytes,
+                         &full[s]);
+          if (geo.v_bytes)
+            tma_bulk_g2s(st + geo.q_bytes + geo.k_bytes, static_cast<const __nv_bfloat16*>(a.v) + t * a.v_stride,
+                         geo.v_bytes, &full[s]);
+        }
+        __syncwarp();
       }
     }
-    if (is_q || (is_k && a.k_out)) {
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_q ? a.q_out : a.k_out) +
-                           (t * (is_q ? a.q_heads : a.k_heads) + head) * kDim;
-      uint4* d4 = reinterpret_cast<uint4*>(dst);
-      d4[pa] = ro_pack(x);
-      d4[pb] = ro_pack(y);
-    }
-    if (!is_q && a.k_cache) {
-      const long long slot = a.slots[t];
-      if (slot >= a.num_slots) {
-        record_error(a.err, MSA_DEVERR_PAGE, t);
-      } else if (slot >= 0) {
-        const long long at = (slot * kKvHeads + head) * kDim;
-        void* cache = is_k ? a.k_cache : a.v_cache;
-        if (a.kv_fp8) {
-          const float scale = is_k ? a.k_scale : a.v_scale;
-          uint2* d2 = reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at);
+    // after a wait that gave up: the last fills may still be landing
+    if (!ok)
+      for (int s = 0; s < kRoStages; ++s) {
+        const int fills = (min(i + 1, n) - s + kRoStages - 1) / kRoStages;
+        if (fills > 0) ro_wait(&full[s], (fills - 1) & 1, a.err, 852);
+      }
+    if (lane == 0) bulk_wait_all();
+  } else {
+    // ---------------- turning warps ----------------
+    const int l = lane % kRoLanes, turned = a.rot.rot_dim / 16;  // lanes of a row that turn their 16 dims
+    const bool cross = !a.rot.interleaved;
+    // pieces of 8 dims: a turned lane of the split form takes piece l and the one rot_dim / 2 further on; every other lane
+    // takes 2 l and 2 l + 1
+    const bool split = cross && l < turned;
+    const int pa = split ? l : 2 * l, pb = split ? l + turned : 2 * l + 1;
+    const int qk = a.q_heads + a.k_heads, rows = a.kv_fp8 ? qk + kKvHeads : qk;  // (bf16 V rows pass untouched)
+    for (int i = 0; i < n; ++i) {
+      const int s = i % kRoStages;
+      if (!__all_sync(0xffffffffu, ro_wait(&full[s], (i / kRoStages) & 1, a.err, 851))) break;
+      uint8_t* st = stages + s * geo.stage;
+      float2 cs[8];
+      if (l < turned) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 v = reinterpret_cast<const float4*>(turn[s])[4 * l + j];
+          cs[2 * j] = make_float2(v.x, v.y);
+          cs[2 * j + 1] = make_float2(v.z, v.w);
+        }
+      }
+#pragma unroll 2
+      for (int h = warp * 4 + lane / kRoLanes; h < rows; h += kRoWarps * 4) {
+        uint4* row = reinterpret_cast<uint4*>(st + h * kRoRow);
+        const bool turns = l < turned && h < qk;
+        if (!turns && h < a.q_heads) continue;
+        float x[8], y[8];
+        ro_unpack(row[pa], x);
+        ro_unpack(row[pb], y);
+        if (turns) {
+          if (cross) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float x0 = x[j], y0 = y[j];
+              x[j] = x0 * cs[j].x - y0 * cs[j].y;
+              y[j] = x0 * cs[j].y + y0 * cs[j].x;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x0 = x[2 * j], x1 = x[2 * j + 1], y0 = y[2 * j], y1 = y[2 * j + 1];
+              x[2 * j] = x0 * cs[j].x - x1 * cs[j].y;
+              x[2 * j + 1] = x0 * cs[j].y + x1 * cs[j].x;
+              y[2 * j] = y0 * cs[4 + j].x - y1 * cs[4 + j].y;
+              y[2 * j + 1] = y0 * cs[4 + j].y + y1 * cs[4 + j].x;
+            }
+          }
+          row[pa] = ro_pack(x);
+          row[pb] = ro_pack(y);
+        }
+        if (a.kv_fp8 && h >= a.q_heads) {
+          uint2* d2 = reinterpret_cast<uint2*>(st + qk * kRoRow + geo.v_bytes + (h - a.q_heads) * kDim);
+          const float scale = h < qk ? a.k_scale : a.v_scale;
           d2[pa] = ro_pack_e4m3(x, scale);
           d2[pb] = ro_pack_e4m3(y, scale);
-        } else {
-          uint4* d4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + at);
-          d4[pa] = ro_pack(x);
-          d4[pb] = ro_pack(y);
         }
       }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&done[s]);
     }
   }
 }
 
 cudaError_t launch_rotary(const RotaryLaunch& L, cudaStream_t stream) {
   if (const cudaError_t e0 = launch_prologue(); e0 != cudaSuccess) return e0;
-  const long long grid = (L.tokens + kRoTokens - 1) / kRoTokens;
-  rotary_kernel<<<static_cast<unsigned>(grid), kRoThreads, 0, stream>>>(L);
+  RoGeom geo;
+  geo.q_bytes = L.q_heads * kRoRow;
+  geo.k_bytes = L.k_heads * kRoRow;
+  geo.v_bytes = L.v ? kKvHeads * kRoRow : 0;
+  geo.stage = (geo.q_bytes + geo.k_bytes + geo.v_bytes + (L.kv_fp8 ? 2 * kKvHeads * kDim : 0) + 127) / 128 * 128;
+  const int bytes = kRoStages * geo.stage;  // at most 4 x 32 KB
+  if (const cudaError_t e = cudaFuncSetAttribute(rotary_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      e != cudaSuccess)
+    return e;
+  // as many CTAs as fit an SM's shared memory (and its threads: six of 320), each through its share of the tokens
+  const int per_sm = std::min(6, 228 * 1024 / (bytes + 3584));
+  const long long grid = std::min<long long>(L.tokens, static_cast<long long>(kNumSMs) * per_sm);
+  rotary_kernel<<<static_cast<unsigned>(grid), kRoThreads, bytes, stream>>>(L, geo);
   return cudaGetLastError();
 }
 
