@@ -1161,6 +1161,10 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         uint4 x[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) x[q] = lds128(src + q * 16 * 128);
+        if (keys < kBlock)
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (row0 + 16 * q >= keys) x[q] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const int r = row0 + 16 * q;
@@ -1171,9 +1175,6 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
             y[2 * i] = ca_widen2(w[i]);
             y[2 * i + 1] = ca_widen2(w[i] >> 16);
           }
-          if (r >= keys)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = 0u;
           sts128(dst + sw128(r, 2 * (piece & 3)), y[0], y[1], y[2], y[3]);
           sts128(dst + sw128(r, 2 * (piece & 3) + 1), y[4], y[5], y[6], y[7]);
         }
