@@ -732,27 +732,28 @@ def _caches(k_cache, v_cache, index):
 
 
 class _Rotary(torch.autograd.Function):
-    """The rotation as an autograd function: the gradient turns back."""
+    """The rotation as an autograd function: its gradient is the rotation back (so it can be
+    differentiated again)."""
 
     @staticmethod
-    def forward(ctx, q, k, positions, inv_freq, axes, interleaved):
+    def forward(ctx, q, k, positions, inv_freq, axes, interleaved, inverse):
         ctx.save_for_backward(positions, inv_freq)
-        ctx.axes, ctx.interleaved = axes, interleaved
-        return msa_rotary(q, k, positions, inv_freq, axes=axes, interleaved=interleaved)
+        ctx.form = axes, interleaved, not inverse
+        return msa_rotary(q, k, positions, inv_freq, axes=axes, interleaved=interleaved, inverse=inverse)
 
     @staticmethod
     def backward(ctx, gq, gk):
-        positions, inv_freq = ctx.saved_tensors
-        dq, dk = msa_rotary(gq.contiguous(), gk.contiguous(), positions, inv_freq, axes=ctx.axes,
-                            interleaved=ctx.interleaved, inverse=True)
-        return dq, dk, None, None, None, None
+        dq, dk = _Rotary.apply(gq.contiguous(), gk.contiguous(), *ctx.saved_tensors, *ctx.form)
+        return dq, dk, None, None, None, None, None
 
 
 def rotary(q, k, positions, inv_freq, *, axes=None, interleaved=False):
     """Differentiable rotary positions: (q, k) rotated as by :func:`msa_rotary`; q and k receive
     gradients through the same kernel turning back."""
+    if k is None:
+        raise TypeError("rotary takes q and k (msa_rotary takes q alone)")
     axes = axes if axes is None or isinstance(axes, tuple) else tuple(axes)
-    return _Rotary.apply(q, k, positions, inv_freq, axes, bool(interleaved))
+    return _Rotary.apply(q, k, positions, inv_freq, axes, bool(interleaved), False)
 
 
 @functools.lru_cache(maxsize=1)

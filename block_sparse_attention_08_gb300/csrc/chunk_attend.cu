@@ -964,7 +964,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
               }
               return true;
             };
-            uint32_t x[4][32];  // the row of S, in four chunks of 32 columns
+            uint32_t x[4][32] = {};  // the row of S, in four chunks of 32 columns
             auto score = [&](int ch, int i) {
               const float v = __uint_as_float(x[ch][i]);
               return kMask && ch * 32 + i >= keys ? -INFINITY : v;

@@ -477,8 +477,8 @@ msa_status msa_unpack(const void* packed, const int64_t* token_rows, int64_t tot
  *   seq_lens, new_lens dev int32 [batch]; 0 <= new_lens[r] <= seq_lens[r] <= max_blocks * 128
  *   page_table   dev int32 [batch, max_blocks]; the entries of the opened pages
  *                are written, every other entry is left as it is
- *   free_pages   dev int32 [free_capacity]: the stack, its top at num_free[0] - 1
- *                (NULL with free_capacity 0)
+ *   free_pages   dev int32 [free_capacity]: the stack of distinct ids, its top at
+ *                num_free[0] - 1 (NULL with free_capacity 0)
  *   num_free     dev int32 [1]
  *   num_slots    slots of the cache, a multiple of 128
  *   capacity     rows of slots and positions (>= the new tokens; a larger one
@@ -540,7 +540,7 @@ msa_status msa_rotary(const msa_rotary_config* rot, const void* q, int64_t q_str
 /* The same rotation of q (64 heads) and k (4 heads), with the rotated k and v
  * written at slots[t] of the paged caches; a row with a negative slot is not
  * inserted, and no other slot is touched.  Two rows with the same slot leave
- * one of the two there.
+ * either's values, or some of each, there.
  *   v         dev bf16 [tokens, 4, 128], v_stride as q_stride
  *   slots     dev int64 [tokens]; one outside the cache is skipped and recorded
  *             (MSA_DEVERR_PAGE, detail = the row)
@@ -575,6 +575,8 @@ msa_status msa_rotary_insert(const msa_rotary_config* rot, const void* q, int64_
  *                in the base-2 domain of the scaled scores
  *   workspace    >= msa_workspace_size(cfg, MSA_MODE_CHUNK, total_tokens, max_blocks)
  * Slots behind a request's last key do not reach its rows, whatever they hold.
+ * (Among a request's own keys, a value of V that is not finite reaches the rows
+ * of all its new tokens from the start of that 128-key block on.)
  * A request with bad lengths (new > seq_lens[r], or seq_lens[r] > max_blocks *
  * 128) gets out 0 and lse -inf (MSA_DEVERR_LENGTH, detail r); the keys of a page
  * whose id is outside the pool are left out (MSA_DEVERR_PAGE, detail = the flat

@@ -89,6 +89,31 @@ def test_single_tokens(batch, cache):
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_more_requests_than_threads(cache):
+    lens = [1 + (r * 37) % 300 for r in range(1300)]
+    news = [min(n, 1 + (r % 7 == 0) + 15 * (r % 50 == 0)) for r, n in enumerate(lens)]
+    Batch(lens, news, cache, seed=4).poison().check()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [[1, 16, 17, 5], [40, 1, 1, 33]])
+def test_values_that_are_not_finite_stay_where_they_are(news, cache):
+    # a NaN query reaches its own row; a NaN key or an infinite value the rows of its request and KV head that see it
+    b = Batch([700, 500, 300, 200], news, cache, seed=6)
+    good = b.call()
+    b.q[0, 5, 3] = math.nan
+    slot = int(b.table[2, 1]) * 128 + 2  # key 130 of request 2: seen by all its new tokens
+    b.k[slot, 1, 7] = torch.tensor(math.nan).to(b.k.dtype)
+    got, lse = b.call()
+    bad = torch.zeros(b.q.shape[:2], dtype=torch.bool, device="cuda")
+    bad[0, 5] = True
+    at = int(b.cu[2])
+    bad[at:at + news[2], 16:32] = True
+    assert bool(torch.isnan(got[bad].float()).all()) and bool(torch.isnan(lse[bad]).all())
+    assert torch.equal(got[~bad], good[0][~bad]) and torch.equal(lse[~bad], good[1][~bad])
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_long_context_is_split_and_joined(cache):
     Batch([40000, 3, 17000], [1, 1, 20], cache).poison().check()
 

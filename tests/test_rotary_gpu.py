@@ -73,6 +73,34 @@ def test_gradient_against_differences():
         assert abs(num - float(dq[t, h, d])) <= tol
 
 
+def test_many_tokens_through_the_ring():
+    # more tokens than CTAs and stages: every CTA's ring goes round several times
+    gen, positions, inv_freq, axes = _setup(6007, 64, 3)
+    q, k = _randn(gen, 6007, 64, 128), _randn(gen, 6007, 4, 128)
+    qo, ko = msa.msa_rotary(q, k, positions, inv_freq, axes=axes)
+    _close(qo, S.rotate(q, positions, inv_freq, axes, False), q, 64, False)
+    _close(ko, S.rotate(k, positions, inv_freq, axes, False), k, 64, False)
+    qkv = torch.cat([q, k, k.flip(0)], 1)
+    slots = torch.randperm(6144, generator=gen, device="cuda")[:6007]
+    k_cache, v_cache = (torch.zeros(6144, 4, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    got = msa.msa_rotary_insert(qkv[:, :64], qkv[:, 64:68], qkv[:, 68:], positions, inv_freq, slots, k_cache, v_cache,
+                                axes=axes)
+    assert torch.equal(got, qo) and torch.equal(k_cache[slots], ko) and torch.equal(v_cache[slots], k.flip(0))
+
+
+def test_differentiated_twice():
+    gen, positions, inv_freq, axes = _setup(9, 128, 2)
+    q, k = _randn(gen, 9, 64, 128).requires_grad_(), _randn(gen, 9, 4, 128).requires_grad_()
+    g = _randn(gen, 9, 64, 128).requires_grad_()
+    out, _ = msa.rotary(q, k, positions, inv_freq, axes=axes)
+    (dq,) = torch.autograd.grad(out, q, g, create_graph=True)
+    h = _randn(gen, 9, 64, 128)
+    (dg,) = torch.autograd.grad(dq, g, h)
+    assert torch.equal(dg, msa.msa_rotary(h, None, positions, inv_freq, axes=axes)[0])
+    with pytest.raises(TypeError):
+        msa.rotary(q, None, positions, inv_freq)
+
+
 @pytest.mark.parametrize("far", [2 ** 20, 2 ** 24 + 1000, 2 ** 31 - 1])
 def test_far_positions_keep_their_angle(far):
     gen, positions, inv_freq, axes = _setup(64, 128, 2, far=far)
