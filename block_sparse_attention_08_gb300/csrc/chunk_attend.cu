@@ -52,7 +52,12 @@ constexpr int kCaBad = 8;             // block flags in flight (at most 5 blocks
 // warps 0-7 softmax, 8 producer, 9 MMA (10 and 11 fill their warpgroup), 12-15 widening
 constexpr int kCaProducerWarp = 8, kCaMmaWarp = 9, kCaWidenWarp = 12;
 constexpr float kCaSlack = 8.f;
-constexpr int kCaShare = 2;           // least units of a share (so that it holds a block's first unit)
+// Units that an item counts besides its blocks, for its start and its end: about what they take, but no more than 2 where
+// shares are short, since a share cannot be shorter than the distance between two blocks' first units.  (17 mixed
+// requests 0.103 ms with 0, 0.092 with 2; E4M3 chunks 0.601 with 0, 0.593 with 2, 0.573 with 4; four short single
+// tokens 0.016 with 0 and 2, 0.019 with 4.)
+constexpr int kCaItemShort = 2, kCaItemLong = 4, kCaLongShare = 128;
+constexpr int kCaShare = kCaItemShort + 2;  // least units of a share
 // tensor memory: S of warpgroup w at 128 w, P over its first half, O at 256 + 128 w
 constexpr uint32_t kCaOCol = 256;
 
@@ -147,6 +152,7 @@ __device__ __forceinline__ long long ca_eighths(long long x) {
 struct CaReq {
   int t0, n, len;
   bool apart;  // a last item of one token is not counted (it is shared out apart)
+  int extra;   // units of an item besides its blocks
   __device__ __forceinline__ bool one() const { return n % kCaTok == 1; }  // the last item has one token
   __device__ __forceinline__ int items() const { return (n + kCaTok - 1) / kCaTok - (apart && one()); }
   __device__ __forceinline__ int blocks(int i) const {
@@ -157,21 +163,25 @@ struct CaReq {
   // units of the items before item i (all of 16 tokens)
   __device__ __forceinline__ long long before(int i) const {
     const long long a = (static_cast<long long>(len) - n + kCaTok - 1) / kCaTok;
-    return 2 * (ca_eighths(a + i) - ca_eighths(a) + i);
+    return 2 * (ca_eighths(a + i) - ca_eighths(a) + i) + static_cast<long long>(extra) * i;
+  }
+  // units of item i
+  __device__ __forceinline__ long long units(int i) const {
+    return extra + static_cast<long long>(weight(i)) * blocks(i);
   }
   __device__ __forceinline__ long long per_head() const {
     const int i = items() - 1;
     if (i < 0) return 0;
-    return before(i) + static_cast<long long>(weight(i)) * blocks(i);
+    return before(i) + units(i);
   }
 };
 __device__ __forceinline__ bool ca_good(const CaArgs& a, long long c0, long long c1, int len) {
   return c0 >= 0 && c0 <= c1 && c1 <= a.tokens && c1 - c0 <= len && (len + kBlock - 1LL) / kBlock <= a.max_blocks;
 }
 // Request r; one with bad lengths has no tokens.
-__device__ __forceinline__ CaReq ca_req(const CaArgs& a, int r, bool apart) {
+__device__ __forceinline__ CaReq ca_req(const CaArgs& a, int r, bool apart, int extra = 0) {
   const int c0 = a.cu[r], c1 = a.cu[r + 1], len = a.seq_lens[r];
-  return ca_good(a, c0, c1, len) ? CaReq{c0, c1 - c0, len, apart} : CaReq{0, 0, 0, apart};
+  return ca_good(a, c0, c1, len) ? CaReq{c0, c1 - c0, len, apart, extra} : CaReq{0, 0, 0, apart, extra};
 }
 // Zeros for the rows of a request with bad lengths (the whole warp).
 __device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
@@ -212,7 +222,7 @@ __device__ __forceinline__ CaShareOf ca_find_share(const CaArgs& a, long long* w
     for (int w = 0; w < kThreads / 32; ++w) total += wsum[w];
     __syncthreads();
   }
-  const long long ctas = min(static_cast<long long>(gridDim.x), (total + kCaShare - 1) / kCaShare + (total == 0));
+  const long long ctas = min(static_cast<long long>(gridDim.x), max(total / kCaShare, 1LL));
   const long long u0 = min(total, total * blockIdx.x / ctas), u1 = min(total, total * (blockIdx.x + 1) / ctas);
   if (u0 < u1) {
     long long base = 0;
@@ -621,8 +631,13 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   // requests with bad lengths
   for (int r = blockIdx.x + gridDim.x * warp; r < a.batch; r += gridDim.x * (kThreads / 32))
     if (!ca_good(a, a.cu[r], a.cu[r + 1], a.seq_lens[r])) ca_refuse(a, r, lane);
-  const CaShareOf share = ca_find_share<kThreads>(
-      a, sm.wsum, &sm.start_r, &sm.start_unit, [&](int r) { return ca_req(a, r, kFp8).per_head(); });
+  int extra = kCaItemShort;
+  auto units_of = [&](int r) { return ca_req(a, r, kFp8, extra).per_head(); };
+  CaShareOf share = ca_find_share<kThreads>(a, sm.wsum, &sm.start_r, &sm.start_unit, units_of);
+  if (share.total > static_cast<long long>(gridDim.x) * kCaLongShare) {
+    extra = kCaItemLong;
+    share = ca_find_share<kThreads>(a, sm.wsum, &sm.start_r, &sm.start_unit, units_of);
+  }
   const long long total = share.total, ctas = share.ctas, u0 = share.u0, u1 = share.u1;
   CaShareOf share1{};
   if constexpr (kFp8)
@@ -655,7 +670,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     bool ok = true;
     if (u0 < u1) {
       int r = sm.start_r;
-      CaReq rq = ca_req(a, r, kFp8);
+      CaReq rq = ca_req(a, r, kFp8, extra);
       long long per = rq.per_head();
       int g = (sm.start_unit >= per) + (sm.start_unit >= 2 * per) + (sm.start_unit >= 3 * per);
       const long long rem = sm.start_unit - g * per;
@@ -672,15 +687,19 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       long long at = u0, item0 = u0 - (rem - rq.before(i));  // where the share goes on, where the item begins
       while (ok) {
         const int blocks = rq.blocks(i), weight = rq.weight(i);
-        const long long end = item0 + static_cast<long long>(blocks) * weight;
+        const long long end = item0 + rq.units(i);
+        // blocks whose first unit is before unit x of the item: block 0 begins at 0, block k > 0 after the item's own units
+        auto begun = [&](long long x) {
+          return x <= 0 ? 0 : 1 + static_cast<int>(max(0LL, x - 1 - rq.extra) >> (weight - 1));
+        };
         CaItem it;
         it.t0 = rq.t0 + kCaTok * i;
         it.ntok = min(kCaTok, rq.n - kCaTok * i);
         it.g = g;
         it.pos0 = rq.len - rq.n + kCaTok * i;
         it.len = rq.len;
-        it.b0 = static_cast<int>((at - item0 + weight - 1) >> (weight - 1));
-        it.nb = static_cast<int>((min(end, u1) - item0 + weight - 1) >> (weight - 1)) - it.b0;
+        it.b0 = begun(at - item0);
+        it.nb = min(blocks, begun(min(end, u1) - item0)) - it.b0;
         const int b = it.b0;
         const bool to_end = b + it.nb == blocks;
         it.slot = b == 0 && to_end ? -1 : static_cast<int>(2 * blockIdx.x + (b == 0));
@@ -761,7 +780,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           if (++g == kKvHeads) {
             g = 0;
             do {
-              rq = ca_req(a, ++r, kFp8);
+              rq = ca_req(a, ++r, kFp8, extra);
             } while (rq.items() == 0);
           }
         }

@@ -89,6 +89,15 @@ def test_single_tokens(batch, cache):
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_every_small_amount_of_work(cache):
+    # few blocks for many CTAs: shares at the least size they can have, with items of one and of two tiles
+    for blocks in range(1, 13):
+        for news in ([9], [1], [16, 1], [3, 12], [2, 2, 11]):
+            lens = [max(m, 128 * max(1, blocks // len(news)) - 5 * i) for i, m in enumerate(news)]
+            Batch(lens, news, cache, seed=blocks).check()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 def test_more_requests_than_threads(cache):
     lens = [1 + (r * 37) % 300 for r in range(1300)]
     news = [min(n, 1 + (r % 7 == 0) + 15 * (r % 50 == 0)) for r, n in enumerate(lens)]
