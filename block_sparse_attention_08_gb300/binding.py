@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libmsa (include/msa.h).
+"""Thin binding of libmsa (include/msa.h), by ctypes and, for the chunked-serving calls, by an
+extension module.
 
 Argument marshalling only: shapes, dtypes and devices are checked, raw
 pointers and the current CUDA stream are passed to the C ABI, and a non-OK
@@ -9,7 +10,7 @@ tensors are allocated with torch when the caller does not pass them.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import math
 import os
 import threading
@@ -113,12 +114,17 @@ def _call(name: str, *args):
     lib = _lib or load()
     st = getattr(lib, name)(*args)
     if st != 0:
-        text = lib.msa_status_string(st).decode()
-        if st == MSA_ERR_CUDA:
-            code = lib.msa_last_cuda_error()
-            text += f": {lib.msa_cuda_error_string(code).decode()} (cudaError {code})"
-        raise MsaError(name, st, text)
+        _fail(name, st)
     return st
+
+
+def _fail(name: str, st: int):
+    lib = load()
+    text = lib.msa_status_string(st).decode()
+    if st == MSA_ERR_CUDA:
+        code = lib.msa_last_cuda_error()
+        text += f": {lib.msa_cuda_error_string(code).decode()} (cudaError {code})"
+    raise MsaError(name, st, text)
 
 
 def make_config(topk: int = 16, init_blocks: int = 0, local_blocks: int = 1, index_dtype="bf16",
@@ -512,56 +518,30 @@ def msa_index_produce_decode(index_q, index_k, index_k_cache, seq_lens, page_tab
 
 
 # ---- chunked serving over the paged cache ------------------------------------------
-# These calls take a few microseconds on the device, so their checks are written to be
-# quick: one test per tensor, the reason only where it fails.  They run on the device of
-# their tensors, whatever the current one is, and share no scratch between calls (the
-# attention takes its own from the caching allocator), so calls on several streams or
-# threads and several captured graphs do not meet.  Without ``workspace`` a device error
-# goes to a word that nothing reads: pass a ``Workspace`` to read it.
+# These calls take a few microseconds on the device, so their checks, outputs and C calls
+# are made by an extension module (csrc/serving_ext.cpp).  They run on the device of their
+# tensors, whatever the current one is, and share no scratch between calls (the attention
+# takes its own from the caching allocator), so calls on several streams or threads and
+# several captured graphs do not meet.  Without ``workspace`` a device error goes to a
+# word that nothing reads: pass a ``Workspace`` to read it.
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_ERROR_WORDS: dict = {}
+_ext = None
 
 
-def _fit(t, name, dtype, shape, index):
-    """t must be a dense tensor of that dtype and shape on CUDA device ``index``."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
-            and t.is_contiguous()):
-        _need(t, name, dtype, shape)
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+def _serving():
+    """The extension module, built with the library."""
+    global _ext
+    if _ext is None:
+        load()
+        spec = importlib.util.spec_from_file_location("msa_serving", _build.EXT)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _ext = module
+    return _ext
 
 
-def _index(t, name):
-    """The CUDA device of the tensor that fixes the call's."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return index
-
-
-def _error_word(index, workspace):
-    """(address, bytes) of the workspace of a call that only needs the error word."""
-    if workspace is not None:
-        if workspace.buf.get_device() != index:
-            raise ValueError(f"workspace is on {workspace.buf.device}, expected cuda:{index}")
-        return workspace.buf.data_ptr(), workspace.nbytes
-    buf = _ERROR_WORDS.get(index)
-    if buf is None:  # never read, so it needs no initial value
-        buf = torch.empty(256, dtype=torch.uint8, device=f"cuda:{index}")
-        if not torch.cuda.is_current_stream_capturing():  # else it belongs to the graph's pool
-            _ERROR_WORDS.setdefault(index, buf)
-    return buf.data_ptr(), 256
-
-
-def _call_on(index, name, *args):
-    """The call ``name(*args, stream)`` on device ``index`` and its current stream."""
-    if torch.cuda.current_device() == index:
-        return _call(name, *args, _raw_stream(index))
-    with torch.cuda.device(index):
-        return _call(name, *args, _raw_stream(index))
+def _buf(workspace):
+    return None if workspace is None else workspace.buf
 
 
 def msa_map_slots(seq_lens, new_lens, page_table, free_pages, num_free, *, num_slots, capacity, cu_seqlens_q=None,
@@ -569,127 +549,17 @@ def msa_map_slots(seq_lens, new_lens, page_table, free_pages, num_free, *, num_s
     """Opens the pages of each request's new tokens (written into ``page_table``) and maps the
     tokens to slots (C: msa_map_slots): returns (cu_seqlens_q int32 [batch + 1], slots int64
     [capacity], positions int32 [capacity], num_free_out int32 [1])."""
-    i32, index = torch.int32, _index(seq_lens, "seq_lens")
-    B, capacity = seq_lens.shape[0], int(capacity)
-    _fit(seq_lens, "seq_lens", i32, (B,), index)
-    _fit(new_lens, "new_lens", i32, (B,), index)
-    mb = _width(page_table, "page_table")
-    _fit(page_table, "page_table", i32, (B, mb), index)
-    _fit(free_pages, "free_pages", i32, (free_pages.shape[0],), index)
-    _fit(num_free, "num_free", i32, (1,), index)
-    dev = seq_lens.device
-    if cu_seqlens_q is None:
-        cu_seqlens_q = torch.empty(B + 1, dtype=i32, device=dev)
-    else:
-        _fit(cu_seqlens_q, "cu_seqlens_q", i32, (B + 1,), index)
-    if slots is None:
-        slots = torch.empty(capacity, dtype=torch.int64, device=dev)
-    else:
-        _fit(slots, "slots", torch.int64, (capacity,), index)
-    if positions is None:
-        positions = torch.empty(capacity, dtype=i32, device=dev)
-    else:
-        _fit(positions, "positions", i32, (capacity,), index)
-    if num_free_out is None:
-        num_free_out = torch.empty(1, dtype=i32, device=dev)
-    else:
-        _fit(num_free_out, "num_free_out", i32, (1,), index)
-    ws, wn = _error_word(index, workspace)
-    _call_on(index, "msa_map_slots", seq_lens.data_ptr(), new_lens.data_ptr(), B, page_table.data_ptr(), mb,
-             free_pages.data_ptr() or None, free_pages.shape[0], num_free.data_ptr(), int(num_slots), capacity,
-             cu_seqlens_q.data_ptr(), slots.data_ptr(), positions.data_ptr(), num_free_out.data_ptr(), ws, wn)
-    return cu_seqlens_q, slots, positions, num_free_out
-
-
-def _width(t, name):
-    """Columns of a matrix."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected two dimensions")
-    return t.shape[1]
-
-
-@functools.lru_cache(maxsize=64)
-def _rotary_config(pairs, num_axes, axes, interleaved):
-    axes = (0,) * pairs if axes is None else tuple(int(a) for a in axes)
-    if len(axes) != pairs:
-        raise ValueError(f"axes has {len(axes)} entries, inv_freq has {pairs}")
-    if any(a < 0 or a >= num_axes for a in axes):
-        raise ValueError(f"axes must lie in [0, {num_axes}), the rows of positions")
-    if pairs > 64:
-        raise ValueError(f"inv_freq has {pairs} entries, at most 64 pairs of a head can turn")
-    cfg = msa_rotary_config(2 * pairs, int(bool(interleaved)), num_axes)
-    for j, a in enumerate(axes):
-        cfg.axis[j] = a
-    return cfg, ctypes.byref(cfg)
-
-
-def _rotary_args(positions, inv_freq, axes, interleaved, tokens, index):
-    """(address of the configuration, of positions, of inv_freq)."""
-    if not isinstance(positions, torch.Tensor) or not isinstance(inv_freq, torch.Tensor):
-        raise TypeError("positions and inv_freq must be torch.Tensors")
-    num_axes = positions.shape[0] if positions.dim() == 2 else 1
-    _fit(positions, "positions", torch.int32, (tokens,) if positions.dim() == 1 else (num_axes, tokens), index)
-    pairs = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
-    _fit(inv_freq, "inv_freq", torch.float32, (pairs,), index)
-    axes = axes if axes is None or isinstance(axes, tuple) else tuple(axes)
-    return _rotary_config(pairs, num_axes, axes, bool(interleaved))[1], positions.data_ptr(), inv_freq.data_ptr()
-
-
-def _token_rows(t, name, tokens, heads, index):
-    """Stride between the tokens of a bf16 [tokens, heads, 128] tensor whose heads are dense."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must have dtype {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape != (tokens, t.shape[1] if heads is None else heads, D):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, D)}")
-    heads = t.shape[1]
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != D and heads > 1):
-        raise ValueError(f"{name} must have dense heads, got strides {t.stride()}")
-    if tokens == 1:
-        return heads * D  # a single token's stride says nothing
-    if s0 < heads * D or s0 % 8:
-        raise ValueError(f"{name} must have tokens a multiple of 8 elements apart that do not overlap, got {s0}")
-    return s0
-
-
-def _tokens(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected three dimensions")
-    return t.shape[0], _index(t, name)
+    r = (_ext or _serving()).map_slots(seq_lens, new_lens, page_table, free_pages, num_free, num_slots, capacity,
+                                       cu_seqlens_q, slots, positions, num_free_out, _buf(workspace))
+    return r if type(r) is tuple else _fail("msa_map_slots", r)
 
 
 def msa_rotary(q, k, positions, inv_freq, *, axes=None, interleaved=False, inverse=False, q_out=None, k_out=None):
     """Rotary positions on q [tokens, heads, 128] and k (or None): returns (q_out, k_out)
     (C: msa_rotary).  ``positions`` int32 [tokens] or [axes, tokens], ``inv_freq`` fp32 [pairs],
     ``axes`` the axis of each pair (default: all 0), ``inverse`` turns back (the gradient)."""
-    T, index = _tokens(q, "q")
-    qs = _token_rows(q, "q", T, None, index)
-    rot, pos, freq = _rotary_args(positions, inv_freq, axes, interleaved, T, index)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    else:
-        _fit(q_out, "q_out", torch.bfloat16, q.shape, index)
-    kp, ks, kh, ko = None, 0, 0, None
-    if k is not None:
-        ks, kh, kp = _token_rows(k, "k", T, None, index), k.shape[1], k.data_ptr()
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
-        else:
-            _fit(k_out, "k_out", torch.bfloat16, k.shape, index)
-        ko = k_out.data_ptr()
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    _call_on(index, "msa_rotary", rot, q.data_ptr(), qs, q.shape[1], kp, ks, kh, pos, freq, T, int(bool(inverse)),
-             q_out.data_ptr(), ko)
-    return q_out, k_out
+    r = (_ext or _serving()).rotary(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out)
+    return r if type(r) is tuple else _fail("msa_rotary", r)
 
 
 def msa_rotary_insert(q, k, v, positions, inv_freq, slots, k_cache, v_cache, *, axes=None, interleaved=False,
@@ -698,37 +568,9 @@ def msa_rotary_insert(q, k, v, positions, inv_freq, slots, k_cache, v_cache, *, 
     written at ``slots`` (int64 [tokens], -1: not inserted) of the paged caches, bf16 or E4M3
     standing for scale * value; returns q_out (C: msa_rotary_insert).  ``k_out`` (optional)
     receives the rotated k as well."""
-    T, index = _tokens(q, "q")
-    qs, ks, vs = (_token_rows(q, "q", T, H, index), _token_rows(k, "k", T, G, index),
-                  _token_rows(v, "v", T, G, index))
-    rot, pos, freq = _rotary_args(positions, inv_freq, axes, interleaved, T, index)
-    _fit(slots, "slots", torch.int64, (T,), index)
-    num, fp8 = _caches(k_cache, v_cache, index)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    else:
-        _fit(q_out, "q_out", torch.bfloat16, (T, H, D), index)
-    if k_out is not None:
-        _fit(k_out, "k_out", torch.bfloat16, (T, G, D), index)
-    ws, wn = _error_word(index, workspace)
-    _call_on(index, "msa_rotary_insert", rot, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, pos, freq,
-             slots.data_ptr(), T, q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), k_cache.data_ptr(),
-             v_cache.data_ptr(), fp8, float(k_scale), float(v_scale), num, ws, wn)
-    return q_out
-
-
-def _caches(k_cache, v_cache, index):
-    """(slots, 1 for E4M3) of a pair of caches."""
-    if not isinstance(k_cache, torch.Tensor):
-        raise TypeError("k_cache must be a torch.Tensor")
-    dt = k_cache.dtype
-    fp8 = dt is torch.float8_e4m3fn or dt is torch.uint8
-    if not fp8 and dt is not torch.bfloat16:
-        raise ValueError(f"k_cache must be bf16, float8_e4m3fn or uint8, got {dt}")
-    num = k_cache.shape[0] if k_cache.dim() else 0
-    _fit(k_cache, "k_cache", dt, (num, G, D), index)
-    _fit(v_cache, "v_cache", dt, (num, G, D), index)
-    return num, int(fp8)
+    r = (_ext or _serving()).rotary_insert(q, k, v, positions, inv_freq, slots, k_cache, v_cache, axes, interleaved,
+                                           k_scale, v_scale, q_out, k_out, _buf(workspace))
+    return r if type(r) is not int else _fail("msa_rotary_insert", r)
 
 
 class _Rotary(torch.autograd.Function):
@@ -743,7 +585,13 @@ class _Rotary(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, gq, gk):
-        dq, dk = _Rotary.apply(gq.contiguous(), gk.contiguous(), *ctx.saved_tensors, *ctx.form)
+        gq, gk = gq.contiguous(), gk.contiguous()
+        if torch.is_grad_enabled():
+            dq, dk = _Rotary.apply(gq, gk, *ctx.saved_tensors, *ctx.form)
+        else:
+            positions, inv_freq = ctx.saved_tensors
+            axes, interleaved, inverse = ctx.form
+            dq, dk = msa_rotary(gq, gk, positions, inv_freq, axes=axes, interleaved=interleaved, inverse=inverse)
         return dq, dk, None, None, None, None, None
 
 
@@ -752,54 +600,7 @@ def rotary(q, k, positions, inv_freq, *, axes=None, interleaved=False):
     gradients through the same kernel turning back."""
     if k is None:
         raise TypeError("rotary takes q and k (msa_rotary takes q alone)")
-    axes = axes if axes is None or isinstance(axes, tuple) else tuple(axes)
     return _Rotary.apply(q, k, positions, inv_freq, axes, bool(interleaved), False)
-
-
-@functools.lru_cache(maxsize=1)
-def _chunk_config():
-    cfg = make_config()
-    return cfg, ctypes.byref(cfg)
-
-
-@functools.lru_cache(maxsize=1024)
-def _chunk_bytes(tokens, max_blocks):
-    return workspace_size(_chunk_config()[0], MODE_CHUNK, tokens, max_blocks)
-
-
-def _attend_chunk(name, want_fp8, kv_scales, q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, scale, out,
-                  lse, workspace):
-    T, index = _tokens(q, "q")
-    _fit(q, "q", torch.bfloat16, (T, H, D), index)
-    num, fp8 = _caches(k_cache, v_cache, index)
-    if fp8 != want_fp8:
-        raise ValueError(f"{name} takes {'float8_e4m3fn or uint8' if want_fp8 else 'bf16'} caches, "
-                         f"got {k_cache.dtype}")
-    mb = _width(page_table, "page_table")
-    B = page_table.shape[0]
-    _fit(page_table, "page_table", torch.int32, (B, mb), index)
-    _fit(seq_lens, "seq_lens", torch.int32, (B,), index)
-    _fit(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,), index)
-    if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    else:
-        _fit(out, "out", torch.bfloat16, (T, H, D), index)
-    if lse is not None:
-        _fit(lse, "lse", torch.float32, (T, H), index)
-    if workspace is None:
-        wn = _chunk_bytes(T, mb)
-        scratch = torch.empty(wn, dtype=torch.uint8, device=q.device)
-        ws = scratch.data_ptr()
-    else:
-        ws, wn = _error_word(index, workspace)
-    _call_on(index, name, _chunk_config()[1], q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *kv_scales,
-             seq_lens.data_ptr(), page_table.data_ptr(), cu_seqlens_q.data_ptr(), B, mb, T, num,
-             _DEFAULT_SCALE if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
-             ws, wn)
-    return out
-
-
-_DEFAULT_SCALE = 1.0 / math.sqrt(D)
 
 
 def msa_attend_chunk(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, *, scale=None, out=None, lse=None,
@@ -808,16 +609,18 @@ def msa_attend_chunk(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, *,
     their keys in the paged cache (C: msa_attend_chunk).  ``lse`` (fp32 [tokens, 64], optional)
     receives the log2 of the softmax denominators.  Rows from cu_seqlens_q[-1] on are left as they
     are."""
-    return _attend_chunk("msa_attend_chunk", 0, (), q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, scale,
-                         out, lse, workspace)
+    r = (_ext or _serving()).attend_chunk(False, q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, 1.0, 1.0,
+                                          scale, out, lse, _buf(workspace))
+    return r if type(r) is not int else _fail("msa_attend_chunk", r)
 
 
 def msa_attend_chunk_fp8kv(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, *, k_scale=1.0, v_scale=1.0,
                            scale=None, out=None, lse=None, workspace=None):
     """:func:`msa_attend_chunk` over E4M3 caches standing for k_scale * k and v_scale * v
     (C: msa_attend_chunk_fp8kv)."""
-    return _attend_chunk("msa_attend_chunk_fp8kv", 1, (float(k_scale), float(v_scale)), q, k_cache, v_cache, seq_lens, page_table,
-                         cu_seqlens_q, scale, out, lse, workspace)
+    r = (_ext or _serving()).attend_chunk(True, q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, k_scale,
+                                          v_scale, scale, out, lse, _buf(workspace))
+    return r if type(r) is not int else _fail("msa_attend_chunk_fp8kv", r)
 
 
 # ---- packing ----------------------------------------------------------------------

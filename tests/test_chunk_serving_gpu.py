@@ -73,3 +73,63 @@ def test_prompts_in_chunks_then_single_tokens(fp8):
     call = msa.msa_attend_chunk_fp8kv if fp8 else msa.msa_attend_chunk
     S.check_attend(call(qd, k_cache, v_cache, S.ints(lens), table, cu, **scales), None, ref, max(lens), 11 if fp8 else 8)
     S.check_attend(sparse, None, ref, max(lens), 11 if fp8 else 8)
+
+
+def test_refusals_of_wrong_tensors():
+    def ints(*shape):
+        return torch.zeros(shape, dtype=torch.int32, device="cuda")
+    q = torch.zeros(4, 64, 128, dtype=torch.bfloat16, device="cuda")
+    c = torch.zeros(256, 4, 128, dtype=torch.bfloat16, device="cuda")
+    freq, slots = torch.ones(64, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
+    attend = [q, c, c, ints(2), ints(2, 3), ints(3)]
+    for where, bad, text in ((0, q.float(), "dtype"), (0, q[:, ::2], "shape"), (0, q.transpose(0, 1)[:4], "shape|contiguous"),
+                             (0, q.repeat(2, 1, 1)[::2], "contiguous"), (1, c[:, :2], "shape"), (1, c.half(), "k_cache must be bf16"),
+                             (2, c[:128], "shape"), (2, c.to(torch.float8_e4m3fn), "dtype"), (3, ints(3), "shape"),
+                             (3, ints(2).long(), "dtype"), (3, ints(2).cpu(), "CUDA"), (4, ints(2, 6)[:, ::2], "contiguous"),
+                             (4, ints(2), "dimensions"), (5, ints(2), "shape")):
+        args = list(attend)
+        args[where] = bad
+        with pytest.raises(ValueError, match=text):
+            msa.msa_attend_chunk(*args)
+    with pytest.raises(ValueError, match="takes float8_e4m3fn or uint8 caches"):
+        msa.msa_attend_chunk_fp8kv(*attend)
+    with pytest.raises(ValueError, match="takes bf16 caches"):
+        msa.msa_attend_chunk(q, c.to(torch.float8_e4m3fn), c.to(torch.float8_e4m3fn), *attend[3:])
+    with pytest.raises(ValueError, match="lse"):
+        msa.msa_attend_chunk(*attend, lse=torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="out"):
+        msa.msa_attend_chunk(*attend, out=q[:3])
+    for kw in ({"scale": 0.0}, {"scale": math.nan}, {"workspace": msa.Workspace(256)}):
+        with pytest.raises(msa.MsaError):
+            msa.msa_attend_chunk(*attend, **kw)
+    with pytest.raises(msa.MsaError):  # no rows
+        msa.msa_attend_chunk(q[:0], *attend[1:])
+    k, pos = q[:, :4].contiguous(), ints(4)
+    for args, text in (((q, k, ints(5), freq), "positions"), ((q, k[:3], pos, freq), "k has shape"),
+                       ((q[:, :, ::2], k, pos, freq), "q has shape"), ((q[..., :64].repeat(1, 1, 2)[:, ::2], k, pos, freq), "dense heads"),
+                       ((q, k, pos, freq.double()), "inv_freq")):
+        with pytest.raises(ValueError, match=text):
+            msa.msa_rotary(*args)
+    with pytest.raises(ValueError, match="tokens"):
+        msa.msa_rotary(q[:1].expand(4, 64, 128), None, pos, freq)
+    with pytest.raises(ValueError, match="k_out without k"):
+        msa.msa_rotary(q, None, pos, freq, k_out=k)
+    with pytest.raises(msa.MsaError):  # 12 pairs: rot_dim 24
+        msa.msa_rotary(q, None, pos, freq[:12].contiguous())
+    insert = [q, k, k, pos, freq, slots, c, c]
+    for where, bad, text in ((2, k.float(), "v must have dtype"), (5, slots.int(), "slots"), (6, c[:, :3], "k_cache"),
+                             (7, c.to(torch.float8_e4m3fn), "v_cache")):
+        args = list(insert)
+        args[where] = bad
+        with pytest.raises(ValueError, match=text):
+            msa.msa_rotary_insert(*args)
+    b8 = c.to(torch.float8_e4m3fn)
+    with pytest.raises(msa.MsaError):
+        msa.msa_rotary_insert(*insert[:6], b8, b8, k_scale=-1.0)
+    slot_args = [ints(2), ints(2), ints(2, 3), ints(5), ints(1)]
+    for kw in ({"num_slots": 100, "capacity": 4}, {"num_slots": 128, "capacity": 0},
+               {"num_slots": 128, "capacity": 4, "num_free_out": slot_args[4]}):
+        with pytest.raises(msa.MsaError):
+            msa.msa_map_slots(*slot_args, **kw)
+    with pytest.raises(ValueError, match="new_lens"):
+        msa.msa_map_slots(slot_args[0], ints(3), *slot_args[2:], num_slots=128, capacity=4)

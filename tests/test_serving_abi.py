@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_sparse_attention_08_gb300 as msa
-from block_sparse_attention_08_gb300.binding import _rotary_config, _token_rows, msa_config, msa_rotary_config
+from block_sparse_attention_08_gb300.binding import msa_config, msa_rotary_config
 
 OK, NULL, SHAPE, DTYPE, WORKSPACE, ALIGN = 0, 1, 2, 3, 4, 5
 FAKE = 0x10000  # 256-byte aligned, never read: every call below is refused first
@@ -87,15 +87,26 @@ def test_attend_chunk(lib):
 
 def test_the_binding_refuses_other_tensors():
     x = torch.zeros(4, 64, 128, dtype=torch.bfloat16)
+    i = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
-        msa.msa_attend_chunk(x, x, x, x, x, x)
+        msa.msa_attend_chunk(x, x, x, i, i[None], i)
+    with pytest.raises(ValueError, match="q has shape .4,., expected 3 dimensions"):
+        msa.msa_attend_chunk(i, x, x, i, i, i)
+    with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+        msa.msa_attend_chunk_fp8kv(None, x, x, i, i[None], i)
     with pytest.raises(ValueError, match="CUDA"):
-        msa.msa_rotary(x, None, torch.zeros(4, dtype=torch.int32), torch.zeros(64))
-    with pytest.raises(ValueError, match="CUDA"):
-        msa.msa_map_slots(*[torch.zeros(1, dtype=torch.int32)] * 5, num_slots=128, capacity=1)
-    with pytest.raises(TypeError):
-        _token_rows(None, "q", 1, 64, 0)
-    with pytest.raises(ValueError, match="axes has 3"):
-        _rotary_config(64, 1, (0, 0, 0), False)
+        msa.msa_rotary(x, None, i, torch.zeros(64))
+    with pytest.raises(ValueError, match="axes has 3 entries, inv_freq has 64"):
+        msa.msa_rotary(x, None, i, torch.zeros(64), axes=(0, 0, 0))
     with pytest.raises(ValueError, match="axes must lie"):
-        _rotary_config(2, 1, (0, 1), False)
+        msa.msa_rotary(x, None, i, torch.zeros(2), axes=[0, 1])
+    with pytest.raises(ValueError, match="at most 64 pairs"):
+        msa.msa_rotary(x, None, i, torch.zeros(65))
+    with pytest.raises(TypeError):
+        msa.msa_rotary(x, None, i, torch.zeros(2), axes=[0, "x"])
+    with pytest.raises(TypeError):
+        msa.msa_rotary_insert(x, x, x, i, torch.zeros(64), i, x, x, k_scale="x")
+    with pytest.raises(ValueError, match="CUDA"):
+        msa.msa_map_slots(i, i, i[None], i, i[:1], num_slots=128, capacity=1)
+    with pytest.raises(TypeError):
+        msa.msa_map_slots(i, i, i[None], i, i[:1], num_slots=128, capacity=1.5)
