@@ -49,7 +49,7 @@ constexpr int kCaQEntry = 4096;       // one token's 16 heads x 128 dims
 constexpr int kCaInfo = 4;            // item descriptors in flight
 constexpr int kCaOnePlaces = 5;       // blocks in flight of one-token items (32 KB each)
 constexpr int kCaBad = 8;             // block flags in flight (at most 5 blocks are)
-// warps 0-7 softmax, 8 producer, 9 MMA (10 and 11 fill their warpgroup), 12-15 widening
+// warps 0-7 softmax, 8 producer, 9 MMA, 10 bad requests (11 fills their warpgroup), 12-15 widening
 constexpr int kCaProducerWarp = 8, kCaMmaWarp = 9, kCaWidenWarp = 12;
 constexpr float kCaSlack = 8.f;
 // Units that an item counts besides its blocks, for its start and its end: about what they take, but no more than 2 where
@@ -118,6 +118,16 @@ struct CaShape {
   static constexpr float kLift = kFp8 ? 7.f : 0.f;
 };
 
+// A CTA's part [u0, u1) of all units.
+struct CaShareOf {
+  long long total, ctas, u0, u1;
+};
+// The request (and the unit in it) where a share begins.
+struct CaStart {
+  long long unit;
+  int r;
+};
+
 template <bool kFp8>
 struct CaSmem {
   uint8_t q[2][kCaTile];
@@ -134,9 +144,9 @@ struct CaSmem {
   uint64_t one_x_full, one_x_done;
   CaItem info[kCaInfo];
   int bad[kCaBad];
-  long long wsum[16];
-  long long start_unit, one_start_unit;
-  int start_r, one_start_r;
+  long long wsum[kFp8 ? 2 : 1][CaShape<kFp8>::kThreads / 32];
+  CaStart start[kFp8 ? 2 : 1];  // of the items, and of the one-token items
+  CaShareOf share[kFp8 ? 2 : 1];
   uint32_t tmem_base;
 };
 
@@ -183,6 +193,11 @@ __device__ __forceinline__ CaReq ca_req(const CaArgs& a, int r, bool apart, int 
   const int c0 = a.cu[r], c1 = a.cu[r + 1], len = a.seq_lens[r];
   return ca_good(a, c0, c1, len) ? CaReq{c0, c1 - c0, len, apart, extra} : CaReq{0, 0, 0, apart, extra};
 }
+// Blocks of a request's last item where that has one token.
+__device__ __forceinline__ long long ca_one_blocks(const CaArgs& a, int r) {
+  const CaReq q = ca_req(a, r, true);
+  return q.one() ? (q.len - 1) / kBlock + 1 : 0;
+}
 // Zeros for the rows of a request with bad lengths (the whole warp).
 __device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
   if (lane == 0) record_error(a.err, MSA_DEVERR_LENGTH, r);
@@ -194,56 +209,70 @@ __device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
     for (long long i = c0 * kHeads + lane; i < c1 * kHeads; i += 32) a.lse[i] = -INFINITY;
 }
 
-// A CTA's part [u0, u1) of all units.
-struct CaShareOf {
-  long long total, ctas, u0, u1;
-};
-// The whole CTA: sums up `per_head(r)` units of each request and KV head, and finds the request (and the unit in it) where
-// this CTA's share begins.
-template <int kThreads, class F>
-__device__ __forceinline__ CaShareOf ca_find_share(const CaArgs& a, long long* wsum, int* start_r, long long* start_unit,
-                                                   F per_head) {
+// The whole CTA: sums up the units of each request, of kN kinds at once (`units_of(r, n)`: per KV head), and finds where this
+// CTA's share of each kind begins.  (The caller's barrier follows.)
+template <int kThreads, int kN, class F>
+__device__ __forceinline__ void ca_find_shares(const CaArgs& a, long long (*wsum)[kThreads / 32], CaStart* start,
+                                               CaShareOf (&share)[kN], F units_of) {
+  constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto units_of = [&](int r) { return r < a.batch ? kKvHeads * per_head(r) : 0LL; };
-  auto warp_incl = [&](long long x) {
+  // the sums up to and with this thread's request of the pass, in the warp; the warps' own sums in wsum
+  auto pass = [&](int r0, long long (&u)[kN], long long (&incl)[kN]) {
+    const int r = r0 + tid;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
+    for (int n = 0; n < kN; ++n) {
+      incl[n] = u[n] = r < a.batch ? kKvHeads * units_of(r, n) : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl[n], d);
+        if (lane >= d) incl[n] += y;
+      }
+      if (lane == 31) wsum[n][warp] = incl[n];
     }
-    return x;
+    __syncthreads();
   };
-  const long long first = units_of(tid);
-  long long total = 0;
-  for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
-    const long long incl = warp_incl(r0 ? units_of(r0 + tid) : first);
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) total += wsum[w];
-    __syncthreads();
-  }
-  const long long ctas = min(static_cast<long long>(gridDim.x), max(total / kCaShare, 1LL));
-  const long long u0 = min(total, total * blockIdx.x / ctas), u1 = min(total, total * (blockIdx.x + 1) / ctas);
-  if (u0 < u1) {
-    long long base = 0;
+  auto split = [&](CaShareOf& s) {
+    s.ctas = min(static_cast<long long>(gridDim.x), max(s.total / kCaShare, 1LL));
+    s.u0 = min(s.total, s.total * blockIdx.x / s.ctas);
+    s.u1 = min(s.total, s.total * (blockIdx.x + 1) / s.ctas);
+  };
+  const bool once = a.batch <= kThreads;
+  long long u[kN], incl[kN], base[kN] = {};
+#pragma unroll
+  for (int n = 0; n < kN; ++n) share[n] = CaShareOf{0, 1, 0, 0};
+  __syncthreads();  // wsum may be in use by a call before
+  if (!once) {
     for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
-      const long long u = r0 ? units_of(r0 + tid) : first, incl = warp_incl(u);
-      if (lane == 31) wsum[warp] = incl;
-      __syncthreads();
-      long long before = base;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += wsum[w];
-        base += wsum[w];
-      }
-      before += incl - u;
-      if (before <= u0 && u0 < before + u) {
-        *start_r = r0 + tid;
-        *start_unit = u0 - before;
-      }
+      pass(r0, u, incl);
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+        for (int w = 0; w < kWarps; ++w) share[n].total += wsum[n][w];
       __syncthreads();
     }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) split(share[n]);
   }
-  return CaShareOf{total, ctas, u0, u1};
+  for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
+    pass(r0, u, incl);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      long long before = base[n];
+#pragma unroll 4
+      for (int w = 0; w < kWarps; ++w) {
+        const long long x = wsum[n][w];
+        if (w < warp) before += x;
+        base[n] += x;
+      }
+      if (once) {
+        share[n].total = base[n];
+        split(share[n]);
+      }
+      before += incl[n] - u[n];
+      if (share[n].u0 < share[n].u1 && before <= share[n].u0 && share[n].u0 < before + u[n])
+        start[n] = CaStart{share[n].u0 - before, r0 + tid};
+    }
+    if (!once) __syncthreads();
+  }
 }
 
 // Instruction descriptors: fp32 accumulation, A and B bf16 (or fp16), M = N = 128; B (V) MN-major for O.
@@ -297,11 +326,6 @@ __device__ __forceinline__ uint32_t ca_widen2(uint32_t x) {
 // k-step s, so Q's fragments hold those dims in the same slots.  O += P V: a transposing ldmatrix gives a lane two
 // dims of two keys, which make one value pair for each of two products, one for the even dims and one for the odd.
 // Bound by HBM: per SM and block 32 KB are copied in and read once.
-__device__ __forceinline__ long long ca_one_blocks(const CaArgs& a, int r) {
-  const CaReq q = ca_req(a, r, true);
-  return q.one() ? (q.len - 1) / kBlock + 1 : 0;
-}
-
 // The copies (the producer warp).
 __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CUtensorMap& vmap, const CaArgs& a,
                                                const CaShareOf& share, CaSmem<true>& sm) {
@@ -314,8 +338,8 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
     int nitem = 0, nblk = 0;
     bool ok = true;
     if (share.u0 < share.u1) {
-      int r = sm.one_start_r;
-      const long long start = sm.one_start_unit;
+      int r = sm.start[1].r;
+      const long long start = sm.start[1].unit;
       long long per = ca_one_blocks(a, r);
       int g = (start >= per) + (start >= 2 * per) + (start >= 3 * per);
       int b = static_cast<int>(start - g * per);
@@ -628,21 +652,21 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // requests with bad lengths
-  for (int r = blockIdx.x + gridDim.x * warp; r < a.batch; r += gridDim.x * (kThreads / 32))
-    if (!ca_good(a, a.cu[r], a.cu[r + 1], a.seq_lens[r])) ca_refuse(a, r, lane);
+  constexpr int kKinds = kFp8 ? 2 : 1;
+  CaShareOf shares[kKinds];
   int extra = kCaItemShort;
-  auto units_of = [&](int r) { return ca_req(a, r, kFp8, extra).per_head(); };
-  CaShareOf share = ca_find_share<kThreads>(a, sm.wsum, &sm.start_r, &sm.start_unit, units_of);
-  if (share.total > static_cast<long long>(gridDim.x) * kCaLongShare) {
+  auto find = [&] {
+    ca_find_shares<kThreads, kKinds>(a, sm.wsum, sm.start, shares, [&](int r, int kind) {
+      return kind ? ca_one_blocks(a, r) : ca_req(a, r, kFp8, extra).per_head();
+    });
+  };
+  find();
+  if (shares[0].total > static_cast<long long>(gridDim.x) * kCaLongShare) {
     extra = kCaItemLong;
-    share = ca_find_share<kThreads>(a, sm.wsum, &sm.start_r, &sm.start_unit, units_of);
+    find();
   }
-  const long long total = share.total, ctas = share.ctas, u0 = share.u0, u1 = share.u1;
-  CaShareOf share1{};
-  if constexpr (kFp8)
-    share1 = ca_find_share<kThreads>(a, sm.wsum, &sm.one_start_r, &sm.one_start_unit,
-                                     [&](int r) { return ca_one_blocks(a, r); });
+  if (tid == 0)
+    for (int n = 0; n < kKinds; ++n) sm.share[n] = shares[n];
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -665,15 +689,16 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       prefetch_tmap(&kmap);
       prefetch_tmap(&vmap);
     }
+    const long long total = sm.share[0].total, ctas = sm.share[0].ctas, u0 = sm.share[0].u0, u1 = sm.share[0].u1;
     CaCut cut{0, 0, 0, 0};
     int nitem = 0, nq = 0, nload = 0, nblk = 0;  // descriptors, Q tiles, K / V tiles and blocks issued
     bool ok = true;
     if (u0 < u1) {
-      int r = sm.start_r;
+      int r = sm.start[0].r;
       CaReq rq = ca_req(a, r, kFp8, extra);
       long long per = rq.per_head();
-      int g = (sm.start_unit >= per) + (sm.start_unit >= 2 * per) + (sm.start_unit >= 3 * per);
-      const long long rem = sm.start_unit - g * per;
+      int g = (sm.start[0].unit >= per) + (sm.start[0].unit >= 2 * per) + (sm.start[0].unit >= 3 * per);
+      const long long rem = sm.start[0].unit - g * per;
       int i = 0;  // the last item that begins at or before unit rem of the head
       for (int lo = 0, hi = rq.items() - 1; lo <= hi;) {
         const int mid = (lo + hi) >> 1;
@@ -805,7 +830,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     }
     __syncwarp();
     roles_done();
-    if constexpr (kFp8) ca_one_produce(kmap, vmap, a, share1, sm);
+    if constexpr (kFp8) ca_one_produce(kmap, vmap, a, sm.share[1], sm);
   } else if (warp == kCaMmaWarp) {
     // ---------------- S and O products ----------------
     // One thread issues them all, and they execute in the order in which they are issued: an S product that overwrites P
@@ -926,6 +951,14 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       mbar_wait(&sm.done, 0, err, 815);
     }
     __syncwarp();
+  } else if (warp == kCaMmaWarp + 1) {
+    // ---------------- requests with bad lengths ----------------
+    for (long long r0 = blockIdx.x; r0 < a.batch; r0 += 32LL * gridDim.x) {
+      const long long r = r0 + static_cast<long long>(lane) * gridDim.x;
+      const bool bad = r < a.batch && !ca_good(a, a.cu[r], a.cu[r + 1], a.seq_lens[r]);
+      for (unsigned m = __ballot_sync(0xffffffffu, bad); m; m &= m - 1)
+        ca_refuse(a, static_cast<int>(r0 + static_cast<long long>(__ffs(m) - 1) * gridDim.x), lane);
+    }
   } else if (warp < 8) {
     // ---------------- softmax, one row per thread; the end of an item ----------------
     ca_regs_up<Shape::kRegsSoftmax>();
@@ -1060,11 +1093,11 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       const long long orow = (static_cast<long long>(it.t0) + tok) * kHeads + h;
       const long long prow = tok * kGroup + (row & 15);
       // f0, f1: what the two warpgroups' sums are multiplied by; l: the row's denominator; dims d0 ..
-      float f0 = 1.f, f1 = 0.f;
+      float f0 = m == -INFINITY ? 0.f : 1.f, f1 = 0.f;
       uint32_t c0 = ocol, c1 = ocol;
       int d0 = 0, nd = kDim;
-      if (!dual) {
-        // both warpgroups hold sums of the same rows: each writes half of their dims
+      const bool shared = !dual && it.nb > 1;  // both warpgroups hold sums of the same rows: each writes half of their dims
+      if (shared) {
         sm.ml[wg][row] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.x_full);
@@ -1078,12 +1111,10 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         c1 = lanes + kCaOCol + 128;
         d0 = 64 * wg;
         nd = 64;
-      } else if (m == -INFINITY) {
-        f0 = 0.f;
       }
       __syncwarp();
       tc::fence_after();
-      if (active) {
+      if (active && (steps > 0 || shared)) {
         const float inv = it.slot >= 0 ? 1.f : l == 0.f ? 0.f : a.v_scale / l;
         f0 *= inv;
         f1 *= inv;
@@ -1091,14 +1122,14 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         for (int d = d0; d < d0 + nd; d += 16) {
           uint32_t u[16], v[16];
           tc::ld_32x32b_x16(c0 + d, u);
-          if (!dual) tc::ld_32x32b_x16(c1 + d, v);
+          if (shared) tc::ld_32x32b_x16(c1 + d, v);
           tc::wait_ld();
           float o[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             // a factor of zero stands for sums that hold nothing: they are not read as numbers
             o[q] = f0 != 0.f ? __uint_as_float(u[q]) * f0 : 0.f;
-            if (!dual && f1 != 0.f) o[q] = fmaf(__uint_as_float(v[q]), f1, o[q]);
+            if (shared && f1 != 0.f) o[q] = fmaf(__uint_as_float(v[q]), f1, o[q]);
           }
           if (valid && it.slot >= 0) {
             float4* p = a.part_o + (static_cast<long long>(it.slot) * (kDim / 4) + d / 4) * a.rows + prow;
@@ -1117,7 +1148,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           else if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : m + log2f(l);
         }
       }
-      if (!dual) {
+      if (shared) {
         // neither goes on to its next O while the other still reads it
         tc::fence_before();
         __syncwarp();
@@ -1231,14 +1262,19 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_join_kernel(const __grid
   const int c = blockIdx.x - (one ? kNumSMs : 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const CaCut cut = (one ? a.cuts1 : a.cuts)[c];
-  if (e >= cut.ntok) return;
+  if (one && e > 0) return;
   const float2* part_ml = one ? a.part1_ml : a.part_ml;
   const float4* part_o = one ? a.part1_o : a.part_o;
   const int rows = one ? kGroup : a.rows;
-  const int parts = cut.last - c + 1;
   auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
-  for (int i = tid; i < parts * kGroup; i += kCaJoinThreads)
+  // asked for with the cut, not after it: the first 32 pieces' (m, l)
+  const int s0 = min(tid / kGroup, kNumSMs - 1 - c);
+  const float2 first = part_ml[static_cast<long long>(slot(s0)) * rows + e * kGroup + tid % kGroup];
+  const CaCut cut = (one ? a.cuts1 : a.cuts)[c];
+  if (e >= cut.ntok) return;
+  const int parts = cut.last - c + 1;
+  if (tid < parts * kGroup) ml[tid / kGroup][tid % kGroup] = first;
+  for (int i = tid + kCaJoinThreads; i < parts * kGroup; i += kCaJoinThreads)
     ml[i / kGroup][i % kGroup] = part_ml[static_cast<long long>(slot(i / kGroup)) * rows + e * kGroup + i % kGroup];
   __syncthreads();
   const long long row0 = (static_cast<long long>(cut.t0) + e) * kHeads + cut.g * kGroup;  // the token's first row
