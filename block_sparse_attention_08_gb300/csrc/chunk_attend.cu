@@ -10,10 +10,10 @@
 //
 // An item is 16 consecutive new tokens of a request and one KV head: 256 rows
 // (token, query head) that share their keys, as two tiles of 128 rows.  Its work
-// is counted in units of one 128-key block and tile, and every CTA takes an
-// equal contiguous share of all units of the batch, wherever that cuts an item
-// (a block belongs to the share that holds its first unit): a long context with
-// one new token is spread over the GPU like a long chunk is.  The
+// is counted in units: a 128-key block of both tiles, or two blocks of one tile
+// (which run side by side, below).  Every CTA takes an equal contiguous share of
+// all units of the batch, wherever that cuts an item: a long context with one
+// new token is spread over the GPU like a long chunk is.  The
 // pieces of a cut item leave (m, sum of p, sum of p v) in scratch, and a second
 // kernel joins them.  Each CTA finds its share itself from the lengths (no
 // planning launch, nothing kept between calls).
@@ -52,12 +52,13 @@ constexpr int kCaBad = 8;             // block flags in flight (at most 5 blocks
 // warps 0-7 softmax, 8 producer, 9 MMA, 10 bad requests (11 fills their warpgroup), 12-15 widening
 constexpr int kCaProducerWarp = 8, kCaMmaWarp = 9, kCaWidenWarp = 12;
 constexpr float kCaSlack = 8.f;
-// Units that an item counts besides its blocks, for its start and its end: about what they take, but no more than 2 where
-// shares are short, since a share cannot be shorter than the distance between two blocks' first units.  (17 mixed
-// requests 0.103 ms with 0, 0.092 with 2; E4M3 chunks 0.601 with 0, 0.593 with 2, 0.573 with 4; four short single
-// tokens 0.016 with 0 and 2, 0.019 with 4.)
-constexpr int kCaItemShort = 2, kCaItemLong = 4, kCaLongShare = 128;
-constexpr int kCaShare = kCaItemShort + 2;  // least units of a share
+// Units that an item counts besides its blocks, for its start and its end: none where shares are short, since a share is
+// at least that much longer than a unit, 1 in shares of 4 units on, 2 from 64 on.  (In half units: 17 mixed requests
+// 0.103 ms with 0, 0.092 with 2; E4M3 chunks 0.601 with 0, 0.593 with 2, 0.573 with 4; four short single tokens
+// 0.016 with 0 and 2, 0.019 with 4.)
+__device__ __forceinline__ int ca_item_units(long long total) {
+  return total >= 64LL * gridDim.x ? 2 : total >= 4LL * gridDim.x ? 1 : 0;
+}
 // tensor memory: S of warpgroup w at 128 w, P over its first half, O at 256 + 128 w
 constexpr uint32_t kCaOCol = 256;
 
@@ -168,17 +169,14 @@ struct CaReq {
   __device__ __forceinline__ int blocks(int i) const {
     return (len - n + min(n, kCaTok * (i + 1)) - 1) / kBlock + 1;
   }
-  // tensor-core work of one block of item i, in units: both tiles, or one
-  __device__ __forceinline__ int weight(int i) const { return n - kCaTok * i > kCaTok / 2 ? 2 : 1; }
+  __device__ __forceinline__ bool dual(int i) const { return n - kCaTok * i > kCaTok / 2; }  // both tiles
   // units of the items before item i (all of 16 tokens)
   __device__ __forceinline__ long long before(int i) const {
     const long long a = (static_cast<long long>(len) - n + kCaTok - 1) / kCaTok;
-    return 2 * (ca_eighths(a + i) - ca_eighths(a) + i) + static_cast<long long>(extra) * i;
+    return ca_eighths(a + i) - ca_eighths(a) + i + static_cast<long long>(extra) * i;
   }
   // units of item i
-  __device__ __forceinline__ long long units(int i) const {
-    return extra + static_cast<long long>(weight(i)) * blocks(i);
-  }
+  __device__ __forceinline__ int units(int i) const { return extra + (dual(i) ? blocks(i) : (blocks(i) + 1) / 2); }
   __device__ __forceinline__ long long per_head() const {
     const int i = items() - 1;
     if (i < 0) return 0;
@@ -193,11 +191,12 @@ __device__ __forceinline__ CaReq ca_req(const CaArgs& a, int r, bool apart, int 
   const int c0 = a.cu[r], c1 = a.cu[r + 1], len = a.seq_lens[r];
   return ca_good(a, c0, c1, len) ? CaReq{c0, c1 - c0, len, apart, extra} : CaReq{0, 0, 0, apart, extra};
 }
-// Blocks of a request's last item where that has one token.
-__device__ __forceinline__ long long ca_one_blocks(const CaArgs& a, int r) {
+// Blocks of a request's last item where that has one token, and its units.
+__device__ __forceinline__ int ca_one_blocks(const CaArgs& a, int r) {
   const CaReq q = ca_req(a, r, true);
   return q.one() ? (q.len - 1) / kBlock + 1 : 0;
 }
+__device__ __forceinline__ int ca_one_units(const CaArgs& a, int r) { return (ca_one_blocks(a, r) + 1) / 2; }
 // Zeros for the rows of a request with bad lengths (the whole warp).
 __device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
   if (lane == 0) record_error(a.err, MSA_DEVERR_LENGTH, r);
@@ -213,7 +212,7 @@ __device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
 // CTA's share of each kind begins.  (The caller's barrier follows.)
 template <int kThreads, int kN, class F>
 __device__ __forceinline__ void ca_find_shares(const CaArgs& a, long long (*wsum)[kThreads / 32], CaStart* start,
-                                               CaShareOf (&share)[kN], F units_of) {
+                                               CaShareOf (&share)[kN], const int (&least)[kN], F units_of) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // the sums up to and with this thread's request of the pass, in the warp; the warps' own sums in wsum
@@ -231,8 +230,8 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, long long (*wsum
     }
     __syncthreads();
   };
-  auto split = [&](CaShareOf& s) {
-    s.ctas = min(static_cast<long long>(gridDim.x), max(s.total / kCaShare, 1LL));
+  auto split = [&](CaShareOf& s, int least) {  // (a share is long enough to hold some block's beginning)
+    s.ctas = min(static_cast<long long>(gridDim.x), max(s.total / least, 1LL));
     s.u0 = min(s.total, s.total * blockIdx.x / s.ctas);
     s.u1 = min(s.total, s.total * (blockIdx.x + 1) / s.ctas);
   };
@@ -250,7 +249,7 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, long long (*wsum
       __syncthreads();
     }
 #pragma unroll
-    for (int n = 0; n < kN; ++n) split(share[n]);
+    for (int n = 0; n < kN; ++n) split(share[n], least[n]);
   }
   for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
     pass(r0, u, incl);
@@ -265,7 +264,7 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, long long (*wsum
       }
       if (once) {
         share[n].total = base[n];
-        split(share[n]);
+        split(share[n], least[n]);
       }
       before += incl[n] - u[n];
       if (share[n].u0 < share[n].u1 && before <= share[n].u0 && share[n].u0 < before + u[n])
@@ -326,6 +325,7 @@ __device__ __forceinline__ uint32_t ca_widen2(uint32_t x) {
 // k-step s, so Q's fragments hold those dims in the same slots.  O += P V: a transposing ldmatrix gives a lane two
 // dims of two keys, which make one value pair for each of two products, one for the even dims and one for the odd.
 // Bound by HBM: per SM and block 32 KB are copied in and read once.
+
 // The copies (the producer warp).
 __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CUtensorMap& vmap, const CaArgs& a,
                                                const CaShareOf& share, CaSmem<true>& sm) {
@@ -340,19 +340,18 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
     if (share.u0 < share.u1) {
       int r = sm.start[1].r;
       const long long start = sm.start[1].unit;
-      long long per = ca_one_blocks(a, r);
-      int g = (start >= per) + (start >= 2 * per) + (start >= 3 * per);
-      int b = static_cast<int>(start - g * per);
+      int per = ca_one_units(a, r);
+      int g = (start >= per) + (start >= 2LL * per) + (start >= 3LL * per);
+      int u = static_cast<int>(start - static_cast<long long>(g) * per);  // the unit in the item
       long long at = share.u0;
       while (true) {
         const CaReq q = ca_req(a, r, true);
-        CaItem it{q.t0 + q.n - 1, 1, g, q.len - 1, q.len, b,
-                  static_cast<int>(min(per - b, share.u1 - at)), 0};
-        const bool to_end = b + it.nb == per;
-        it.slot = b == 0 && to_end ? -1 : static_cast<int>(2 * blockIdx.x + (b == 0));
-        const long long end = at + per - b;
-        if (b == 0 && !to_end) cut = CaCut{it.t0, 1, g, static_cast<int>((end * share.ctas - 1) / share.total)};
-        at += it.nb;
+        const int blocks = (q.len - 1) / kBlock + 1, to = static_cast<int>(min(static_cast<long long>(per), u + share.u1 - at));
+        const int b = 2 * u;
+        CaItem it{q.t0 + q.n - 1, 1, g, q.len - 1, q.len, b, min(blocks, 2 * to) - b, 0};
+        it.slot = u == 0 && to == per ? -1 : static_cast<int>(2 * blockIdx.x + (u == 0));
+        if (u == 0 && to < per) cut = CaCut{it.t0, 1, g, static_cast<int>(((at + per) * share.ctas - 1) / share.total)};
+        at += to - u;
         const int is = nitem % kCaInfo;
         if (!(ok = ca_wait(&sm.one_info_empty[is], ((nitem / kCaInfo) & 1) ^ 1, err, 840))) break;
         if (lane == 0) {
@@ -382,11 +381,11 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
           }
         }
         if (!ok || at >= share.u1) break;
-        b = 0;
+        u = 0;
         if (++g == kKvHeads) {
           g = 0;
           do {
-            per = ca_one_blocks(a, ++r);
+            per = ca_one_units(a, ++r);
           } while (per == 0);
         }
       }
@@ -654,17 +653,15 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
 
   constexpr int kKinds = kFp8 ? 2 : 1;
   CaShareOf shares[kKinds];
-  int extra = kCaItemShort;
+  int extra = 0, least[kKinds] = {};
   auto find = [&] {
-    ca_find_shares<kThreads, kKinds>(a, sm.wsum, sm.start, shares, [&](int r, int kind) {
-      return kind ? ca_one_blocks(a, r) : ca_req(a, r, kFp8, extra).per_head();
+    for (int n = 0; n < kKinds; ++n) least[n] = n ? 1 : 1 + extra;
+    ca_find_shares<kThreads, kKinds>(a, sm.wsum, sm.start, shares, least, [&](int r, int kind) -> long long {
+      return kind ? ca_one_units(a, r) : ca_req(a, r, kFp8, extra).per_head();
     });
   };
   find();
-  if (shares[0].total > static_cast<long long>(gridDim.x) * kCaLongShare) {
-    extra = kCaItemLong;
-    find();
-  }
+  if ((extra = ca_item_units(shares[0].total)) > 0) find();
   if (tid == 0)
     for (int n = 0; n < kKinds; ++n) sm.share[n] = shares[n];
   tc::fence_before();
@@ -711,11 +708,13 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       }
       long long at = u0, item0 = u0 - (rem - rq.before(i));  // where the share goes on, where the item begins
       while (ok) {
-        const int blocks = rq.blocks(i), weight = rq.weight(i);
+        const int blocks = rq.blocks(i);
+        const bool dual = rq.dual(i);
         const long long end = item0 + rq.units(i);
-        // blocks whose first unit is before unit x of the item: block 0 begins at 0, block k > 0 after the item's own units
+        // blocks that begin before unit x of the item: the first at 0, the others after the item's own units
         auto begun = [&](long long x) {
-          return x <= 0 ? 0 : 1 + static_cast<int>(max(0LL, x - 1 - rq.extra) >> (weight - 1));
+          const int units = x <= 0 ? 0 : 1 + static_cast<int>(max(0LL, x - 1 - rq.extra));
+          return min(blocks, dual ? units : 2 * units);
         };
         CaItem it;
         it.t0 = rq.t0 + kCaTok * i;
@@ -724,12 +723,12 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         it.pos0 = rq.len - rq.n + kCaTok * i;
         it.len = rq.len;
         it.b0 = begun(at - item0);
-        it.nb = min(blocks, begun(min(end, u1) - item0)) - it.b0;
+        it.nb = begun(min(end, u1) - item0) - it.b0;
         const int b = it.b0;
         const bool to_end = b + it.nb == blocks;
         it.slot = b == 0 && to_end ? -1 : static_cast<int>(2 * blockIdx.x + (b == 0));
-        // the share that holds the first unit of the item's last block
-        if (b == 0 && !to_end) cut = CaCut{it.t0, it.ntok, g, static_cast<int>(((end - weight + 1) * ctas - 1) / total)};
+        // the share that holds the item's last unit
+        if (b == 0 && !to_end) cut = CaCut{it.t0, it.ntok, g, static_cast<int>((end * ctas - 1) / total)};
         at = end;
         item0 = end;
         if (it.nb > 0) {
