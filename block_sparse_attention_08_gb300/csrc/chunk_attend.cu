@@ -1246,52 +1246,54 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   }
 }
 
-// Joins the pieces of the items that were cut: CTA (c, e) token e of the item that begins in share c, 16 rows (the
-// token's heads).  The pieces' (m, l) go to shared memory; a warp per row turns them into factors; then thread (four
-// dims, row) adds up its values, the loads of eight pieces in flight at once.  Bound by the latency of those three
-// rounds, so the rows are spread over as many CTAs as there are tokens.
+// Joins the pieces of the items that were cut.  CTA (c, e) takes token e of the item that begins in share c, 16 rows (the
+// token's heads); behind those, one CTA per share the one-token item that begins there.  The pieces' (m, l) go to shared
+// memory; a warp per row turns them into factors; then thread (row, four dims) adds up its values, the loads of
+// eight pieces in flight at once.  Bound by the latency of those rounds, so the rows are spread over as many CTAs as
+// there are tokens.  (With four tokens to a CTA, and the factors in each thread, the whole call took 20 us instead of
+// 14 for four short requests; with 256 threads, two values each, 20 instead of 16 for one of 63 blocks.)
 constexpr int kCaJoinThreads = kGroup * kDim / 4;
 __global__ void __launch_bounds__(kCaJoinThreads) chunk_join_kernel(const __grid_constant__ CaArgs a) {
-  __shared__ float factor[kNumSMs][kGroup];
-  __shared__ float2 ml[kNumSMs][kGroup];
+  __shared__ float2 ml[kNumSMs][kGroup];  // then .x: the piece's factor
   __shared__ float inv[kGroup];
   __shared__ __align__(16) uint2 out[kGroup][kDim / 4];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, e = blockIdx.y;
-  const bool one = blockIdx.x >= kNumSMs;  // of the one-token items over an E4M3 cache
-  const int c = blockIdx.x - (one ? kNumSMs : 0);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int e = blockIdx.x / kNumSMs, c = blockIdx.x % kNumSMs;
+  const bool one = e * kGroup >= a.rows;  // a one-token item over an E4M3 cache
+  const int e0 = one ? 0 : e * kGroup;    // first row in the item
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (one && e > 0) return;
   const float2* part_ml = one ? a.part1_ml : a.part_ml;
   const float4* part_o = one ? a.part1_o : a.part_o;
-  const int rows = one ? kGroup : a.rows;
+  const long long rows = one ? kGroup : a.rows;
+  // the pieces lie in slots 2 c + 1, 2 (c + 1), 2 (c + 2), ..
   auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
   // asked for with the cut, not after it: the first 32 pieces' (m, l)
-  const int s0 = min(tid / kGroup, kNumSMs - 1 - c);
-  const float2 first = part_ml[static_cast<long long>(slot(s0)) * rows + e * kGroup + tid % kGroup];
+  const float2 first = part_ml[slot(min(tid / kGroup, kNumSMs - 1 - c)) * rows + e0 + tid % kGroup];
   const CaCut cut = (one ? a.cuts1 : a.cuts)[c];
-  if (e >= cut.ntok) return;
+  if (e0 >= cut.ntok * kGroup) return;
   const int parts = cut.last - c + 1;
   if (tid < parts * kGroup) ml[tid / kGroup][tid % kGroup] = first;
   for (int i = tid + kCaJoinThreads; i < parts * kGroup; i += kCaJoinThreads)
-    ml[i / kGroup][i % kGroup] = part_ml[static_cast<long long>(slot(i / kGroup)) * rows + e * kGroup + i % kGroup];
+    ml[i / kGroup][i % kGroup] = part_ml[slot(i / kGroup) * rows + e0 + i % kGroup];
   __syncthreads();
-  const long long row0 = (static_cast<long long>(cut.t0) + e) * kHeads + cut.g * kGroup;  // the token's first row
+  const long long row0 = (static_cast<long long>(cut.t0) + e0 / kGroup) * kHeads + cut.g * kGroup;  // the token's first row
   {
+    const int w = warp;
     float m = -INFINITY, l = 0.f;
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, ml[s][warp].x);
+    for (int s = lane; s < parts; s += 32) m = fmaxf(m, ml[s][w].x);
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     for (int s = lane; s < parts; s += 32) {
-      const float f = ml[s][warp].x == -INFINITY ? 0.f : ex2(ml[s][warp].x - m);
-      factor[s][warp] = f;
-      l = fmaf(f, ml[s][warp].y, l);
+      const float f = ml[s][w].x == -INFINITY ? 0.f : ex2(ml[s][w].x - m);
+      ml[s][w].x = f;
+      l = fmaf(f, ml[s][w].y, l);
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     if (lane == 0) {
-      inv[warp] = l == 0.f ? 0.f : a.v_scale / l;
-      if (a.lse) a.lse[row0 + warp] = l == 0.f ? -INFINITY : m + log2f(l);
+      inv[w] = l == 0.f ? 0.f : a.v_scale / l;
+      if (a.lse) a.lse[row0 + w] = l == 0.f ? -INFINITY : m + log2f(l);
     }
   }
   __syncthreads();
@@ -1299,8 +1301,8 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_join_kernel(const __grid
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int s = 0; s < parts; ++s) {
-    const float4 x = part_o[(static_cast<long long>(slot(s)) * (kDim / 4) + d4) * rows + e * kGroup + row];
-    const float f = factor[s][row];
+    const float4 x = part_o[(slot(s) * static_cast<long long>(kDim / 4) + d4) * rows + e0 + row];
+    const float f = ml[s][row].x;
     o.x = fmaf(f, x.x, o.x);
     o.y = fmaf(f, x.y, o.y);
     o.z = fmaf(f, x.z, o.z);
@@ -1422,7 +1424,8 @@ cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream) {
                                      : ca_launch<false>(qmap, kmap, vmap, a, stream);
       e != cudaSuccess)
     return e;
-  return ca_launch_dependent(chunk_join_kernel, dim3(L.kv_fp8 ? 2 * kNumSMs : kNumSMs, a.rows / kGroup), kCaJoinThreads, 0, stream, a);
+  return ca_launch_dependent(chunk_join_kernel, dim3(kNumSMs * (a.rows / kGroup + (L.kv_fp8 ? 1 : 0))), kCaJoinThreads, 0,
+                             stream, a);
 }
 
 }  // namespace msa
