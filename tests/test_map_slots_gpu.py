@@ -114,3 +114,19 @@ def test_repeated_and_captured_calls_agree():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(first, list(out) + [args[2]]))
+
+
+def test_more_rows_than_threads_at_once():
+    # beyond 4 * 152 CTAs of 512 threads a CTA takes several passes over its rows; requests begin inside them
+    lens = [400_000, 5, 300_001, 0, 129, 131_072]
+    news = [400_000, 3, 299_999, 0, 1, 131_072]
+    have = [S.pages(n - m) for n, m in zip(lens, news)]
+    width = max(S.pages(n) for n in lens)
+    opened = sum(S.pages(n) for n in lens) - sum(have)
+    ids = list(range(sum(have) + opened + 2))
+    random.Random(1).shuffle(ids)
+    table = [[ids.pop() for _ in range(h)] + [0] * (width - h) for h in have]
+    slots = (sum(have) + len(ids)) * S.PAGE
+    for capacity in (sum(news), sum(news) + 70_001):
+        *want, errors = S.map_slots(lens, news, table, ids, len(ids), slots, capacity)
+        assert not errors and _run(lens, news, table, ids, len(ids), slots, capacity) == tuple(want)
