@@ -53,11 +53,11 @@ constexpr int kCaBad = 8;             // block flags in flight (at most 5 blocks
 constexpr int kCaProducerWarp = 8, kCaMmaWarp = 9, kCaWidenWarp = 12;
 constexpr float kCaSlack = 8.f;
 // Units that an item counts besides its blocks, for its start and its end: none where shares are short, since a share is
-// at least that much longer than a unit, 1 in shares of 4 units on, 2 from 64 on.  (In half units: 17 mixed requests
+// at least that much longer than a unit, 1 in shares of 4 units on, 2 from 16 on.  (In half units: 17 mixed requests
 // 0.103 ms with 0, 0.092 with 2; E4M3 chunks 0.601 with 0, 0.593 with 2, 0.573 with 4; four short single tokens
-// 0.016 with 0 and 2, 0.019 with 4.)
+// 0.016 with 0 and 2, 0.019 with 4.  2048 tokens of a request without a past, 32 units a share: 0.097 with 2, 0.089 with 4.)
 __device__ __forceinline__ int ca_item_units(long long total) {
-  return total >= 64LL * gridDim.x ? 2 : total >= 4LL * gridDim.x ? 1 : 0;
+  return total >= 16LL * gridDim.x ? 2 : total >= 4LL * gridDim.x ? 1 : 0;
 }
 // tensor memory: S of warpgroup w at 128 w, P over its first half, O at 256 + 128 w
 constexpr uint32_t kCaOCol = 256;
@@ -123,34 +123,6 @@ struct CaShape {
 struct CaShareOf {
   long long total, ctas, u0, u1;
 };
-// The request (and the unit in it) where a share begins.
-struct CaStart {
-  long long unit;
-  int r;
-};
-
-template <bool kFp8>
-struct CaSmem {
-  uint8_t q[2][kCaTile];
-  uint8_t kv[CaShape<kFp8>::kTiles][kCaTile];
-  uint8_t raw[CaShape<kFp8>::kRaw][kFp8 ? kCaHalf : 16];
-  float2 ml[2][128];
-  uint64_t q_full[2], q_ready[2], q_empty[2];  // q_ready: as fp16 (E4M3 cache)
-  uint64_t kv_full[CaShape<kFp8>::kTiles], kv_empty[CaShape<kFp8>::kTiles];
-  uint64_t raw_full[CaShape<kFp8>::kRaw], raw_empty[CaShape<kFp8>::kRaw];
-  uint64_t s_full[2], p_full[2], o_full[2], x_full, x_done, done;
-  uint64_t info_full[kCaInfo], info_empty[kCaInfo];
-  // one-token items: K and V bytes of a block per place (over kv and raw), descriptors, the warps' meeting
-  uint64_t one_full[kCaOnePlaces], one_empty[kCaOnePlaces], one_info_full[kCaInfo], one_info_empty[kCaInfo];
-  uint64_t one_x_full, one_x_done;
-  CaItem info[kCaInfo];
-  int bad[kCaBad];
-  long long wsum[kFp8 ? 2 : 1][CaShape<kFp8>::kThreads / 32];
-  CaStart start[kFp8 ? 2 : 1];  // of the items, and of the one-token items
-  CaShareOf share[kFp8 ? 2 : 1];
-  uint32_t tmem_base;
-};
-
 // ---- the units of a request --------------------------------------------------------
 
 // sum of floor(y / 8) over 0 <= y < x
@@ -182,6 +154,8 @@ struct CaReq {
     if (i < 0) return 0;
     return before(i) + units(i);
   }
+  // units of the last item where that has one token and is shared out apart
+  __device__ __forceinline__ int one_units() const { return one() ? ((len - 1) / kBlock + 2) / 2 : 0; }
 };
 __device__ __forceinline__ bool ca_good(const CaArgs& a, long long c0, long long c1, int len) {
   return c0 >= 0 && c0 <= c1 && c1 <= a.tokens && c1 - c0 <= len && (len + kBlock - 1LL) / kBlock <= a.max_blocks;
@@ -191,12 +165,6 @@ __device__ __forceinline__ CaReq ca_req(const CaArgs& a, int r, bool apart, int 
   const int c0 = a.cu[r], c1 = a.cu[r + 1], len = a.seq_lens[r];
   return ca_good(a, c0, c1, len) ? CaReq{c0, c1 - c0, len, apart, extra} : CaReq{0, 0, 0, apart, extra};
 }
-// Blocks of a request's last item where that has one token, and its units.
-__device__ __forceinline__ int ca_one_blocks(const CaArgs& a, int r) {
-  const CaReq q = ca_req(a, r, true);
-  return q.one() ? (q.len - 1) / kBlock + 1 : 0;
-}
-__device__ __forceinline__ int ca_one_units(const CaArgs& a, int r) { return (ca_one_blocks(a, r) + 1) / 2; }
 // Zeros for the rows of a request with bad lengths (the whole warp).
 __device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
   if (lane == 0) record_error(a.err, MSA_DEVERR_LENGTH, r);
@@ -208,19 +176,57 @@ __device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
     for (long long i = c0 * kHeads + lane; i < c1 * kHeads; i += 32) a.lse[i] = -INFINITY;
 }
 
-// The whole CTA: sums up the units of each request, of kN kinds at once (`units_of(r, n)`: per KV head), and finds where this
-// CTA's share of each kind begins.  (The caller's barrier follows.)
-template <int kThreads, int kN, class F>
-__device__ __forceinline__ void ca_find_shares(const CaArgs& a, long long (*wsum)[kThreads / 32], CaStart* start,
-                                               CaShareOf (&share)[kN], const int (&least)[kN], F units_of) {
-  constexpr int kWarps = kThreads / 32;
+// The request (and the unit in it) where a share begins.
+struct CaStart {
+  long long unit;
+  int r;
+  CaReq q;
+};
+
+template <bool kFp8>
+struct CaSmem {
+  uint8_t q[2][kCaTile];
+  uint8_t kv[CaShape<kFp8>::kTiles][kCaTile];
+  uint8_t raw[CaShape<kFp8>::kRaw][kFp8 ? kCaHalf : 16];
+  float2 ml[2][128];  // before the roles begin: the warps' sums
+  uint64_t q_full[2], q_ready[2], q_empty[2];  // q_ready: as fp16 (E4M3 cache)
+  uint64_t kv_full[CaShape<kFp8>::kTiles], kv_empty[CaShape<kFp8>::kTiles];
+  uint64_t raw_full[CaShape<kFp8>::kRaw], raw_empty[CaShape<kFp8>::kRaw];
+  uint64_t s_full[2], p_full[2], o_full[2], x_full, x_done, done;
+  uint64_t info_full[kCaInfo], info_empty[kCaInfo];
+  // one-token items: K and V bytes of a block per place (over kv and raw), descriptors, the warps' meeting
+  uint64_t one_full[kCaOnePlaces], one_empty[kCaOnePlaces], one_info_full[kCaInfo], one_info_empty[kCaInfo];
+  uint64_t one_x_full, one_x_done;
+  CaItem info[kCaInfo];
+  int bad[kCaBad];
+  CaStart start[kFp8 ? 2 : 1];  // of the items, and of the one-token items
+  CaShareOf share[kFp8 ? 2 : 1];
+  int extra;  // units of an item besides its blocks
+  uint32_t tmem_base;
+};
+
+// The whole CTA: sums up the requests' units and finds this CTA's share of each kind, and where it begins.  The units that an
+// item counts besides its blocks depend on the total, so the items are summed up beside their blocks.  (The caller's barrier
+// follows.)
+template <bool kFp8>
+__device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm) {
+  constexpr int kThreads = CaShape<kFp8>::kThreads, kWarps = kThreads / 32, kKinds = kFp8 ? 2 : 1, kN = kKinds + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the sums up to and with this thread's request of the pass, in the warp; the warps' own sums in wsum
-  auto pass = [&](int r0, long long (&u)[kN], long long (&incl)[kN]) {
+  // all KV heads' units without the items' own, items, and units of one-token items: of this thread's request, and of the
+  // warp's requests up to and with it (the warps' own sums in wsum)
+  long long (*wsum)[kWarps] = reinterpret_cast<long long (*)[kWarps]>(&sm.ml[0][0]);
+  static_assert(kN * kWarps * sizeof(long long) <= sizeof(sm.ml), "wsum lies over ml");
+  CaReq q{};
+  long long u[kN], incl[kN], base[kN] = {};
+  auto pass = [&](int r0) {
     const int r = r0 + tid;
+    q = r < a.batch ? ca_req(a, r, kFp8) : CaReq{};
+    u[0] = kKvHeads * q.per_head();
+    u[1] = kKvHeads * static_cast<long long>(q.items());
+    if constexpr (kFp8) u[2] = kKvHeads * static_cast<long long>(q.one_units());
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      incl[n] = u[n] = r < a.batch ? kKvHeads * units_of(r, n) : 0;
+      incl[n] = u[n];
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, incl[n], d);
@@ -230,47 +236,63 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, long long (*wsum
     }
     __syncthreads();
   };
-  auto split = [&](CaShareOf& s, int least) {  // (a share is long enough to hold some block's beginning)
-    s.ctas = min(static_cast<long long>(gridDim.x), max(s.total / least, 1LL));
-    s.u0 = min(s.total, s.total * blockIdx.x / s.ctas);
-    s.u1 = min(s.total, s.total * (blockIdx.x + 1) / s.ctas);
+  CaShareOf share[kKinds];
+  int extra = 0;
+  auto split = [&](const long long (&total)[kN]) {
+    extra = ca_item_units(total[0]);
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k) {
+      CaShareOf& s = share[k];
+      s.total = k ? total[kN - 1] : total[0] + extra * total[1];
+      // (a share is long enough to hold some block's beginning)
+      s.ctas = min(static_cast<long long>(gridDim.x), max(s.total / (k ? 1 : 1 + extra), 1LL));
+      s.u0 = min(s.total, s.total * blockIdx.x / s.ctas);
+      s.u1 = min(s.total, s.total * (blockIdx.x + 1) / s.ctas);
+    }
   };
   const bool once = a.batch <= kThreads;
-  long long u[kN], incl[kN], base[kN] = {};
-#pragma unroll
-  for (int n = 0; n < kN; ++n) share[n] = CaShareOf{0, 1, 0, 0};
-  __syncthreads();  // wsum may be in use by a call before
   if (!once) {
     for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
-      pass(r0, u, incl);
+      pass(r0);
 #pragma unroll
       for (int n = 0; n < kN; ++n)
-        for (int w = 0; w < kWarps; ++w) share[n].total += wsum[n][w];
+        for (int w = 0; w < kWarps; ++w) base[n] += wsum[n][w];
       __syncthreads();
     }
+    split(base);
 #pragma unroll
-    for (int n = 0; n < kN; ++n) split(share[n], least[n]);
+    for (int n = 0; n < kN; ++n) base[n] = 0;
   }
   for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
-    pass(r0, u, incl);
+    pass(r0);
+    const int warps = min(kWarps, (a.batch - r0 + 31) / 32);  // that hold requests
+    long long before[kN];
 #pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      long long before = base[n];
-#pragma unroll 4
-      for (int w = 0; w < kWarps; ++w) {
+    for (int n = 0; n < kN; ++n) before[n] = base[n] + incl[n] - u[n];
+    for (int w = 0; w < warps; ++w) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
         const long long x = wsum[n][w];
-        if (w < warp) before += x;
+        if (w < warp) before[n] += x;
         base[n] += x;
       }
-      if (once) {
-        share[n].total = base[n];
-        split(share[n], least[n]);
+    }
+    if (once) split(base);
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k) {
+      const CaShareOf& s = share[k];
+      const long long from = k ? before[kN - 1] : before[0] + extra * before[1], n = k ? u[kN - 1] : u[0] + extra * u[1];
+      if (s.u0 < s.u1 && from <= s.u0 && s.u0 < from + n) {
+        q.extra = k ? 0 : extra;
+        sm.start[k] = CaStart{s.u0 - from, r0 + tid, q};
       }
-      before += incl[n] - u[n];
-      if (share[n].u0 < share[n].u1 && before <= share[n].u0 && share[n].u0 < before + u[n])
-        start[n] = CaStart{share[n].u0 - before, r0 + tid};
     }
     if (!once) __syncthreads();
+  }
+  if (tid == 0) {
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k) sm.share[k] = share[k];
+    sm.extra = extra;
   }
 }
 
@@ -340,12 +362,12 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
     if (share.u0 < share.u1) {
       int r = sm.start[1].r;
       const long long start = sm.start[1].unit;
-      int per = ca_one_units(a, r);
+      CaReq q = sm.start[1].q;
+      int per = q.one_units();
       int g = (start >= per) + (start >= 2LL * per) + (start >= 3LL * per);
       int u = static_cast<int>(start - static_cast<long long>(g) * per);  // the unit in the item
       long long at = share.u0;
       while (true) {
-        const CaReq q = ca_req(a, r, true);
         const int blocks = (q.len - 1) / kBlock + 1, to = static_cast<int>(min(static_cast<long long>(per), u + share.u1 - at));
         const int b = 2 * u;
         CaItem it{q.t0 + q.n - 1, 1, g, q.len - 1, q.len, b, min(blocks, 2 * to) - b, 0};
@@ -385,7 +407,8 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
         if (++g == kKvHeads) {
           g = 0;
           do {
-            per = ca_one_units(a, ++r);
+            q = ca_req(a, ++r, true);
+            per = q.one_units();
           } while (per == 0);
         }
       }
@@ -647,23 +670,16 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     tc::alloc(&sm.tmem_base, 512);
     tc::relinquish();
   }
+  if (tid == 32 * kCaProducerWarp) {
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+  }
   // the kernel before has completed; the joining kernel may be launched behind this one
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  constexpr int kKinds = kFp8 ? 2 : 1;
-  CaShareOf shares[kKinds];
-  int extra = 0, least[kKinds] = {};
-  auto find = [&] {
-    for (int n = 0; n < kKinds; ++n) least[n] = n ? 1 : 1 + extra;
-    ca_find_shares<kThreads, kKinds>(a, sm.wsum, sm.start, shares, least, [&](int r, int kind) -> long long {
-      return kind ? ca_one_units(a, r) : ca_req(a, r, kFp8, extra).per_head();
-    });
-  };
-  find();
-  if ((extra = ca_item_units(shares[0].total)) > 0) find();
-  if (tid == 0)
-    for (int n = 0; n < kKinds; ++n) sm.share[n] = shares[n];
+  ca_find_shares<kFp8>(a, sm);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -681,18 +697,14 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   if (warp >= 8 && warp < kCaWidenWarp) ca_regs_down<Shape::kRegsIssue>();
   if (warp == kCaProducerWarp) {
     // ---------------- the share's items, and their copies ----------------
-    if (lane == 0) {
-      prefetch_tmap(&qmap);
-      prefetch_tmap(&kmap);
-      prefetch_tmap(&vmap);
-    }
     const long long total = sm.share[0].total, ctas = sm.share[0].ctas, u0 = sm.share[0].u0, u1 = sm.share[0].u1;
     CaCut cut{0, 0, 0, 0};
     int nitem = 0, nq = 0, nload = 0, nblk = 0;  // descriptors, Q tiles, K / V tiles and blocks issued
     bool ok = true;
     if (u0 < u1) {
+      const int extra = sm.extra;
       int r = sm.start[0].r;
-      CaReq rq = ca_req(a, r, kFp8, extra);
+      CaReq rq = sm.start[0].q;
       long long per = rq.per_head();
       int g = (sm.start[0].unit >= per) + (sm.start[0].unit >= 2 * per) + (sm.start[0].unit >= 3 * per);
       const long long rem = sm.start[0].unit - g * per;
@@ -727,8 +739,6 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         const int b = it.b0;
         const bool to_end = b + it.nb == blocks;
         it.slot = b == 0 && to_end ? -1 : static_cast<int>(2 * blockIdx.x + (b == 0));
-        // the share that holds the item's last unit
-        if (b == 0 && !to_end) cut = CaCut{it.t0, it.ntok, g, static_cast<int>((end * ctas - 1) / total)};
         at = end;
         item0 = end;
         if (it.nb > 0) {
@@ -797,6 +807,8 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           }
         }
         }
+        // (here, not before the copies: a division) the share that holds the item's last unit
+        if (b == 0 && !to_end) cut = CaCut{it.t0, it.ntok, g, static_cast<int>((end * ctas - 1) / total)};
         if (!ok || at >= u1) break;
         // the next item (the share goes on, so there is one)
         if (++i == rq.items()) {
