@@ -29,11 +29,22 @@
 //
 // That widening writes and reads every tile once more, and shared memory's rate
 // then bounds an item of one new token, which needs only 16 of a tile's 128 rows
-// (0.49 ms for 16 tokens over 128k E4M3 keys, 65% of the copy rate).  So over an
+// (0.48 ms for 16 tokens over 128k E4M3 keys, 0.32 ms as below).  So over an
 // E4M3 cache the items of one token are shared out apart, after the others, and
 // the softmax warps compute them with warp-level products straight from the
 // copied bytes: each warp takes a quarter of every second block's keys, with
 // sums of its own in registers, joined at the item's end.
+//
+// Chunks are bound on chip.  2048 tokens over 32k keys run at 1.75 PFLOP/s in
+// bf16 (1.22 ms, tensor pipe 75% active; 92% of a library product's rate): S
+// reads Q and K from shared memory at its full 128 bytes a cycle, and the
+// softmax of a warpgroup starts only when its S is done.  An item costs about
+// two units besides its blocks: 0.5 us for its last O product, 2.4 for its rows'
+// stores, 1 for the first block's softmax, none of it beside other products.
+// An E4M3 cache adds the widening and leaves the softmax fewer registers
+// (1.43 ms).  Single tokens over long contexts are bound by HBM (64 requests,
+// 4.0 GB: 0.59 ms, 6.8 TB/s), short ones by latency: 3.7 us without any work,
+// 8.1 with one block.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -341,12 +352,13 @@ __device__ __forceinline__ uint32_t ca_widen2(uint32_t x) {
   return y;
 }
 
-// Warps 0 to 3 take the even blocks, 32 keys each, warps 4 to 7 the odd ones (with 16 keys of every block each, a warp's
-// chain of dependent steps took 1.05 us a block).  S = Q K^T by m16n8k16 products (the 16 query heads
-// are their rows): a 16-bit ldmatrix of K gives a lane four consecutive bytes of one key, dims 16 s + 4 t .. + 3 of
+// Warps 0 to 3 take the even blocks, 32 keys each, warps 4 to 7 the odd ones: a warp's chain of dependent steps then has two
+// blocks' time.  S = Q K^T by m16n8k16 products (the 16 query heads are their rows): a 16-bit ldmatrix of K gives a lane four consecutive bytes of one key, dims 16 s + 4 t .. + 3 of
 // k-step s, so Q's fragments hold those dims in the same slots.  O += P V: a transposing ldmatrix gives a lane two
 // dims of two keys, which make one value pair for each of two products, one for the even dims and one for the odd.
-// Bound by HBM: per SM and block 32 KB are copied in and read once.
+// Bound by HBM: per SM and block 32 KB are copied in and read once.  (16 tokens over 128k keys, 2.15 GB: 0.32 ms, 6.7 TB/s.
+// A bf16 cache's one-token items stay with the others: computed this way they were no faster over long contexts, and two
+// kinds of shares after each other made 17 mixed requests 118 us instead of 95.)
 
 // The copies (the producer warp).
 __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CUtensorMap& vmap, const CaArgs& a,
@@ -1210,7 +1222,6 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         const int load = 2 * base + j, rs = load % Shape::kRaw, st = load % kTiles;
         const bool is_v = ca_is_v(j, nb);
         if (!(ok = ca_wait(&sm.raw_full[rs], (load / Shape::kRaw) & 1, err, 831))) break;
-        if (!(ok = ca_wait(&sm.kv_empty[st], ((load / kTiles) & 1) ^ 1, err, 832))) break;
         // V rows behind the last key become zero: their weight is zero, but they may hold anything
         int keys = kBlock;
         if (is_v) {
@@ -1222,6 +1233,9 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         uint4 x[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) x[q] = lds128(src + q * 16 * 128);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.raw_empty[rs]);
+        if (!(ok = ca_wait(&sm.kv_empty[st], ((load / kTiles) & 1) ^ 1, err, 832))) break;
         if (keys < kBlock)
 #pragma unroll
           for (int q = 0; q < 8; ++q)
@@ -1241,10 +1255,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.raw_empty[rs]);
-          mbar_arrive(&sm.kv_full[st]);
-        }
+        if (lane == 0) mbar_arrive(&sm.kv_full[st]);
         if (j == 0) widen_q(ntok);
       }
       base += nb;
@@ -1290,23 +1301,20 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_join_kernel(const __grid
     ml[i / kGroup][i % kGroup] = part_ml[slot(i / kGroup) * rows + e0 + i % kGroup];
   __syncthreads();
   const long long row0 = (static_cast<long long>(cut.t0) + e0 / kGroup) * kHeads + cut.g * kGroup;  // the token's first row
-  {
-    const int w = warp;
-    float m = -INFINITY, l = 0.f;
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, ml[s][w].x);
+  float m = -INFINITY, l = 0.f;  // of row `warp`
+  for (int s = lane; s < parts; s += 32) m = fmaxf(m, ml[s][warp].x);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    for (int s = lane; s < parts; s += 32) {
-      const float f = ml[s][w].x == -INFINITY ? 0.f : ex2(ml[s][w].x - m);
-      ml[s][w].x = f;
-      l = fmaf(f, ml[s][w].y, l);
-    }
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  for (int s = lane; s < parts; s += 32) {
+    const float f = ml[s][warp].x == -INFINITY ? 0.f : ex2(ml[s][warp].x - m);
+    ml[s][warp].x = f;
+    l = fmaf(f, ml[s][warp].y, l);
+  }
 #pragma unroll
-    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (lane == 0) {
-      inv[w] = l == 0.f ? 0.f : a.v_scale / l;
-      if (a.lse) a.lse[row0 + w] = l == 0.f ? -INFINITY : m + log2f(l);
-    }
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  if (lane == 0) {
+    inv[warp] = l == 0.f ? 0.f : a.v_scale / l;
+    if (a.lse) a.lse[row0 + warp] = l == 0.f ? -INFINITY : m + log2f(l);
   }
   __syncthreads();
   const int row = tid % kGroup, d4 = tid / kGroup;

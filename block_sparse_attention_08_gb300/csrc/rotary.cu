@@ -21,7 +21,10 @@
 // members of its pairs; the producer copies the stage out, to q_out and (as they
 // lie there, or from the E4M3 bytes that the warps leave beside them) to the
 // caches' slots.  So no thread holds data that is on its way, and an SM has
-// kRoStages tokens of each of its CTAs in flight, 18 KB each.
+// kRoStages tokens of each of its CTAs in flight, 18 KB each.  16384 tokens with
+// insertion (604 MB): 99 us, 6.1 TB/s; 8191 into E4M3 caches (294 MB): 53 us,
+// 5.5 TB/s; forward and backward of 16384 (1.14 GB): 193 us, 5.9 TB/s; 64
+// tokens: 4.1 us.
 #include <algorithm>
 
 #include "launch.h"
