@@ -32,8 +32,12 @@
 // (0.48 ms for 16 tokens over 128k E4M3 keys, 0.32 ms as below).  So over an
 // E4M3 cache the items of one token are shared out apart, after the others, and
 // the softmax warps compute them with warp-level products straight from the
-// copied bytes: each warp takes a quarter of every second block's keys, with
-// sums of its own in registers, joined at the item's end.
+// copied bytes: each warp takes some of a block's keys, with sums of its own in
+// registers, joined at the item's end.  Over a bf16 cache that saves an item's
+// way through tensor memory (64 tokens over 300 to 900 keys: 28 us instead of
+// 36; over 4k to 64k keys 0.58 ms either way), but not what a second kind of
+// shares costs: it is done where all items have one token (17 mixed requests
+// took 0.118 ms with two kinds, 0.095 with one).
 //
 // Chunks are bound on chip.  2048 tokens over 32k keys run at 1.75 PFLOP/s in
 // bf16 (1.22 ms, tensor pipe 75% active; 92% of a library product's rate): S
@@ -210,9 +214,10 @@ struct CaSmem {
   uint64_t one_x_full, one_x_done;
   CaItem info[kCaInfo];
   int bad[kCaBad];
-  CaStart start[kFp8 ? 2 : 1];  // of the items, and of the one-token items
-  CaShareOf share[kFp8 ? 2 : 1];
-  int extra;  // units of an item besides its blocks
+  CaStart start[2];  // of the items, and of the one-token items
+  CaShareOf share[2];
+  int extra;   // units of an item besides its blocks
+  bool apart;  // the one-token items are shared out apart, after the others
   uint32_t tmem_base;
 };
 
@@ -221,9 +226,10 @@ struct CaSmem {
 // follows.)
 template <bool kFp8>
 __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm) {
-  constexpr int kThreads = CaShape<kFp8>::kThreads, kWarps = kThreads / 32, kKinds = kFp8 ? 2 : 1, kN = kKinds + 1;
+  constexpr int kThreads = CaShape<kFp8>::kThreads, kWarps = kThreads / 32, kN = 3;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // all KV heads' units without the items' own, items, and units of one-token items: of this thread's request, and of the
+  // all KV heads' units without the items' own, items (bf16: the one-token ones too), and units of one-token items: of this
+  // thread's request, and of the
   // warp's requests up to and with it (the warps' own sums in wsum)
   long long (*wsum)[kWarps] = reinterpret_cast<long long (*)[kWarps]>(&sm.ml[0][0]);
   static_assert(kN * kWarps * sizeof(long long) <= sizeof(sm.ml), "wsum lies over ml");
@@ -231,10 +237,10 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm
   long long u[kN], incl[kN], base[kN] = {};
   auto pass = [&](int r0) {
     const int r = r0 + tid;
-    q = r < a.batch ? ca_req(a, r, kFp8) : CaReq{};
+    q = r < a.batch ? ca_req(a, r, true) : CaReq{};
     u[0] = kKvHeads * q.per_head();
-    u[1] = kKvHeads * static_cast<long long>(q.items());
-    if constexpr (kFp8) u[2] = kKvHeads * static_cast<long long>(q.one_units());
+    u[1] = kKvHeads * static_cast<long long>(q.items() + (!kFp8 && q.one()));
+    u[2] = kKvHeads * static_cast<long long>(q.one_units());
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       incl[n] = u[n];
@@ -247,14 +253,22 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm
     }
     __syncthreads();
   };
-  CaShareOf share[kKinds];
+  CaShareOf share[2];
   int extra = 0;
+  bool apart = true;
+  // the units of either kind, out of the sums
+  auto units = [&](const long long (&x)[kN], int k) {
+    if (kFp8 || apart) return k ? x[2] : x[0] + extra * x[1];
+    return k ? 0LL : x[0] + x[2] + extra * x[1];
+  };
   auto split = [&](const long long (&total)[kN]) {
-    extra = ca_item_units(total[0]);
+    apart = kFp8 || total[0] == 0;  // (bf16: only where there are no others)
+    extra = 0;
+    extra = ca_item_units(units(total, 0));
 #pragma unroll
-    for (int k = 0; k < kKinds; ++k) {
+    for (int k = 0; k < 2; ++k) {
       CaShareOf& s = share[k];
-      s.total = k ? total[kN - 1] : total[0] + extra * total[1];
+      s.total = units(total, k);
       // (a share is long enough to hold some block's beginning)
       s.ctas = min(static_cast<long long>(gridDim.x), max(s.total / (k ? 1 : 1 + extra), 1LL));
       s.u0 = min(s.total, s.total * blockIdx.x / s.ctas);
@@ -290,11 +304,12 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm
     }
     if (once) split(base);
 #pragma unroll
-    for (int k = 0; k < kKinds; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const CaShareOf& s = share[k];
-      const long long from = k ? before[kN - 1] : before[0] + extra * before[1], n = k ? u[kN - 1] : u[0] + extra * u[1];
+      const long long from = units(before, k), n = units(u, k);
       if (s.u0 < s.u1 && from <= s.u0 && s.u0 < from + n) {
         q.extra = k ? 0 : extra;
+        q.apart = apart;
         sm.start[k] = CaStart{s.u0 - from, r0 + tid, q};
       }
     }
@@ -302,8 +317,9 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm
   }
   if (tid == 0) {
 #pragma unroll
-    for (int k = 0; k < kKinds; ++k) sm.share[k] = share[k];
+    for (int k = 0; k < 2; ++k) sm.share[k] = share[k];
     sm.extra = extra;
+    sm.apart = apart;
   }
 }
 
@@ -343,7 +359,7 @@ __device__ __forceinline__ void ca_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// ---- one-token items over an E4M3 cache ----------------------------------------------
+// ---- one-token items ----------------------------------------------------------------
 
 // Two E4M3 values (the low and the high byte of the low half of x) as fp16, exactly.
 __device__ __forceinline__ uint32_t ca_widen2(uint32_t x) {
@@ -352,24 +368,24 @@ __device__ __forceinline__ uint32_t ca_widen2(uint32_t x) {
   return y;
 }
 
-// Warps 0 to 3 take the even blocks, 32 keys each, warps 4 to 7 the odd ones: a warp's chain of dependent steps then has two
-// blocks' time.  S = Q K^T by m16n8k16 products (the 16 query heads are their rows): a 16-bit ldmatrix of K gives a lane four consecutive bytes of one key, dims 16 s + 4 t .. + 3 of
-// k-step s, so Q's fragments hold those dims in the same slots.  O += P V: a transposing ldmatrix gives a lane two
-// dims of two keys, which make one value pair for each of two products, one for the even dims and one for the odd.
-// Bound by HBM: per SM and block 32 KB are copied in and read once.  (16 tokens over 128k keys, 2.15 GB: 0.32 ms, 6.7 TB/s.
-// A bf16 cache's one-token items stay with the others: computed this way they were no faster over long contexts, and two
-// kinds of shares after each other made 17 mixed requests 118 us instead of 95.)
+// Products of m16n8k16, the 16 query heads their rows, from the copied pages.  E4M3: warps 0 to 3 take the even blocks, 32
+// keys each, warps 4 to 7 the odd ones.  S = Q K^T: a 16-bit ldmatrix of K gives a lane four consecutive bytes of one key,
+// dims 16 s + 4 t .. + 3 of k-step s, so Q's fragments hold those dims in the same slots.  O += P V: a transposing ldmatrix
+// gives a lane two dims of two keys, which make one value pair for each of two products, one for the even dims and one for the
+// odd.  bf16: each warp takes 16 keys of every block, K and V in places of their own.  Bound by HBM: each page is copied in
+// and read once.  (16 tokens over 128k keys, E4M3, 2.15 GB: 0.32 ms, 6.7 TB/s.)
 
 // The copies (the producer warp).
+template <bool kFp8>
 __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CUtensorMap& vmap, const CaArgs& a,
-                                               const CaShareOf& share, CaSmem<true>& sm) {
+                                               const CaShareOf& share, CaSmem<kFp8>& sm) {
   const int lane = threadIdx.x & 31;
   DevError* err = a.err;
   uint8_t* places = &sm.kv[0][0];
-  static_assert(sizeof(sm.kv) + sizeof(sm.raw) >= kCaOnePlaces * 2 * kCaHalf, "the places lie over kv and raw");
+  static_assert(sizeof(sm.kv) + sizeof(sm.raw) >= kCaOnePlaces * kCaTile, "the places lie over kv and raw");
   {
     CaCut cut{0, 0, 0, 0};
-    int nitem = 0, nblk = 0;
+    int nitem = 0, nplace = 0;  // descriptors and places filled
     bool ok = true;
     if (share.u0 < share.u1) {
       int r = sm.start[1].r;
@@ -395,23 +411,29 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
         ++nitem;
         const int32_t* row = a.page_table + static_cast<long long>(r) * a.max_blocks + b;
         int ids = 0, ids_next = lane < it.nb ? row[lane] : 0;
-        for (int k = 0; k < it.nb; ++k, ++nblk) {
+        for (int k = 0; k < it.nb && ok; ++k) {
           if ((k & 31) == 0) {
             ids = ids_next;
             ids_next = k + 32 + lane < it.nb ? row[k + 32 + lane] : 0;
           }
           int page = __shfl_sync(0xffffffffu, ids, k & 31);
           const bool bad = page < 0 || page >= a.num_pages;
-          const int s = nblk % kCaOnePlaces;
-          if (!(ok = ca_wait(&sm.one_empty[s], ((nblk / kCaOnePlaces) & 1) ^ 1, err, 841))) break;
-          if (lane == 0) {
-            if (bad) record_error(err, MSA_DEVERR_PAGE, static_cast<long long>(r) * a.max_blocks + b + k);
-            page = bad ? 0 : page;
-            sm.bad[s] = bad;
-            uint8_t* st = places + s * 2 * kCaHalf;
-            mbar_expect_tx(&sm.one_full[s], 2 * kCaHalf);
-            tma_load_3d(st, &kmap, 0, g, page * kBlock, &sm.one_full[s]);
-            tma_load_3d(st + kCaHalf, &vmap, 0, g, page * kBlock, &sm.one_full[s]);
+          if (bad) {
+            if (lane == 0) record_error(err, MSA_DEVERR_PAGE, static_cast<long long>(r) * a.max_blocks + b + k);
+            page = 0;
+          }
+          // E4M3: K and V to one place; bf16: to one each
+#pragma unroll
+          for (int kv = 0; kv < (kFp8 ? 1 : 2); ++kv, ++nplace) {
+            const int s = nplace % kCaOnePlaces;
+            if (!(ok = ca_wait(&sm.one_empty[s], ((nplace / kCaOnePlaces) & 1) ^ 1, err, 841))) break;
+            if (lane == 0) {
+              sm.bad[s] = bad;
+              uint8_t* st = places + s * kCaTile;
+              mbar_expect_tx(&sm.one_full[s], kCaTile);
+              tma_load_3d(st, kv ? &vmap : &kmap, 0, g, page * kBlock, &sm.one_full[s]);
+              tma_load_3d(st + kCaHalf, kFp8 || kv ? &vmap : &kmap, kFp8 ? 0 : 64, g, page * kBlock, &sm.one_full[s]);
+            }
           }
         }
         if (!ok || at >= share.u1) break;
@@ -425,7 +447,7 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
         }
       }
     }
-    if (lane == 0) a.cuts1[blockIdx.x] = cut;
+    if (lane == 0) (kFp8 ? a.cuts1 : a.cuts)[blockIdx.x] = cut;
     if (ok && ca_wait(&sm.one_info_empty[nitem % kCaInfo], ((nitem / kCaInfo) & 1) ^ 1, err, 842) && lane == 0) {
       sm.info[nitem % kCaInfo] = CaItem{0, 0, 0, 0, 0, 0, 0, 0};
       mbar_arrive(&sm.one_info_full[nitem % kCaInfo]);
@@ -433,14 +455,15 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
     __syncwarp();
     if (lane == 0)  // no copy may still be landing when the CTA exits
       for (int s = 0; s < kCaOnePlaces; ++s) {
-        const int fills = (nblk - s + kCaOnePlaces - 1) / kCaOnePlaces;
+        const int fills = (nplace - s + kCaOnePlaces - 1) / kCaOnePlaces;
         if (fills > 0) mbar_wait(&sm.one_full[s], (fills - 1) & 1, err, 843);
       }
   }
 }
 
 // The sums (warps 0 to 7).
-__device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<true>& sm, int warp) {
+template <bool kFp8>
+__device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm, int warp) {
   const int lane = threadIdx.x & 31;
   DevError* err = a.err;
   uint8_t* places = &sm.kv[0][0];
@@ -448,7 +471,7 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<true>& sm,
     const int g8 = lane >> 2, t4 = lane & 3, mi = lane >> 3;
     float* sums = reinterpret_cast<float*>(&sm.q[0][0]);  // [8 warps][16 rows][128] at an item's end
     float2* ml = &sm.ml[0][0];                            // [8 warps][16 rows]
-    int nblk = 0;
+    int nplace = 0;
     uint32_t xcount = 0;
     for (int n = 0;; ++n) {
       const int is = n % kCaInfo;
@@ -457,117 +480,178 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<true>& sm,
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.one_info_empty[is]);
       if (it.nb == 0) break;
-      // Q rows g8 and g8 + 8 as fp16, k-step s: dims 16 s + 4 t .. + 3 in slots 2t, 2t + 1, 2t + 8, 2t + 9
+      // Q rows g8 and g8 + 8, the A operand.  bf16: k-step s holds dims 16 s + 2t, + 1, + 8, + 9.  E4M3 (as fp16): dims
+      // 16 s + 4 t .. + 3 in the same slots, which is where a lane's four bytes of K go.
       uint32_t qa[8][4];
       {
-        const uint2* q0 = reinterpret_cast<const uint2*>(
-            a.q + (static_cast<long long>(it.t0) * kHeads + it.g * kGroup + g8) * kDim + 4 * t4);
-        const uint2* q1 = q0 + 8 * kDim / 4;
+        const __nv_bfloat16* q0 = a.q + (static_cast<long long>(it.t0) * kHeads + it.g * kGroup + g8) * kDim;
+        const __nv_bfloat16* q1 = q0 + 8 * kDim;
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-          const uint2 x = q0[4 * s], y = q1[4 * s];
-          qa[s][0] = pack_f16(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u));
-          qa[s][1] = pack_f16(__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u));
-          qa[s][2] = pack_f16(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
-          qa[s][3] = pack_f16(__uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u));
+          if constexpr (kFp8) {
+            const uint2 x = reinterpret_cast<const uint2*>(q0 + 4 * t4)[4 * s], y = reinterpret_cast<const uint2*>(q1 + 4 * t4)[4 * s];
+            qa[s][0] = pack_f16(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u));
+            qa[s][1] = pack_f16(__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u));
+            qa[s][2] = pack_f16(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+            qa[s][3] = pack_f16(__uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u));
+          } else {
+            qa[s][0] = *reinterpret_cast<const uint32_t*>(q0 + 16 * s + 2 * t4);
+            qa[s][1] = *reinterpret_cast<const uint32_t*>(q1 + 16 * s + 2 * t4);
+            qa[s][2] = *reinterpret_cast<const uint32_t*>(q0 + 16 * s + 2 * t4 + 8);
+            qa[s][3] = *reinterpret_cast<const uint32_t*>(q1 + 16 * s + 2 * t4 + 8);
+          }
         }
       }
-      constexpr float kLift = CaShape<true>::kLift;
+      constexpr float kLift = CaShape<kFp8>::kLift;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g8, g8 + 8; l: this lane's part
-      float o[16][4];  // [2 c + e]: dims 16 c + 2 n + e of rows g8 (0, 1) and g8 + 8 (2, 3), n = 2t and 2t + 1
+      // rows g8 (0, 1) and g8 + 8 (2, 3).  bf16: [n]: dims 8 n + 2t, + 1.  E4M3: [2 c + e]: dims 16 c + 4t + e, + 2 + e.
+      float o[16][4];
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      bool ok = true;
-      for (int k = 0; k < it.nb; ++k, ++nblk) {
-        const int s = nblk % kCaOnePlaces;
-        if (!(ok = ca_wait(&sm.one_full[s], (nblk / kCaOnePlaces) & 1, err, 845))) break;
-        // keys of this warp's 32 that count
-        const int keys = (sm.bad[s] ? 0 : min(kBlock, it.len - (it.b0 + k) * kBlock)) - 32 * (warp & 3);
-        if ((nblk & 1) == (warp >> 2) && keys > 0) {
-          const uint32_t kt = smem_u32(places + s * 2 * kCaHalf), vt = kt + kCaHalf;
-          const int mrow = 32 * (warp & 3) + 8 * (mi & 1) + (lane & 7);  // this lane's row address for ldmatrix
-          float x[4][4] = {};  // keys 8 i + 2t, + 1 of rows g8 (0, 1) and g8 + 8 (2, 3)
+      // The weights of a group of keys: x holds their scores, keys 8 i + 2t, + 1 of rows g8 (0, 1) and g8 + 8 (2, 3); the
+      // first `keys` count.  Raises the reference where a maximum passes it by kCaSlack, adds to l, and leaves P as the A
+      // operand of k-steps of 16 keys.
+      auto weigh = [&](auto& x, auto& pa, int keys) {
+        constexpr int kTiles = sizeof(x) / sizeof(x[0]);
+        if (keys < 8 * kTiles)
 #pragma unroll
-          for (int c = 0; c < 8; c += 2)
+          for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t kr[4];  // keys 16 u .. + 7 and .. + 15 of k-step c, then of k-step c + 1
-              ldsm_x4(kr, kt + sw128(mrow + 16 * u, c + (mi >> 1)));
-              mma_f16(x[2 * u], qa[c], ca_widen2(kr[0]), ca_widen2(kr[0] >> 16));
-              mma_f16(x[2 * u + 1], qa[c], ca_widen2(kr[1]), ca_widen2(kr[1] >> 16));
-              mma_f16(x[2 * u], qa[c + 1], ca_widen2(kr[2]), ca_widen2(kr[2] >> 16));
-              mma_f16(x[2 * u + 1], qa[c + 1], ca_widen2(kr[3]), ca_widen2(kr[3] >> 16));
-            }
-          if (keys < 32)
+            for (int e = 0; e < 4; ++e)
+              if (8 * i + 2 * t4 + (e & 1) >= keys) x[i][e] = -INFINITY;
+        float mx[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int h = 0; h < 2; ++h) {
+          float v = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (8 * i + 2 * t4 + (e & 1) >= keys) x[i][e] = -INFINITY;
-          uint32_t pa[2][4];
-          float mx[2];
+          for (int i = 0; i < kTiles; ++i) v = fmax3(v, x[i][2 * h], x[i][2 * h + 1]);
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+          mx[h] = v * a.scale_log2 - kLift;
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + kCaSlack || mx[1] > m[1] + kCaSlack)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float v = fmaxf(fmax3(x[0][2 * h], x[0][2 * h + 1], x[1][2 * h]),
-                            fmax3(x[1][2 * h + 1], x[2][2 * h], x[2][2 * h + 1]));
-            v = fmax3(v, x[3][2 * h], x[3][2 * h + 1]);
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            mx[h] = v * a.scale_log2 - kLift;
-          }
-          if (__any_sync(0xffffffffu, mx[0] > m[0] + kCaSlack || mx[1] > m[1] + kCaSlack)) {
+            const bool raise = mx[h] > m[h] + kCaSlack;
+            const float f = raise && m[h] != -INFINITY ? ex2(m[h] - mx[h]) : 1.f;
+            if (raise) m[h] = mx[h];
+            l[h] *= f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const bool raise = mx[h] > m[h] + kCaSlack;
-              const float f = raise && m[h] != -INFINITY ? ex2(m[h] - mx[h]) : 1.f;
-              if (raise) m[h] = mx[h];
-              l[h] *= f;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                o[i][2 * h] *= f;
-                o[i][2 * h + 1] *= f;
-              }
+            for (int i = 0; i < 16; ++i) {
+              o[i][2 * h] *= f;
+              o[i][2 * h + 1] *= f;
             }
           }
+          __syncwarp();
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float mu = m[h] == -INFINITY ? 0.f : m[h];
+        for (int h = 0; h < 2; ++h) {
+          const float mu = m[h] == -INFINITY ? 0.f : m[h];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float p0 = ex2(fmaf(x[i][2 * h], a.scale_log2, -mu)),
-                          p1 = ex2(fmaf(x[i][2 * h + 1], a.scale_log2, -mu));
-              pa[i >> 1][2 * (i & 1) + h] = pack_f16(p0, p1);
-              l[h] += p0 + p1;
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            // keys behind the last have no weight, but their values may be anything: they are taken as zero
-            const int left = keys - 16 * u;
-            const uint32_t lo = (2 * t4 < left ? 0xffffu : 0u) | (2 * t4 + 1 < left ? 0xffff0000u : 0u);
-            const uint32_t hi = (2 * t4 + 8 < left ? 0xffffu : 0u) | (2 * t4 + 9 < left ? 0xffff0000u : 0u);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t vr[4];  // keys 16 u .. + 7 and .. + 15 of dims 32 j .., then of dims 32 j + 16 ..
-              ldsm_x4_t(vr, vt + sw128(mrow + 16 * u, 2 * j + (mi >> 1)));
-              if (left < 16) {
-                vr[0] &= lo;
-                vr[1] &= hi;
-                vr[2] &= lo;
-                vr[3] &= hi;
-              }
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                // bytes of a register: key 2t dims 2n and 2n + 1, key 2t + 1 dims 2n and 2n + 1
-                const uint32_t b0 = __byte_perm(vr[2 * c], 0, 0x3120), b1 = __byte_perm(vr[2 * c + 1], 0, 0x3120);
-                mma_f16(o[4 * j + 2 * c], pa[u], ca_widen2(b0), ca_widen2(b1));
-                mma_f16(o[4 * j + 2 * c + 1], pa[u], ca_widen2(b0 >> 16), ca_widen2(b1 >> 16));
-              }
-            }
+          for (int i = 0; i < kTiles; ++i) {
+            const float p0 = ex2(fmaf(x[i][2 * h], a.scale_log2, -mu)), p1 = ex2(fmaf(x[i][2 * h + 1], a.scale_log2, -mu));
+            pa[i >> 1][2 * (i & 1) + h] = kFp8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+            l[h] += p0 + p1;
           }
         }
+      };
+      // keys behind the last have no weight, but their values may be anything: they are taken as zero (a register of a
+      // transposed V holds keys 2t and 2t + 1, of the first or the second eight)
+      auto cut_v = [&](uint32_t (&vr)[4], int keys) {
+        const uint32_t lo = (2 * t4 < keys ? 0xffffu : 0u) | (2 * t4 + 1 < keys ? 0xffff0000u : 0u);
+        const uint32_t hi = (2 * t4 + 8 < keys ? 0xffffu : 0u) | (2 * t4 + 9 < keys ? 0xffff0000u : 0u);
+        vr[0] &= lo;
+        vr[1] &= hi;
+        vr[2] &= lo;
+        vr[3] &= hi;
+      };
+      auto release = [&](int s) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.one_empty[s]);
+      };
+      bool ok = true;
+      for (int k = 0; k < it.nb; ++k) {
+        const int s = nplace % kCaOnePlaces;
+        if (!(ok = ca_wait(&sm.one_full[s], (nplace / kCaOnePlaces) & 1, err, 845))) break;
+        const int block_keys = sm.bad[s] ? 0 : min(kBlock, it.len - (it.b0 + k) * kBlock);
+        const uint32_t kt = smem_u32(places + s * kCaTile);
+        if constexpr (kFp8) {
+          ++nplace;
+          const int keys = block_keys - 32 * (warp & 3);  // of this warp's 32
+          if ((nplace & 1) == (warp >> 2) && keys > 0) {
+            const uint32_t vt = kt + kCaHalf;
+            const int mrow = 32 * (warp & 3) + 8 * (mi & 1) + (lane & 7);  // this lane's row address for ldmatrix
+            float x[4][4] = {};
+#pragma unroll
+            for (int c = 0; c < 8; c += 2)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                uint32_t kr[4];  // keys 16 u .. + 7 and .. + 15 of k-step c, then of k-step c + 1
+                ldsm_x4(kr, kt + sw128(mrow + 16 * u, c + (mi >> 1)));
+                mma_f16(x[2 * u], qa[c], ca_widen2(kr[0]), ca_widen2(kr[0] >> 16));
+                mma_f16(x[2 * u + 1], qa[c], ca_widen2(kr[1]), ca_widen2(kr[1] >> 16));
+                mma_f16(x[2 * u], qa[c + 1], ca_widen2(kr[2]), ca_widen2(kr[2] >> 16));
+                mma_f16(x[2 * u + 1], qa[c + 1], ca_widen2(kr[3]), ca_widen2(kr[3] >> 16));
+              }
+            uint32_t pa[2][4];
+            weigh(x, pa, keys);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t vr[4];  // keys 16 u .. + 7 and .. + 15 of dims 32 j .., then of dims 32 j + 16 ..
+                ldsm_x4_t(vr, vt + sw128(mrow + 16 * u, 2 * j + (mi >> 1)));
+                if (keys < 16 * (u + 1)) cut_v(vr, keys - 16 * u);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  // bytes of a register: key 2t dims 2n and 2n + 1, key 2t + 1 dims 2n and 2n + 1
+                  const uint32_t b0 = __byte_perm(vr[2 * c], 0, 0x3120), b1 = __byte_perm(vr[2 * c + 1], 0, 0x3120);
+                  mma_f16(o[4 * j + 2 * c], pa[u], ca_widen2(b0), ca_widen2(b1));
+                  mma_f16(o[4 * j + 2 * c + 1], pa[u], ca_widen2(b0 >> 16), ca_widen2(b1 >> 16));
+                }
+              }
+          }
+          release(s);
+        } else {
+          const int keys = block_keys - 16 * warp;  // of this warp's 16
+          const int mrow = 16 * warp + 8 * (mi >> 1) + (lane & 7), vrow = 16 * warp + 8 * (mi & 1) + (lane & 7);
+          uint32_t pa[1][4];
+          if (keys > 0) {
+            float x[4][4] = {};  // two chains of products per eight keys, added up below
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t kr[4];  // keys 0-7, both halves of k-step c, then keys 8-15
+              ldsm_x4(kr, kt + (c >> 2) * kCaHalf + sw128(mrow, 2 * (c & 3) + (mi & 1)));
+              mma_bf16(x[2 * (c & 1)], qa[c], kr[0], kr[1]);
+              mma_bf16(x[2 * (c & 1) + 1], qa[c], kr[2], kr[3]);
+            }
+            float y[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[i][e] = x[i][e] + x[i + 2][e];
+            release(s);
+            weigh(y, pa, keys);
+          } else {
+            release(s);
+          }
+          ++nplace;
+          const int sv = nplace % kCaOnePlaces;
+          if (!(ok = ca_wait(&sm.one_full[sv], (nplace / kCaOnePlaces) & 1, err, 848))) break;
+          ++nplace;
+          if (keys > 0) {
+            const uint32_t vt = smem_u32(places + sv * kCaTile);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t vr[4];  // keys 0-7 and 8-15 of dims 16 j .. + 7, then of dims 16 j + 8 ..
+              ldsm_x4_t(vr, vt + (j >> 2) * kCaHalf + sw128(vrow, 2 * (j & 3) + (mi >> 1)));
+              if (keys < 16) cut_v(vr, keys);
+              mma_bf16(o[2 * j], pa[0], vr[0], vr[1]);
+              mma_bf16(o[2 * j + 1], pa[0], vr[2], vr[3]);
+            }
+          }
+          release(sv);
+        }
       }
       if (!ok) break;
       // ---- the end of the item: the warps' sums meet in shared memory; each warp joins and writes two rows ----
@@ -577,10 +661,19 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<true>& sm,
         l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
         const int row = g8 + 8 * h;
         if (t4 == 0) ml[warp * 16 + row] = make_float2(m[h], l[h]);
+        // (the row's 64-byte pieces permuted: eight rows, eight banks)
+        float* to = sums + (warp * 16 + row) * kDim;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)  // dims 16 c + 4t .. + 3 (the row's 64-byte pieces permuted: eight rows, eight banks)
-          *reinterpret_cast<float4*>(sums + (warp * 16 + row) * kDim + 16 * (c ^ g8) + 4 * t4) =
-              make_float4(o[2 * c][2 * h], o[2 * c + 1][2 * h], o[2 * c][2 * h + 1], o[2 * c + 1][2 * h + 1]);
+        for (int c = 0; c < 8; ++c) {
+          if constexpr (kFp8) {
+            *reinterpret_cast<float4*>(to + 16 * (c ^ g8) + 4 * t4) =
+                make_float4(o[2 * c][2 * h], o[2 * c + 1][2 * h], o[2 * c][2 * h + 1], o[2 * c + 1][2 * h + 1]);
+          } else {
+            *reinterpret_cast<float2*>(to + 16 * (c ^ g8) + 2 * t4) = make_float2(o[2 * c][2 * h], o[2 * c][2 * h + 1]);
+            *reinterpret_cast<float2*>(to + 16 * (c ^ g8) + 8 + 2 * t4) =
+                make_float2(o[2 * c + 1][2 * h], o[2 * c + 1][2 * h + 1]);
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.one_x_full);
@@ -604,8 +697,9 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<true>& sm,
           v.w = fmaf(f, x.w, v.w);
         }
         if (it.slot >= 0) {
-          a.part1_o[(static_cast<long long>(it.slot) * (kDim / 4) + lane) * kGroup + row] = v;
-          if (lane == 0) a.part1_ml[it.slot * kGroup + row] = make_float2(top, sum);
+          const long long rows = kFp8 ? kGroup : a.rows;
+          (kFp8 ? a.part1_o : a.part_o)[(static_cast<long long>(it.slot) * (kDim / 4) + lane) * rows + row] = v;
+          if (lane == 0) (kFp8 ? a.part1_ml : a.part_ml)[it.slot * rows + row] = make_float2(top, sum);
         } else {
           const long long orow = static_cast<long long>(it.t0) * kHeads + it.g * kGroup + row;
           const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
@@ -700,7 +794,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   // All roles of all warps are done: tensor memory may be released, and the tiles' places copied into again.
   auto roles_done = [&] {
     tc::fence_before();
-    if (kFp8) fence_proxy_async_smem();
+    if (kFp8) fence_proxy_async_smem();  // (bf16: either there are other items, or one-token items)
     __syncwarp();
     asm volatile("barrier.sync 1, %0;" ::"n"(kThreads) : "memory");
   };
@@ -828,7 +922,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           if (++g == kKvHeads) {
             g = 0;
             do {
-              rq = ca_req(a, ++r, kFp8, extra);
+              rq = ca_req(a, ++r, kFp8 || sm.apart, extra);
             } while (rq.items() == 0);
           }
         }
@@ -853,7 +947,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     }
     __syncwarp();
     roles_done();
-    if constexpr (kFp8) ca_one_produce(kmap, vmap, a, sm.share[1], sm);
+    if (kFp8 || sm.apart) ca_one_produce<kFp8>(kmap, vmap, a, sm.share[1], sm);
   } else if (warp == kCaMmaWarp) {
     // ---------------- S and O products ----------------
     // One thread issues them all, and they execute in the order in which they are issued: an S product that overwrites P
@@ -1181,7 +1275,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       }
     }
     roles_done();
-    if constexpr (kFp8) ca_one_attend(a, sm, warp);
+    if (kFp8 || sm.apart) ca_one_attend<kFp8>(a, sm, warp);
   } else if (kFp8 && warp >= kCaWidenWarp) {
     // ---------------- E4M3 pages and bf16 queries to fp16 ----------------
     ca_regs_down<Shape::kRegsWiden>();

@@ -105,7 +105,7 @@ def test_more_requests_than_threads(cache):
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
-@pytest.mark.parametrize("news", [[1, 16, 17, 5], [40, 1, 1, 33]])
+@pytest.mark.parametrize("news", [[1, 16, 17, 5], [40, 1, 1, 33], [1, 1, 1, 1]])
 def test_values_that_are_not_finite_stay_where_they_are(news, cache):
     # a NaN query reaches its own row; a NaN key or an infinite value the rows of its request and KV head that see it
     b = Batch([700, 500, 300, 200], news, cache, seed=6)
@@ -123,15 +123,17 @@ def test_values_that_are_not_finite_stay_where_they_are(news, cache):
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
-def test_long_context_is_split_and_joined(cache):
-    Batch([40000, 3, 17000], [1, 1, 20], cache).poison().check()
+@pytest.mark.parametrize("news", [[1, 1, 20], [1, 1, 1]])
+def test_long_context_is_split_and_joined(news, cache):
+    Batch([40000, 3, 17000], news, cache).poison().check()
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 @pytest.mark.parametrize("order", ["up", "down", "one"])
-def test_maximum_that_moves(order, cache):
+@pytest.mark.parametrize("news", [[40, 1], [1, 1]])
+def test_maximum_that_moves(news, order, cache):
     # scores that grow (or fall) from block to block by tens of units, and one key that takes nearly all the weight
-    b = Batch([1500, 700], [40, 1], cache, seed=5)
+    b = Batch([1500, 700], news, cache, seed=5)
     pos = torch.arange(1500, device="cuda")
     size = {"up": pos / 150, "down": 10 - pos / 150, "one": torch.where(pos == 611, 20.0, 0.1)}[order]
     for r in range(2):
@@ -180,6 +182,35 @@ def test_bad_lengths_and_pages(cache):
     b.table[0, :4] = -5
     got, lse = b.call()
     assert bool((got[:10] == 0).all()) and bool((lse[:10] == -math.inf).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_bad_lengths_and_pages_of_single_tokens(cache):
+    b = Batch([500, 700, 300, 400, 260, 0], [1, 1, 1, 1, 1, 0], cache, seed=8).poison()
+    width = b.table.shape[1]
+    ws = msa.Workspace(4096 + msa.workspace_size(msa.make_config(), 4, b.q.shape[0], width))
+    bad = b.seq.clone()
+    bad[0], bad[1] = 0, width * 128 + 1
+    seq, b.seq = b.seq, bad
+    got, lse = b.call(workspace=ws)
+    assert ws.read_device_error() in ((3, 0), (3, 1))
+    assert bool((got[:2] == 0).all()) and bool((lse[:2] == -math.inf).all())
+    ref = S.attend(b.q, b.k, b.v, b.lens, b.table, b.cu, SCALE, **b.scales)
+    S.check_attend(got[2:], lse[2:], [x[2:] for x in ref], max(b.lens), 11 if b.fp8 else 8)
+    b.seq = seq
+    # bad pages, the last (cut inside) among them, and a request without a good one
+    b.table[0, 1], b.table[3, 0], b.table[4, 2] = -1, b.k.shape[0] // 128, 2 ** 30
+    b.check(workspace=ws, skip=((0, 1), (3, 0), (4, 2)))
+    assert ws.read_device_error() in ((1, 1), (1, 3 * width), (1, 4 * width + 2))
+    b.table[2, :3] = -5
+    got, lse = b.call()
+    assert bool((got[2] == 0).all()) and bool((lse[2] == -math.inf).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_more_single_tokens_than_threads(cache):
+    lens = [1 + (r * 53) % 400 for r in range(1100)]
+    Batch(lens, [int(r % 3 > 0) for r in range(1100)], cache, seed=9).poison().check()
 
 
 def test_unused_table_entries_are_not_read():
