@@ -39,16 +39,15 @@
 // shares costs: it is done where all items have one token (17 mixed requests
 // took 0.118 ms with two kinds, 0.095 with one).
 //
-// Chunks are bound on chip.  2048 tokens over 32k keys run at 1.75 PFLOP/s in
-// bf16 (1.22 ms, tensor pipe 75% active; 92% of a library product's rate): S
-// reads Q and K from shared memory at its full 128 bytes a cycle, and the
-// softmax of a warpgroup starts only when its S is done.  An item costs about
-// two units besides its blocks: 0.5 us for its last O product, 2.4 for its rows'
+// Chunks are bound on chip.  2048 tokens over 32k keys take 1.22 to 1.25 ms in
+// bf16 (1.7 PFLOP/s, tensor pipe 75% active, 90% of a library product's rate):
+// what is left is the way from S over the softmax to O.  An item costs about two
+// units besides its blocks: 0.5 us for its last O product, 2.4 for its rows'
 // stores, 1 for the first block's softmax, none of it beside other products.
-// An E4M3 cache adds the widening and leaves the softmax fewer registers
-// (1.43 ms).  Single tokens over long contexts are bound by HBM (64 requests,
-// 4.0 GB: 0.59 ms, 6.8 TB/s), short ones by latency: 3.7 us without any work,
-// 8.1 with one block.
+// An E4M3 cache adds the widening (without it 7% less) and leaves the softmax
+// fewer registers (5%): 1.43 ms.  Single tokens over long contexts are bound by
+// HBM (64 requests, 4.0 GB: 0.59 ms, 6.8 TB/s), short ones by latency: 4.7 us
+// without any work, 8.2 with one block.
 #include <cuda_fp16.h>
 
 #include <type_traits>

@@ -511,9 +511,9 @@ msa_status msa_map_slots(const int32_t* seq_lens, const int32_t* new_lens, int b
  * rot_dim / 2 pairs: (x[j], x[j + rot_dim / 2]), or (x[2j], x[2j + 1]) when
  * interleaved.  Pair j turns by positions[axis[j]][t] * inv_freq[j]:
  *   a' = a cos - b sin, b' = a sin + b cos;
- * the dims from rot_dim on pass unchanged.  The angle is taken from the exact
- * product (reduced in binary64, so a position of a million keeps its fraction),
- * the rotation is computed in fp32 and rounded once.
+ * the dims from rot_dim on pass unchanged.  The angle is reduced to a fraction of
+ * a turn before it is rounded (so a position of a million keeps its fraction), the
+ * rotation is computed in fp32 and rounded once.
  * rot_dim: a multiple of 16 in [16, 128]; 1 <= num_axes <= 4; axis[j] < num_axes
  * for j < rot_dim / 2. */
 typedef struct {
