@@ -33,6 +33,8 @@ static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 struct Layout {
   size_t scores = 0, att_tickets = 0, partials = 0, plan = 0, bm = 0, total = 0;
 };
+// The chunk attention's scratch lies behind the decode attention's counters, so that one workspace may serve both.
+static size_t chunk_scratch_offset() { return kHeaderBytes + up256(attend_tickets_bytes()); }
 static Layout layout(int mode, long long n, int max_blocks, int topk) {
   Layout L;
   size_t off = kHeaderBytes;
@@ -101,7 +103,7 @@ msa_status msa_workspace_size(const msa_config* cfg, int mode, int64_t n, int ma
     return MSA_OK;
   }
   if (mode == MSA_MODE_CHUNK) {
-    *bytes = kHeaderBytes + attend_chunk_bytes(n, max_blocks);
+    *bytes = chunk_scratch_offset() + attend_chunk_bytes(n, max_blocks);
     return MSA_OK;
   }
   if (mode != MSA_MODE_DECODE && mode != MSA_MODE_PREFILL && mode != MSA_MODE_PREFILL_BWD) return MSA_ERR_SHAPE;
@@ -561,7 +563,7 @@ static msa_status attend_chunk(const msa_config* cfg, const void* q, const void*
     return MSA_ERR_SHAPE;
   if (!(scale > 0.f) || !std::isfinite(scale)) return MSA_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return MSA_ERR_ALIGN;
-  if ((st = check_ws(workspace, workspace_bytes, kHeaderBytes + attend_chunk_bytes(total_tokens, max_blocks))) !=
+  if ((st = check_ws(workspace, workspace_bytes, chunk_scratch_offset() + attend_chunk_bytes(total_tokens, max_blocks))) !=
       MSA_OK)
     return st;
   ChunkLaunch L{};
@@ -581,7 +583,7 @@ static msa_status attend_chunk(const msa_config* cfg, const void* q, const void*
   L.scale = scale;
   L.out = out;
   L.lse = lse;
-  L.scratch = static_cast<uint8_t*>(workspace) + kHeaderBytes;
+  L.scratch = static_cast<uint8_t*>(workspace) + chunk_scratch_offset();
   L.err = static_cast<DevError*>(workspace);
   return cuda_result(launch_attend_chunk(L, static_cast<cudaStream_t>(stream)));
 }

@@ -119,7 +119,7 @@ msa_status msa_config_check(const msa_config* cfg);
  *   MSA_MODE_PACK   : n = batch * seq of the document map, max_blocks = batch.
  *   MSA_MODE_PREFILL_BWD: as MSA_MODE_PREFILL, for msa_sparse_attend_prefill_backward.
  *   MSA_MODE_CHUNK  : n = total new tokens, max_blocks = blocks per row of the page table,
- *                     for msa_attend_chunk; only its first 256 bytes need the zero-fill.
+ *                     for msa_attend_chunk (alone, it needs its first 256 bytes zero-filled).
  * The workspace must be zero-filled once before its first use (see
  * msa_workspace_init), which clears the device error word and the decode
  * scorer's page-claim counter in its first 256 bytes, and the completion
@@ -130,6 +130,8 @@ msa_status msa_config_check(const msa_config* cfg);
  * the decode attention's counters (one per CTA) sit at a fixed offset that no
  * decode call of any batch or max_blocks writes over, so one workspace serves
  * decode calls of any size whose msa_workspace_size fits in it, in any order.
+ * The chunk-serving calls write no counter either, so it may serve them in
+ * between (with a size that fits both).
  * The prefill layouts do not keep that region: a workspace that served a
  * prefill or backward call must be zero-filled again before it serves a
  * decode attention call.  After a call whose device error word reads

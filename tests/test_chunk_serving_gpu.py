@@ -133,3 +133,39 @@ def test_refusals_of_wrong_tensors():
             msa.msa_map_slots(*slot_args, **kw)
     with pytest.raises(ValueError, match="new_lens"):
         msa.msa_map_slots(slot_args[0], ints(3), *slot_args[2:], num_slots=128, capacity=4)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_workspace_for_chunks_and_the_sparse_decode(fp8):
+    """A step of chunks between two decode steps leaves the decode calls' counters in a shared workspace alone."""
+    gen = torch.Generator("cuda").manual_seed(3)
+    lens = [5000, 700, 3000, 129]
+    table, pool = S.page_table(lens)
+    dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    k, v = (torch.randn(pool * 128, 4, 128, generator=gen, device="cuda").to(dt) for _ in range(2))
+    index = torch.randn(pool * 128, 1, 128, generator=gen, device="cuda").bfloat16()
+    iq = torch.randn(4, 4, 128, generator=gen, device="cuda").bfloat16()
+    q = torch.randn(4, 64, 128, generator=gen, device="cuda").bfloat16()
+    news = [40, 1, 17, 8]
+    qc = torch.randn(sum(news), 64, 128, generator=gen, device="cuda").bfloat16()
+    cfg, width = msa.make_config(), table.shape[1]
+    ws = msa.Workspace(max(msa.workspace_size(cfg, 0, 4, width), msa.workspace_size(cfg, 4, sum(news), width)))
+    decode = msa.msa_sparse_attend_decode_fp8kv if fp8 else msa.msa_sparse_attend_decode
+    chunk = msa.msa_attend_chunk_fp8kv if fp8 else msa.msa_attend_chunk
+
+    def steps(workspace):
+        out = []
+        for i in range(3):
+            q2k = msa.msa_select_blocks_decode(iq, index, S.ints(lens), page_table=table, workspace=workspace)
+            out += [q2k, decode(q, k, v, q2k, S.ints(lens), page_table=table, workspace=workspace)]
+            out.append(chunk(qc, k, v, S.ints(lens), table, S.offsets(news), workspace=workspace))
+            out.append(chunk(qc[:4], k, v, S.ints(lens), table, S.offsets([1] * 4), workspace=workspace))
+        return out
+    shared = steps(ws)
+    assert ws.read_device_error()[0] == 0
+    for i, (a, b) in enumerate(zip(shared[:8] + shared, shared[4:] + steps(None))):
+        if i % 4 == 1:
+            # the decode attention may join its pieces in another order: one bf16 step, and fp32 sums of values below 8
+            assert bool(((a.float() - b.float()).abs() <= 2.0 ** -7 * a.float().abs() + 2.0 ** -16).all())
+        else:
+            assert torch.equal(a, b)
