@@ -44,8 +44,7 @@
 // what is left is the way from S over the softmax to O.  An item costs about two
 // units besides its blocks: 0.5 us for its last O product, 2.4 for its rows'
 // stores, 1 for the first block's softmax, none of it beside other products.
-// An E4M3 cache adds the widening (without it 7% less) and leaves the softmax
-// fewer registers (5%): 1.43 ms.  Single tokens over long contexts are bound by
+// An E4M3 cache adds the widening and leaves the softmax fewer registers: 1.38 ms.  Single tokens over long contexts are bound by
 // HBM (64 requests, 4.0 GB: 0.59 ms, 6.8 TB/s), short ones by latency: 4.7 us
 // without any work, 8.2 with one block.
 #include <cuda_fp16.h>
@@ -126,8 +125,10 @@ struct CaShape {
   static constexpr int kWiden = kFp8 ? 4 : 0;  // widening warps
   static constexpr int kThreads = 32 * (kCaWidenWarp + kWiden);
   // registers per thread of the roles, out of the launch's 168 (384 threads) or 128 (512 threads) a thread:
-  // 256 * 216 + 128 * 72 = 384 * 168, and 256 * 184 + 128 * 64 + 128 * 80 = 512 * 128
-  static constexpr int kRegsSoftmax = kFp8 ? 184 : 216, kRegsIssue = kFp8 ? 64 : 72, kRegsWiden = 80;
+  // 256 * 216 + 128 * 72 = 384 * 168, and 256 * 200 + 256 * 56 = 512 * 128.  (With 184 the softmax of E4M3 chunks cost 5%.
+  // Two widening warps in the issuing warps' group leave it 216: chunks 1% faster, but items of few tokens, bound by the
+  // widening, made 17 mixed requests 126 us instead of 115.)
+  static constexpr int kRegsSoftmax = kFp8 ? 200 : 216, kRegsIssue = kFp8 ? 56 : 72;
   // fp16 weights are kept near the top of their range (at most 2^(kLift + kCaSlack) = 2^15), so that small ones
   // stay normal down to 2^-21 of the largest
   static constexpr float kLift = kFp8 ? 7.f : 0.f;
@@ -188,6 +189,16 @@ __device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
     out[i] = make_uint4(0u, 0u, 0u, 0u);
   if (a.lse)
     for (long long i = c0 * kHeads + lane; i < c1 * kHeads; i += 32) a.lse[i] = -INFINITY;
+}
+
+// This CTA's part of the requests with bad lengths (one warp).
+__device__ __forceinline__ void ca_refuse_bad(const CaArgs& a, int lane) {
+  for (long long r0 = blockIdx.x; r0 < a.batch; r0 += 32LL * gridDim.x) {
+    const long long r = r0 + static_cast<long long>(lane) * gridDim.x;
+    const bool bad = r < a.batch && !ca_good(a, a.cu[r], a.cu[r + 1], a.seq_lens[r]);
+    for (unsigned m = __ballot_sync(0xffffffffu, bad); m; m &= m - 1)
+      ca_refuse(a, static_cast<int>(r0 + static_cast<long long>(__ffs(m) - 1) * gridDim.x), lane);
+  }
 }
 
 // The request (and the unit in it) where a share begins.
@@ -799,7 +810,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   };
   // A wait that gives up (recorded in the error word) ends its role, so a broken pipeline ends after one bounded wait
   // per role.
-  if (warp >= 8 && warp < kCaWidenWarp) ca_regs_down<Shape::kRegsIssue>();
+  if (warp >= 8) ca_regs_down<Shape::kRegsIssue>();
   if (warp == kCaProducerWarp) {
     // ---------------- the share's items, and their copies ----------------
     const long long total = sm.share[0].total, ctas = sm.share[0].ctas, u0 = sm.share[0].u0, u1 = sm.share[0].u1;
@@ -1069,12 +1080,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     __syncwarp();
   } else if (warp == kCaMmaWarp + 1) {
     // ---------------- requests with bad lengths ----------------
-    for (long long r0 = blockIdx.x; r0 < a.batch; r0 += 32LL * gridDim.x) {
-      const long long r = r0 + static_cast<long long>(lane) * gridDim.x;
-      const bool bad = r < a.batch && !ca_good(a, a.cu[r], a.cu[r + 1], a.seq_lens[r]);
-      for (unsigned m = __ballot_sync(0xffffffffu, bad); m; m &= m - 1)
-        ca_refuse(a, static_cast<int>(r0 + static_cast<long long>(__ffs(m) - 1) * gridDim.x), lane);
-    }
+    ca_refuse_bad(a, lane);
   } else if (warp < 8) {
     // ---------------- softmax, one row per thread; the end of an item ----------------
     ca_regs_up<Shape::kRegsSoftmax>();
@@ -1277,8 +1283,8 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     if (kFp8 || sm.apart) ca_one_attend<kFp8>(a, sm, warp);
   } else if (kFp8 && warp >= kCaWidenWarp) {
     // ---------------- E4M3 pages and bf16 queries to fp16 ----------------
-    ca_regs_down<Shape::kRegsWiden>();
-    const int wt = tid & 127;
+    constexpr int kLanes = 128, kStep = kLanes / 8;  // kStep: rows at once
+    const int wt = tid - 32 * kCaWidenWarp;
     // Eight lanes take 16-byte pieces of two neighbouring rows, the odd row's from the other half: they read and write
     // eight different 16-byte banks of the swizzled tiles.
     const int i8 = wt & 7, odd = i8 >> 2, piece = (i8 & 3) + 4 * (((wt >> 3) & 1) ^ odd), row0 = 2 * (wt >> 4) + odd;
@@ -1290,7 +1296,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         const int s = nq & 1, bytes = min(8, ntok - 8 * q) * kCaQEntry;
         if (!(ok = ca_wait(&sm.q_full[s], (nq >> 1) & 1, err, 833))) break;
         const uint32_t at = smem_u32(sm.q[s]);
-        for (int o = wt * 16; o < bytes; o += 128 * 16) {
+        for (int o = wt * 16; o < bytes; o += kLanes * 16) {
           const uint4 v = lds128(at + o);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           uint32_t y[4];
@@ -1323,28 +1329,37 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         }
         const uint32_t src = smem_u32(sm.raw[kFp8 ? rs : 0]) + sw128(row0, piece);
         const uint32_t dst = smem_u32(sm.kv[st]) + (piece >> 2) * kCaHalf;
-        uint4 x[8];
+        const uint32_t dst0 = dst + sw128(row0, 2 * (piece & 3)), dst1 = dst + sw128(row0, 2 * (piece & 3) + 1);
+        // four rows at a time, the next four asked for before
+        constexpr int kBatches = kBlock / kStep / 4;
+        uint4 x[2][4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = lds128(src + q * 16 * 128);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.raw_empty[rs]);
+        for (int q = 0; q < 4; ++q) x[0][q] = lds128(src + q * kStep * 128);
         if (!(ok = ca_wait(&sm.kv_empty[st], ((load / kTiles) & 1) ^ 1, err, 832))) break;
-        if (keys < kBlock)
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (row0 + 16 * q >= keys) x[q] = make_uint4(0u, 0u, 0u, 0u);
+        for (int n = 0; n < kBatches; ++n) {
+          if (n + 1 < kBatches)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int r = row0 + 16 * q;
-          const uint32_t w[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
-          uint32_t y[8];
+            for (int q = 0; q < 4; ++q) x[(n + 1) & 1][q] = lds128(src + (4 * n + 4 + q) * kStep * 128);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            y[2 * i] = ca_widen2(w[i]);
-            y[2 * i + 1] = ca_widen2(w[i] >> 16);
+          for (int q = 0; q < 4; ++q) {
+            const int down = (4 * n + q) * kStep;  // rows below row0, a multiple of the swizzle's eight
+            uint4 v = x[n & 1][q];
+            if (keys < kBlock && row0 + down >= keys) v = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              y[2 * i] = ca_widen2(w[i]);
+              y[2 * i + 1] = ca_widen2(w[i] >> 16);
+            }
+            sts128(dst0 + down * 128, y[0], y[1], y[2], y[3]);
+            sts128(dst1 + down * 128, y[4], y[5], y[6], y[7]);
           }
-          sts128(dst + sw128(r, 2 * (piece & 3)), y[0], y[1], y[2], y[3]);
-          sts128(dst + sw128(r, 2 * (piece & 3) + 1), y[4], y[5], y[6], y[7]);
+          if (n + 2 == kBatches) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.raw_empty[rs]);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
