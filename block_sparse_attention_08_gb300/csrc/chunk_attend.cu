@@ -234,23 +234,22 @@ struct CaSmem {
 // The whole CTA: sums up the requests' units and finds this CTA's share of each kind, and where it begins.  The units that an
 // item counts besides its blocks depend on the total, so the items are summed up beside their blocks.  (The caller's barrier
 // follows.)
-template <bool kFp8>
+template <bool kFp8, bool kOne>
 __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm) {
-  constexpr int kThreads = CaShape<kFp8>::kThreads, kWarps = kThreads / 32, kN = 3;
+  constexpr int kThreads = CaShape<kFp8>::kThreads, kWarps = kThreads / 32, kKinds = kOne ? 2 : 1, kN = kOne ? 3 : 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // all KV heads' units without the items' own, items (bf16: the one-token ones too), and units of one-token items: of this
-  // thread's request, and of the
-  // warp's requests up to and with it (the warps' own sums in wsum)
+  // thread's request, and of the warp's requests up to and with it (the warps' own sums in wsum)
   long long (*wsum)[kWarps] = reinterpret_cast<long long (*)[kWarps]>(&sm.ml[0][0]);
   static_assert(kN * kWarps * sizeof(long long) <= sizeof(sm.ml), "wsum lies over ml");
   CaReq q{};
   long long u[kN], incl[kN], base[kN] = {};
   auto pass = [&](int r0) {
     const int r = r0 + tid;
-    q = r < a.batch ? ca_req(a, r, true) : CaReq{};
+    q = r < a.batch ? ca_req(a, r, kOne) : CaReq{};
     u[0] = kKvHeads * q.per_head();
-    u[1] = kKvHeads * static_cast<long long>(q.items() + (!kFp8 && q.one()));
-    u[2] = kKvHeads * static_cast<long long>(q.one_units());
+    u[1] = kKvHeads * static_cast<long long>(q.items() + (kOne && !kFp8 && q.one()));
+    if constexpr (kOne) u[2] = kKvHeads * static_cast<long long>(q.one_units());
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       incl[n] = u[n];
@@ -263,20 +262,21 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm
     }
     __syncthreads();
   };
-  CaShareOf share[2];
+  CaShareOf share[kKinds];
   int extra = 0;
-  bool apart = true;
+  bool apart = kOne;
   // the units of either kind, out of the sums
   auto units = [&](const long long (&x)[kN], int k) {
-    if (kFp8 || apart) return k ? x[2] : x[0] + extra * x[1];
-    return k ? 0LL : x[0] + x[2] + extra * x[1];
+    if (!kOne) return x[0] + extra * x[1];
+    if (kFp8 || apart) return k ? x[kN - 1] : x[0] + extra * x[1];
+    return k ? 0LL : x[0] + x[kN - 1] + extra * x[1];
   };
   auto split = [&](const long long (&total)[kN]) {
-    apart = kFp8 || total[0] == 0;  // (bf16: only where there are no others)
+    apart = kOne && (kFp8 || total[0] == 0);  // (bf16: only where there are no others)
     extra = 0;
     extra = ca_item_units(units(total, 0));
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < kKinds; ++k) {
       CaShareOf& s = share[k];
       s.total = units(total, k);
       // (a share is long enough to hold some block's beginning)
@@ -314,7 +314,7 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm
     }
     if (once) split(base);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < kKinds; ++k) {
       const CaShareOf& s = share[k];
       const long long from = units(before, k), n = units(u, k);
       if (s.u0 < s.u1 && from <= s.u0 && s.u0 < from + n) {
@@ -327,7 +327,7 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm
   }
   if (tid == 0) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) sm.share[k] = share[k];
+    for (int k = 0; k < kKinds; ++k) sm.share[k] = share[k];
     sm.extra = extra;
     sm.apart = apart;
   }
@@ -726,7 +726,8 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm,
   }
 }
 
-template <bool kFp8>
+// kOne: one-token items may be computed apart (over an E4M3 cache always)
+template <bool kFp8, bool kOne>
 __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kernel(
     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CaArgs a) {
@@ -795,7 +796,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  ca_find_shares<kFp8>(a, sm);
+  ca_find_shares<kFp8, kOne>(a, sm);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -932,7 +933,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           if (++g == kKvHeads) {
             g = 0;
             do {
-              rq = ca_req(a, ++r, kFp8 || sm.apart, extra);
+              rq = ca_req(a, ++r, kOne && sm.apart, extra);
             } while (rq.items() == 0);
           }
         }
@@ -957,7 +958,8 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     }
     __syncwarp();
     roles_done();
-    if (kFp8 || sm.apart) ca_one_produce<kFp8>(kmap, vmap, a, sm.share[1], sm);
+    if constexpr (kOne)
+      if (sm.apart) ca_one_produce<kFp8>(kmap, vmap, a, sm.share[1], sm);
   } else if (warp == kCaMmaWarp) {
     // ---------------- S and O products ----------------
     // One thread issues them all, and they execute in the order in which they are issued: an S product that overwrites P
@@ -1280,7 +1282,8 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       }
     }
     roles_done();
-    if (kFp8 || sm.apart) ca_one_attend<kFp8>(a, sm, warp);
+    if constexpr (kOne)
+      if (sm.apart) ca_one_attend<kFp8>(a, sm, warp);
   } else if (kFp8 && warp >= kCaWidenWarp) {
     // ---------------- E4M3 pages and bf16 queries to fp16 ----------------
     constexpr int kLanes = 128, kStep = kLanes / 8;  // kStep: rows at once
@@ -1502,16 +1505,16 @@ static cudaError_t ca_launch_dependent(void (*kernel)(Params...), dim3 grid, int
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kOne>
 static cudaError_t ca_launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, const CaArgs& a,
                              cudaStream_t stream) {
   constexpr size_t bytes = sizeof(CaSmem<kFp8>);
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-  if (const cudaError_t e = cudaFuncSetAttribute(chunk_attend_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (const cudaError_t e = cudaFuncSetAttribute(chunk_attend_kernel<kFp8, kOne>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(bytes));
       e != cudaSuccess)
     return e;
-  return ca_launch_dependent(chunk_attend_kernel<kFp8>, dim3(kNumSMs), CaShape<kFp8>::kThreads, bytes, stream, qmap, kmap,
+  return ca_launch_dependent(chunk_attend_kernel<kFp8, kOne>, dim3(kNumSMs), CaShape<kFp8>::kThreads, bytes, stream, qmap, kmap,
                              vmap, a);
 }
 
@@ -1548,8 +1551,11 @@ cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream) {
   p += ca_up(kCaRows1 * sizeof(float2));
   a.part1_o = reinterpret_cast<float4*>(p);
   a.err = L.err;
-  if (const cudaError_t e = L.kv_fp8 ? ca_launch<true>(qmap, kmap, vmap, a, stream)
-                                     : ca_launch<false>(qmap, kmap, vmap, a, stream);
+  // A batch of single tokens has no more of them than requests.  (The code for such batches cost others 0.4 us a call, and
+  // 16 tokens over 32k keys 3.)
+  if (const cudaError_t e = L.kv_fp8 ? ca_launch<true, true>(qmap, kmap, vmap, a, stream)
+                            : L.tokens <= L.batch ? ca_launch<false, true>(qmap, kmap, vmap, a, stream)
+                                                  : ca_launch<false, false>(qmap, kmap, vmap, a, stream);
       e != cudaSuccess)
     return e;
   return ca_launch_dependent(chunk_join_kernel, dim3(kNumSMs * (a.rows / kGroup + (L.kv_fp8 ? 1 : 0))), kCaJoinThreads, 0,

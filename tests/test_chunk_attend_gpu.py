@@ -53,8 +53,9 @@ class Batch:
     def check(self, scale=SCALE, skip=(), **kw):
         got, lse = self.call(scale, **kw)
         n = sum(self.news)
-        ref = S.attend(self.q[:n], self.k, self.v, self.lens, self.table, self.cu, scale, skip=skip, **self.scales)
-        S.check_attend(got[:n], lse[:n], ref, max(self.lens), 11 if self.fp8 else 8)
+        if n:
+            ref = S.attend(self.q[:n], self.k, self.v, self.lens, self.table, self.cu, scale, skip=skip, **self.scales)
+            S.check_attend(got[:n], lse[:n], ref, max(self.lens), 11 if self.fp8 else 8)
         assert bool((got[n:] == 77.0).all()) and bool((lse[n:] == 123.0).all())  # rows behind the last request
         return got, lse
 
@@ -205,6 +206,15 @@ def test_bad_lengths_and_pages_of_single_tokens(cache):
     b.table[2, :3] = -5
     got, lse = b.call()
     assert bool((got[2] == 0).all()) and bool((lse[2] == -math.inf).all())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news", [[0, 3, 0, 0, 1, 0], [17] + [0] * 10 + [1] * 4 + [0] * 9, [0, 0, 2], [0, 1, 0], [0, 0]])
+def test_fewer_tokens_than_requests(news, cache):
+    # single tokens alone or beside others, among requests that bring none
+    lens = [max(m, 1 + (r * 631) % 1500) for r, m in enumerate(news)]
+    Batch(lens, news, cache, seed=len(news), rows=max(sum(news), 1)).poison().check()
+    Batch(lens, news, cache, seed=len(news), rows=len(news)).poison().check()
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
