@@ -130,3 +130,22 @@ def test_more_rows_than_threads_at_once():
     for capacity in (sum(news), sum(news) + 70_001):
         *want, errors = S.map_slots(lens, news, table, ids, len(ids), slots, capacity)
         assert not errors and _run(lens, news, table, ids, len(ids), slots, capacity) == tuple(want)
+
+
+def test_outputs_given_and_new_agree():
+    # new outputs are parts of one allocation: whole tensors to their user all the same
+    lens, news, table, free, num_free, num_slots = _case(5, 9, 700, 90)
+    t = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (table, free)]
+    args = S.ints(lens), S.ints(news), t[0], t[1], S.ints([num_free])
+    sizes = {"num_slots": num_slots, "capacity": sum(news) + 3}
+    new = msa.msa_map_slots(*args, **sizes)
+    given = [torch.full_like(x, 5) for x in new]
+    out = msa.msa_map_slots(*args, **sizes, **dict(zip(("cu_seqlens_q", "slots", "positions", "num_free_out"), given)))
+    for a, b, c in zip(new, out, given):
+        assert torch.equal(a, b) and torch.equal(a, c) and b.data_ptr() == c.data_ptr()
+        assert a.is_contiguous() and a.clone().tolist() == a.tolist()
+    # writing one leaves the others
+    keep = [x.clone() for x in new]
+    for i, x in enumerate(new):
+        x.fill_(-9)
+        assert all(torch.equal(a, b) for a, b in zip(new[i + 1:], keep[i + 1:]))
