@@ -802,8 +802,11 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   tc::fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
 
+  // (where all items are one-token items computed apart, the tiles' roles have nothing to do: 0.2 us less)
+  const bool tiles = !kOne || sm.share[0].total > 0;
   // All roles of all warps are done: tensor memory may be released, and the tiles' places copied into again.
   auto roles_done = [&] {
+    if (!tiles) return;
     tc::fence_before();
     if (kFp8) fence_proxy_async_smem();  // (bf16: either there are other items, or one-token items)
     __syncwarp();
@@ -940,7 +943,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       }
     }
     if (lane == 0) a.cuts[blockIdx.x] = cut;
-    if (ok && ca_wait(&sm.info_empty[nitem % kCaInfo], ((nitem / kCaInfo) & 1) ^ 1, err, 804) && lane == 0) {
+    if (tiles && ok && ca_wait(&sm.info_empty[nitem % kCaInfo], ((nitem / kCaInfo) & 1) ^ 1, err, 804) && lane == 0) {
       sm.info[nitem % kCaInfo] = CaItem{0, 0, 0, 0, 0, 0, 0, 0};
       mbar_arrive(&sm.info_full[nitem % kCaInfo]);
     }
@@ -971,7 +974,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     const bool leader = ca_elect();
     int base = 0, nq = 0;         // blocks and Q tiles of the items before
     uint32_t pcount[2] = {0, 0};  // P tiles taken
-    bool ok = true;
+    bool ok = tiles;
     for (int n = 0; ok; ++n) {
       const int is = n % kCaInfo;
       if (!(ok = ca_wait(&sm.info_full[is], (n / kCaInfo) & 1, err, 810))) break;
@@ -1075,7 +1078,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       nq += dual ? 2 : 1;
     }
     // every product has finished before tensor memory is released
-    if (leader) {
+    if (leader && tiles) {
       tc::commit(&sm.done);
       mbar_wait(&sm.done, 0, err, 815);
     }
@@ -1091,7 +1094,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     const uint32_t scol = lanes + 128 * wg, ocol = lanes + kCaOCol + 128 * wg;
     int base = 0;
     uint32_t scount = 0, ocount = 0, xcount = 0;
-    bool ok = true;
+    bool ok = tiles;
     for (int n = 0; ok; ++n) {
       const int is = n % kCaInfo;
       if (!(ok = ca_wait(&sm.info_full[is], (n / kCaInfo) & 1, err, 820))) break;
@@ -1292,7 +1295,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     // eight different 16-byte banks of the swizzled tiles.
     const int i8 = wt & 7, odd = i8 >> 2, piece = (i8 & 3) + 4 * (((wt >> 3) & 1) ^ odd), row0 = 2 * (wt >> 4) + odd;
     int base = 0, nq = 0;
-    bool ok = true;
+    bool ok = tiles;
     // the item's queries
     auto widen_q = [&](int ntok) {
       for (int q = 0; q < (ntok > 8 ? 2 : 1) && ok; ++q, ++nq) {
