@@ -1490,24 +1490,6 @@ static bool ca_encode_kv(CUtensorMap* map, const void* base, cuuint64_t slots, b
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A launch as a programmatic dependent of the kernel before it on the stream: the launch overlaps that kernel's end, and
-// nothing is read or written before it has completed (griddepcontrol.wait).
-template <class... Params, class... Args>
-static cudaError_t ca_launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t bytes,
-                                       cudaStream_t stream, const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <bool kFp8, bool kOne>
 static cudaError_t ca_launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, const CaArgs& a,
                              cudaStream_t stream) {
@@ -1517,7 +1499,7 @@ static cudaError_t ca_launch(const CUtensorMap& qmap, const CUtensorMap& kmap, c
                                                  static_cast<int>(bytes));
       e != cudaSuccess)
     return e;
-  return ca_launch_dependent(chunk_attend_kernel<kFp8, kOne>, dim3(kNumSMs), CaShape<kFp8>::kThreads, bytes, stream, qmap, kmap,
+  return launch_dependent(chunk_attend_kernel<kFp8, kOne>, dim3(kNumSMs), CaShape<kFp8>::kThreads, bytes, stream, qmap, kmap,
                              vmap, a);
 }
 
@@ -1561,7 +1543,7 @@ cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream) {
                                                   : ca_launch<false, false>(qmap, kmap, vmap, a, stream);
       e != cudaSuccess)
     return e;
-  return ca_launch_dependent(chunk_join_kernel, dim3(kNumSMs * (a.rows / kGroup + (L.kv_fp8 ? 1 : 0))), kCaJoinThreads, 0,
+  return launch_dependent(chunk_join_kernel, dim3(kNumSMs * (a.rows / kGroup + (L.kv_fp8 ? 1 : 0))), kCaJoinThreads, 0,
                              stream, a);
 }
 

@@ -154,4 +154,22 @@ cudaError_t launch_wait_check(DevError* err, long long* waits_ns, cudaStream_t s
 msa_status run_gather(const void* src, const int64_t* rows, long long n, long long row_bytes, void* dst,
                       cudaStream_t stream, bool scatter);
 
+// A launch as a programmatic dependent of the kernel before it on the stream: the launch overlaps that kernel's end, and
+// nothing is read or written before it has completed (griddepcontrol.wait).
+template <class... Params, class... Args>
+inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t bytes,
+                                    cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace msa

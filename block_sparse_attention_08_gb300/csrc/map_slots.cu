@@ -76,6 +76,9 @@ __global__ void __launch_bounds__(kMsThreads) map_slots_kernel(SlotsLaunch a, in
   const int tid = threadIdx.x;
   const long long row0 = static_cast<long long>(blockIdx.x) * rows;
   const long long row1 = min(a.capacity, row0 + rows);
+  // the kernel before has completed; the next may be launched behind this one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   long long free_top = *a.num_free;
   if (free_top < 0 || free_top > a.free_capacity) free_top = 0;
   // the id of the j-th opened page, -1 if the stack holds a bad one
@@ -169,8 +172,8 @@ cudaError_t launch_map_slots(const SlotsLaunch& L, cudaStream_t stream) {
   if (const cudaError_t e0 = launch_prologue(); e0 != cudaSuccess) return e0;
   constexpr long long kOnce = static_cast<long long>(kMsCtas) * kMsThreads;
   const long long rows = (L.capacity + kOnce - 1) / kOnce * kMsThreads, grid = (L.capacity + rows - 1) / rows;
-  map_slots_kernel<<<static_cast<unsigned>(grid), kMsThreads, 0, stream>>>(L, static_cast<int>(rows));
-  return cudaGetLastError();
+  return launch_dependent(map_slots_kernel, dim3(static_cast<unsigned>(grid)), kMsThreads, 0, stream, L,
+                          static_cast<int>(rows));
 }
 
 }  // namespace msa

@@ -110,6 +110,9 @@ __global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constan
     fence_mbar_init();
   }
   __syncthreads();
+  // the kernel before has completed; the next may be launched behind this one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long t0 = blockIdx.x;
   const int n = static_cast<int>((a.tokens - t0 + gridDim.x - 1) / gridDim.x);  // tokens of this CTA
   auto token = [&](int i) { return t0 + static_cast<long long>(i) * gridDim.x; };
@@ -271,8 +274,7 @@ cudaError_t launch_rotary(const RotaryLaunch& L, cudaStream_t stream) {
   // as many CTAs as fit an SM's shared memory (and its threads: six of 320), each through its share of the tokens
   const int per_sm = std::min(6, 228 * 1024 / (bytes + 3584));
   const long long grid = std::min<long long>(L.tokens, static_cast<long long>(kNumSMs) * per_sm);
-  rotary_kernel<<<static_cast<unsigned>(grid), kRoThreads, bytes, stream>>>(L, geo);
-  return cudaGetLastError();
+  return launch_dependent(rotary_kernel, dim3(static_cast<unsigned>(grid)), kRoThreads, bytes, stream, L, geo);
 }
 
 }  // namespace msa
