@@ -573,34 +573,13 @@ def msa_rotary_insert(q, k, v, positions, inv_freq, slots, k_cache, v_cache, *, 
     return r if type(r) is not int else _fail("msa_rotary_insert", r)
 
 
-class _Rotary(torch.autograd.Function):
-    """The rotation as an autograd function: its gradient is the rotation back (so it can be
-    differentiated again)."""
-
-    @staticmethod
-    def forward(ctx, q, k, positions, inv_freq, axes, interleaved, inverse):
-        ctx.save_for_backward(positions, inv_freq)
-        ctx.form = axes, interleaved, not inverse
-        return msa_rotary(q, k, positions, inv_freq, axes=axes, interleaved=interleaved, inverse=inverse)
-
-    @staticmethod
-    def backward(ctx, gq, gk):
-        gq, gk = gq.contiguous(), gk.contiguous()
-        if torch.is_grad_enabled():
-            dq, dk = _Rotary.apply(gq, gk, *ctx.saved_tensors, *ctx.form)
-        else:
-            positions, inv_freq = ctx.saved_tensors
-            axes, interleaved, inverse = ctx.form
-            dq, dk = msa_rotary(gq, gk, positions, inv_freq, axes=axes, interleaved=interleaved, inverse=inverse)
-        return dq, dk, None, None, None, None, None
-
-
 def rotary(q, k, positions, inv_freq, *, axes=None, interleaved=False):
     """Differentiable rotary positions: (q, k) rotated as by :func:`msa_rotary`; q and k receive
-    gradients through the same kernel turning back."""
+    gradients through the same kernel turning back (which can be differentiated again)."""
     if k is None:
         raise TypeError("rotary takes q and k (msa_rotary takes q alone)")
-    return _Rotary.apply(q, k, positions, inv_freq, axes, bool(interleaved), False)
+    r = (_ext or _serving()).rotary_autograd(q, k, positions, inv_freq, axes, interleaved)
+    return r if type(r) is tuple else _fail("msa_rotary", r)
 
 
 def msa_attend_chunk(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, *, scale=None, out=None, lse=None,

@@ -15,10 +15,13 @@
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <atomic>
 #include <cmath>
+#include <cstring>
+#include <stdexcept>
 #include <sstream>
 #include <string>
 
@@ -34,6 +37,10 @@ struct Raise {
   std::string text;
 };
 struct Raised {};  // one that Python has set already
+struct Refused : std::runtime_error {  // a call that libmsa refused
+  explicit Refused(msa_status st) : std::runtime_error(std::string("libmsa: ") + msa_status_string(st)), status(st) {}
+  msa_status status;
+};
 
 using Sizes = std::initializer_list<int64_t>;
 
@@ -181,6 +188,8 @@ PyObject* entry(const char* name, Py_ssize_t have, Py_ssize_t want, F body) {
   } catch (const Raise& e) {
     PyErr_SetString(e.type, e.text.c_str());
   } catch (const Raised&) {
+  } catch (const Refused& e) {
+    return PyLong_FromLong(e.status);
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
@@ -329,6 +338,65 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The rotation as an autograd function: its gradient is the rotation back (so it can be differentiated again).
+struct Rotary : torch::autograd::Function<Rotary> {
+  static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx, const at::Tensor& q,
+                                                const at::Tensor& k, const at::Tensor& positions,
+                                                const at::Tensor& inv_freq, const msa_rotary_config& rot, bool inverse) {
+    ctx->save_for_backward({positions, inv_freq});
+    ctx->saved_data["rot"] = std::string(reinterpret_cast<const char*>(&rot), sizeof(rot));
+    ctx->saved_data["inverse"] = inverse;
+    return turn(q, k, positions, inv_freq, rot, inverse);
+  }
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
+                                                 torch::autograd::variable_list grads) {
+    const auto saved = ctx->get_saved_variables();
+    msa_rotary_config rot;
+    std::memcpy(&rot, ctx->saved_data["rot"].toStringRef().data(), sizeof(rot));
+    const bool inverse = !ctx->saved_data["inverse"].toBool();
+    // (a gradient may come in any layout, and begin anywhere)
+    auto dense = [](const at::Tensor& t) {
+      const at::Tensor c = t.contiguous();
+      return reinterpret_cast<uintptr_t>(c.const_data_ptr()) % 16 ? c.clone() : c;
+    };
+    const at::Tensor gq = dense(grads[0]), gk = dense(grads[1]);
+    torch::autograd::variable_list out = c10::GradMode::is_enabled() ? apply(gq, gk, saved[0], saved[1], rot, inverse)
+                                      : turn(gq, gk, saved[0], saved[1], rot, inverse);
+    out.resize(6);  // none for the other arguments
+    return out;
+  }
+  static torch::autograd::variable_list turn(const at::Tensor& q, const at::Tensor& k, const at::Tensor& positions,
+                                             const at::Tensor& inv_freq, const msa_rotary_config& rot, bool inverse) {
+    const c10::cuda::CUDAGuard guard(q.get_device());
+    const at::Tensor qo = at::empty(q.sizes(), q.options()), ko = at::empty(k.sizes(), k.options());
+    const int64_t tokens = q.size(0);
+    auto stride = [&](const at::Tensor& t) { return tokens == 1 ? t.size(1) * kD : t.stride(0); };
+    const msa_status st =
+        msa_rotary(&rot, q.const_data_ptr(), stride(q), static_cast<int>(q.size(1)), k.const_data_ptr(), stride(k),
+                   static_cast<int>(k.size(1)), positions.const_data_ptr<int32_t>(), inv_freq.const_data_ptr<float>(),
+                   tokens, inverse, qo.data_ptr(), ko.data_ptr(), c10::cuda::getCurrentCUDAStream(q.get_device()).stream());
+    if (st != MSA_OK) throw Refused(st);
+    return {qo, ko};
+  }
+};
+
+// q, k, positions, inv_freq, axes, interleaved
+PyObject* rotary_autograd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("rotary_autograd", n, 6, [&]() -> PyObject* {
+    const at::Tensor &q = tensor_of(a[0], "q", 3), &k = tensor_of(a[1], "k", 3);
+    const at::Tensor &positions = tensor(a[2], "positions"), &inv_freq = tensor_of(a[3], "inv_freq", 1);
+    const msa_rotary_config rot = rotary_form(positions, inv_freq, a[4], a[5]);
+    const c10::DeviceIndex d = device_of(q, "q");
+    const int64_t tokens = q.size(0);
+    token_stride(q, "q", tokens, -1, d);
+    token_stride(k, "k", tokens, -1, d);
+    fit_angles(positions, inv_freq, tokens, d);
+    if (tokens < 1) return PyLong_FromLong(MSA_ERR_SHAPE);
+    const auto out = Rotary::apply(q, k, positions, inv_freq, rot, false);
+    return pack({out[0], out[1]});
+  });
+}
+
 // A pair of caches [slots, 4, 128]: whether they hold E4M3 bytes.
 bool fit_caches(const at::Tensor& k, const at::Tensor& v, c10::DeviceIndex d) {
   const at::ScalarType type = k.scalar_type();
@@ -428,7 +496,7 @@ using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
 PyMethodDef method(const char* name, Fast f) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
 }
-PyMethodDef kMethods[] = {method("map_slots", map_slots), method("rotary", rotary),
+PyMethodDef kMethods[] = {method("map_slots", map_slots), method("rotary", rotary), method("rotary_autograd", rotary_autograd),
                           method("rotary_insert", rotary_insert), method("attend_chunk", attend_chunk),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "msa_serving", nullptr, -1, kMethods};

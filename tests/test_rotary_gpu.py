@@ -216,3 +216,37 @@ def test_captured_backward():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_gradient_of_one_output_and_refusals():
+    gen = torch.Generator("cuda").manual_seed(9)
+    q = torch.randn(5, 64, 128, generator=gen, device="cuda").bfloat16().requires_grad_()
+    k = torch.randn(5, 4, 128, generator=gen, device="cuda").bfloat16().requires_grad_()
+    pos = torch.arange(5, device="cuda", dtype=torch.int32)
+    inv = torch.ones(16, device="cuda")
+    qo, ko = msa.rotary(q, k, pos, inv)
+    g = torch.randn(5, 64, 128, generator=gen, device="cuda").bfloat16()
+    gq, gk = torch.autograd.grad(qo, (q, k), g, allow_unused=True)
+    assert torch.equal(gq, msa.msa_rotary(g, None, pos, inv, inverse=True)[0])
+    assert gk is None or not gk.any()
+    # a gradient that is one value for all, and one of another layout
+    gq, gk = torch.autograd.grad(msa.rotary(q, k, pos, inv), (q, k),
+                                 (torch.ones(1, 1, 1, device="cuda").bfloat16().expand(5, 64, 128),
+                                  torch.ones(128, 4, 5, device="cuda").bfloat16().permute(2, 1, 0)))
+    one = msa.msa_rotary(torch.ones_like(q), torch.ones_like(k), pos, inv, inverse=True)
+    assert torch.equal(gq, one[0]) and torch.equal(gk, one[1])
+    odd = torch.randn(5 * 64 * 128 + 3, generator=gen, device="cuda").bfloat16()[3:].view(5, 64, 128)  # 6 bytes off
+    (gq,) = torch.autograd.grad(msa.rotary(q, k, pos, inv)[0], q, odd)
+    assert torch.equal(gq, msa.msa_rotary(odd.clone(), None, pos, inv, inverse=True)[0])
+    with torch.no_grad():
+        assert not msa.rotary(q, k, pos, inv)[0].requires_grad
+    with pytest.raises(msa.MsaError):
+        msa.rotary(q, k, pos, torch.ones(12, device="cuda"))  # 24 dims: not a multiple of 16
+    with pytest.raises(msa.MsaError):
+        msa.rotary(q, k, pos.repeat(5, 1), inv)  # five axes
+    with pytest.raises(ValueError):
+        msa.rotary(q, k.cpu(), pos, inv)
+    with pytest.raises(TypeError):
+        msa.rotary(q, None, pos, inv)
+    # refused calls leave no error behind
+    assert torch.equal(msa.rotary(q, k, pos, inv)[0], qo)
