@@ -125,10 +125,11 @@ struct CaShape {
   static constexpr int kWiden = kFp8 ? 4 : 0;  // widening warps
   static constexpr int kThreads = 32 * (kCaWidenWarp + kWiden);
   // registers per thread of the roles, out of the launch's 168 (384 threads) or 128 (512 threads) a thread:
-  // 256 * 216 + 128 * 72 = 384 * 168, and 256 * 200 + 256 * 56 = 512 * 128.  (With 184 the softmax of E4M3 chunks cost 5%.
+  // 256 * 216 + 128 * 72 = 384 * 168, and 256 * 208 + 128 * 56 + 128 * 40 = 512 * 128.  (With 184 for the softmax, E4M3
+  // chunks took 6% more.
   // Two widening warps in the issuing warps' group leave it 216: chunks 1% faster, but items of few tokens, bound by the
   // widening, made 17 mixed requests 126 us instead of 115.)
-  static constexpr int kRegsSoftmax = kFp8 ? 200 : 216, kRegsIssue = kFp8 ? 56 : 72;
+  static constexpr int kRegsSoftmax = kFp8 ? 208 : 216, kRegsIssue = kFp8 ? 56 : 72, kRegsWiden = 40;
   // fp16 weights are kept near the top of their range (at most 2^(kLift + kCaSlack) = 2^15), so that small ones
   // stay normal down to 2^-21 of the largest
   static constexpr float kLift = kFp8 ? 7.f : 0.f;
@@ -814,7 +815,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   };
   // A wait that gives up (recorded in the error word) ends its role, so a broken pipeline ends after one bounded wait
   // per role.
-  if (warp >= 8) ca_regs_down<Shape::kRegsIssue>();
+  if (warp >= 8 && warp < kCaWidenWarp) ca_regs_down<Shape::kRegsIssue>();
   if (warp == kCaProducerWarp) {
     // ---------------- the share's items, and their copies ----------------
     const long long total = sm.share[0].total, ctas = sm.share[0].ctas, u0 = sm.share[0].u0, u1 = sm.share[0].u1;
@@ -1202,8 +1203,8 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
             }
             l += sum;
           };
-          if (masked) block(std::true_type{});
-          else block(std::false_type{});
+          if (!masked) block(std::false_type{});
+          else block(std::true_type{});
           tc::wait_st();
         }
         tc::fence_before();
@@ -1289,6 +1290,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       if (sm.apart) ca_one_attend<kFp8>(a, sm, warp);
   } else if (kFp8 && warp >= kCaWidenWarp) {
     // ---------------- E4M3 pages and bf16 queries to fp16 ----------------
+    ca_regs_down<Shape::kRegsWiden>();
     constexpr int kLanes = 128, kStep = kLanes / 8;  // kStep: rows at once
     const int wt = tid - 32 * kCaWidenWarp;
     // Eight lanes take 16-byte pieces of two neighbouring rows, the odd row's from the other half: they read and write
@@ -1336,20 +1338,20 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         const uint32_t src = smem_u32(sm.raw[kFp8 ? rs : 0]) + sw128(row0, piece);
         const uint32_t dst = smem_u32(sm.kv[st]) + (piece >> 2) * kCaHalf;
         const uint32_t dst0 = dst + sw128(row0, 2 * (piece & 3)), dst1 = dst + sw128(row0, 2 * (piece & 3) + 1);
-        // four rows at a time, the next four asked for before
-        constexpr int kBatches = kBlock / kStep / 4;
-        uint4 x[2][4];
+        // two rows at a time, the next two asked for before
+        constexpr int kBatches = kBlock / kStep / 2;
+        uint4 x[2][2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[0][q] = lds128(src + q * kStep * 128);
+        for (int q = 0; q < 2; ++q) x[0][q] = lds128(src + q * kStep * 128);
         if (!(ok = ca_wait(&sm.kv_empty[st], ((load / kTiles) & 1) ^ 1, err, 832))) break;
 #pragma unroll
         for (int n = 0; n < kBatches; ++n) {
           if (n + 1 < kBatches)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[(n + 1) & 1][q] = lds128(src + (4 * n + 4 + q) * kStep * 128);
+            for (int q = 0; q < 2; ++q) x[(n + 1) & 1][q] = lds128(src + (2 * n + 2 + q) * kStep * 128);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int down = (4 * n + q) * kStep;  // rows below row0, a multiple of the swizzle's eight
+          for (int q = 0; q < 2; ++q) {
+            const int down = (2 * n + q) * kStep;  // rows below row0, a multiple of the swizzle's eight
             uint4 v = x[n & 1][q];
             if (keys < kBlock && row0 + down >= keys) v = make_uint4(0u, 0u, 0u, 0u);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
