@@ -44,9 +44,10 @@
 // what is left is the way from S over the softmax to O.  An item costs about two
 // units besides its blocks: 0.5 us for its last O product, 2.4 for its rows'
 // stores, 1 for the first block's softmax, none of it beside other products.
-// An E4M3 cache adds the widening and leaves the softmax fewer registers: 1.38 ms.  Single tokens over long contexts are bound by
-// HBM (64 requests, 4.0 GB: 0.59 ms, 6.8 TB/s), short ones by latency: 4.7 us
-// without any work, 8.2 with one block.
+// An E4M3 cache adds the widening and leaves the softmax fewer registers:
+// 1.38 ms.  Single tokens over long contexts are bound by HBM (64 requests,
+// 4.0 GB: 0.58 ms, 6.9 TB/s), short ones by latency: 4.6 us without any work,
+// 8.2 with one block.
 #include <cuda_fp16.h>
 
 #include <type_traits>
