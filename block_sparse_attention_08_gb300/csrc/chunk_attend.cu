@@ -345,8 +345,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 bytes in one store: a whole sector of the row
-__device__ __forceinline__ void ca_store32(void* p, const uint32_t (&y)[8]) {
+// 32 bytes of a row: where rows begin on 32 bytes (wide) in one store, a whole sector; `out` may begin on 16 bytes
+// only, and then in two.
+__device__ __forceinline__ void ca_store32(void* p, const uint32_t (&y)[8], bool wide) {
+  if (!wide) {
+    stg128(p, y[0], y[1], y[2], y[3]);
+    stg128(static_cast<uint8_t*>(p) + 16, y[4], y[5], y[6], y[7]);
+    return;
+  }
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(y[0]), "r"(y[1]), "r"(y[2]),
                "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
                : "memory");
@@ -1268,7 +1274,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
             uint32_t y[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) y[q] = pack_bf16(o[2 * q], o[2 * q + 1]);
-            ca_store32(a.out + orow * kDim + d, y);
+            ca_store32(a.out + orow * kDim + d, y, (reinterpret_cast<uintptr_t>(a.out) & 31) == 0);
           }
           __syncwarp();
         }
