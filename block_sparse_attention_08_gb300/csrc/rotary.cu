@@ -36,6 +36,7 @@ constexpr int kRoWarps = 9;    // turning warps: four rows each at a time, so 72
 constexpr int kRoStages = 4;
 constexpr int kRoThreads = 32 * (kRoWarps + 1);
 constexpr int kRoRow = kDim * 2;
+constexpr int kRoMaxStage = 2 * kHeads * kRoRow;  // 64 heads of q and of k (with insertion 72 rows and 1 KB)
 
 // (cos, sin) of position * inv_freq.
 __device__ __forceinline__ float2 ro_turn(int position, float inv_freq) {
@@ -267,8 +268,12 @@ cudaError_t launch_rotary(const RotaryLaunch& L, cudaStream_t stream) {
   geo.k_bytes = L.k_heads * kRoRow;
   geo.v_bytes = L.v ? kKvHeads * kRoRow : 0;
   geo.stage = (geo.q_bytes + geo.k_bytes + geo.v_bytes + (L.kv_fp8 ? 2 * kKvHeads * kDim : 0) + 127) / 128 * 128;
-  const int bytes = kRoStages * geo.stage;  // at most 4 x 32 KB
-  if (const cudaError_t e = cudaFuncSetAttribute(rotary_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const int bytes = kRoStages * geo.stage;
+  // The limit belongs to the kernel, not to the call: it is set to the same value by every call, since one thread's smaller
+  // limit between another's setting and launch would refuse that launch.
+  static_assert(kRoMaxStage >= (kHeads + 2 * kKvHeads) * kRoRow + 2 * kKvHeads * kDim, "a stage with insertion");
+  if (const cudaError_t e = cudaFuncSetAttribute(rotary_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kRoStages * kRoMaxStage);
       e != cudaSuccess)
     return e;
   // as many CTAs as fit an SM's shared memory (and its threads: six of 320), each through its share of the tokens

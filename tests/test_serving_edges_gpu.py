@@ -1,6 +1,8 @@
 """Calls of the chunk-serving functions at the borders of what they accept: addresses, threads, frequencies, lengths,
 buffers that change behind autograd."""
+import ctypes
 import math
+import subprocess
 
 import pytest
 import torch
@@ -35,3 +37,60 @@ def test_outputs_that_begin_on_16_bytes(lens, news, fp8):
         assert call(*args, out=out) is out
         assert torch.equal(out, want)
         assert bool((room[:at] == 5).all()) and bool((room[at + want.numel():] == 5).all())
+
+
+HAMMER = r"""
+#include <pthread.h>
+typedef int (*rotary_t)(const void*, const void*, long long, int, const void*, long long, int, const void*, const void*,
+                        long long, int, void*, void*, void*);
+typedef struct { rotary_t f; const void *rot, *q, *k, *positions, *inv_freq; void *qo, *ko, *stream;
+                 int q_heads, k_heads, tokens, times, refused; } call;
+static void* work(void* p) {
+  call* c = p;
+  for (int i = 0; i < c->times; ++i)
+    c->refused += c->f(c->rot, c->q, 128 * c->q_heads, c->q_heads, c->k, 128 * c->k_heads, c->k_heads, c->positions,
+                       c->inv_freq, c->tokens, 0, c->qo, c->ko, c->stream) != 0;
+  return 0;
+}
+void hammer(call* c, int n) {
+  pthread_t t[8];
+  for (int i = 0; i < n; ++i) pthread_create(&t[i], 0, work, &c[i]);
+  for (int i = 0; i < n; ++i) pthread_join(t[i], 0);
+}
+"""
+
+
+class _Call(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("f", "rot", "q", "k", "positions", "inv_freq", "qo", "ko", "stream")] + \
+               [(n, ctypes.c_int) for n in ("q_heads", "k_heads", "tokens", "times", "refused")]
+
+
+def test_rotary_of_different_head_counts_from_several_threads(tmp_path):
+    # shared memory of 2, 72 and 128 KB in turn; without the interpreter between the calls
+    (tmp_path / "hammer.c").write_text(HAMMER)
+    subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-pthread", str(tmp_path / "hammer.c"), "-o", str(tmp_path / "h.so")],
+                   check=True)
+    hammer = ctypes.CDLL(str(tmp_path / "h.so")).hammer
+    lib = msa.load()
+    rot = msa.binding.msa_rotary_config(128, 0, 1)
+    gen = torch.Generator("cuda").manual_seed(0)
+    pos = torch.randint(1000, (5,), generator=gen, device="cuda", dtype=torch.int32)
+    inv = torch.rand(64, generator=gen, device="cuda")
+    heads = ((1, 1), (64, 64), (64, 4))
+    calls, data, streams = (_Call * 3)(), [], [torch.cuda.Stream() for _ in heads]
+    for c, s, (qh, kh) in zip(calls, streams, heads):
+        x = [torch.randn(5, h, 128, generator=gen, device="cuda").bfloat16() for h in (qh, kh)]
+        y = [torch.empty_like(a) for a in x]
+        data.append((x, y))
+        c.f = ctypes.cast(lib.msa_rotary, ctypes.c_void_p).value
+        c.rot = ctypes.addressof(rot)
+        c.q, c.k, c.qo, c.ko = (a.data_ptr() for a in x + y)
+        c.positions, c.inv_freq, c.stream = pos.data_ptr(), inv.data_ptr(), s.cuda_stream
+        c.q_heads, c.k_heads, c.tokens, c.times = qh, kh, 5, 500
+    torch.cuda.synchronize()
+    for _ in range(20):
+        hammer(calls, 3)
+        torch.cuda.synchronize()
+    assert [c.refused for c in calls] == [0, 0, 0]
+    for x, y in data:
+        assert all(torch.equal(a, b) for a, b in zip(msa.msa_rotary(*x, pos, inv), y))
