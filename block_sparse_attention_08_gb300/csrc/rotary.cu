@@ -8,10 +8,13 @@
 // The angle of a far position keeps nothing of its fraction in fp32, so it is
 // reduced to a fraction of a turn before it is rounded: with u = inv_freq /
 // (2 pi) as a sum of two floats (exact products by fused multiply-adds), the
-// position times u loses less than 2^-25 of a turn as long as the position is
-// a float; one from 2^24 on takes the product in binary64.  Sine and cosine are
-// those of that fraction, once per token and pair, shared by all heads; the
-// rotation is fp32, rounded once to the output type.
+// position times u is a sum of two floats, whose whole turns are dropped.  Below
+// 2^20 turns, for a position that is a float, the last sum's rounding is 2^-25 of
+// a turn and the others together less than 2^-25; a position from 2^24 on, or
+// more turns, takes the product in pairs of binary64 (1 / (2 pi) to 106 bits).
+// Either way the fraction is within 2^-24 of a turn, for |inv_freq| up to 2^32.
+// Sine and cosine are those of that fraction, once per token and pair, shared by
+// all heads; the rotation is fp32, rounded once to the output type.
 //
 // Each row is read once and written once: bound by HBM.  A CTA takes every
 // gridDim-th token through a ring of stages in shared memory: a producer warp
@@ -42,15 +45,17 @@ constexpr int kRoMaxStage = 2 * kHeads * kRoRow;  // 64 heads of q and of k (wit
 __device__ __forceinline__ float2 ro_turn(int position, float inv_freq) {
   // 1 / (2 pi) as the sum of two floats
   constexpr float kHi = 0.15915494f, kLo = static_cast<float>(0.15915494309189535 - static_cast<double>(kHi));
+  const float p = static_cast<float>(position);
+  const float u = inv_freq * kHi, u_lo = fmaf(inv_freq, kLo, fmaf(inv_freq, kHi, -u)), t = p * u;
   float turns;
-  if (abs(position) < (1 << 24)) {
-    const float p = static_cast<float>(position);
-    const float u = inv_freq * kHi, u_lo = fmaf(inv_freq, kLo, fmaf(inv_freq, kHi, -u));
-    const float t = p * u, t_lo = fmaf(p, u_lo, fmaf(p, u, -t));
+  if (position > -(1 << 24) && position < (1 << 24) && fabsf(t) < 0x1p20f) {
+    const float t_lo = fmaf(p, u_lo, fmaf(p, u, -t));  // less than 2^-2
     turns = (t - rintf(t)) + t_lo;
   } else {
-    const double t = static_cast<double>(position) * inv_freq * 0.15915494309189535;
-    turns = static_cast<float>(t - rint(t));
+    constexpr double kHi2 = 0x1.45f306dc9c883p-3, kLo2 = -0x1.6b01ec5417056p-57;
+    const double f = inv_freq, x = position * f, x_lo = fma(static_cast<double>(position), f, -x);
+    const double y = x * kHi2, y_lo = fma(x, kLo2, fma(x, kHi2, -y)) + x_lo * kHi2;  // at most 2^9 (|y| < 2^61)
+    turns = static_cast<float>((y - rint(y)) + (y_lo - rint(y_lo)));
   }
   float s, c;
   sincospif(2.f * turns, &s, &c);

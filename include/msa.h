@@ -514,8 +514,9 @@ msa_status msa_map_slots(const int32_t* seq_lens, const int32_t* new_lens, int b
  * interleaved.  Pair j turns by positions[axis[j]][t] * inv_freq[j]:
  *   a' = a cos - b sin, b' = a sin + b cos;
  * the dims from rot_dim on pass unchanged.  The angle is reduced to a fraction of
- * a turn before it is rounded (so a position of a million keeps its fraction), the
- * rotation is computed in fp32 and rounded once.
+ * a turn before it is rounded, so every int32 position keeps its fraction: it is
+ * within 2^-24 of a turn for |inv_freq| up to 2^32.  The rotation is computed in
+ * fp32 and rounded once.
  * rot_dim: a multiple of 16 in [16, 128]; 1 <= num_axes <= 4; axis[j] < num_axes
  * for j < rot_dim / 2. */
 typedef struct {

@@ -3,6 +3,7 @@ buffers that change behind autograd."""
 import ctypes
 import math
 import subprocess
+from fractions import Fraction
 
 import pytest
 import torch
@@ -94,3 +95,24 @@ def test_rotary_of_different_head_counts_from_several_threads(tmp_path):
     assert [c.refused for c in calls] == [0, 0, 0]
     for x, y in data:
         assert all(torch.equal(a, b) for a, b in zip(msa.msa_rotary(*x, pos, inv), y))
+
+
+def test_angles_of_any_position_and_frequency():
+    # (cos, sin) against whole-number arithmetic.  Tolerance: half a bf16 step of the value, 2^-8, and the angle: 2^-24 of a
+    # turn is 2^-21.3 in the value, the functions' and the rotation's own errors below 2^-22: 2^-20.5 in all.
+    two_pi = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+    inv = torch.tensor([2.0 ** e for e in (-30, -10, -3, -1, 0)] + [1.5, 3.7, 100.0, 9876.54321, 1e6, 1.23e9, 2.0 ** 32],
+                       device="cuda")
+    inv = torch.cat([inv, inv[:4] * 0.777])  # 16 pairs
+    gen = torch.Generator().manual_seed(0)
+    positions = [0, 1, -1, 2 ** 24 - 1, 2 ** 24, 2 ** 24 + 1, -2 ** 24, 2 ** 31 - 1, -2 ** 31]
+    positions += [int(torch.randint(2 ** (e - 1), 2 ** e, (1,), generator=gen)) for e in range(2, 32) for _ in range(6)]
+    x = torch.zeros(len(positions), 1, 128, dtype=torch.bfloat16, device="cuda")
+    x[..., :16] = 1
+    y = msa.msa_rotary(x, None, S.ints(positions), inv)[0][:, 0].double().cpu()
+    for t, p in enumerate(positions):
+        for j, f in enumerate(inv.tolist()):
+            turns = p * Fraction(f) / two_pi
+            angle = float((turns - round(turns)) * two_pi)
+            for got, want in ((y[t, j], math.cos(angle)), (y[t, j + 16], math.sin(angle))):
+                assert abs(float(got) - want) <= 2.0 ** -8 * abs(want) + 2.0 ** -20.5, (p, f)
