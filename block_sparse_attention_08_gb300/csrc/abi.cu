@@ -561,7 +561,8 @@ static msa_status attend_chunk(const msa_config* cfg, const void* q, const void*
   if (batch < 1 || max_blocks < 1 || max_blocks > 0x7fffffff / kBlock || total_tokens < 1 ||
       total_tokens >= (1LL << 31) || num_slots < 1 || num_slots >= (1LL << 31) || num_slots % kBlock)
     return MSA_ERR_SHAPE;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return MSA_ERR_SHAPE;
+  // A score's factor has to be a normal number too: an infinite one makes NaN of a score of zero, a zero one of a masked key.
+  if (!(scale > 0.f) || !std::isnormal(chunk_scale_log2(scale, k_scale))) return MSA_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return MSA_ERR_ALIGN;
   if ((st = check_ws(workspace, workspace_bytes, chunk_scratch_offset() + attend_chunk_bytes(total_tokens, max_blocks))) !=
       MSA_OK)

@@ -1527,7 +1527,7 @@ cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream) {
   a.max_blocks = L.max_blocks;
   a.num_pages = static_cast<int>(L.num_slots / kBlock);
   a.tokens = L.tokens;
-  a.scale_log2 = L.scale * 1.4426950408889634f * L.k_scale;
+  a.scale_log2 = chunk_scale_log2(L.scale, L.k_scale);
   a.v_scale = L.v_scale;
   a.out = static_cast<__nv_bfloat16*>(L.out);
   a.lse = L.lse;

@@ -127,6 +127,8 @@ struct ChunkLaunch {
   DevError* err;
 };
 cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream);
+// What it multiplies the products of q and the cache's values by: the score in base 2.
+inline float chunk_scale_log2(float scale, float k_scale) { return scale * 1.4426950408889634f * k_scale; }
 size_t attend_chunk_bytes(long long tokens, int max_blocks);
 // First step of every launcher.  Clears the calling thread's last CUDA error
 // (the launches are checked with cudaGetLastError, which reports the calling

@@ -572,7 +572,8 @@ msa_status msa_rotary_insert(const msa_rotary_config* rot, const void* q, int64_
  *   page_table   dev int32 [batch, max_blocks]
  *   cu_seqlens_q dev int32 [batch + 1], cu_seqlens_q[0] = 0, not decreasing; rows from
  *                cu_seqlens_q[batch] on are not read, and their out and lse not written
- *   scale        finite and > 0
+ *   scale        finite and > 0; scale * log2(e) (E4M3: * k_scale) in fp32, a score's
+ *                factor in base 2, has to be a normal number (else MSA_ERR_SHAPE)
  *   out          dev bf16 [total_tokens, 64, 128]
  *   lse          dev fp32 [total_tokens, 64] or NULL: log2 of the softmax denominator
  *                in the base-2 domain of the scaled scores
