@@ -96,6 +96,13 @@ at::Tensor output(PyObject* o, const char* name, at::ScalarType type, at::IntArr
   return t;
 }
 
+// Tells autograd that a call wrote tensors that the caller had before (undefined ones are skipped): a graph that saved one,
+// as the rotation saves its positions, then refuses its backward instead of reading the new values.
+void changed(std::initializer_list<at::Tensor> written) {
+  for (const at::Tensor& t : written)
+    if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // New outputs of one call as parts of one allocation (four of them took 3 us more): next(type, n) gives the next.
 class Parts {
  public:
@@ -253,7 +260,9 @@ PyObject* map_slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            slots.data_ptr<int64_t>(), positions.data_ptr<int32_t>(), left.data_ptr<int32_t>(), ws.at,
                            ws.bytes, stream);
     });
-    return st == MSA_OK ? pack({cu, slots, positions, left}) : PyLong_FromLong(st);
+    if (st != MSA_OK) return PyLong_FromLong(st);
+    changed({table, cu, slots, positions, left});
+    return pack({cu, slots, positions, left});
   });
 }
 
@@ -334,7 +343,9 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
                         inv_freq.const_data_ptr<float>(), tokens, inverse, qo.data_ptr(),
                         ko.defined() ? ko.data_ptr() : nullptr, stream);
     });
-    return st == MSA_OK ? pack({qo, ko}) : PyLong_FromLong(st);
+    if (st != MSA_OK) return PyLong_FromLong(st);
+    changed({qo, ko});
+    return pack({qo, ko});
   });
 }
 
@@ -435,7 +446,9 @@ PyObject* rotary_insert(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                ko.defined() ? ko.data_ptr() : nullptr, k_cache.data_ptr(), v_cache.data_ptr(), fp8, k_scale,
                                v_scale, k_cache.size(0), ws.at, ws.bytes, stream);
     });
-    return st == MSA_OK ? wrap(qo) : PyLong_FromLong(st);
+    if (st != MSA_OK) return PyLong_FromLong(st);
+    changed({qo, ko, k_cache, v_cache});
+    return wrap(qo);
   });
 }
 
@@ -488,7 +501,9 @@ PyObject* attend_chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  : msa_attend_chunk(&cfg, q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), lp, tp, cp, b, w, tokens,
                                     k.size(0), scale, out.data_ptr(), sp, ws.at, ws.bytes, stream);
     });
-    return st == MSA_OK ? wrap(out) : PyLong_FromLong(st);
+    if (st != MSA_OK) return PyLong_FromLong(st);
+    changed({out, lse});
+    return wrap(out);
   });
 }
 

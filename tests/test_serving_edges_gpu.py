@@ -116,3 +116,53 @@ def test_angles_of_any_position_and_frequency():
             angle = float((turns - round(turns)) * two_pi)
             for got, want in ((y[t, j], math.cos(angle)), (y[t, j + 16], math.sin(angle))):
                 assert abs(float(got) - want) <= 2.0 ** -8 * abs(want) + 2.0 ** -20.5, (p, f)
+
+
+def test_positions_refilled_before_the_backward_are_noticed():
+    # a buffer of positions that the next slot map writes: the rotation back would turn by the wrong angles
+    table, free, num = S.ints([[0, 1]]), S.ints([0, 1]), S.ints([2])
+    new = msa.msa_map_slots(S.ints([9]), S.ints([9]), table, free, num, num_slots=256, capacity=9)
+    again = dict(zip(("cu_seqlens_q", "slots", "positions", "num_free_out"), new))
+    q, k = (torch.ones(9, h, 128, device="cuda").bfloat16().requires_grad_() for h in (64, 4))
+    inv = torch.full((64,), 0.01, device="cuda")
+    out = msa.rotary(q, k, new[2], inv)
+    grads = [torch.ones_like(x) for x in out]
+    torch.autograd.grad(out, (q, k), grads)
+    out = msa.rotary(q, k, new[2], inv)
+    msa.msa_map_slots(S.ints([200]), S.ints([9]), table, free, num, num_slots=256, capacity=9, **again)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(out, (q, k), grads)
+    # a refused call changes nothing
+    out = msa.rotary(q, k, new[2], inv)
+    with pytest.raises(msa.MsaError):
+        msa.msa_map_slots(S.ints([200]), S.ints([9]), table, free, num, num_slots=100, capacity=9, **again)
+    torch.autograd.grad(out, (q, k), grads)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tensors_that_a_call_writes_are_marked_as_changed(fp8):
+    q, k = torch.ones(3, 64, 128, device="cuda").bfloat16(), torch.ones(3, 4, 128, device="cuda").bfloat16()
+    inv, pos, slots = torch.full((64,), 0.01, device="cuda"), S.ints([0, 1, 2]), torch.arange(3, device="cuda")
+    caches = [torch.zeros(128, 4, 128, device="cuda").to(torch.float8_e4m3fn if fp8 else torch.bfloat16) for _ in range(2)]
+    table, cu, lens = S.ints([[0]]), S.ints([0, 3]), S.ints([3])
+    lse = torch.empty(3, 64, device="cuda")
+    qo, ko, out = q.clone(), k.clone(), q.clone()
+    read = [q, k, pos, inv, slots, cu, lens]
+
+    def versions(*x):
+        return [t._version for t in x]
+    before = versions(*read)
+    for call, written in (
+            (lambda: msa.msa_rotary(q, k, pos, inv, q_out=qo, k_out=ko), (qo, ko)),
+            (lambda: msa.msa_rotary_insert(q, k, k, pos, inv, slots, *caches, q_out=qo, k_out=ko), (qo, ko, *caches)),
+            (lambda: msa.msa_rotary_insert(q, k, k, pos, inv, slots, *caches), caches),
+            (lambda: (msa.msa_attend_chunk_fp8kv if fp8 else msa.msa_attend_chunk)(q, *caches, lens, table, cu, out=out, lse=lse),
+             (out, lse)),
+            (lambda: msa.msa_map_slots(lens, lens, table, S.ints([0]), S.ints([1]), num_slots=128, capacity=3), (table,))):
+        was = versions(*written)
+        call()
+        assert all(b > a for a, b in zip(was, versions(*written)))
+    assert versions(*read) == before
+    with torch.inference_mode():  # tensors without a version
+        x = msa.msa_rotary(q.clone(), None, pos, inv, q_out=torch.empty_like(q))[0]
+    assert torch.equal(x, msa.msa_rotary(q, None, pos, inv)[0])
