@@ -1,8 +1,11 @@
-"""Builds libmsa.so (the CUDA kernels and the C ABI) for sm_103a with nvcc, and
-the extension module that calls it for the chunked-serving functions with g++.
+"""Builds libmsa.so (the CUDA kernels and the C ABI) for sm_103a with nvcc, and,
+for the calls that go through it, the extension module of the chunked-serving
+functions with g++.
 
 Both are built in-tree under ``_build/`` so the process that loads them loads
-them from the repository.  Translation units compile in parallel.
+them from the repository.  Translation units compile in parallel.  The module
+needs what libmsa does not (g++, Python's headers, a PyTorch with CUDA), so it
+is built and loaded only where one of its functions is called.
 """
 from __future__ import annotations
 
@@ -12,8 +15,6 @@ import shutil
 import subprocess
 import sysconfig
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
@@ -22,7 +23,7 @@ LIB = os.path.join(BUILD, "libmsa.so")
 SOURCES = ["abi.cu", "decode_select.cu", "sparse_attend.cu", "prefill_select.cu", "prefill_attend.cu", "pack.cu",
            "diag.cu", "index_produce.cu", "map_slots.cu", "rotary.cu", "chunk_attend.cu"]
 EXT_SOURCE = "serving_ext.cpp"
-EXT = os.path.join(BUILD, f"msa_serving-{torch.__version__}.so")  # of this PyTorch
+GXX = "g++"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 
@@ -34,66 +35,80 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libmsa")
 
 
-def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "msa.h"))
-    return files
+def ext_path() -> str:
+    """The extension module of this PyTorch and this Python (it uses the whole interface of both)."""
+    import torch
+    return os.path.join(BUILD, f"msa_serving-{torch.__version__}-{sysconfig.get_config_var('SOABI')}.so")
+
+
+def _stale(built, files) -> bool:
+    return not os.path.exists(built) or any(os.path.getmtime(f) > os.path.getmtime(built) for f in files)
+
+
+def _header():
+    return os.path.join(INCLUDE, "msa.h")
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(EXT):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    """Whether libmsa is."""
+    return not _stale(LIB, [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != EXT_SOURCE] + [_header()])
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+def _run(cmd, what):
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"{what}: {e}") from e
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
+def _link(cmd, to):
+    tmp = to + f".tmp{os.getpid()}"
+    _run([*cmd, "-o", tmp], "link failed")
+    os.replace(tmp, to)
+
+
+def _compile_ext() -> str:
+    import torch
+    home = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, EXT_SOURCE.replace(".cpp", ".o"))
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    _run([GXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in include),
+          "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj], f"{GXX} failed on {EXT_SOURCE}")
+    return obj
+
+
+def build(force: bool = False, verbose: bool = False, serving: bool = False) -> str:
+    """Builds what is missing or stale of libmsa and, with ``serving``, of the extension module."""
+    lib = force or not up_to_date()
+    ext = serving and (force or _stale(ext_path(), [os.path.join(CSRC, EXT_SOURCE), _header()]))
+    if not lib and not ext:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    nvcc = _nvcc()
 
     def compile_one(src):
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        cmd = [nvcc, *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        out = _run([_nvcc(), *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj], f"nvcc failed on {src}")
         if verbose:
-            print(r.stdout + r.stderr)
+            print(out)
         return obj
-
-    home = os.path.dirname(torch.__file__)
-
-    def compile_ext():
-        obj = os.path.join(BUILD, EXT_SOURCE.replace(".cpp", ".o"))
-        include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
-                   sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
-               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in include),
-               "-c", os.path.join(CSRC, EXT_SOURCE), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on {EXT_SOURCE}:\n{r.stdout}\n{r.stderr}")
-        return obj
-
-    def link(cmd, to):
-        tmp = to + f".tmp{os.getpid()}"
-        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, to)
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ext = ex.submit(compile_ext)
-        objs = list(ex.map(compile_one, SOURCES))
-    link([nvcc, *ARCH, "-shared", *objs], LIB)
-    # the extension finds libmsa beside itself, and PyTorch's libraries where the process has loaded them
-    link(["g++", "-shared", ext.result(), f"-L{BUILD}", "-l:libmsa.so", "-Wl,-rpath,$ORIGIN",
-          f"-L{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
-          "-lc10_cuda"], EXT)
+        ext_obj = ex.submit(_compile_ext) if ext else None
+        if lib:
+            _link([_nvcc(), *ARCH, "-shared", *ex.map(compile_one, SOURCES)], LIB)
+        if ext:
+            import torch
+            # the module finds libmsa beside itself, and PyTorch's libraries where the process has loaded them
+            _link([GXX, "-shared", ext_obj.result(), f"-L{BUILD}", "-l:libmsa.so", "-Wl,-rpath,$ORIGIN",
+                   f"-L{os.path.join(os.path.dirname(torch.__file__), 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                   "-ltorch_cuda", "-lc10", "-lc10_cuda"], ext_path())
     return LIB
 
 
 if __name__ == "__main__":
-    print(build(force=True, verbose=True))
+    print(build(force=True, verbose=True, serving=True))

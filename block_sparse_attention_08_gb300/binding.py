@@ -529,11 +529,15 @@ _ext = None
 
 
 def _serving():
-    """The extension module, built with the library."""
+    """The extension module, built where it is missing or stale.  Raises when it cannot be built or loaded: there is no
+    other path (the other calls do without it)."""
     global _ext
-    if _ext is None:
-        load()
-        spec = importlib.util.spec_from_file_location("msa_serving", _build.EXT)
+    load()
+    with _lock:
+        if _ext is not None:
+            return _ext
+        _build.build(serving=True)
+        spec = importlib.util.spec_from_file_location("msa_serving", _build.ext_path())
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         _ext = module

@@ -1,9 +1,15 @@
 """Borders of the chunk-serving calls that need no GPU."""
 import ctypes
+import os
+import subprocess
+import sys
+import sysconfig
 
 import pytest
+import torch
 
 import block_sparse_attention_08_gb300 as msa
+from block_sparse_attention_08_gb300 import _build, binding
 from block_sparse_attention_08_gb300.binding import msa_config
 
 OK, NULL, SHAPE, DTYPE, WORKSPACE, ALIGN = 0, 1, 2, 3, 4, 5
@@ -28,3 +34,31 @@ def test_a_score_factor_that_is_no_normal_number_is_refused(lib):
                                  (0.088, 1e-38, SHAPE), (0.088, 3e38, WORKSPACE), (10.0, 3e38, SHAPE)):
         assert lib.msa_attend_chunk_fp8kv(ctypes.byref(cfg), FAKE, FAKE, FAKE, k_scale, 1.0, *tail, scale, FAKE, None, FAKE, 0,
                                           None) == code, (scale, k_scale)
+
+
+def test_the_other_calls_do_without_the_extension_module(monkeypatch):
+    # no g++ and no module of this PyTorch and Python: libmsa loads, and only a call that needs the module raises
+    monkeypatch.setattr(_build, "GXX", "no-such-compiler")
+    monkeypatch.setattr(_build, "ext_path", lambda: os.path.join(_build.BUILD, "no-such-module.so"))
+    for name in ("_lib", "_ext"):
+        monkeypatch.setattr(binding, name, None)
+    assert _build.build() == _build.LIB and _build.up_to_date()
+    assert msa.make_config().topk == 16
+    x, i = torch.zeros(4, 64, 128, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(RuntimeError, match="no-such-compiler"):
+        msa.msa_rotary(x, None, i, torch.zeros(64))
+    assert msa.make_config().topk == 16
+
+
+def test_the_extension_module_is_named_after_python_too():
+    name = os.path.basename(_build.ext_path())
+    assert torch.__version__ in name and sysconfig.get_config_var("SOABI") in name
+
+
+def test_libmsa_builds_without_pytorch():
+    # (the package itself takes torch tensors; its build does not)
+    code = ("import sys, importlib.util as u; sys.modules['torch'] = None; "
+            f"s = u.spec_from_file_location('b', {_build.__file__!r}); m = u.module_from_spec(s); s.loader.exec_module(m); "
+            "print(m.build())")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == _build.LIB, r.stderr
