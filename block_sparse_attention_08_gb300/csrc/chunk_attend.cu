@@ -1064,8 +1064,9 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         }
       }
       ok = __all_sync(0xffffffffu, ok);
-      const int lv = 2 * base + 2 * nb - 1, sv = lv % kTiles, keys = keys_of(nb - 1);
+      const int lv = 2 * base + 2 * nb - 1, sv = lv % kTiles;
       ok = ok && ca_wait(&sm.kv_full[sv], (lv / kTiles) & 1, err, 816);
+      const int keys = keys_of(nb - 1);  // (the block's flag, written before its copies were asked for: behind the wait)
       if (!kFp8 && ok && (keys & 15)) {
         // V rows behind the last key, up to the end of their 16-row step: their weight is zero, but they may hold
         // anything, so they become zero too (the whole warp)

@@ -11,6 +11,7 @@ import torch
 import block_sparse_attention_08_gb300 as msa
 from block_sparse_attention_08_gb300 import _build, binding
 from block_sparse_attention_08_gb300.binding import msa_config
+from _kernel_consts import _source
 
 OK, NULL, SHAPE, DTYPE, WORKSPACE, ALIGN = 0, 1, 2, 3, 4, 5
 FAKE = 0x10000  # 256-byte aligned, never read: every call below is refused first
@@ -62,3 +63,12 @@ def test_libmsa_builds_without_pytorch():
             "print(m.build())")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == _build.LIB, r.stderr
+
+
+def test_the_last_blocks_flag_is_read_behind_the_wait_for_its_tile():
+    # every lane of the issuing warp reads the flag that the producer wrote before the block's copies: only a lane's own
+    # wait for the copies orders its read
+    text = _source("chunk_attend.cu")
+    a = text.index("const int lv = 2 * base + 2 * nb - 1")
+    part = text[a:text.index("fence_proxy_async_smem", a)]
+    assert 0 < part.index("ca_wait(&sm.kv_full[sv]") < part.index("keys_of(nb - 1)")
