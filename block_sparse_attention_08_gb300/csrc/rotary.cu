@@ -155,11 +155,11 @@ __global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constan
       return true;
     };
     bool ok = true;
-    int i = 0;
+    int filled = 0;  // tokens asked for
     for (int base = 0; base < n + kRoStages && ok; base += kRoStages) {
 #pragma unroll
       for (int s = 0; s < kRoStages; ++s) {
-        i = base + s;
+        const int i = base + s;
         if (i >= n + kRoStages || !ok) break;
         if (i >= kRoStages && i - kRoStages < n) ok = copy_out(i - kRoStages, slots[s]);
         if (!ok || i >= n) continue;
@@ -191,13 +191,14 @@ __global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constan
             tma_bulk_g2s(st + geo.q_bytes + geo.k_bytes, static_cast<const __nv_bfloat16*>(a.v) + t * a.v_stride,
                          geo.v_bytes, &full[s]);
         }
+        ++filled;
         __syncwarp();
       }
     }
-    // after a wait that gave up: the last fills may still be landing
+    // after a wait that gave up: the last fill of each stage may still be landing
     if (!ok)
       for (int s = 0; s < kRoStages; ++s) {
-        const int fills = (min(i + 1, n) - s + kRoStages - 1) / kRoStages;
+        const int fills = (filled - s + kRoStages - 1) / kRoStages;
         if (fills > 0) ro_wait(&full[s], (fills - 1) & 1, a.err, 852);
       }
     if (lane == 0) bulk_wait_all();
