@@ -87,6 +87,14 @@ __device__ __forceinline__ void ro_copy_out(void* dst, const void* src, uint32_t
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                : "memory");
 }
+// NaN in a token's rows of q_out and k_out (the whole warp): 16 bytes, eight bf16 NaN, at a time.
+__device__ __noinline__ void ro_mark(void* q_out, int q_bytes, void* k_out, int k_bytes, long long t) {
+  constexpr uint32_t kNan = 0x7fff7fffu;
+  const int lane = threadIdx.x & 31;
+  for (int o = 16 * lane; o < q_bytes; o += 16 * 32) stg128(static_cast<uint8_t*>(q_out) + t * q_bytes + o, kNan, kNan, kNan, kNan);
+  if (k_out)
+    for (int o = 16 * lane; o < k_bytes; o += 16 * 32) stg128(static_cast<uint8_t*>(k_out) + t * k_bytes + o, kNan, kNan, kNan, kNan);
+}
 // A bounded wait; the error word may be missing.
 __device__ __forceinline__ bool ro_wait(uint64_t* bar, uint32_t parity, DevError* err, int where) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -133,6 +141,7 @@ __global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constan
     int p0 = at0[t0], p1 = at1[t0];
     long long slots[kRoStages];  // of the tokens in flight
     const bool insert = a.k_cache != nullptr;
+    int out = 0;  // tokens copied out
     // copies token i's stage out
     auto copy_out = [&](int i, long long slot) {
       const int s = i % kRoStages;
@@ -152,6 +161,7 @@ __global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constan
         }
         bulk_commit();
       }
+      ++out;
       return true;
     };
     bool ok = true;
@@ -195,12 +205,15 @@ __global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constan
         __syncwarp();
       }
     }
-    // after a wait that gave up: the last fill of each stage may still be landing
-    if (!ok)
+    if (!ok) {
+      // after a wait that gave up: the last fill of each stage may still be landing, and the tokens that were not copied out
+      // get NaN rows (a call without an error word shows it there)
       for (int s = 0; s < kRoStages; ++s) {
         const int fills = (filled - s + kRoStages - 1) / kRoStages;
         if (fills > 0) ro_wait(&full[s], (fills - 1) & 1, a.err, 852);
       }
+      for (int j = out; j < n; ++j) ro_mark(a.q_out, geo.q_bytes, a.k_out, geo.k_bytes, token(j));
+    }
     if (lane == 0) bulk_wait_all();
   } else {
     // ---------------- turning warps ----------------

@@ -534,6 +534,8 @@ typedef struct {
  *   inverse   1 turns by the negative angle: the backward, dq from q_out's gradient
  *   q_out     dev bf16 [tokens, q_heads, 128] dense; may be q itself where q is dense
  *             (no other overlap); k_out likewise
+ * A bounded on-chip wait that gives up (a hardware failure: this call has no error word,
+ * msa_rotary_insert's reads MSA_DEVERR_TIMEOUT) leaves NaN in the rows it did not write.
  * Errors: MSA_ERR_NULL, MSA_ERR_SHAPE, MSA_ERR_ALIGN, MSA_ERR_CUDA. */
 msa_status msa_rotary(const msa_rotary_config* rot, const void* q, int64_t q_stride, int q_heads,
                       const void* k, int64_t k_stride, int k_heads, const int32_t* positions,

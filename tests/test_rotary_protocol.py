@@ -32,6 +32,13 @@ def last_fills(filled):
     return [eval(e, {"filled": filled, "s": s, "kRoStages": STAGES}) for s in range(STAGES)]
 
 
+def marks():
+    """Whether the producer's branch behind a wait that gave up marks the rows of the tokens that were not copied out."""
+    a = TEXT.index("    if (!ok)")
+    return "for (int j = out; j < n; ++j) ro_mark(a.q_out, geo.q_bytes, a.k_out, geo.k_bytes, token(j));" in \
+        TEXT[a:TEXT.index("bulk_wait_all();", a)]
+
+
 class Bar:
     def __init__(self, n):
         self.n, self.pending, self.done = n, n, 0
@@ -51,7 +58,7 @@ class Sim:
         self.table = [None] * STAGES         # the token whose angles a stage holds
         self.readers = [0] * STAGES
         self.loads, self.copies = [], []     # (stage, token) on its way in; a copy out
-        self.out = []                        # tokens copied out
+        self.out, self.nan = [], []          # tokens copied out, tokens whose rows are marked
 
     def wait(self, bar, need, token):
         """Until `need` phases are done, seen as the kernel sees them: by the parity of the last of them.  `token`: whose
@@ -65,7 +72,7 @@ class Sim:
         return ok
 
     def producer(self):
-        filled, ok = 0, True
+        filled, out, ok = 0, 0, True
         for i in range(self.n + STAGES):
             s = i % STAGES
             if i >= STAGES and i - STAGES < self.n:
@@ -74,6 +81,7 @@ class Sim:
                 if not ok:
                     break
                 self.copies.append((s, i - STAGES))
+                out += 1
             if i >= self.n:
                 continue
             assert not self.readers[s] or self.mistake, "a table rewritten while it is read"
@@ -91,6 +99,7 @@ class Sim:
                     last = self.wait(self.full[s], fills, 0)
                     last.doomed = s + (fills - 1) * STAGES == self.lost
                     yield last
+            self.nan += range(out, self.n) if marks() else []
         while self.copies:  # (not a bounded wait either)
             yield lambda: not self.copies
 
@@ -180,3 +189,13 @@ def test_an_end_without_the_last_wait_is_reported():
         except AssertionError:
             reported += 1
     assert reported >= 10, f"reported in {reported} of 40 runs"
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_a_token_that_was_not_copied_out_is_marked(seed):
+    # no row is left as it was: it is turned, or NaN
+    rng = random.Random(seed)
+    n = rng.randint(1, 30)
+    sim = Sim(n, rng, lost=rng.randrange(n)).run()
+    assert sorted(sim.out + sim.nan) == list(range(n))
+    assert not Sim(n, rng).run().nan
