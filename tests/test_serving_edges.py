@@ -1,6 +1,7 @@
 """Borders of the chunk-serving calls that need no GPU."""
 import ctypes
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -11,7 +12,7 @@ import torch
 import block_sparse_attention_08_gb300 as msa
 from block_sparse_attention_08_gb300 import _build, binding
 from block_sparse_attention_08_gb300.binding import msa_config
-from _kernel_consts import _source
+from _kernel_consts import _source, kconst
 
 OK, NULL, SHAPE, DTYPE, WORKSPACE, ALIGN = 0, 1, 2, 3, 4, 5
 FAKE = 0x10000  # 256-byte aligned, never read: every call below is refused first
@@ -72,3 +73,16 @@ def test_the_last_blocks_flag_is_read_behind_the_wait_for_its_tile():
     a = text.index("const int lv = 2 * base + 2 * nb - 1")
     part = text[a:text.index("fence_proxy_async_smem", a)]
     assert 0 < part.index("ca_wait(&sm.kv_full[sv]") < part.index("keys_of(nb - 1)")
+
+
+def test_the_rotary_grid_is_resident_at_once(tmp_path):
+    # the CTAs per SM that the launch counts on have to fit its 65536 registers and 2048 threads (registers are given to a
+    # warp in units of 8 a thread)
+    r = subprocess.run([_build._nvcc(), *_build.ARCH, *_build.FLAGS, "-Xptxas", "-v", "-c",
+                        os.path.join(_build.CSRC, "rotary.cu"), "-o", str(tmp_path / "rotary.o")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    regs = max(int(x) for x in re.findall(r"Used (\d+) registers", r.stderr))
+    threads = kconst("kRoThreads", "rotary.cu")
+    per_sm = re.search(r"per_sm = std::min\((\w+),", _source("rotary.cu")).group(1)
+    per_sm = int(per_sm) if per_sm.isdigit() else kconst(per_sm, "rotary.cu")
+    assert per_sm * threads <= 2048 and per_sm * threads * (-(-regs // 8) * 8) <= 65536, (per_sm, regs)
