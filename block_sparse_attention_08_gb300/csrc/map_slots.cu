@@ -57,6 +57,9 @@ __device__ __forceinline__ MsSum ms_scan(MsSum x, MsSum* warp_sums, MsSum* total
   return MsSum{before.tokens + s.tokens - x.tokens, before.pages + s.pages - x.pages};
 }
 
+// Pages of n positions (n + kBlock - 1 may pass 2^31).
+__device__ __forceinline__ int ms_pages(int n) { return static_cast<int>((static_cast<unsigned>(n) + kBlock - 1) / kBlock); }
+
 // The last i < n with a[i] <= x (a[0] <= x).
 __device__ __forceinline__ int ms_last_le(const int* a, int n, int x) {
   int lo = 0, hi = n - 1;
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kMsThreads) map_slots_kernel(SlotsLaunch a, in
          t += kMsThreads) {
       const int i = ms_last_le(cu, m, static_cast<int>(t));
       const int p = old[i] + static_cast<int>(t) - cu[i];
-      const int page = p / kBlock, have = (old[i] + kBlock - 1) / kBlock;
+      const int page = p / kBlock, have = ms_pages(old[i]);
       int id;
       if (page >= have) {
         id = opened(off[i] + page - have);
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(kMsThreads) map_slots_kernel(SlotsLaunch a, in
     // this CTA's opened pages among the pass's
     for (int j = off[0] + blockIdx.x * kMsThreads + tid; j < off[m]; j += gridDim.x * kMsThreads) {
       const int i = ms_last_le(off, m, j);
-      const int page = (old[i] + kBlock - 1) / kBlock + j - off[i];
+      const int page = ms_pages(old[i]) + j - off[i];
       a.page_table[static_cast<long long>(r0 + i) * a.max_blocks + page] = opened(j);
     }
     cut = cut || m < n;

@@ -166,3 +166,23 @@ def test_tensors_that_a_call_writes_are_marked_as_changed(fp8):
     with torch.inference_mode():  # tensors without a version
         x = msa.msa_rotary(q.clone(), None, pos, inv, q_out=torch.empty_like(q))[0]
     assert torch.equal(x, msa.msa_rotary(q, None, pos, inv)[0])
+
+
+def test_slots_of_the_longest_requests():
+    # lengths up to 2^31 - 1: a table of 2^24 pages; the pages of an old length next to 2^31
+    width = 2 ** 24
+    table = torch.full((2, width), 3, dtype=torch.int32, device="cuda")
+    longest = 2 ** 31 - 1
+    # request 0's token lies in a page that it holds; request 1's open its last page
+    lens, news, free = S.ints([longest, longest]), S.ints([1, 200]), S.ints([7, 5])
+    ws = msa.Workspace(256)
+    cu, slots, positions, left = msa.msa_map_slots(lens, news, table, free, S.ints([2]), num_slots=1024, capacity=201, workspace=ws)
+    assert ws.read_device_error() == (0, 0)
+    assert cu.tolist() == [0, 1, 201] and int(left) == 1
+    at = [longest - 1] + list(range(longest - 200, longest))
+    assert positions.tolist() == at
+    pages = [3] + [5 if p // 128 == width - 1 else 3 for p in at[1:]]
+    assert slots.tolist() == [i * 128 + p % 128 for i, p in zip(pages, at)]
+    assert int(table[1, -1]) == 5
+    table[1, -1] = 3
+    assert bool((table == 3).all())
