@@ -3,6 +3,7 @@ buffers that change behind autograd."""
 import ctypes
 import math
 import subprocess
+import threading
 from fractions import Fraction
 
 import pytest
@@ -186,3 +187,95 @@ def test_slots_of_the_longest_requests():
     assert int(table[1, -1]) == 5
     table[1, -1] = 3
     assert bool((table == 3).all())
+
+
+def test_calls_from_several_threads_at_once():
+    # four threads, a stream each, all kinds of calls in turn: each gets the results of calls made one at a time
+    def work(seed):
+        lens, news = [700 + 300 * seed, 40, 3000], [1 + 5 * seed, 1, 17]
+        table, pool = S.page_table(lens, seed=seed)
+        gen = torch.Generator("cuda").manual_seed(seed)
+        t = sum(news)
+        qkv = torch.randn(t, 72, 128, generator=gen, device="cuda").bfloat16()
+        dt = torch.float8_e4m3fn if seed % 2 else torch.bfloat16
+        k_cache, v_cache = (torch.randn(pool * 128, 4, 128, generator=gen, device="cuda").to(dt) for _ in range(2))
+        inv = torch.rand(64, generator=gen, device="cuda")
+        out = []
+        for _ in range(12):
+            cu, slots, pos, left = msa.msa_map_slots(S.ints(lens), S.ints(news), table, S.ints([0]), S.ints([0]),
+                                                     num_slots=pool * 128, capacity=t)
+            q = msa.msa_rotary_insert(qkv[:, :64], qkv[:, 64:68], qkv[:, 68:], pos, inv, slots, k_cache, v_cache)
+            a, b = q[:, :8 + seed].detach().clone().requires_grad_(), qkv[:, 64:65 + seed].detach().clone().requires_grad_()
+            y = msa.rotary(a, b, pos, inv)
+            out += [cu, slots, pos, left, q, *y, *torch.autograd.grad(y, (a, b), [x * 2 for x in y]),
+                    (msa.msa_attend_chunk_fp8kv if seed % 2 else msa.msa_attend_chunk)(q, k_cache, v_cache, S.ints(lens), table, cu)]
+        torch.cuda.current_stream().synchronize()
+        return out
+
+    want, got = [work(i) for i in range(4)], [None] * 4
+
+    def on_thread(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got[i] = work(i)
+        except BaseException as e:  # told on the test's thread
+            got[i] = e
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=on_thread, args=(i,)) for i in range(4)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    for w, g in zip(want, got):
+        assert not isinstance(g, BaseException), g
+        assert len(w) == len(g) and all(torch.equal(a, b) for a, b in zip(w, g))
+
+
+def test_transforms_that_the_rotation_does_not_have_are_refused():
+    pos, inv = S.ints([0, 1, 2]), torch.ones(64, device="cuda")
+    x = torch.ones(2, 3, 4, 128, device="cuda").bfloat16()
+    with pytest.raises(RuntimeError):
+        torch.vmap(lambda a: msa.rotary(a, a, pos, inv)[0])(x)
+    with torch.autograd.forward_ad.dual_level():
+        with pytest.raises(RuntimeError):
+            msa.rotary(torch.autograd.forward_ad.make_dual(x[0], x[1]), x[0], pos, inv)
+    assert torch.isfinite(msa.rotary(x[0], x[0], pos, inv)[0]).all()
+
+
+def test_a_captured_step_refilled_between_replays():
+    # a captured serving step whose lengths, tables and positions change between replays, a workspace given by its caller
+    lens, news, width, pool = [100, 300], [3, 1], 8, 16
+    gen = torch.Generator("cuda").manual_seed(5)
+    seq, new = S.ints(lens), S.ints(news)
+    table, free = torch.full((2, width), -1, dtype=torch.int32, device="cuda"), torch.randperm(pool, generator=gen, device="cuda").int()
+    left = S.ints([pool])
+    caches = [torch.full((pool * 128, 4, 128), math.nan, device="cuda").bfloat16() for _ in range(2)]
+    cap = 8
+    qkv = torch.empty(cap, 72, 128, dtype=torch.bfloat16, device="cuda")
+    inv = torch.rand(64, generator=gen, device="cuda")
+    ws = msa.Workspace(msa.workspace_size(msa.make_config(), 4, 512, width))
+
+    def step(rows, x):
+        cu, slots, pos, now = msa.msa_map_slots(seq, new, table, free, left, num_slots=pool * 128, capacity=rows, workspace=ws)
+        q = msa.msa_rotary_insert(x[:, :64], x[:, 64:68], x[:, 68:], pos, inv, slots, *caches, workspace=ws)
+        out = msa.msa_attend_chunk(q, *caches, seq, table, cu, workspace=ws)
+        left.copy_(now)
+        return q, out, cu
+    # the prompts, eagerly
+    new.copy_(seq)
+    step(400, torch.randn(400, 72, 128, generator=gen, device="cuda").bfloat16())
+    torch.cuda.synchronize()
+    graph, saved = torch.cuda.CUDAGraph(), [x.clone() for x in (left, table)]
+    with torch.cuda.graph(graph):
+        q, out, cu = step(cap, qkv)
+    left.copy_(saved[0]), table.copy_(saved[1])
+    for news in ([3, 1], [1, 1], [1, 7], [5, 0], [1, 1]):
+        lens = [n + m for n, m in zip(lens, news)]
+        seq.copy_(S.ints(lens)), new.copy_(S.ints(news))
+        qkv.copy_(torch.randn(cap, 72, 128, generator=gen, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ws.read_device_error()[0] == 0 and cu.tolist() == S.offsets(news).tolist()
+        t = sum(news)
+        ref = S.attend(q[:t], *caches, lens, table, cu, SCALE)
+        S.check_attend(out[:t], None, ref, max(lens), 8)
