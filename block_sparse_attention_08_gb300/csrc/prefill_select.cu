@@ -449,8 +449,10 @@ cudaError_t launch_prefill_select(const msa_config& cfg, const void* index_q, co
   int* level_cnt = level_base + max_tiles;
   int* n_tiles = level_cnt + max_tiles;
   const size_t plan_smem = (3 * static_cast<size_t>(max_tiles) + 2) * sizeof(int);
-  if (plan_smem > 200 * 1024) return cudaErrorInvalidValue;  // the ABI rejects longer documents first
-  cudaFuncSetAttribute(prefill_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(plan_smem));
+  constexpr int kPlanSmem = 200 * 1024;
+  if (plan_smem > kPlanSmem) return cudaErrorInvalidValue;  // the ABI rejects longer documents first
+  // (the limit is the kernel's, not the call's: a value of this call's own would refuse a longer one of another thread's)
+  cudaFuncSetAttribute(prefill_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanSmem);
   prefill_plan_kernel<<<1, 1024, plan_smem, stream>>>(cu_seqlens, num_docs, max_tiles, sorted_docs, level_base,
                                                       level_cnt, n_tiles, err);
   cudaError_t e = cudaGetLastError();
