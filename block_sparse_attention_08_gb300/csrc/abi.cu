@@ -602,7 +602,8 @@ msa_status msa_attend_chunk_fp8kv(const msa_config* cfg, const void* q, const vo
                                   const int32_t* cu_seqlens_q, int batch, int max_blocks, int64_t total_tokens,
                                   int64_t num_slots, float scale, void* out, float* lse, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-  if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+  // a row's factor is v_scale over its denominator, at most 2^15 for each of 2^31 keys: it stays a normal number
+  if (!(k_scale > 0.f) || !(v_scale >= 0x1p-80f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
     return MSA_ERR_SHAPE;
   return attend_chunk(cfg, q, k_cache, v_cache, 1, k_scale, v_scale, seq_lens, page_table, cu_seqlens_q, batch,
                       max_blocks, total_tokens, num_slots, scale, out, lse, workspace, workspace_bytes, stream);

@@ -600,9 +600,10 @@ msa_status msa_attend_chunk(const msa_config* cfg, const void* q, const void* k_
                             void* stream);
 
 /* The same over an FP8 cache: k_cache, v_cache dev uint8 [num_slots, 4, 128],
- * E4M3 bytes standing for k_scale * k and v_scale * v (finite, > 0), as
- * msa_sparse_attend_decode_fp8kv: the E4M3 values and q enter fp16 products (q
- * is exact for |q| in 2^-14 .. 65504), the softmax weights in fp16. */
+ * E4M3 bytes standing for k_scale * k and v_scale * v (finite, k_scale > 0,
+ * v_scale >= 2^-80, else MSA_ERR_SHAPE), as msa_sparse_attend_decode_fp8kv: the
+ * E4M3 values and q enter fp16 products (q is exact for |q| in 2^-14 .. 65504; a
+ * larger one becomes infinite, and its rows NaN), the softmax weights in fp16. */
 msa_status msa_attend_chunk_fp8kv(const msa_config* cfg, const void* q, const void* k_cache,
                                   const void* v_cache, float k_scale, float v_scale,
                                   const int32_t* seq_lens, const int32_t* page_table,

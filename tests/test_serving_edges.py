@@ -38,6 +38,15 @@ def test_a_score_factor_that_is_no_normal_number_is_refused(lib):
                                           None) == code, (scale, k_scale)
 
 
+def test_a_value_scale_too_small_for_a_rows_factor_is_refused(lib):
+    # v_scale over a denominator of up to 2^46 has to be a normal number: one of 1e-38 kept five bits of it
+    cfg = msa_config()
+    lib.msa_config_default(ctypes.byref(cfg))
+    tail = [FAKE, FAKE, FAKE, 4, 9, 100, 1280, 0.088, FAKE, None, FAKE, 0, None]
+    for v_scale, code in ((1e-38, SHAPE), (2.0 ** -81, SHAPE), (2.0 ** -80, WORKSPACE), (3e38, WORKSPACE)):
+        assert lib.msa_attend_chunk_fp8kv(ctypes.byref(cfg), FAKE, FAKE, FAKE, 1.0, v_scale, *tail) == code, v_scale
+
+
 def test_the_other_calls_do_without_the_extension_module(monkeypatch):
     # no g++ and no module of this PyTorch and Python: libmsa loads, and only a call that needs the module raises
     monkeypatch.setattr(_build, "GXX", "no-such-compiler")
