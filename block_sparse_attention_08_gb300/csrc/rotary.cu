@@ -142,11 +142,14 @@ __global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constan
     int p0 = at0[t0], p1 = at1[t0];
     long long slots[kRoStages];  // of the tokens in flight
     const bool insert = a.k_cache != nullptr;
-    int out = 0;  // tokens copied out
+    int out = 0;  // where a wait gave up: tokens copied out
     // copies token i's stage out
     auto copy_out = [&](int i, long long slot) {
       const int s = i % kRoStages;
-      if (!__all_sync(0xffffffffu, ro_wait(&done[s], (i / kRoStages) & 1, a.err, 850))) return false;
+      if (!__all_sync(0xffffffffu, ro_wait(&done[s], (i / kRoStages) & 1, a.err, 850))) {
+        out = i;
+        return false;
+      }
       if (lane == 0) {
         const long long t = token(i);
         const uint8_t* st = stages + s * geo.stage;
@@ -162,11 +165,9 @@ __global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constan
         }
         bulk_commit();
       }
-      ++out;
       return true;
     };
     bool ok = true;
-    int filled = 0;  // tokens asked for
     for (int base = 0; base < n + kRoStages && ok; base += kRoStages) {
 #pragma unroll
       for (int s = 0; s < kRoStages; ++s) {
@@ -202,13 +203,13 @@ __global__ void __launch_bounds__(kRoThreads) rotary_kernel(const __grid_constan
             tma_bulk_g2s(st + geo.q_bytes + geo.k_bytes, static_cast<const __nv_bfloat16*>(a.v) + t * a.v_stride,
                          geo.v_bytes, &full[s]);
         }
-        ++filled;
         __syncwarp();
       }
     }
     if (!ok) {
       // after a wait that gave up: the last fill of each stage may still be landing, and the tokens that were not copied out
       // get NaN rows (a call without an error word shows it there)
+      const int filled = min(out + kRoStages, n);  // tokens asked for: a stage is filled again once it has been copied out
       for (int s = 0; s < kRoStages; ++s) {
         const int fills = (filled - s + kRoStages - 1) / kRoStages;
         if (fills > 0) ro_wait(&full[s], (fills - 1) & 1, a.err, 852);

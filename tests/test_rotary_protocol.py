@@ -25,8 +25,11 @@ def count(barrier):
     return int(e) if e.isdigit() else kconst(e, FILE)
 
 
-def last_fills(filled):
-    """Fills of each stage that the producer waits for after a wait that gave up, by the kernel's expression."""
+def last_fills(out, n):
+    """Fills of each stage that the producer waits for after a wait that gave up, by the kernel's expressions: `out` of n
+    tokens have been copied out."""
+    e = re.search(r"const int filled = ([^;]+);", TEXT).group(1)
+    filled = eval(e, {"out": out, "n": n, "kRoStages": STAGES, "min": min})
     e = re.search(r"const int fills = ([^;]+);", TEXT).group(1).replace("/", "//")
     assert "filled" in e
     return [eval(e, {"filled": filled, "s": s, "kRoStages": STAGES}) for s in range(STAGES)]
@@ -93,7 +96,7 @@ class Sim:
             self.loads.append((s, i))
             filled += 1
         if not ok:
-            for s, fills in enumerate(last_fills(filled)):
+            for s, fills in enumerate(last_fills(out, self.n)):
                 if fills > 0 and self.mistake != "no last wait":
                     assert fills == len(range(s, filled, STAGES)), f"stage {s}: waits for fill {fills}"
                     last = self.wait(self.full[s], fills, 0)
