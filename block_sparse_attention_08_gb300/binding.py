@@ -523,7 +523,8 @@ def msa_index_produce_decode(index_q, index_k, index_k_cache, seq_lens, page_tab
 # tensors, whatever the current one is, and share no scratch between calls (the attention
 # takes its own from the caching allocator), so calls on several streams or threads and
 # several captured graphs do not meet.  Without ``workspace`` a device error goes to a
-# word that nothing reads: pass a ``Workspace`` to read it.
+# word that nothing reads: pass a ``Workspace`` to read it.  Tensors that a call writes
+# for its caller are marked as changed for autograd.
 
 _ext = None
 
@@ -552,7 +553,9 @@ def msa_map_slots(seq_lens, new_lens, page_table, free_pages, num_free, *, num_s
                   slots=None, positions=None, num_free_out=None, workspace=None):
     """Opens the pages of each request's new tokens (written into ``page_table``) and maps the
     tokens to slots (C: msa_map_slots): returns (cu_seqlens_q int32 [batch + 1], slots int64
-    [capacity], positions int32 [capacity], num_free_out int32 [1])."""
+    [capacity], positions int32 [capacity], num_free_out int32 [1]).  That pages or rows ran out
+    (MSA_DEVERR_FULL), or a length or page is bad, can be read from ``workspace`` alone, a
+    ``Workspace`` of 256 bytes or more; without one it shows only in cu_seqlens_q and slots."""
     r = (_ext or _serving()).map_slots(seq_lens, new_lens, page_table, free_pages, num_free, num_slots, capacity,
                                        cu_seqlens_q, slots, positions, num_free_out, _buf(workspace))
     return r if type(r) is tuple else _fail("msa_map_slots", r)
@@ -561,7 +564,8 @@ def msa_map_slots(seq_lens, new_lens, page_table, free_pages, num_free, *, num_s
 def msa_rotary(q, k, positions, inv_freq, *, axes=None, interleaved=False, inverse=False, q_out=None, k_out=None):
     """Rotary positions on q [tokens, heads, 128] and k (or None): returns (q_out, k_out)
     (C: msa_rotary).  ``positions`` int32 [tokens] or [axes, tokens], ``inv_freq`` fp32 [pairs],
-    ``axes`` the axis of each pair (default: all 0), ``inverse`` turns back (the gradient)."""
+    ``axes`` the axis of each pair (default: all 0), ``inverse`` turns back (the gradient).  The
+    outputs carry no gradient: :func:`rotary` is differentiable."""
     r = (_ext or _serving()).rotary(q, k, positions, inv_freq, axes, interleaved, inverse, q_out, k_out)
     return r if type(r) is tuple else _fail("msa_rotary", r)
 
@@ -571,7 +575,7 @@ def msa_rotary_insert(q, k, v, positions, inv_freq, slots, k_cache, v_cache, *, 
     """Rotary positions on q [tokens, 64, 128] and k [tokens, 4, 128], with the rotated k and v
     written at ``slots`` (int64 [tokens], -1: not inserted) of the paged caches, bf16 or E4M3
     standing for scale * value; returns q_out (C: msa_rotary_insert).  ``k_out`` (optional)
-    receives the rotated k as well."""
+    receives the rotated k as well.  Slots outside the cache are skipped and told to ``workspace``."""
     r = (_ext or _serving()).rotary_insert(q, k, v, positions, inv_freq, slots, k_cache, v_cache, axes, interleaved,
                                            k_scale, v_scale, q_out, k_out, _buf(workspace))
     return r if type(r) is not int else _fail("msa_rotary_insert", r)
@@ -579,7 +583,8 @@ def msa_rotary_insert(q, k, v, positions, inv_freq, slots, k_cache, v_cache, *, 
 
 def rotary(q, k, positions, inv_freq, *, axes=None, interleaved=False):
     """Differentiable rotary positions: (q, k) rotated as by :func:`msa_rotary`; q and k receive
-    gradients through the same kernel turning back (which can be differentiated again)."""
+    gradients through the same kernel turning back (which can be differentiated again).  Positions
+    that are written before the backward make it raise."""
     if k is None:
         raise TypeError("rotary takes q and k (msa_rotary takes q alone)")
     r = (_ext or _serving()).rotary_autograd(q, k, positions, inv_freq, axes, interleaved)
@@ -591,7 +596,9 @@ def msa_attend_chunk(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, *,
     """bf16 out [tokens, 64, 128]: each request's new tokens (rows cu_seqlens_q[r] ..) attend to all
     their keys in the paged cache (C: msa_attend_chunk).  ``lse`` (fp32 [tokens, 64], optional)
     receives the log2 of the softmax denominators.  Rows from cu_seqlens_q[-1] on are left as they
-    are."""
+    are.  Bad lengths and pages are told to ``workspace`` (at least ``workspace_size(cfg, 4, tokens,
+    page_table.shape[1])`` bytes); a request with bad lengths gets zeros and lse -inf.  A bf16 decode
+    step does best with as many rows of q as requests."""
     r = (_ext or _serving()).attend_chunk(False, q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, 1.0, 1.0,
                                           scale, out, lse, _buf(workspace))
     return r if type(r) is not int else _fail("msa_attend_chunk", r)

@@ -39,8 +39,9 @@
 // shares costs: it is done where all items have one token (17 mixed requests
 // took 0.118 ms with two kinds, 0.095 with one).
 //
-// Chunks are bound on chip.  2048 tokens over 32k keys take 1.22 to 1.25 ms in
-// bf16 (1.7 PFLOP/s, tensor pipe 74% active, 90% of a library product's rate):
+// Chunks are bound on chip.  2048 tokens over 32k keys take 1.22 ms in bf16 (1.7
+// PFLOP/s, tensor pipe 74% active, 92% of a library product's rate), and 1.31 to
+// 1.35 ms in a row, where power bounds the clock:
 // what is left is the way from S over the softmax to O.  An item costs about two
 // units besides its blocks: 0.5 us for its last O product, 2.4 for its rows'
 // stores, 1 for the first block's softmax, none of it beside other products.

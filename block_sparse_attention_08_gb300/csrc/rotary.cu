@@ -25,9 +25,10 @@
 // lie there, or from the E4M3 bytes that the warps leave beside them) to the
 // caches' slots.  So no thread holds data that is on its way, and an SM has
 // kRoStages tokens of each of its CTAs in flight, 18 KB each.  16384 tokens with
-// insertion (604 MB): 99 us, 6.1 TB/s; 8191 into E4M3 caches (294 MB): 53 us,
-// 5.5 TB/s; forward and backward of 16384 (1.14 GB): 193 us, 5.9 TB/s; 64
-// tokens: 4.1 us.
+// insertion (604 MB): 98 us, 6.2 TB/s; 8191 into E4M3 caches (294 MB): 51.5 us,
+// 5.7 TB/s; forward and backward of 16384 (1.14 GB): 195 us, 5.9 TB/s; 64
+// tokens: 3.6 us.  With few heads a CTA's producer, a token after the other,
+// bounds it (65536 tokens of 8 + 1 heads, 302 MB: 210 us).
 #include <algorithm>
 
 #include "launch.h"
@@ -298,7 +299,7 @@ cudaError_t launch_rotary(const RotaryLaunch& L, cudaStream_t stream) {
       e != cudaSuccess)
     return e;
   // As many CTAs as are resident at once, by registers and shared memory, each through its share of the tokens.  (Six where
-  // shared memory held six: 600 tokens of 8 + 1 heads 6.3 us instead of 4.9, 65536 tokens 204 us either way.)
+  // shared memory held six: 600 tokens of 8 + 1 heads 6.3 us instead of 5.0, 65536 tokens 204 us either way.)
   const int per_sm = std::min(kRoResident, 228 * 1024 / (bytes + 3584));
   const long long grid = std::min<long long>(L.tokens, static_cast<long long>(kNumSMs) * per_sm);
   return launch_dependent(rotary_kernel, dim3(static_cast<unsigned>(grid)), kRoThreads, bytes, stream, L, geo);

@@ -543,8 +543,8 @@ msa_status msa_rotary(const msa_rotary_config* rot, const void* q, int64_t q_str
                       void* stream);
 
 /* The same rotation of q (64 heads) and k (4 heads), with the rotated k and v
- * written at slots[t] of the paged caches; a row with a negative slot is not
- * inserted, and no other slot is touched.  Two rows with the same slot leave
+ * written at slots[t] of the paged caches; a row with a negative slot is rotated
+ * into q_out (and k_out) but not inserted, and no other slot is touched.  Two rows with the same slot leave
  * either's values, or some of each, there.
  *   v         dev bf16 [tokens, 4, 128], v_stride as q_stride
  *   slots     dev int64 [tokens]; one outside the cache is skipped and recorded
@@ -591,6 +591,8 @@ msa_status msa_rotary_insert(const msa_rotary_config* rot, const void* q, int64_
  * the unrounded weights.  A repeated call gives the same bits (where a request's
  * keys are split follows the lengths of the whole batch, so another batch may
  * round its rows differently).
+ * Over a bf16 cache a batch of single tokens has a faster form, taken where
+ * total_tokens <= batch: a decode step does best with as many rows as requests.
  * Errors: MSA_ERR_NULL, MSA_ERR_SHAPE, MSA_ERR_ALIGN, MSA_ERR_WORKSPACE, MSA_ERR_CUDA. */
 msa_status msa_attend_chunk(const msa_config* cfg, const void* q, const void* k_cache,
                             const void* v_cache, const int32_t* seq_lens,
