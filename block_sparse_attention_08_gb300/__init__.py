@@ -15,17 +15,20 @@ from .binding import (  # noqa: F401
     msa_attend_chunk,
     msa_attend_chunk_fp8kv,
     msa_check_bounded_wait,
+    msa_dequantize_gather,
     msa_index_produce_decode,
     msa_index_produce_prefill,
     msa_map_slots,
     msa_pack,
     msa_pack_metadata,
+    msa_quantize_insert,
     msa_rotary,
     msa_rotary_insert,
     msa_select_blocks_decode,
     msa_select_blocks_prefill,
     msa_sparse_attend_decode,
     msa_sparse_attend_decode_fp8kv,
+    msa_sparse_attend_decode_int8kv,
     msa_sparse_attend_decode_mxfp8,
     msa_sparse_attend_prefill,
     msa_sparse_attend_prefill_backward,

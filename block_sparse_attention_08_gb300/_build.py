@@ -21,7 +21,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmsa.so")
 SOURCES = ["abi.cu", "decode_select.cu", "sparse_attend.cu", "prefill_select.cu", "prefill_attend.cu", "pack.cu",
-           "diag.cu", "index_produce.cu", "map_slots.cu", "rotary.cu", "chunk_attend.cu"]
+           "diag.cu", "index_produce.cu", "map_slots.cu", "rotary.cu", "chunk_attend.cu", "quantize.cu"]
 EXT_SOURCE = "serving_ext.cpp"
 GXX = "g++"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -76,6 +76,9 @@ _SIGS = {
     "msa_map_slots": [P, P, I, P, I, P, I64, P, I64, I64, P, P, P, P, P, SZ, P],
     "msa_rotary": [ROT, P, I64, I, P, I64, I, P, P, I64, I, P, P, P],
     "msa_rotary_insert": [ROT, P, I64, P, I64, P, I64, P, P, P, I64, P, P, P, P, I, F, F, I64, P, SZ, P],
+    "msa_quantize_insert": [P, I64, P, I64, P, I64, P, P, P, P, I64, P, SZ, P],
+    "msa_dequantize_gather": [P, P, P, P, I64, P, P, P, I, I, I64, P, P, P, SZ, P],
+    "msa_sparse_attend_decode_int8kv": [CFG, P, P, P, P, P, P, P, P, I, I, I64, F, P, P, SZ, P],
     "msa_attend_chunk": [CFG, P, P, P, P, P, P, I, I, I64, I64, F, P, P, P, SZ, P],
     "msa_attend_chunk_fp8kv": [CFG, P, P, P, F, F, P, P, P, I, I, I64, I64, F, P, P, P, SZ, P],
 }
@@ -611,6 +614,37 @@ def msa_attend_chunk_fp8kv(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens
     r = (_ext or _serving()).attend_chunk(True, q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, k_scale,
                                           v_scale, scale, out, lse, _buf(workspace))
     return r if type(r) is not int else _fail("msa_attend_chunk_fp8kv", r)
+
+
+# ---- the int8 K/V cache -----------------------------------------------------------------
+# (through the extension module, as the calls above)
+
+def msa_quantize_insert(k, v, slots, k_cache, v_cache, k_scales, v_scales, *, workspace=None):
+    """Writes k and v (bf16 [tokens, 4, 128]) at ``slots`` (int64 [tokens], -1: not inserted) of an int8 cache: int8
+    [num_slots, 4, 128], with one bf16 power-of-two scale per row in k_scales and v_scales [num_slots / 128, 4, 128]
+    (C: msa_quantize_insert).  Slots outside the cache are skipped and told to ``workspace``."""
+    r = (_ext or _serving()).quantize_insert(k, v, slots, k_cache, v_cache, k_scales, v_scales, _buf(workspace))
+    return None if r is None else _fail("msa_quantize_insert", r)
+
+
+def msa_dequantize_gather(k_cache, v_cache, k_scales, v_scales, page_table, cu_seqlens, total_tokens, *, starts=None,
+                          k_out=None, v_out=None, workspace=None):
+    """(k, v) bf16 [total_tokens, 4, 128] of the requests' contexts: row cu_seqlens[r] + i is position ``starts[r]`` + i (default:
+    from 0) of request r (C: msa_dequantize_gather).  Rows from cu_seqlens[-1] on are left as they are (new outputs:
+    uninitialised).  Bad ranges and pages give zeros and are told to ``workspace``."""
+    r = (_ext or _serving()).dequantize_gather(k_cache, v_cache, k_scales, v_scales, page_table, cu_seqlens, total_tokens,
+                                               starts, k_out, v_out, _buf(workspace))
+    return r if type(r) is tuple else _fail("msa_dequantize_gather", r)
+
+
+def msa_sparse_attend_decode_int8kv(q, k_cache, v_cache, k_scales, v_scales, q2k, seq_lens, page_table, *, scale=None,
+                                    out=None, workspace=None):
+    """bf16 out [batch, 64, 128] over the blocks of ``q2k`` of an int8 cache (C: msa_sparse_attend_decode_int8kv).  Without
+    ``workspace`` each stream has scratch of its own, and each captured graph; a ``Workspace`` (of
+    ``workspace_size(cfg, 0, batch, page_table.shape[1])`` bytes) also tells bad lengths, blocks and pages."""
+    r = (_ext or _serving()).sparse_attend_int8(q, k_cache, v_cache, k_scales, v_scales, q2k, seq_lens, page_table, scale,
+                                                out, _buf(workspace))
+    return r if type(r) is not int else _fail("msa_sparse_attend_decode_int8kv", r)
 
 
 # ---- packing ----------------------------------------------------------------------

@@ -205,8 +205,8 @@ static msa_status attend_decode(const msa_config* cfg, const void* q, const void
                                 const int32_t* q2k, const int32_t* seq_lens, const int32_t* page_table,
                                 const int64_t* cu_seqlens_k, int batch, int max_blocks, int64_t num_slots,
                                 float scale, void* out, uint8_t* out_q, uint8_t* out_scale, void* workspace,
-                                size_t workspace_bytes, void* stream, int kv_fp8 = 0, float k_scale = 1.f,
-                                float v_scale = 1.f) {
+                                size_t workspace_bytes, void* stream, int kv = 0, float k_scale = 1.f,
+                                float v_scale = 1.f, const void* k_scales = nullptr, const void* v_scales = nullptr) {
   msa_status st = msa_config_check(cfg);
   if (st != MSA_OK) return st;
   if (!q || !k_cache || !v_cache || !q2k || (!out && !(out_q && out_scale))) return MSA_ERR_NULL;
@@ -225,7 +225,7 @@ static msa_status attend_decode(const msa_config* cfg, const void* q, const void
   cudaError_t e = launch_sparse_attend(geo, q, k_cache, v_cache, q2k, cfg->topk, scale, out, out_q, out_scale,
                                        reinterpret_cast<float*>(ws + L.partials),
                                        reinterpret_cast<int*>(ws + L.att_tickets), reinterpret_cast<DevError*>(ws), s,
-                                       kv_fp8, k_scale, v_scale);
+                                       kv, k_scale, v_scale, k_scales, v_scales);
   return cuda_result(e);
 }
 
@@ -548,6 +548,62 @@ msa_status msa_rotary_insert(const msa_rotary_config* rot, const void* q, int64_
   L.num_slots = num_slots;
   L.err = static_cast<DevError*>(workspace);
   return cuda_result(launch_rotary(L, static_cast<cudaStream_t>(stream)));
+}
+
+// An int8 cache: its tensors and its size.
+static msa_status check_int8(const void* k_cache, const void* v_cache, const void* k_scales, const void* v_scales,
+                             int64_t num_slots) {
+  if (!k_cache || !v_cache || !k_scales || !v_scales) return MSA_ERR_NULL;
+  if (num_slots < 1 || num_slots >= (1LL << 31) || num_slots % kBlock) return MSA_ERR_SHAPE;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) || !aligned16(v_scales)) return MSA_ERR_ALIGN;
+  return MSA_OK;
+}
+
+msa_status msa_quantize_insert(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slots,
+                               int64_t tokens, void* k_cache, void* v_cache, void* k_scales, void* v_scales,
+                               int64_t num_slots, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!k || !v || !slots) return MSA_ERR_NULL;
+  msa_status st = check_int8(k_cache, v_cache, k_scales, v_scales, num_slots);
+  if (st != MSA_OK) return st;
+  if (tokens < 1 || tokens >= (1LL << 31) || k_stride % 8 || k_stride < kKvHeads * kDim || v_stride % 8 ||
+      v_stride < kKvHeads * kDim)
+    return MSA_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v)) return MSA_ERR_ALIGN;
+  if ((st = check_ws(workspace, workspace_bytes, kHeaderBytes)) != MSA_OK) return st;
+  const QuantizeLaunch L{k, v, k_stride, v_stride, slots, tokens, k_cache, v_cache, k_scales, v_scales, num_slots,
+                         static_cast<DevError*>(workspace)};
+  return cuda_result(launch_quantize(L, static_cast<cudaStream_t>(stream)));
+}
+
+msa_status msa_dequantize_gather(const void* k_cache, const void* v_cache, const void* k_scales, const void* v_scales,
+                                 int64_t num_slots, const int32_t* page_table, const int32_t* starts,
+                                 const int32_t* cu_seqlens, int batch, int max_blocks, int64_t total_tokens, void* k_out,
+                                 void* v_out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!page_table || !cu_seqlens || !k_out || !v_out) return MSA_ERR_NULL;
+  msa_status st = check_int8(k_cache, v_cache, k_scales, v_scales, num_slots);
+  if (st != MSA_OK) return st;
+  if (batch < 1 || max_blocks < 1 || max_blocks > 0x7fffffff / kBlock || total_tokens < 1 || total_tokens >= (1LL << 31))
+    return MSA_ERR_SHAPE;
+  if (!aligned16(k_out) || !aligned16(v_out)) return MSA_ERR_ALIGN;
+  if ((st = check_ws(workspace, workspace_bytes, kHeaderBytes)) != MSA_OK) return st;
+  const DequantizeLaunch L{k_cache, v_cache, k_scales, v_scales, num_slots, page_table, starts, cu_seqlens, batch,
+                           max_blocks, total_tokens, k_out, v_out, static_cast<DevError*>(workspace)};
+  return cuda_result(launch_dequantize(L, static_cast<cudaStream_t>(stream)));
+}
+
+msa_status msa_sparse_attend_decode_int8kv(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
+                                           const void* k_scales, const void* v_scales, const int32_t* q2k,
+                                           const int32_t* seq_lens, const int32_t* page_table, int batch, int max_blocks,
+                                           int64_t num_slots, float scale, void* out, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  msa_status st = msa_config_check(cfg);
+  if (st != MSA_OK) return st;
+  if (!out || !page_table) return MSA_ERR_NULL;
+  if ((st = check_int8(k_cache, v_cache, k_scales, v_scales, num_slots)) != MSA_OK) return st;
+  // (as the chunk attention: a factor that is no normal number would make NaN of a score of zero or of a masked key)
+  if (!(scale > 0.f) || !std::isnormal(chunk_scale_log2(scale, 1.f))) return MSA_ERR_SHAPE;
+  return attend_decode(cfg, q, k_cache, v_cache, q2k, seq_lens, page_table, nullptr, batch, max_blocks, num_slots, scale,
+                       out, nullptr, nullptr, workspace, workspace_bytes, stream, 2, 1.f, 1.f, k_scales, v_scales);
 }
 
 static msa_status attend_chunk(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,

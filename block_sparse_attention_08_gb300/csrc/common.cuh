@@ -307,6 +307,25 @@ __device__ __forceinline__ float2 mul2(float a0, float a1, float b0, float b1) {
   return d;
 }
 __device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+// ---- int8 to bf16 -----------------------------------------------------------------
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Two int8 values as bf16x2, exactly, from halves 0x43uu (u: the value's byte): with its low seven bits the bf16 number
+// 128 + (u & 127), with its top bit alone 128, or 256 for a negative one; their difference is the value.
+__device__ __forceinline__ uint32_t i8_pair(uint32_t t) {
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(t & 0xff7fff7fu), "r"(t & 0xff80ff80u));
+  return d;
+}
+// Bytes 0 and 1 / 2 and 3 / 0 and 2 / 1 and 3 of a word.
+__device__ __forceinline__ uint32_t i8_lo2(uint32_t w) { return i8_pair(__byte_perm(w, 0x43434343u, 0x4140)); }
+__device__ __forceinline__ uint32_t i8_hi2(uint32_t w) { return i8_pair(__byte_perm(w, 0x43434343u, 0x4342)); }
+__device__ __forceinline__ uint32_t i8_even2(uint32_t w) { return i8_pair(__byte_perm(w, 0x43434343u, 0x4240)); }
+__device__ __forceinline__ uint32_t i8_odd2(uint32_t w) { return i8_pair(__byte_perm(w, 0x43434343u, 0x4341)); }
+
 // (a, b) -> bf16x2 hi = round(a, b) and lo = round(residuals): hi + lo holds
 // a and b to about 16 significant bits.
 __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {

@@ -28,11 +28,13 @@ cudaError_t launch_decode_select(const msa_config& cfg, const void* index_q, con
 // (zero between calls: the top-k kernel puts it back once the scorer grid has
 // completed).
 constexpr size_t kSelSchedOffset = 128;
-// kv_fp8: the K / V caches hold E4M3 bytes standing for k_scale * k and v_scale * v.
+// kv: the K / V caches hold bf16 (0), E4M3 bytes standing for k_scale * k and v_scale * v (1), or int8 with the rows' scales
+// in k_scales and v_scales (2).
 cudaError_t launch_sparse_attend(const AttnGeom& geo, const void* q, const void* k, const void* v,
                                  const int32_t* q2k, int topk, float scale, void* out, uint8_t* out_q,
                                  uint8_t* out_scale, float* partials, int* tickets, DevError* err,
-                                 cudaStream_t stream, int kv_fp8 = 0, float k_scale = 1.f, float v_scale = 1.f);
+                                 cudaStream_t stream, int kv = 0, float k_scale = 1.f, float v_scale = 1.f,
+                                 const void* k_scales = nullptr, const void* v_scales = nullptr);
 size_t attend_partials_bytes();
 size_t attend_tickets_bytes();
 size_t prefill_plan_ints(int num_docs, int max_tiles);
@@ -110,6 +112,29 @@ struct RotaryLaunch {
   DevError* err;
 };
 cudaError_t launch_rotary(const RotaryLaunch& L, cudaStream_t stream);
+// One msa_quantize_insert or msa_dequantize_gather call (arguments as declared in msa.h).
+struct QuantizeLaunch {
+  const void *k, *v;
+  long long k_stride, v_stride;
+  const int64_t* slots;
+  long long tokens;
+  void *k_cache, *v_cache, *k_scales, *v_scales;
+  long long num_slots;
+  DevError* err;
+};
+cudaError_t launch_quantize(const QuantizeLaunch& L, cudaStream_t stream);
+struct DequantizeLaunch {
+  const void *k_cache, *v_cache, *k_scales, *v_scales;
+  long long num_slots;
+  const int32_t* page_table;
+  const int32_t* starts;  // may be null: 0
+  const int32_t* cu;
+  int batch, max_blocks;
+  long long tokens;
+  void *k_out, *v_out;
+  DevError* err;
+};
+cudaError_t launch_dequantize(const DequantizeLaunch& L, cudaStream_t stream);
 // One chunk attention call.
 struct ChunkLaunch {
   const void *q, *k, *v;

@@ -21,6 +21,8 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <map>
+#include <mutex>
 #include <stdexcept>
 #include <sstream>
 #include <string>
@@ -507,12 +509,151 @@ PyObject* attend_chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// An int8 cache: its caches [slots, 4, 128], and its scales by page, KV head and slot.
+void fit_int8(const at::Tensor& k, const at::Tensor& v, const at::Tensor& ks, const at::Tensor& vs, c10::DeviceIndex d) {
+  const int64_t slots = k.size(0);
+  fit(k, "k_cache", at::kChar, {slots, kG, kD}, d);
+  fit(v, "v_cache", at::kChar, {slots, kG, kD}, d);
+  if (slots % kD)
+    throw Raise{PyExc_ValueError, "k_cache has " + std::to_string(slots) + " slots, expected a multiple of 128"};
+  fit(ks, "k_scales", at::kBFloat16, {slots / kD, kG, kD}, d);
+  fit(vs, "v_scales", at::kBFloat16, {slots / kD, kG, kD}, d);
+}
+
+// k, v, slots, k_cache, v_cache, k_scales, v_scales, workspace
+PyObject* quantize_insert(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("quantize_insert", n, 8, [&]() -> PyObject* {
+    const at::Tensor &k = tensor_of(a[0], "k", 3), &v = tensor_of(a[1], "v", 3);
+    const c10::DeviceIndex d = device_of(k, "k");
+    const at::Tensor &slots = tensor(a[2], "slots"), &kc = tensor_of(a[3], "k_cache", 3), &vc = tensor(a[4], "v_cache"),
+                     &ks = tensor(a[5], "k_scales"), &vs = tensor(a[6], "v_scales");
+    const int64_t tokens = k.size(0), k_stride = token_stride(k, "k", tokens, kG, d),
+                  v_stride = token_stride(v, "v", tokens, kG, d);
+    fit(slots, "slots", at::kLong, {tokens}, d);
+    fit_int8(kc, vc, ks, vs, d);
+    if (tokens < 1) return PyLong_FromLong(MSA_ERR_SHAPE);
+    const Space ws = error_word(a[7], d);
+    const msa_status st = run(d, [&](void* stream) {
+      return msa_quantize_insert(k.const_data_ptr(), k_stride, v.const_data_ptr(), v_stride, slots.const_data_ptr<int64_t>(),
+                                 tokens, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), kc.size(0), ws.at,
+                                 ws.bytes, stream);
+    });
+    if (st != MSA_OK) return PyLong_FromLong(st);
+    changed({kc, vc, ks, vs});
+    Py_RETURN_NONE;
+  });
+}
+
+// k_cache, v_cache, k_scales, v_scales, page_table, cu_seqlens, total_tokens, starts, k_out, v_out, workspace
+PyObject* dequantize_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("dequantize_gather", n, 11, [&]() -> PyObject* {
+    const at::Tensor& kc = tensor_of(a[0], "k_cache", 3);
+    const c10::DeviceIndex d = device_of(kc, "k_cache");
+    const at::Tensor &vc = tensor(a[1], "v_cache"), &ks = tensor(a[2], "k_scales"), &vs = tensor(a[3], "v_scales"),
+                     &table = tensor_of(a[4], "page_table", 2), &cu = tensor(a[5], "cu_seqlens");
+    const int64_t tokens = whole(a[6]), batch = table.size(0), width = table.size(1);
+    fit_int8(kc, vc, ks, vs, d);
+    fit(table, "page_table", at::kInt, {batch, width}, d);
+    fit(cu, "cu_seqlens", at::kInt, {batch + 1}, d);
+    at::Tensor starts;
+    if (a[7] != Py_None) {
+      starts = tensor(a[7], "starts");
+      fit(starts, "starts", at::kInt, {batch}, d);
+    }
+    if (tokens < 1 || tokens > INT32_MAX || batch < 1 || batch > INT32_MAX || width < 1 || width > INT32_MAX)
+      return PyLong_FromLong(MSA_ERR_SHAPE);
+    const at::Tensor ko = output(a[8], "k_out", at::kBFloat16, {tokens, kG, kD}, d),
+                     vo = output(a[9], "v_out", at::kBFloat16, {tokens, kG, kD}, d);
+    const Space ws = error_word(a[10], d);
+    const msa_status st = run(d, [&](void* stream) {
+      return msa_dequantize_gather(kc.const_data_ptr(), vc.const_data_ptr(), ks.const_data_ptr(), vs.const_data_ptr(),
+                                   kc.size(0), table.const_data_ptr<int32_t>(),
+                                   starts.defined() ? starts.const_data_ptr<int32_t>() : nullptr,
+                                   cu.const_data_ptr<int32_t>(), static_cast<int>(batch), static_cast<int>(width), tokens,
+                                   ko.data_ptr(), vo.data_ptr(), ws.at, ws.bytes, stream);
+    });
+    if (st != MSA_OK) return PyLong_FromLong(st);
+    changed({ko, vo});
+    return pack({ko, vo});
+  });
+}
+
+// Scratch of the decode attention, zero-filled before its first use: one buffer for each device and stream, kept for the
+// process and replaced by a larger one where a call needs that.  A capture gets one of its own (with the memset), which belongs
+// to the graph.
+Space decode_scratch(c10::DeviceIndex index, size_t bytes) {
+  const c10::cuda::CUDAGuard guard(index);
+  const c10::cuda::CUDAStream stream = c10::cuda::getCurrentCUDAStream(index);
+  auto fresh = [&] {
+    at::Tensor t = at::empty({static_cast<int64_t>(bytes)},
+                             at::TensorOptions().dtype(at::kByte).device(c10::Device(c10::kCUDA, index)));
+    if (const msa_status st = msa_workspace_init(t.data_ptr(), bytes, stream.stream()); st != MSA_OK) throw Refused(st);
+    return t;
+  };
+  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
+    at::Tensor t = fresh();
+    return {t.data_ptr(), bytes, t};
+  }
+  static std::mutex mu;
+  static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>;
+  const std::lock_guard<std::mutex> lock(mu);
+  at::Tensor& t = (*kept)[{index, stream.stream()}];
+  if (!t.defined() || static_cast<size_t>(t.nbytes()) < bytes) t = fresh();
+  return {t.data_ptr(), static_cast<size_t>(t.nbytes()), t};
+}
+
+// q, k_cache, v_cache, k_scales, v_scales, q2k, seq_lens, page_table, scale, out, workspace
+PyObject* sparse_attend_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("sparse_attend_int8", n, 11, [&]() -> PyObject* {
+    const at::Tensor& q = tensor_of(a[0], "q", 3);
+    const c10::DeviceIndex d = device_of(q, "q");
+    const at::Tensor &kc = tensor_of(a[1], "k_cache", 3), &vc = tensor(a[2], "v_cache"), &ks = tensor(a[3], "k_scales"),
+                     &vs = tensor(a[4], "v_scales"), &q2k = tensor_of(a[5], "q2k", 3), &lens = tensor(a[6], "seq_lens"),
+                     &table = tensor_of(a[7], "page_table", 2);
+    const float scale = a[8] == Py_None ? 0.088388347648318447f : static_cast<float>(number(a[8]));  // 1 / sqrt(128)
+    const int64_t batch = q.size(0), width = table.size(1), topk = q2k.size(2);
+    fit(q, "q", at::kBFloat16, {batch, kH, kD}, d);
+    fit_int8(kc, vc, ks, vs, d);
+    fit(q2k, "q2k", at::kInt, {kG, batch, topk}, d);
+    fit(lens, "seq_lens", at::kInt, {batch}, d);
+    fit(table, "page_table", at::kInt, {batch, width}, d);
+    if (batch < 1 || batch > INT32_MAX || width < 1 || width > INT32_MAX || topk < 1 || topk > 16)
+      return PyLong_FromLong(MSA_ERR_SHAPE);
+    const at::Tensor out = output(a[9], "out", at::kBFloat16, q.sizes(), d);
+    msa_config cfg;
+    msa_config_default(&cfg);
+    cfg.topk = static_cast<int>(topk);
+    cfg.local_blocks = 0;
+    Space ws;
+    if (a[10] == Py_None) {
+      size_t bytes = 0;
+      const msa_status st = msa_workspace_size(&cfg, MSA_MODE_DECODE, batch, static_cast<int>(width), &bytes);
+      if (st != MSA_OK) return PyLong_FromLong(st);
+      ws = decode_scratch(d, bytes);
+    } else {
+      ws = error_word(a[10], d);
+    }
+    const msa_status st = run(d, [&](void* stream) {
+      return msa_sparse_attend_decode_int8kv(&cfg, q.const_data_ptr(), kc.const_data_ptr(), vc.const_data_ptr(),
+                                             ks.const_data_ptr(), vs.const_data_ptr(), q2k.const_data_ptr<int32_t>(),
+                                             lens.const_data_ptr<int32_t>(), table.const_data_ptr<int32_t>(),
+                                             static_cast<int>(batch), static_cast<int>(width), kc.size(0), scale,
+                                             out.data_ptr(), ws.at, ws.bytes, stream);
+    });
+    if (st != MSA_OK) return PyLong_FromLong(st);
+    changed({out});
+    return wrap(out);
+  });
+}
+
 using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
 PyMethodDef method(const char* name, Fast f) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
 }
 PyMethodDef kMethods[] = {method("map_slots", map_slots), method("rotary", rotary), method("rotary_autograd", rotary_autograd),
                           method("rotary_insert", rotary_insert), method("attend_chunk", attend_chunk),
+                          method("quantize_insert", quantize_insert), method("dequantize_gather", dequantize_gather),
+                          method("sparse_attend_int8", sparse_attend_int8),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "msa_serving", nullptr, -1, kMethods};
 

@@ -54,6 +54,9 @@
 
 namespace msa {
 
+// The K / V caches' types (the template parameter kKv below).
+constexpr int kKvBf16 = 0, kKvE4m3 = 1, kKvI8 = 2;
+
 constexpr int kAttStages = 6;
 constexpr int kChunkKeys = 64;
 constexpr int kBoxBytes = kChunkKeys * 128;        // 64 rows x 128 bytes (64 bf16 dims, or 128 E4M3 dims)
@@ -106,7 +109,7 @@ struct SegInfo {
 };
 
 // The chunk ring: 64-key chunks of K and V (bf16: 4 boxes of 64 dims, 32 KB;
-// FP8: one 128-byte box each, 16 KB), 6 stages.
+// FP8 and int8: one 128-byte box each, 16 KB), 6 stages.
 //
 // With an FP8 cache the attention is bound by its consumer warps' issue, not
 // by bytes, so two CTAs share an SM (six consumer warps per SM) on its 96 KB of
@@ -118,13 +121,13 @@ struct SegInfo {
 // 31.4 -> 27.2 us.  A bf16 ring of 96 KB would leave each warp a single stage,
 // nothing landing while it computes: slower (18.4 -> 20.9 us on the 4-request
 // workload), so bf16 stays at one CTA per SM.
-template <int kFp8, int kSplit>
+template <int kKv, int kSplit>
 struct AttShape {
-  static constexpr int kStageBytes = kFp8 ? kAttStage8Bytes : kAttStageBytes;
+  static constexpr int kStageBytes = kKv ? kAttStage8Bytes : kAttStageBytes;
   static constexpr int kStages = kAttStages;
-  static constexpr int kCtasPerSm = kFp8 ? 2 : 1;
-  static constexpr int kQSlots = kFp8 ? 1 : kSegSlots;             // Q tiles in the segment ring
-  static constexpr int kCombSlots = kFp8 ? 1 : kConsumerWarps - 1;  // stream-K: where states meet
+  static constexpr int kCtasPerSm = kKv ? 2 : 1;
+  static constexpr int kQSlots = kKv ? 1 : kSegSlots;             // Q tiles in the segment ring
+  static constexpr int kCombSlots = kKv ? 1 : kConsumerWarps - 1;  // stream-K: where states meet
 };
 
 // Where the consumer warps' states meet (stream-K only).
@@ -137,11 +140,12 @@ struct AttComb {
 template <int kSlots>
 struct AttComb<1, kSlots> {};
 
-template <int kFp8, int kSplit>
+template <int kKv, int kSplit>
 struct AttSmem {
-  using Shape = AttShape<kFp8, kSplit>;
+  using Shape = AttShape<kKv, kSplit>;
   alignas(1024) uint8_t stage[Shape::kStages][Shape::kStageBytes];
   alignas(1024) uint8_t qtile[Shape::kQSlots][2 * kQBoxBytes];
+  uint32_t scales[kKv == kKvI8 ? Shape::kStages : 1][kKv == kKvI8 ? kChunkKeys : 4];  // int8: K's, then V's, bf16
   AttComb<kSplit, Shape::kCombSlots> c;
   SegInfo seg[Shape::kQSlots];
   uint64_t full[Shape::kStages];
@@ -162,13 +166,13 @@ struct CombRef {
 // Stream-K: the shared buffer (the merged state over warp 1's slot, which warp
 // 0 has read by then; with one slot the warps take turns); cluster form: stage
 // `who`, which belongs to warp `who`.
-template <int kFp8, int kSplit>
-__device__ __forceinline__ CombRef comb_ref(AttSmem<kFp8, kSplit>& sm, int who) {
+template <int kKv, int kSplit>
+__device__ __forceinline__ CombRef comb_ref(AttSmem<kKv, kSplit>& sm, int who) {
   if constexpr (kSplit != 0) {
     float* base = reinterpret_cast<float*>(&sm.stage[who][0]);
     return CombRef{base, base + kGroup * kCombStride, base + kGroup * kCombStride + kGroup};
   } else {
-    const int slot = who > 0 ? (who - 1) % AttShape<kFp8, kSplit>::kCombSlots : 0;
+    const int slot = who > 0 ? (who - 1) % AttShape<kKv, kSplit>::kCombSlots : 0;
     return CombRef{&sm.c.comb[slot][0][0], sm.c.comb_m[slot], sm.c.comb_l[slot]};
   }
 }
@@ -197,7 +201,7 @@ struct WarpState {
 // values of the pair are the consecutive dims 16 c + 4 t4 .. + 3 -- stored and
 // loaded as one float4, in the natural order, so everything that reads the
 // states back (the merges, the output) sees plain rows.
-template <int kFp8>
+template <int kKv>
 __device__ __forceinline__ void state_to_smem(const WarpState& st, const CombRef& c, int g8, int t4) {
   if (t4 == 0) {
     c.m[g8] = st.m0;
@@ -205,7 +209,7 @@ __device__ __forceinline__ void state_to_smem(const WarpState& st, const CombRef
     c.l[g8] = st.l0;
     c.l[g8 + 8] = st.l1;
   }
-  if constexpr (kFp8 != 0) {
+  if constexpr (kKv != 0) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       *reinterpret_cast<float4*>(c.row(g8) + 16 * k + 4 * t4) =
@@ -222,7 +226,7 @@ __device__ __forceinline__ void state_to_smem(const WarpState& st, const CombRef
   }
 }
 
-template <int kFp8>
+template <int kKv>
 __device__ __forceinline__ void merge_from_smem(WarpState& st, const CombRef& c, int g8, int t4) {
   const float mb0 = c.m[g8], mb1 = c.m[g8 + 8];
   const float M0 = fmaxf(st.m0, mb0), M1 = fmaxf(st.m1, mb1);
@@ -233,7 +237,7 @@ __device__ __forceinline__ void merge_from_smem(WarpState& st, const CombRef& c,
   st.l1 = st.l1 * fa1 + c.l[g8 + 8] * fb1;
   st.m0 = M0;
   st.m1 = M1;
-  if constexpr (kFp8 != 0) {
+  if constexpr (kKv != 0) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float4 x = *reinterpret_cast<const float4*>(c.row(g8) + 16 * k + 4 * t4);
@@ -259,6 +263,9 @@ __device__ __forceinline__ void merge_from_smem(WarpState& st, const CombRef& c,
     }
   }
 }
+
+// The low (e = 0) or high value of a bf16 pair.
+__device__ __forceinline__ float bf16_of(uint32_t w, int e) { return __uint_as_float(e ? w & 0xffff0000u : w << 16); }
 
 // Two E4M3 values, rounded to nearest (ties to even) and saturated at +-448;
 // `lo` in the low byte.
@@ -297,15 +304,15 @@ __device__ __forceinline__ void store_mxfp8_64(const float* v, float inv, uint8_
   }
 }
 
-// The 16-bit type of P: bf16 (a bf16 K/V cache) or fp16 (an FP8 K/V cache,
-// converted to fp16 on chip).
-template <int kFp8>
+// The 16-bit type of P: bf16 (a bf16 K/V cache, or an int8 one converted to bf16
+// on chip) or fp16 (an FP8 K/V cache, converted to fp16).
+template <int kKv>
 __device__ __forceinline__ float round16(float x) {
-  return kFp8 ? __half2float(__float2half_rn(x)) : bf16_round(x);
+  return kKv == kKvE4m3 ? __half2float(__float2half_rn(x)) : bf16_round(x);
 }
-template <int kFp8>
+template <int kKv>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  if (kFp8) {
+  if (kKv == kKvE4m3) {
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
   }
@@ -336,6 +343,21 @@ __device__ __forceinline__ uint32_t e4m3_hi2(uint32_t w) { return e4m3_hb_to_f16
 __device__ __forceinline__ uint32_t e4m3_even2(uint32_t w) { return e4m3_hb_to_f16x2_s8(__byte_perm(w, 0u, 0x2404)); }
 __device__ __forceinline__ uint32_t e4m3_odd2(uint32_t w) { return e4m3_hb_to_f16x2_s8(__byte_perm(w, 0u, 0x3414)); }
 
+// The same of an 8-bit cache's words, in the type that its products take.
+template <int kKv>
+__device__ __forceinline__ uint32_t lo2(uint32_t w) { return kKv == kKvI8 ? i8_lo2(w) : e4m3_lo2(w); }
+template <int kKv>
+__device__ __forceinline__ uint32_t hi2(uint32_t w) { return kKv == kKvI8 ? i8_hi2(w) : e4m3_hi2(w); }
+template <int kKv>
+__device__ __forceinline__ uint32_t even2(uint32_t w) { return kKv == kKvI8 ? i8_even2(w) : e4m3_even2(w); }
+template <int kKv>
+__device__ __forceinline__ uint32_t odd2(uint32_t w) { return kKv == kKvI8 ? i8_odd2(w) : e4m3_odd2(w); }
+template <int kKv>
+__device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (kKv == kKvI8) mma_bf16(c, a, b0, b1);
+  else mma_f16(c, a, b0, b1);
+}
+
 constexpr int kMaxCluster = 8;
 
 // Cluster split (kSplit): the CTAs of one cluster each hold their share of a
@@ -352,7 +374,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kPushStride = kDim + 4;
 constexpr int kPushFloats = 2 * kGroup + kGroup * kPushStride;
 
-template <int kFp8, class Smem>
+template <int kKv, class Smem>
 __device__ __forceinline__ void split_finish(Smem& sm, int csize, int warp, int lane, float v_scale,
                                              __nv_bfloat16* __restrict__ out, uint8_t* __restrict__ out_q,
                                              uint8_t* __restrict__ out_scale) {
@@ -416,7 +438,7 @@ __device__ __forceinline__ void split_finish(Smem& sm, int csize, int warp, int 
       ag[4 * d + 3] += v.w * f;
     }
   }
-  const float inv = Lg > 0.f ? (kFp8 ? v_scale : 1.f) / Lg : 0.f;
+  const float inv = Lg > 0.f ? (kKv == kKvE4m3 ? v_scale : 1.f) / Lg : 0.f;
   const long long oelem = (static_cast<long long>(qi) * kHeads + g * kGroup + row) * kDim + d0;
   if (out_q) {
     store_mxfp8_64(ag, inv, out_q + oelem, out_scale + oelem / 32);
@@ -431,26 +453,28 @@ __device__ __forceinline__ void split_finish(Smem& sm, int csize, int warp, int 
 }
 
 // out_q / out_scale: when non-null, the output is emitted as MXFP8 there
-// instead of bf16 in `out`.  kFp8: the K / V caches hold E4M3 bytes;
-// scale_log2 then includes 2^8 k_scale, and v_scale (2^8 times the cache's) multiplies the output.
+// instead of bf16 in `out`.  kKv: the type of the K / V caches.  E4M3: scale_log2
+// includes 2^8 k_scale, and v_scale (2^8 times the cache's) multiplies the output.
+// int8: k_scales, v_scales hold each row's scale, by page, KV head and slot.
 // kSplit: launched in clusters of csize CTAs, one cluster per (query, KV
 // head) segment; CTA rank r takes units [r topk / csize, (r + 1) topk / csize)
 // of it, and the cluster merges on chip (split_finish).  Otherwise stream-K:
 // the units are split evenly over the grid and cut segments are merged
 // through fp32 partials in global memory and a ticket per segment.
-template <int kFp8, int kSplit>
-__global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerSm) sparse_attend_kernel(
+template <int kKv, int kSplit>
+__global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm) sparse_attend_kernel(
     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
     const __grid_constant__ CUtensorMap qmap, const int32_t* __restrict__ q2k, AttnGeom geo, int topk,
-    float scale_log2, float v_scale, __nv_bfloat16* __restrict__ out, uint8_t* __restrict__ out_q,
+    float scale_log2, float v_scale, const __nv_bfloat16* __restrict__ k_scales,
+    const __nv_bfloat16* __restrict__ v_scales, __nv_bfloat16* __restrict__ out, uint8_t* __restrict__ out_q,
     uint8_t* __restrict__ out_scale, float* __restrict__ partials, int* __restrict__ tickets, int csize,
     DevError* err) {
   extern __shared__ uint8_t smem_raw[];
-  AttSmem<kFp8, kSplit>& sm = *reinterpret_cast<AttSmem<kFp8, kSplit>*>(
+  AttSmem<kKv, kSplit>& sm = *reinterpret_cast<AttSmem<kKv, kSplit>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kStg = AttShape<kFp8, kSplit>::kStages;
-  constexpr int kQS = AttShape<kFp8, kSplit>::kQSlots;
+  constexpr int kStg = AttShape<kKv, kSplit>::kStages;
+  constexpr int kQS = AttShape<kKv, kSplit>::kQSlots;
   const long long N = static_cast<long long>(geo.nq) * kKvHeads * topk;
   const long long G = gridDim.x;
   long long lo, hi;
@@ -504,7 +528,7 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
         c0.m[lane] = -INFINITY;
         c0.l[lane] = 0.f;
       }
-      split_finish<kFp8>(sm, csize, warp, lane, v_scale, out, out_q, out_scale);
+      split_finish<kKv>(sm, csize, warp, lane, v_scale, out, out_q, out_scale);
     }
     return;
   }
@@ -561,10 +585,15 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
             mbar_wait(&sm.empty[s], static_cast<uint32_t>(((sc / kStg) & 1) ^ 1), err, 200);
             const int row = static_cast<int>(r0 + ch * kChunkKeys);
             uint8_t* st = sm.stage[s];
-            if (kFp8) {
-              mbar_expect_tx(&sm.full[s], kAttStage8Bytes);
+            if (kKv) {
+              mbar_expect_tx(&sm.full[s], kAttStage8Bytes + (kKv == kKvI8 ? 4 * kChunkKeys : 0));
               tma_load_3d(st, &kmap, 0, g, row, &sm.full[s]);
               tma_load_3d(st + kBoxBytes, &vmap, 0, g, row, &sm.full[s]);
+              if constexpr (kKv == kKvI8) {
+                const long long at = (r0 / kBlock * kKvHeads + g) * kBlock + ch * kChunkKeys;
+                tma_bulk_g2s(&sm.scales[s][0], k_scales + at, 2 * kChunkKeys, &sm.full[s]);
+                tma_bulk_g2s(&sm.scales[s][kChunkKeys / 2], v_scales + at, 2 * kChunkKeys, &sm.full[s]);
+              }
             } else {
               mbar_expect_tx(&sm.full[s], kAttStageBytes);
               tma_load_3d(st + 0 * kBoxBytes, &kmap, 0, g, row, &sm.full[s]);
@@ -593,7 +622,7 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
       }
     }
     __syncwarp();
-    if constexpr (kSplit != 0) split_finish<kFp8>(sm, csize, warp, lane, v_scale, out, out_q, out_scale);
+    if constexpr (kSplit != 0) split_finish<kKv>(sm, csize, warp, lane, v_scale, out, out_q, out_scale);
     return;
   }
 
@@ -616,8 +645,8 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
     uint32_t qa[8][4];
     {
       const uint32_t qt = smem_u32(sm.qtile[ss]);
-      if constexpr (kFp8 != 0) {
-        // fp16, k slots permuted as the K fragments are (S = Q K^T below):
+      if constexpr (kKv != 0) {
+        // (E4M3: as fp16) k slots permuted as the K fragments are (S = Q K^T below):
         // slots 2t, 2t+1, 2t+8, 2t+9 of k-step s hold dims 16s + 4t .. + 3
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
@@ -625,10 +654,10 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
           const uint32_t off = (kk >> 2) * kQBoxBytes + 8 * (t4 & 1);
           const uint2 a = lds64(qt + off + sw128(g8, chunk));
           const uint2 b = lds64(qt + off + sw128(g8 + 8, chunk));
-          qa[kk][0] = bf16x2_to_f16x2(a.x);
-          qa[kk][1] = bf16x2_to_f16x2(b.x);
-          qa[kk][2] = bf16x2_to_f16x2(a.y);
-          qa[kk][3] = bf16x2_to_f16x2(b.y);
+          qa[kk][0] = kKv == kKvE4m3 ? bf16x2_to_f16x2(a.x) : a.x;
+          qa[kk][1] = kKv == kKvE4m3 ? bf16x2_to_f16x2(b.x) : b.x;
+          qa[kk][2] = kKv == kKvE4m3 ? bf16x2_to_f16x2(a.y) : a.y;
+          qa[kk][3] = kKv == kKvE4m3 ? bf16x2_to_f16x2(b.y) : b.y;
         }
       } else {
         const int qrow = (lane & 7) + 8 * ((lane >> 3) & 1);
@@ -679,8 +708,8 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
         float sacc[8][4];
 #pragma unroll
         for (int p = 0; p < 8; ++p) sacc[p][0] = sacc[p][1] = sacc[p][2] = sacc[p][3] = 0.f;
-        if constexpr (kFp8 != 0) {
-          // E4M3 K rows are 128 bytes: a 16-byte chunk is one k-step of 16 dims.
+        if constexpr (kKv != 0) {
+          // E4M3 (or int8) K rows are 128 bytes: a 16-byte chunk is one k-step of 16 dims.
           // ldmatrix (16-bit view) gives a lane 4 consecutive bytes, dims
           // 16s + 4t .. + 3 of one key, converted in registers into the B
           // fragment whose slots the Q fragments above were permuted to match.
@@ -692,10 +721,10 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
             for (int kk = 0; kk < 8; kk += 2) {
               uint32_t kr[4];  // keys lo / hi of k-step kk, then of k-step kk + 1
               ldsm_x4(kr, stg + sw128(krow, kk + (mi >> 1)));
-              mma_f16(sacc[2 * kp], qa[kk], e4m3_lo2(kr[0]), e4m3_hi2(kr[0]));
-              mma_f16(sacc[2 * kp + 1], qa[kk], e4m3_lo2(kr[1]), e4m3_hi2(kr[1]));
-              mma_f16(sacc[2 * kp], qa[kk + 1], e4m3_lo2(kr[2]), e4m3_hi2(kr[2]));
-              mma_f16(sacc[2 * kp + 1], qa[kk + 1], e4m3_lo2(kr[3]), e4m3_hi2(kr[3]));
+              mma8<kKv>(sacc[2 * kp], qa[kk], lo2<kKv>(kr[0]), hi2<kKv>(kr[0]));
+              mma8<kKv>(sacc[2 * kp + 1], qa[kk], lo2<kKv>(kr[1]), hi2<kKv>(kr[1]));
+              mma8<kKv>(sacc[2 * kp], qa[kk + 1], lo2<kKv>(kr[2]), hi2<kKv>(kr[2]));
+              mma8<kKv>(sacc[2 * kp + 1], qa[kk + 1], lo2<kKv>(kr[3]), hi2<kKv>(kr[3]));
             }
           }
         } else {
@@ -720,8 +749,10 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const bool ok = 8 * p + 2 * t4 + e < valid;
-            sacc[p][e] = ok ? sacc[p][e] * scale_log2 : -INFINITY;
-            sacc[p][2 + e] = ok ? sacc[p][2 + e] * scale_log2 : -INFINITY;
+            // (int8: with the key's own scale)
+            const float f = kKv == kKvI8 ? scale_log2 * bf16_of(sm.scales[s][kKv == kKvI8 ? 4 * p + t4 : 0], e) : scale_log2;
+            sacc[p][e] = ok ? sacc[p][e] * f : -INFINITY;
+            sacc[p][2 + e] = ok ? sacc[p][2 + e] * f : -INFINITY;
             mx0 = fmaxf(mx0, sacc[p][e]);
             mx1 = fmaxf(mx1, sacc[p][2 + e]);
           }
@@ -740,10 +771,10 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
         float rs0 = 0.f, rs1 = 0.f;
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-          sacc[p][0] = round16<kFp8>(exp2f(sacc[p][0] - mu0));
-          sacc[p][1] = round16<kFp8>(exp2f(sacc[p][1] - mu0));
-          sacc[p][2] = round16<kFp8>(exp2f(sacc[p][2] - mu1));
-          sacc[p][3] = round16<kFp8>(exp2f(sacc[p][3] - mu1));
+          sacc[p][0] = round16<kKv>(exp2f(sacc[p][0] - mu0));
+          sacc[p][1] = round16<kKv>(exp2f(sacc[p][1] - mu0));
+          sacc[p][2] = round16<kKv>(exp2f(sacc[p][2] - mu1));
+          sacc[p][3] = round16<kKv>(exp2f(sacc[p][3] - mu1));
           rs0 += sacc[p][0] + sacc[p][1];
           rs1 += sacc[p][2] + sacc[p][3];
         }
@@ -756,17 +787,30 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
           st.o[nd][2] *= al1;
           st.o[nd][3] *= al1;
         }
-        // ---- O += P V, one k-step per 16 keys (P exact in bf16 after the rounding above) ----
+        if constexpr (kKv == kKvI8) {
+          // the values' scales go into the weights that multiply them (a masked key's may be anything: its weight stays zero)
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const uint32_t vs = sm.scales[s][kChunkKeys / 2 + 4 * p + t4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float f = 8 * p + 2 * t4 + e < valid ? bf16_of(vs, e) : 0.f;
+              sacc[p][e] *= f;
+              sacc[p][2 + e] *= f;
+            }
+          }
+        }
+        // ---- O += P V, one k-step per 16 keys (P exact in 16 bits after the rounding above; int8: with a power of two) ----
 #pragma unroll
         for (int kp = 0; kp < 4; ++kp) {
           if (16 * kp >= valid) break;
-          const uint32_t pa[4] = {pack16<kFp8>(sacc[2 * kp][0], sacc[2 * kp][1]),
-                                  pack16<kFp8>(sacc[2 * kp][2], sacc[2 * kp][3]),
-                                  pack16<kFp8>(sacc[2 * kp + 1][0], sacc[2 * kp + 1][1]),
-                                  pack16<kFp8>(sacc[2 * kp + 1][2], sacc[2 * kp + 1][3])};
+          const uint32_t pa[4] = {pack16<kKv>(sacc[2 * kp][0], sacc[2 * kp][1]),
+                                  pack16<kKv>(sacc[2 * kp][2], sacc[2 * kp][3]),
+                                  pack16<kKv>(sacc[2 * kp + 1][0], sacc[2 * kp + 1][1]),
+                                  pack16<kKv>(sacc[2 * kp + 1][2], sacc[2 * kp + 1][3])};
           const int vrow = 16 * kp + 8 * (mi & 1) + (lane & 7);
-          if constexpr (kFp8 != 0) {
-            // The transposing ldmatrix (16-bit view) of E4M3 V gives a lane
+          if constexpr (kKv != 0) {
+            // The transposing ldmatrix (16-bit view) of 8-bit V gives a lane
             // keys 2t, 2t+1 of dims 2g, 2g+1 of a 16-dim block: bytes 0 / 2 are
             // the pair of the even dim, 1 / 3 that of the odd one, so the block
             // feeds two n-tiles, its even and its odd dims (st.o[2c], [2c+1]).
@@ -774,10 +818,10 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
             for (int c = 0; c < 8; c += 2) {
               uint32_t vr[4];  // keys lo / hi of block c, then of block c + 1
               ldsm_x4_t(vr, stg + kBoxBytes + sw128(vrow, c + (mi >> 1)));
-              mma_f16(st.o[2 * c], pa, e4m3_even2(vr[0]), e4m3_even2(vr[1]));
-              mma_f16(st.o[2 * c + 1], pa, e4m3_odd2(vr[0]), e4m3_odd2(vr[1]));
-              mma_f16(st.o[2 * c + 2], pa, e4m3_even2(vr[2]), e4m3_even2(vr[3]));
-              mma_f16(st.o[2 * c + 3], pa, e4m3_odd2(vr[2]), e4m3_odd2(vr[3]));
+              mma8<kKv>(st.o[2 * c], pa, even2<kKv>(vr[0]), even2<kKv>(vr[1]));
+              mma8<kKv>(st.o[2 * c + 1], pa, odd2<kKv>(vr[0]), odd2<kKv>(vr[1]));
+              mma8<kKv>(st.o[2 * c + 2], pa, even2<kKv>(vr[2]), even2<kKv>(vr[3]));
+              mma8<kKv>(st.o[2 * c + 3], pa, odd2<kKv>(vr[2]), odd2<kKv>(vr[3]));
             }
           } else {
 #pragma unroll
@@ -801,29 +845,29 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
     st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, 2);
     st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, 1);
     st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, 2);
-    if constexpr (kSplit == 0 && AttShape<kFp8, kSplit>::kCombSlots == 1) {
+    if constexpr (kSplit == 0 && AttShape<kKv, kSplit>::kCombSlots == 1) {
       // one slot: warp 2, then warp 1, hands its state to warp 0 (warp 0 has
       // read it before it reaches the next segment's first meeting, the only
       // place the slot is written again)
       consumer_sync();
-      if (warp == 2) state_to_smem<kFp8>(st, comb_ref(sm, 1), g8, t4);
+      if (warp == 2) state_to_smem<kKv>(st, comb_ref(sm, 1), g8, t4);
       consumer_sync();
-      if (warp == 0) merge_from_smem<kFp8>(st, comb_ref(sm, 1), g8, t4);
+      if (warp == 0) merge_from_smem<kKv>(st, comb_ref(sm, 1), g8, t4);
       consumer_sync();
-      if (warp == 1) state_to_smem<kFp8>(st, comb_ref(sm, 1), g8, t4);
+      if (warp == 1) state_to_smem<kKv>(st, comb_ref(sm, 1), g8, t4);
       consumer_sync();
       if (warp > 0) continue;  // warps 1 and 2 go on to the next segment
-      merge_from_smem<kFp8>(st, comb_ref(sm, 1), g8, t4);
+      merge_from_smem<kKv>(st, comb_ref(sm, 1), g8, t4);
     } else {
       consumer_sync();
-      if (warp > 0) state_to_smem<kFp8>(st, comb_ref(sm, warp), g8, t4);
+      if (warp > 0) state_to_smem<kKv>(st, comb_ref(sm, warp), g8, t4);
       consumer_sync();
       if (warp > 0) continue;  // warps 1 and 2 go on to the next segment
 #pragma unroll
-      for (int w = 1; w < kConsumerWarps; ++w) merge_from_smem<kFp8>(st, comb_ref(sm, w), g8, t4);
+      for (int w = 1; w < kConsumerWarps; ++w) merge_from_smem<kKv>(st, comb_ref(sm, w), g8, t4);
     }
     __syncwarp();
-    state_to_smem<kFp8>(st, comb_ref(sm, 0), g8, t4);  // staging for coalesced stores (read only by warp 0)
+    state_to_smem<kKv>(st, comb_ref(sm, 0), g8, t4);  // staging for coalesced stores (read only by warp 0)
     __syncwarp();
     if constexpr (kSplit != 0) continue;  // the cluster merges slot 0 (split_finish)
     // ---- warp 0 writes: lane -> row lane/2, 64 dims ----
@@ -835,7 +879,7 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
     const long long oelem = (static_cast<long long>(qi) * kHeads + g * kGroup + row) * kDim + d0;
     __nv_bfloat16* orow = out_q ? nullptr : out + oelem;
     if (complete) {
-      const float inv = Lsum > 0.f ? (kFp8 ? v_scale : 1.f) / Lsum : 0.f;
+      const float inv = Lsum > 0.f ? (kKv == kKvE4m3 ? v_scale : 1.f) / Lsum : 0.f;
       if (out_q) {
         store_mxfp8_64(src, inv, out_q + oelem, out_scale + oelem / 32);
       } else {
@@ -925,7 +969,7 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
             ag[4 * d + 3] += xv[d].w * f;
           }
         }
-        const float inv = Lg > 0.f ? (kFp8 ? v_scale : 1.f) / Lg : 0.f;
+        const float inv = Lg > 0.f ? (kKv == kKvE4m3 ? v_scale : 1.f) / Lg : 0.f;
         if (out_q) {
           store_mxfp8_64(ag, inv, out_q + oelem, out_scale + oelem / 32);
         } else {
@@ -939,7 +983,7 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kFp8, kSplit>::kCtasPerS
       }
     }
   }
-  if constexpr (kSplit != 0) split_finish<kFp8>(sm, csize, warp, lane, v_scale, out, out_q, out_scale);
+  if constexpr (kSplit != 0) split_finish<kKv>(sm, csize, warp, lane, v_scale, out, out_q, out_scale);
 }
 
 // ---- host side --------------------------------------------------------------------
@@ -985,12 +1029,12 @@ static bool make_q_map(CUtensorMap* map, const void* base, long long nq) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kFp8, int kSplit>
-constexpr size_t att_smem() { return sizeof(AttSmem<kFp8, kSplit>) + 1024; }
+template <int kKv, int kSplit>
+constexpr size_t att_smem() { return sizeof(AttSmem<kKv, kSplit>) + 1024; }
 static_assert(att_smem<0, 0>() <= 227 * 1024 && att_smem<0, 1>() <= 227 * 1024, "shared memory of the decode attention");
-// two CTAs of the FP8 forms per SM (228 KB of shared memory per SM, 1 KB of it per CTA reserved)
-static_assert(2 * (att_smem<1, 0>() + 1024) <= 228 * 1024 && 2 * (att_smem<1, 1>() + 1024) <= 228 * 1024,
-              "shared memory of the decode attention, FP8 K/V");
+// two CTAs of the 8-bit forms per SM (int8 needs the most) (228 KB of shared memory per SM, 1 KB of it per CTA reserved)
+static_assert(2 * (att_smem<kKvI8, 0>() + 1024) <= 228 * 1024 && 2 * (att_smem<kKvI8, 1>() + 1024) <= 228 * 1024,
+              "shared memory of the decode attention, 8-bit K/V");
 
 // The stream-K grid: at most kCtasPerSm CTAs per SM (2 with an FP8 cache).
 constexpr int kMaxStreamKCtas = 2 * kNumSMs;
@@ -998,19 +1042,31 @@ size_t attend_partials_bytes() { return 2ull * kMaxStreamKCtas * kPartialFloats 
 // one merge counter per CTA of the persistent grid
 size_t attend_tickets_bytes() { return static_cast<size_t>(kMaxStreamKCtas) * sizeof(int); }
 
+using AttKernel = decltype(&sparse_attend_kernel<kKvBf16, 0>);
+struct AttForm {
+  AttKernel kernel;
+  size_t smem;
+};
+template <int kKv, int kSplit>
+constexpr AttForm att_form_of() { return AttForm{sparse_attend_kernel<kKv, kSplit>, att_smem<kKv, kSplit>()}; }
+static AttForm att_form(int kv, bool split) {
+  if (kv == kKvI8) return split ? att_form_of<kKvI8, 1>() : att_form_of<kKvI8, 0>();
+  if (kv == kKvE4m3) return split ? att_form_of<kKvE4m3, 1>() : att_form_of<kKvE4m3, 0>();
+  return split ? att_form_of<kKvBf16, 1>() : att_form_of<kKvBf16, 0>();
+}
+
 // How many clusters of c CTAs of the split kernel can be resident at once
 // (cudaOccupancyMaxActiveClusters, asked once per device, K/V type and c; 0
 // when the query fails, which keeps the stream-K kernel for that call).
-static int max_active_clusters(int kv_fp8, int c) {
+static int max_active_clusters(int kv, int c) {
   static std::mutex mu;
-  static int cache[64][2][kMaxCluster + 1];
-  static bool done[64][2][kMaxCluster + 1];
+  static int cache[64][3][kMaxCluster + 1];
+  static bool done[64][3][kMaxCluster + 1];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
-  if (done[dev][kv_fp8][c]) return cache[dev][kv_fp8][c];
-  const size_t smem = kv_fp8 ? att_smem<1, 1>() : att_smem<0, 1>();
-  auto kern = kv_fp8 ? sparse_attend_kernel<1, 1> : sparse_attend_kernel<0, 1>;
+  if (done[dev][kv][c]) return cache[dev][kv][c];
+  const auto [kern, smem] = att_form(kv, true);
   int n = 0;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>(c * 16));
@@ -1028,37 +1084,39 @@ static int max_active_clusters(int kv_fp8, int c) {
     cudaGetLastError();  // a failed query leaves no error behind for the launch that follows
     return 0;            // and is asked again next time (it is not kept)
   }
-  cache[dev][kv_fp8][c] = n;
-  done[dev][kv_fp8][c] = true;
+  cache[dev][kv][c] = n;
+  done[dev][kv][c] = true;
   return n;
 }
 
 cudaError_t launch_sparse_attend(const AttnGeom& geo, const void* q, const void* k, const void* v,
                                  const int32_t* q2k, int topk, float scale, void* out, uint8_t* out_q,
                                  uint8_t* out_scale, float* partials, int* tickets, DevError* err,
-                                 cudaStream_t stream, int kv_fp8, float k_scale, float v_scale) {
+                                 cudaStream_t stream, int kv, float k_scale, float v_scale, const void* k_scales,
+                                 const void* v_scales) {
   if (const cudaError_t e0 = launch_prologue(); e0 != cudaSuccess) return e0;
   CUtensorMap kmap, vmap, qmap;
-  const bool maps = kv_fp8 ? make_kv_map8(&kmap, k, geo.num_rows) && make_kv_map8(&vmap, v, geo.num_rows)
+  const bool maps = kv ? make_kv_map8(&kmap, k, geo.num_rows) && make_kv_map8(&vmap, v, geo.num_rows)
                            : make_kv_map(&kmap, k, geo.num_rows) && make_kv_map(&vmap, v, geo.num_rows);
   if (!maps || !make_q_map(&qmap, q, geo.nq)) return cudaErrorInvalidValue;
   // An FP8 cache holds k / k_scale and v / v_scale, and the kernel reads its
   // bytes as fp16 values times 2^-8 (e4m3_hb_to_f16x2_s8): 2^8 goes into both scales.
-  const float scale_log2 = scale * (kv_fp8 ? 256.f * k_scale : 1.f) * 1.4426950408889634f;
+  const float scale_log2 = scale * (kv == kKvE4m3 ? 256.f * k_scale : 1.f) * 1.4426950408889634f;
   const long long S = static_cast<long long>(geo.nq) * kKvHeads;  // (query, KV head) segments
   const long long N = S * topk;
   // Few segments (small batches): one cluster of C CTAs per segment, merged
   // on chip -- the largest C in {8, 4, 2} with C <= topk (every CTA gets a
-  // unit), at most one CTA per SM (two with an FP8 cache), and every cluster
+  // unit), at most one CTA per SM (two with an 8-bit cache), and every cluster
   // resident at once.  Otherwise stream-K over the whole grid, one CTA per SM.
-  const long long per_sm = kv_fp8 ? AttShape<1, 1>::kCtasPerSm : AttShape<0, 1>::kCtasPerSm;
+  const long long per_sm = kv ? AttShape<kKvE4m3, 1>::kCtasPerSm : AttShape<kKvBf16, 1>::kCtasPerSm;
   int C = 0;
   for (int c = kMaxCluster; c >= 2 && !C; c >>= 1) {
     if (c > topk || S * c > per_sm * kNumSMs) continue;
-    const int fit = max_active_clusters(kv_fp8, c);
+    const int fit = max_active_clusters(kv, c);
     if (fit > 0 && S <= fit) C = c;
   }
-  const size_t smem = C ? (kv_fp8 ? att_smem<1, 1>() : att_smem<0, 1>()) : (kv_fp8 ? att_smem<1, 0>() : att_smem<0, 0>());
+  const auto [kern, smem] = att_form(kv, C > 0);
+  const auto *ks = static_cast<const __nv_bfloat16*>(k_scales), *vss = static_cast<const __nv_bfloat16*>(v_scales);
   // a programmatic dependent of the previous kernel in the stream (the kernel
   // waits for that grid before touching memory), so its launch and prologue
   // overlap the decode top-k
@@ -1071,7 +1129,7 @@ cudaError_t launch_sparse_attend(const AttnGeom& geo, const void* q, const void*
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  const float vs = kv_fp8 ? 256.f * v_scale : 1.f;
+  const float vs = kv == kKvE4m3 ? 256.f * v_scale : 1.f;
   auto* o = static_cast<__nv_bfloat16*>(out);
   if (C) {
     lc.gridDim = dim3(static_cast<unsigned>(S * C));
@@ -1080,22 +1138,19 @@ cudaError_t launch_sparse_attend(const AttnGeom& geo, const void* q, const void*
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     lc.numAttrs = 2;
-    auto kern = kv_fp8 ? sparse_attend_kernel<1, 1> : sparse_attend_kernel<0, 1>;
     cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    return cudaLaunchKernelEx(&lc, kern, kmap, vmap, qmap, q2k, geo, topk, scale_log2, vs, o, out_q, out_scale,
+    return cudaLaunchKernelEx(&lc, kern, kmap, vmap, qmap, q2k, geo, topk, scale_log2, vs, ks, vss, o, out_q, out_scale,
                               static_cast<float*>(nullptr), static_cast<int*>(nullptr), C, err);
   }
   // At least 4 units per CTA: a segment is then shared by at most ~topk/4 + 1
   // CTAs, which bounds the partials its last CTA has to merge.
   long long grid_l = (N + 3) / 4;
-  const long long max_ctas = static_cast<long long>(kv_fp8 ? AttShape<1, 0>::kCtasPerSm : AttShape<0, 0>::kCtasPerSm) *
-                             kNumSMs;
+  const long long max_ctas = per_sm * kNumSMs;
   if (grid_l > max_ctas) grid_l = max_ctas;
   if (grid_l < 1) grid_l = 1;
   lc.gridDim = dim3(static_cast<unsigned>(grid_l));
-  auto kern = kv_fp8 ? sparse_attend_kernel<1, 0> : sparse_attend_kernel<0, 0>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  return cudaLaunchKernelEx(&lc, kern, kmap, vmap, qmap, q2k, geo, topk, scale_log2, vs, o, out_q, out_scale,
+  return cudaLaunchKernelEx(&lc, kern, kmap, vmap, qmap, q2k, geo, topk, scale_log2, vs, ks, vss, o, out_q, out_scale,
                             partials, tickets, 1, err);
 }
 

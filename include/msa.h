@@ -614,6 +614,65 @@ msa_status msa_attend_chunk_fp8kv(const msa_config* cfg, const void* q, const vo
                                   float* lse, void* workspace, size_t workspace_bytes,
                                   void* stream);
 
+/* ---- the int8 K/V cache ---------------------------------------------------------
+ * A third form of the paged cache, beside bf16 and E4M3 with one scale per cache: the 128
+ * values of a token and KV head as int8 n and one bf16 scale s, each standing for n * s.
+ *   k_cache, v_cache   dev int8 [num_slots, 4, 128]
+ *   k_scales, v_scales dev bf16 [num_slots / 128, 4, 128]: by page, KV head and slot in the page
+ *   num_slots          a multiple of 128
+ * The scales need no calibration, and 7 bits of magnitude are 8 to 16 times E4M3's steps near a
+ * row's largest value.  msa_quantize_insert writes powers of two, with which n * s is a bf16
+ * number; the readers take any finite bf16 scale (n * s is then rounded to bf16 once where
+ * it is read back or enters a product). */
+
+/* Quantises K and V rows as they are written at their slots.  Per row of 128 values x:
+ * s = 2^(e - 6), 2^e the power of two at or below max |x| (e >= -127; a row of zeros: s = 2^-133),
+ * n = x / s rounded to nearest (ties to even), at most 127 in magnitude.  A row that holds an
+ * infinity or a NaN gets s = NaN and reads back as NaN.  The result does not depend on the
+ * order of anything: the same rows give the same bytes.
+ *   k, v      dev bf16 [tokens, 4, 128], consecutive tokens k_stride (v_stride) elements apart
+ *             (a multiple of 8, >= 512: slices of a fused projection's output)
+ *   slots     dev int64 [tokens], as msa_map_slots writes them; a negative one is not inserted, one
+ *             outside the cache is skipped and recorded (MSA_DEVERR_PAGE, detail = the row).  Two
+ *             rows with the same slot leave either's values, or some of each, there
+ *   workspace >= 256 bytes (only its device error word is used)
+ * Errors: MSA_ERR_NULL, MSA_ERR_SHAPE, MSA_ERR_ALIGN, MSA_ERR_WORKSPACE, MSA_ERR_CUDA. */
+msa_status msa_quantize_insert(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               const int64_t* slots, int64_t tokens, void* k_cache, void* v_cache,
+                               void* k_scales, void* v_scales, int64_t num_slots, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Reads ranges of the requests' contexts back as packed bf16 K and V (the layout that the
+ * prefill calls take): row cu_seqlens[r] + i is position starts[r] + i of request r.
+ *   page_table dev int32 [batch, max_blocks]
+ *   starts     dev int32 [batch], or NULL: from position 0
+ *   cu_seqlens dev int32 [batch + 1], cu_seqlens[0] = 0, not decreasing; rows from cu_seqlens[batch] on
+ *              are left as they are
+ *   k_out, v_out dev bf16 [total_tokens, 4, 128], which hold cu_seqlens[batch] <= total_tokens rows
+ * The rows of a request with a bad range (starts[r] < 0, or an end behind max_blocks * 128) become
+ * zero (MSA_DEVERR_LENGTH, detail r), and so do those of a page id outside the pool
+ * (MSA_DEVERR_PAGE, detail = the flat page-table index).
+ *   workspace  >= 256 bytes (only its device error word is used)
+ * Errors: MSA_ERR_NULL, MSA_ERR_SHAPE, MSA_ERR_ALIGN, MSA_ERR_WORKSPACE, MSA_ERR_CUDA. */
+msa_status msa_dequantize_gather(const void* k_cache, const void* v_cache, const void* k_scales,
+                                 const void* v_scales, int64_t num_slots, const int32_t* page_table,
+                                 const int32_t* starts, const int32_t* cu_seqlens, int batch,
+                                 int max_blocks, int64_t total_tokens, void* k_out, void* v_out,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* msa_sparse_attend_decode over an int8 cache, which is paged (page_table is required).  The
+ * int8 values enter the bf16 products exactly; a key's scale multiplies its score in fp32, a
+ * value's scale its softmax weight (rounded to bf16 before; the row sum is over the rounded ones).
+ * What lies behind a request's last key does not reach its rows, whatever it holds.
+ *   scale finite and > 0, scale * log2(e) a normal fp32 number (else MSA_ERR_SHAPE)
+ * Other arguments, the output and the errors as msa_sparse_attend_decode. */
+msa_status msa_sparse_attend_decode_int8kv(const msa_config* cfg, const void* q, const void* k_cache,
+                                           const void* v_cache, const void* k_scales,
+                                           const void* v_scales, const int32_t* q2k,
+                                           const int32_t* seq_lens, const int32_t* page_table, int batch,
+                                           int max_blocks, int64_t num_slots, float scale, void* out,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
