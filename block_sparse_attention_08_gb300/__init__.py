@@ -14,6 +14,10 @@ from .binding import (  # noqa: F401
     make_config,
     msa_attend_chunk,
     msa_attend_chunk_fp8kv,
+    msa_attend_chunk_int8kv,
+    msa_attend_shared,
+    msa_attend_shared_fp8kv,
+    msa_attend_shared_int8kv,
     msa_check_bounded_wait,
     msa_dequantize_gather,
     msa_index_produce_decode,

@@ -21,7 +21,7 @@ from . import _build
 
 H, G, D, DI, BLOCK = 64, 4, 128, 128, 128
 MSA_ERR_CUDA = 6  # msa_status for a failed CUDA call
-MODE_DECODE, MODE_PREFILL, MODE_PACK, MODE_PREFILL_BWD, MODE_CHUNK = 0, 1, 2, 3, 4
+MODE_DECODE, MODE_PREFILL, MODE_PACK, MODE_PREFILL_BWD, MODE_CHUNK, MODE_SHARED = 0, 1, 2, 3, 4, 5
 INDEX_DTYPES = {"bf16": 0, "e4m3": 1}
 DEVICE_ERRORS = {0: "none", 1: "page id outside the pool", 2: "block id outside the query's range",
                  3: "sequence length out of range", 4: "bounded on-chip wait gave up",
@@ -81,6 +81,10 @@ _SIGS = {
     "msa_sparse_attend_decode_int8kv": [CFG, P, P, P, P, P, P, P, P, I, I, I64, F, P, P, SZ, P],
     "msa_attend_chunk": [CFG, P, P, P, P, P, P, I, I, I64, I64, F, P, P, P, SZ, P],
     "msa_attend_chunk_fp8kv": [CFG, P, P, P, F, F, P, P, P, I, I, I64, I64, F, P, P, P, SZ, P],
+    "msa_attend_chunk_int8kv": [CFG, P, P, P, P, P, P, P, P, I, I, I64, I64, F, P, P, P, SZ, P],
+    "msa_attend_shared": [CFG, P, P, P, P, P, P, I, I, P, P, I, I64, I64, F, P, P, P, SZ, P],
+    "msa_attend_shared_fp8kv": [CFG, P, P, P, F, F, P, P, P, I, I, P, P, I, I64, I64, F, P, P, P, SZ, P],
+    "msa_attend_shared_int8kv": [CFG, P, P, P, P, P, P, P, P, I, I, P, P, I, I64, I64, F, P, P, P, SZ, P],
 }
 EXPORTS = tuple(_SIGS) + ("msa_status_string", "msa_last_cuda_error", "msa_cuda_error_string")
 
@@ -602,18 +606,39 @@ def msa_attend_chunk(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, *,
     are.  Bad lengths and pages are told to ``workspace`` (at least ``workspace_size(cfg, 4, tokens,
     page_table.shape[1])`` bytes); a request with bad lengths gets zeros and lse -inf.  A bf16 decode
     step does best with as many rows of q as requests."""
-    r = (_ext or _serving()).attend_chunk(False, q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, 1.0, 1.0,
-                                          scale, out, lse, _buf(workspace))
-    return r if type(r) is not int else _fail("msa_attend_chunk", r)
+    return _attend("msa_attend_chunk", 0, q, k_cache, v_cache, 1.0, 1.0, seq_lens, page_table, cu_seqlens_q, None, None, scale, out,
+                   lse, workspace)
 
 
 def msa_attend_chunk_fp8kv(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, *, k_scale=1.0, v_scale=1.0,
                            scale=None, out=None, lse=None, workspace=None):
     """:func:`msa_attend_chunk` over E4M3 caches standing for k_scale * k and v_scale * v
     (C: msa_attend_chunk_fp8kv)."""
-    r = (_ext or _serving()).attend_chunk(True, q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, k_scale,
-                                          v_scale, scale, out, lse, _buf(workspace))
-    return r if type(r) is not int else _fail("msa_attend_chunk_fp8kv", r)
+    return _attend("msa_attend_chunk_fp8kv", 1, q, k_cache, v_cache, k_scale, v_scale, seq_lens, page_table, cu_seqlens_q, None, None,
+                   scale, out, lse, workspace)
+
+
+def msa_attend_shared(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, group_offsets, shared_lens, *, scale=None,
+                      out=None, lse=None, workspace=None):
+    """:func:`msa_attend_chunk` for a batch whose requests share prefixes (C: msa_attend_shared): requests
+    ``group_offsets[g]`` .. ``group_offsets[g + 1]`` - 1 have the first ``shared_lens[g]`` tokens in common, in the same pages
+    (int32 [groups + 1] and [groups]; whole pages of 128 count).  Those are read for 16 tokens of the group at once.  A request
+    with fewer tokens before its new ones than its group shares has bad lengths.  ``workspace``: at least
+    ``workspace_size(cfg, 5, tokens, page_table.shape[1])`` bytes."""
+    return _attend("msa_attend_shared", 0, q, k_cache, v_cache, 1.0, 1.0, seq_lens, page_table, cu_seqlens_q, group_offsets,
+                   shared_lens, scale, out, lse, workspace)
+
+
+def msa_attend_shared_fp8kv(q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, group_offsets, shared_lens, *,
+                            k_scale=1.0, v_scale=1.0, scale=None, out=None, lse=None, workspace=None):
+    """:func:`msa_attend_shared` over E4M3 caches standing for k_scale * k and v_scale * v (C: msa_attend_shared_fp8kv)."""
+    return _attend("msa_attend_shared_fp8kv", 1, q, k_cache, v_cache, k_scale, v_scale, seq_lens, page_table, cu_seqlens_q,
+                   group_offsets, shared_lens, scale, out, lse, workspace)
+
+
+def _attend(name, kind, *args):
+    r = (_ext or _serving()).attend_chunk(kind, *args[:-1], _buf(args[-1]))
+    return r if type(r) is not int else _fail(name, r)
 
 
 # ---- the int8 K/V cache -----------------------------------------------------------------
@@ -645,6 +670,20 @@ def msa_sparse_attend_decode_int8kv(q, k_cache, v_cache, k_scales, v_scales, q2k
     r = (_ext or _serving()).sparse_attend_int8(q, k_cache, v_cache, k_scales, v_scales, q2k, seq_lens, page_table, scale,
                                                 out, _buf(workspace))
     return r if type(r) is not int else _fail("msa_sparse_attend_decode_int8kv", r)
+
+
+def msa_attend_chunk_int8kv(q, k_cache, v_cache, k_scales, v_scales, seq_lens, page_table, cu_seqlens_q, *, scale=None, out=None,
+                            lse=None, workspace=None):
+    """:func:`msa_attend_chunk` over an int8 cache (C: msa_attend_chunk_int8kv)."""
+    return _attend("msa_attend_chunk_int8kv", 2, q, k_cache, v_cache, k_scales, v_scales, seq_lens, page_table, cu_seqlens_q, None,
+                   None, scale, out, lse, workspace)
+
+
+def msa_attend_shared_int8kv(q, k_cache, v_cache, k_scales, v_scales, seq_lens, page_table, cu_seqlens_q, group_offsets,
+                             shared_lens, *, scale=None, out=None, lse=None, workspace=None):
+    """:func:`msa_attend_shared` over an int8 cache (C: msa_attend_shared_int8kv)."""
+    return _attend("msa_attend_shared_int8kv", 2, q, k_cache, v_cache, k_scales, v_scales, seq_lens, page_table, cu_seqlens_q,
+                   group_offsets, shared_lens, scale, out, lse, workspace)
 
 
 # ---- packing ----------------------------------------------------------------------

@@ -106,6 +106,10 @@ msa_status msa_workspace_size(const msa_config* cfg, int mode, int64_t n, int ma
     *bytes = chunk_scratch_offset() + attend_chunk_bytes(n, max_blocks);
     return MSA_OK;
   }
+  if (mode == MSA_MODE_SHARED) {
+    *bytes = chunk_scratch_offset() + attend_shared_bytes(n);
+    return MSA_OK;
+  }
   if (mode != MSA_MODE_DECODE && mode != MSA_MODE_PREFILL && mode != MSA_MODE_PREFILL_BWD) return MSA_ERR_SHAPE;
   if (mode != MSA_MODE_DECODE && !prefill_attend_fits(n, max_blocks * kBlock, cfg->topk)) return MSA_ERR_SHAPE;
   *bytes = layout(mode, n, max_blocks, cfg->topk).total;
@@ -606,30 +610,41 @@ msa_status msa_sparse_attend_decode_int8kv(const msa_config* cfg, const void* q,
                        out, nullptr, nullptr, workspace, workspace_bytes, stream, 2, 1.f, 1.f, k_scales, v_scales);
 }
 
-static msa_status attend_chunk(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
-                               int kv_fp8, float k_scale, float v_scale, const int32_t* seq_lens,
-                               const int32_t* page_table, const int32_t* cu_seqlens_q, int batch, int max_blocks,
-                               int64_t total_tokens, int64_t num_slots, float scale, void* out, float* lse,
-                               void* workspace, size_t workspace_bytes, void* stream) {
+static msa_status attend_chunk(const msa_config* cfg, ChunkLaunch L, void* workspace, size_t workspace_bytes, void* stream) {
   msa_status st = msa_config_check(cfg);
   if (st != MSA_OK) return st;
-  if (!q || !k_cache || !v_cache || !seq_lens || !page_table || !cu_seqlens_q || !out) return MSA_ERR_NULL;
-  if (batch < 1 || max_blocks < 1 || max_blocks > 0x7fffffff / kBlock || total_tokens < 1 ||
-      total_tokens >= (1LL << 31) || num_slots < 1 || num_slots >= (1LL << 31) || num_slots % kBlock)
+  if (!L.q || !L.k || !L.v || !L.seq_lens || !L.page_table || !L.cu || !L.out) return MSA_ERR_NULL;
+  if (L.batch < 1 || L.max_blocks < 1 || L.max_blocks > 0x7fffffff / kBlock || L.tokens < 1 || L.tokens >= (1LL << 31) ||
+      L.num_slots < 1 || L.num_slots >= (1LL << 31) || L.num_slots % kBlock)
     return MSA_ERR_SHAPE;
+  if (L.groups < 0 || L.groups > L.batch) return MSA_ERR_SHAPE;
+  if (L.groups && (!L.group_offsets || !L.shared_lens)) return MSA_ERR_NULL;
+  if (L.kv == 2)
+    if ((st = check_int8(L.k, L.v, L.k_scales, L.v_scales, L.num_slots)) != MSA_OK) return st;
   // A score's factor has to be a normal number too: an infinite one makes NaN of a score of zero, a zero one of a masked key.
-  if (!(scale > 0.f) || !std::isnormal(chunk_scale_log2(scale, k_scale))) return MSA_ERR_SHAPE;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return MSA_ERR_ALIGN;
-  if ((st = check_ws(workspace, workspace_bytes, chunk_scratch_offset() + attend_chunk_bytes(total_tokens, max_blocks))) !=
-      MSA_OK)
-    return st;
+  if (!(L.scale > 0.f) || !std::isnormal(chunk_scale_log2(L.scale, L.k_scale))) return MSA_ERR_SHAPE;
+  if (!aligned16(L.q) || !aligned16(L.k) || !aligned16(L.v) || !aligned16(L.out)) return MSA_ERR_ALIGN;
+  const size_t need = L.groups ? attend_shared_bytes(L.tokens) : attend_chunk_bytes(L.tokens, L.max_blocks);
+  if ((st = check_ws(workspace, workspace_bytes, chunk_scratch_offset() + need)) != MSA_OK) return st;
+  L.scratch = static_cast<uint8_t*>(workspace) + chunk_scratch_offset();
+  L.err = static_cast<DevError*>(workspace);
+  return cuda_result(launch_attend_chunk(L, static_cast<cudaStream_t>(stream)));
+}
+// An FP8 cache's scales: a row's factor is v_scale over its denominator, at most 2^15 for each of 2^31 keys: it stays a normal
+// number.
+static bool chunk_scales_fit(float k_scale, float v_scale) {
+  return k_scale > 0.f && v_scale >= 0x1p-80f && std::isfinite(k_scale) && std::isfinite(v_scale);
+}
+// The arguments that all these calls share.
+static ChunkLaunch chunk_launch(const void* q, const void* k_cache, const void* v_cache, int kv, const int32_t* seq_lens,
+                                const int32_t* page_table, const int32_t* cu_seqlens_q, int batch, int max_blocks,
+                                int64_t total_tokens, int64_t num_slots, float scale, void* out, float* lse) {
   ChunkLaunch L{};
   L.q = q;
   L.k = k_cache;
   L.v = v_cache;
-  L.kv_fp8 = kv_fp8;
-  L.k_scale = k_scale;
-  L.v_scale = v_scale;
+  L.kv = kv;
+  L.k_scale = L.v_scale = 1.f;
   L.seq_lens = seq_lens;
   L.page_table = page_table;
   L.cu = cu_seqlens_q;
@@ -640,17 +655,15 @@ static msa_status attend_chunk(const msa_config* cfg, const void* q, const void*
   L.scale = scale;
   L.out = out;
   L.lse = lse;
-  L.scratch = static_cast<uint8_t*>(workspace) + chunk_scratch_offset();
-  L.err = static_cast<DevError*>(workspace);
-  return cuda_result(launch_attend_chunk(L, static_cast<cudaStream_t>(stream)));
+  return L;
 }
 
 msa_status msa_attend_chunk(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
                             const int32_t* seq_lens, const int32_t* page_table, const int32_t* cu_seqlens_q,
                             int batch, int max_blocks, int64_t total_tokens, int64_t num_slots, float scale,
                             void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-  return attend_chunk(cfg, q, k_cache, v_cache, 0, 1.f, 1.f, seq_lens, page_table, cu_seqlens_q, batch, max_blocks,
-                      total_tokens, num_slots, scale, out, lse, workspace, workspace_bytes, stream);
+  return attend_chunk(cfg, chunk_launch(q, k_cache, v_cache, 0, seq_lens, page_table, cu_seqlens_q, batch, max_blocks,
+                                        total_tokens, num_slots, scale, out, lse), workspace, workspace_bytes, stream);
 }
 
 msa_status msa_attend_chunk_fp8kv(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
@@ -658,11 +671,70 @@ msa_status msa_attend_chunk_fp8kv(const msa_config* cfg, const void* q, const vo
                                   const int32_t* cu_seqlens_q, int batch, int max_blocks, int64_t total_tokens,
                                   int64_t num_slots, float scale, void* out, float* lse, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-  // a row's factor is v_scale over its denominator, at most 2^15 for each of 2^31 keys: it stays a normal number
-  if (!(k_scale > 0.f) || !(v_scale >= 0x1p-80f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
-    return MSA_ERR_SHAPE;
-  return attend_chunk(cfg, q, k_cache, v_cache, 1, k_scale, v_scale, seq_lens, page_table, cu_seqlens_q, batch,
-                      max_blocks, total_tokens, num_slots, scale, out, lse, workspace, workspace_bytes, stream);
+  if (!chunk_scales_fit(k_scale, v_scale)) return MSA_ERR_SHAPE;
+  ChunkLaunch L = chunk_launch(q, k_cache, v_cache, 1, seq_lens, page_table, cu_seqlens_q, batch, max_blocks, total_tokens,
+                               num_slots, scale, out, lse);
+  L.k_scale = k_scale;
+  L.v_scale = v_scale;
+  return attend_chunk(cfg, L, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_attend_chunk_int8kv(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
+                                   const void* k_scales, const void* v_scales, const int32_t* seq_lens,
+                                   const int32_t* page_table, const int32_t* cu_seqlens_q, int batch, int max_blocks,
+                                   int64_t total_tokens, int64_t num_slots, float scale, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  ChunkLaunch L = chunk_launch(q, k_cache, v_cache, 2, seq_lens, page_table, cu_seqlens_q, batch, max_blocks, total_tokens,
+                               num_slots, scale, out, lse);
+  L.k_scales = k_scales;
+  L.v_scales = v_scales;
+  return attend_chunk(cfg, L, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_attend_shared(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* seq_lens, const int32_t* page_table, const int32_t* cu_seqlens_q, int batch,
+                             int max_blocks, const int32_t* group_offsets, const int32_t* shared_lens, int groups,
+                             int64_t total_tokens, int64_t num_slots, float scale, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  ChunkLaunch L = chunk_launch(q, k_cache, v_cache, 0, seq_lens, page_table, cu_seqlens_q, batch, max_blocks, total_tokens,
+                               num_slots, scale, out, lse);
+  L.group_offsets = group_offsets;
+  L.shared_lens = shared_lens;
+  L.groups = groups;
+  return attend_chunk(cfg, L, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_attend_shared_fp8kv(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
+                                   float k_scale, float v_scale, const int32_t* seq_lens, const int32_t* page_table,
+                                   const int32_t* cu_seqlens_q, int batch, int max_blocks, const int32_t* group_offsets,
+                                   const int32_t* shared_lens, int groups, int64_t total_tokens, int64_t num_slots,
+                                   float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  if (!chunk_scales_fit(k_scale, v_scale)) return MSA_ERR_SHAPE;
+  ChunkLaunch L = chunk_launch(q, k_cache, v_cache, 1, seq_lens, page_table, cu_seqlens_q, batch, max_blocks, total_tokens,
+                               num_slots, scale, out, lse);
+  L.k_scale = k_scale;
+  L.v_scale = v_scale;
+  L.group_offsets = group_offsets;
+  L.shared_lens = shared_lens;
+  L.groups = groups;
+  return attend_chunk(cfg, L, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_attend_shared_int8kv(const msa_config* cfg, const void* q, const void* k_cache, const void* v_cache,
+                                    const void* k_scales, const void* v_scales, const int32_t* seq_lens,
+                                    const int32_t* page_table, const int32_t* cu_seqlens_q, int batch, int max_blocks,
+                                    const int32_t* group_offsets, const int32_t* shared_lens, int groups,
+                                    int64_t total_tokens, int64_t num_slots, float scale, void* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  ChunkLaunch L = chunk_launch(q, k_cache, v_cache, 2, seq_lens, page_table, cu_seqlens_q, batch, max_blocks, total_tokens,
+                               num_slots, scale, out, lse);
+  L.k_scales = k_scales;
+  L.v_scales = v_scales;
+  L.group_offsets = group_offsets;
+  L.shared_lens = shared_lens;
+  L.groups = groups;
+  return attend_chunk(cfg, L, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -51,6 +51,7 @@
 // 8.2 with one block.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "launch.h"
@@ -90,11 +91,21 @@ struct CaItem {
   int t0, ntok, g;  // first row of q, tokens, KV head
   int pos0, len;    // position of the first token, keys of the request
   int b0, nb;
-  int slot;         // partial slot, or -1: the piece is the whole item
+  int slot;         // partial slot, or -1: the piece is the whole item (kCaOwn, kCaShared: to be joined with other items)
+  int row;          // row of the page table
 };
+// Whole items of a token's own keys, and of those that its group shares: their sums go to the token's place.
+constexpr int kCaOwn = -2, kCaShared = -3;
 // For the joining kernel: an item that begins in CTA c and ends in CTA `last`.
 struct CaCut {
   int t0, ntok, g, last;
+};
+
+// The sums of whole items, and where a token's pieces are (CaPieces).
+struct CaTokens {
+  float4* o;    // [tokens][4][32][16]
+  float2* ml;   // [tokens][4][16]
+  int32_t* at;  // [tokens][4]
 };
 
 struct CaArgs {
@@ -116,10 +127,22 @@ struct CaArgs {
   float4* part1_o;  // [2 kNumSMs][32][16]
   float2* part1_ml; // [2 kNumSMs][16]
   DevError* err;
+  // int8: the rows' scales
+  const __nv_bfloat16 *k_scales, *v_scales;
+  // shared prefixes: groups of requests, and what each token's items left, by (token, KV head)
+  const int32_t *group_offsets, *shared_lens;
+  int groups;
+  CaTokens own, shared;
 };
 
-template <bool kFp8>
+// The caches' types (the template parameter kKv below).
+constexpr int kCaBf16 = 0, kCaE4m3 = 1, kCaI8 = 2;
+
+template <int kKv>
 struct CaShape {
+  static constexpr bool kFp8 = kKv != kCaBf16;  // 8-bit values (int8 as well): copied as they are, then widened
+  static constexpr bool kF16 = kKv == kCaE4m3;  // Q, K, V and P enter the products as fp16
+  static constexpr int kOnePlaces = kKv == kCaI8 ? 4 : kCaOnePlaces;  // (int8: the scales lie in the fifth's place)
   // 16-bit K / V tiles.  (E4M3: with 3 of them and 4 copied ones, the places of widened tiles came free too late: 0.63 ms
   // instead of 0.60 for 2548 tokens in chunks over 4k to 12k keys.)
   static constexpr int kTiles = kFp8 ? 4 : 5;
@@ -134,7 +157,7 @@ struct CaShape {
   static constexpr int kRegsSoftmax = kFp8 ? 208 : 216, kRegsIssue = kFp8 ? 56 : 72, kRegsWiden = 40;
   // fp16 weights are kept near the top of their range (at most 2^(kLift + kCaSlack) = 2^15), so that small ones
   // stay normal down to 2^-21 of the largest
-  static constexpr float kLift = kFp8 ? 7.f : 0.f;
+  static constexpr float kLift = kF16 ? 7.f : 0.f;
 };
 
 // A CTA's part [u0, u1) of all units.
@@ -149,21 +172,29 @@ __device__ __forceinline__ long long ca_eighths(long long x) {
   return 4 * q * (q - 1) + q * (x & 7);
 }
 // A request's n new tokens at positions len - n .. len - 1, as ceil(n / 16) items per KV head; item i sees the
-// blocks up to its last token's.
-struct CaReq {
+// blocks up to its last token's, without the first `skip` ones (which its group shares).  With `whole`: the n tokens of a
+// group's requests, which all see the blocks of the `len` shared keys.
+struct CaReqOf {
   int t0, n, len;
   bool apart;  // a last item of one token is not counted (it is shared out apart)
   int extra;   // units of an item besides its blocks
-  __device__ __forceinline__ bool one() const { return n % kCaTok == 1; }  // the last item has one token
+  int skip, row;  // (with shared prefixes alone) row: of the page table
+  bool whole;
+};
+template <bool kShared>
+struct CaReq : CaReqOf {
+  __device__ __forceinline__ bool one() const { return !(kShared && whole) && n % kCaTok == 1; }  // the last item has one token
   __device__ __forceinline__ int items() const { return (n + kCaTok - 1) / kCaTok - (apart && one()); }
   __device__ __forceinline__ int blocks(int i) const {
-    return (len - n + min(n, kCaTok * (i + 1)) - 1) / kBlock + 1;
+    if (kShared && whole) return len / kBlock;
+    return (len - n + min(n, kCaTok * (i + 1)) - 1) / kBlock + 1 - (kShared ? skip : 0);
   }
   __device__ __forceinline__ bool dual(int i) const { return n - kCaTok * i > kCaTok / 2; }  // both tiles
   // units of the items before item i (all of 16 tokens)
   __device__ __forceinline__ long long before(int i) const {
+    if (kShared && whole) return static_cast<long long>(len / kBlock + extra) * i;
     const long long a = (static_cast<long long>(len) - n + kCaTok - 1) / kCaTok;
-    return ca_eighths(a + i) - ca_eighths(a) + i + static_cast<long long>(extra) * i;
+    return ca_eighths(a + i) - ca_eighths(a) + i + static_cast<long long>(extra - (kShared ? skip : 0)) * i;
   }
   // units of item i
   __device__ __forceinline__ int units(int i) const { return extra + (dual(i) ? blocks(i) : (blocks(i) + 1) / 2); }
@@ -173,17 +204,77 @@ struct CaReq {
     return before(i) + units(i);
   }
   // units of the last item where that has one token and is shared out apart
-  __device__ __forceinline__ int one_units() const { return one() ? ((len - 1) / kBlock + 2) / 2 : 0; }
+  __device__ __forceinline__ int one_units() const { return one() ? ((len - 1) / kBlock + 2 - (kShared ? skip : 0)) / 2 : 0; }
+  // the items' sums are joined with others'
+  __device__ __forceinline__ bool joined() const { return kShared && (whole || skip > 0); }
 };
 __device__ __forceinline__ bool ca_good(const CaArgs& a, long long c0, long long c1, int len) {
   return c0 >= 0 && c0 <= c1 && c1 <= a.tokens && c1 - c0 <= len && (len + kBlock - 1LL) / kBlock <= a.max_blocks;
 }
-// Request r; one with bad lengths has no tokens.
-__device__ __forceinline__ CaReq ca_req(const CaArgs& a, int r, bool apart, int extra = 0) {
-  const int c0 = a.cu[r], c1 = a.cu[r + 1], len = a.seq_lens[r];
-  return ca_good(a, c0, c1, len) ? CaReq{c0, c1 - c0, len, apart, extra} : CaReq{0, 0, 0, apart, extra};
+// The requests of group g, the blocks that they share (0: none) and their tokens.  A group whose requests bring 16 tokens
+// or more on average fills its items without sharing, so it shares nothing; neither does one with offsets that are no range.
+struct CaGroup {
+  int r0, r1, blocks, t0, n;
+};
+__device__ __forceinline__ CaGroup ca_group(const CaArgs& a, int g) {
+  const int r0 = a.group_offsets[g], r1 = a.group_offsets[g + 1], blocks = a.shared_lens[g] / kBlock;
+  if (r0 < 0 || r1 > a.batch || r1 <= r0 || r1 - r0 < 2 || blocks < 1) return CaGroup{r0, r1, 0, 0, 0};
+  const long long c0 = a.cu[r0], c1 = a.cu[r1];
+  if (c0 < 0 || c1 < c0 || c1 > a.tokens || c1 - c0 >= static_cast<long long>(kCaTok) * (r1 - r0)) return CaGroup{r0, r1, 0, 0, 0};
+  return CaGroup{r0, r1, min(blocks, a.max_blocks), static_cast<int>(c0), static_cast<int>(c1 - c0)};
 }
+// The blocks that request r shares with its group.
+__device__ __forceinline__ int ca_skip(const CaArgs& a, int r) {
+  int lo = 0, hi = a.groups;  // the first group that ends behind r
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (a.group_offsets[mid + 1] > r) hi = mid;
+    else lo = mid + 1;
+  }
+  if (lo == a.groups) return 0;
+  const CaGroup g = ca_group(a, lo);
+  return g.r0 <= r ? g.blocks : 0;
+}
+// Whether request r is good, and the blocks that it shares.
+template <bool kShared>
+__device__ __forceinline__ bool ca_good_request(const CaArgs& a, int r, int c0, int c1, int len, int& skip) {
+  skip = kShared ? ca_skip(a, r) : 0;
+  return ca_good(a, c0, c1, len) && (!kShared || c0 == c1 || len - (c1 - c0) >= skip * kBlock);
+}
+// Entry r of the list of work: a request, with shared prefixes the groups before them; one with bad lengths has no tokens.
+template <bool kShared>
+__device__ __forceinline__ CaReq<kShared> ca_req(const CaArgs& a, int r, bool apart, int extra = 0) {
+  CaReq<kShared> q{CaReqOf{0, 0, 0, apart, extra, 0, 0, false}};
+  if (kShared) {
+    if (r < a.groups) {
+      const CaGroup g = ca_group(a, r);
+      if (g.blocks) q.t0 = g.t0, q.n = g.n, q.len = g.blocks * kBlock, q.row = g.r0, q.whole = true;
+      return q;
+    }
+    r -= a.groups;
+  }
+  const int c0 = a.cu[r], c1 = a.cu[r + 1], len = a.seq_lens[r];
+  int skip;
+  if (ca_good_request<kShared>(a, r, c0, c1, len, skip)) q.t0 = c0, q.n = c1 - c0, q.len = len, q.skip = skip, q.row = r;
+  return q;
+}
+// For the joining kernel where prefixes are shared: the pieces of a token's own item, and of its group's.
+struct CaPieces {
+  // join: there is something to join; shared: so is a part of the group's; cut: pieces of CTAs first .. last, else the token's
+  // place; one: of one-token items; e: the token's number in its item
+  bool join, shared, cut, one;
+  int first, last, e;
+  __device__ __forceinline__ int32_t code() const {
+    return join | shared << 1 | cut << 2 | one << 3 | e << 4 | first << 8 | last << 16;
+  }
+  __device__ static __forceinline__ CaPieces of(int32_t x) {
+    return CaPieces{(x & 1) != 0, (x & 2) != 0, (x & 4) != 0, (x & 8) != 0, min(x >> 8 & 255, kNumSMs - 1),
+                    min(x >> 16 & 255, kNumSMs - 1), x >> 4 & 15};
+  }
+};
+static_assert(kNumSMs <= 256 && kCaTok <= 16, "the fields of a CaPieces code");
 // Zeros for the rows of a request with bad lengths (the whole warp).
+template <bool kShared>
 __device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
   if (lane == 0) record_error(a.err, MSA_DEVERR_LENGTH, r);
   const long long c0 = max(0, a.cu[r]), c1 = min(a.tokens, static_cast<long long>(a.cu[r + 1]));
@@ -192,15 +283,19 @@ __device__ __noinline__ void ca_refuse(const CaArgs& a, int r, int lane) {
     out[i] = make_uint4(0u, 0u, 0u, 0u);
   if (a.lse)
     for (long long i = c0 * kHeads + lane; i < c1 * kHeads; i += 32) a.lse[i] = -INFINITY;
+  if (kShared)
+    for (long long i = c0 * kKvHeads + lane; i < c1 * kKvHeads; i += 32) a.own.at[i] = 0;
 }
 
 // This CTA's part of the requests with bad lengths (one warp).
+template <bool kShared>
 __device__ __forceinline__ void ca_refuse_bad(const CaArgs& a, int lane) {
   for (long long r0 = blockIdx.x; r0 < a.batch; r0 += 32LL * gridDim.x) {
     const long long r = r0 + static_cast<long long>(lane) * gridDim.x;
-    const bool bad = r < a.batch && !ca_good(a, a.cu[r], a.cu[r + 1], a.seq_lens[r]);
+    int skip;
+    const bool bad = r < a.batch && !ca_good_request<kShared>(a, static_cast<int>(r), a.cu[r], a.cu[r + 1], a.seq_lens[r], skip);
     for (unsigned m = __ballot_sync(0xffffffffu, bad); m; m &= m - 1)
-      ca_refuse(a, static_cast<int>(r0 + static_cast<long long>(__ffs(m) - 1) * gridDim.x), lane);
+      ca_refuse<kShared>(a, static_cast<int>(r0 + static_cast<long long>(__ffs(m) - 1) * gridDim.x), lane);
   }
 }
 
@@ -208,18 +303,19 @@ __device__ __forceinline__ void ca_refuse_bad(const CaArgs& a, int lane) {
 struct CaStart {
   long long unit;
   int r;
-  CaReq q;
+  CaReqOf q;
 };
 
-template <bool kFp8>
+template <int kKv>
 struct CaSmem {
+  static constexpr bool kFp8 = kKv != kCaBf16;
   uint8_t q[2][kCaTile];
-  uint8_t kv[CaShape<kFp8>::kTiles][kCaTile];
-  uint8_t raw[CaShape<kFp8>::kRaw][kFp8 ? kCaHalf : 16];
+  uint8_t kv[CaShape<kKv>::kTiles][kCaTile];
+  uint8_t raw[CaShape<kKv>::kRaw][kFp8 ? kCaHalf : 16];
   float2 ml[2][128];  // before the roles begin: the warps' sums
   uint64_t q_full[2], q_ready[2], q_empty[2];  // q_ready: as fp16 (E4M3 cache)
-  uint64_t kv_full[CaShape<kFp8>::kTiles], kv_empty[CaShape<kFp8>::kTiles];
-  uint64_t raw_full[CaShape<kFp8>::kRaw], raw_empty[CaShape<kFp8>::kRaw];
+  uint64_t kv_full[CaShape<kKv>::kTiles], kv_empty[CaShape<kKv>::kTiles];
+  uint64_t raw_full[CaShape<kKv>::kRaw], raw_empty[CaShape<kKv>::kRaw];
   uint64_t s_full[2], p_full[2], o_full[2], x_full, x_done, done;
   uint64_t info_full[kCaInfo], info_empty[kCaInfo];
   // one-token items: K and V bytes of a block per place (over kv and raw), descriptors, the warps' meeting
@@ -237,21 +333,23 @@ struct CaSmem {
 // The whole CTA: sums up the requests' units and finds this CTA's share of each kind, and where it begins.  The units that an
 // item counts besides its blocks depend on the total, so the items are summed up beside their blocks.  (The caller's barrier
 // follows.)
-template <bool kFp8, bool kOne>
-__device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm) {
-  constexpr int kThreads = CaShape<kFp8>::kThreads, kWarps = kThreads / 32, kKinds = kOne ? 2 : 1, kN = kOne ? 3 : 2;
+template <int kKv, bool kOne, bool kShared>
+__device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kKv>& sm) {
+  constexpr bool kFp8 = CaShape<kKv>::kFp8;
+  const int entries = a.batch + (kShared ? a.groups : 0);
+  constexpr int kThreads = CaShape<kKv>::kThreads, kWarps = kThreads / 32, kKinds = kOne ? 2 : 1, kN = kOne ? 3 : 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // all KV heads' units without the items' own, items (bf16: the one-token ones too), and units of one-token items: of this
   // thread's request, and of the warp's requests up to and with it (the warps' own sums in wsum)
   long long (*wsum)[kWarps] = reinterpret_cast<long long (*)[kWarps]>(&sm.ml[0][0]);
   static_assert(kN * kWarps * sizeof(long long) <= sizeof(sm.ml), "wsum lies over ml");
-  CaReq q{};
+  CaReq<kShared> q{};
   long long u[kN], incl[kN], base[kN] = {};
   auto pass = [&](int r0) {
     const int r = r0 + tid;
-    q = r < a.batch ? ca_req(a, r, kOne) : CaReq{};
+    q = r < entries ? ca_req<kShared>(a, r, kOne) : CaReq<kShared>{};
     u[0] = kKvHeads * q.per_head();
-    u[1] = kKvHeads * static_cast<long long>(q.items() + (kOne && !kFp8 && q.one()));
+    u[1] = kKvHeads * static_cast<long long>(q.items() + (kOne && !kFp8 && !kShared && q.one()));
     if constexpr (kOne) u[2] = kKvHeads * static_cast<long long>(q.one_units());
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
@@ -271,11 +369,11 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm
   // the units of either kind, out of the sums
   auto units = [&](const long long (&x)[kN], int k) {
     if (!kOne) return x[0] + extra * x[1];
-    if (kFp8 || apart) return k ? x[kN - 1] : x[0] + extra * x[1];
+    if (kFp8 || kShared || apart) return k ? x[kN - 1] : x[0] + extra * x[1];
     return k ? 0LL : x[0] + x[kN - 1] + extra * x[1];
   };
   auto split = [&](const long long (&total)[kN]) {
-    apart = kOne && (kFp8 || total[0] == 0);  // (bf16: only where there are no others)
+    apart = kOne && (kFp8 || kShared || total[0] == 0);  // (bf16: only where there are no others)
     extra = 0;
     extra = ca_item_units(units(total, 0));
 #pragma unroll
@@ -288,9 +386,9 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm
       s.u1 = min(s.total, s.total * (blockIdx.x + 1) / s.ctas);
     }
   };
-  const bool once = a.batch <= kThreads;
+  const bool once = entries <= kThreads;
   if (!once) {
-    for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
+    for (int r0 = 0; r0 < entries; r0 += kThreads) {
       pass(r0);
 #pragma unroll
       for (int n = 0; n < kN; ++n)
@@ -301,9 +399,9 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kFp8>& sm
 #pragma unroll
     for (int n = 0; n < kN; ++n) base[n] = 0;
   }
-  for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
+  for (int r0 = 0; r0 < entries; r0 += kThreads) {
     pass(r0);
-    const int warps = min(kWarps, (a.batch - r0 + 31) / 32);  // that hold requests
+    const int warps = min(kWarps, (entries - r0 + 31) / 32);  // that hold requests
     long long before[kN];
 #pragma unroll
     for (int n = 0; n < kN; ++n) before[n] = base[n] + incl[n] - u[n];
@@ -395,9 +493,11 @@ __device__ __forceinline__ uint32_t ca_widen2(uint32_t x) {
 // and read once.  (16 tokens over 128k keys, E4M3, 2.15 GB: 0.32 ms, 6.7 TB/s.)
 
 // The copies (the producer warp).
-template <bool kFp8>
+template <int kKv, bool kShared>
 __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CUtensorMap& vmap, const CaArgs& a,
-                                               const CaShareOf& share, CaSmem<kFp8>& sm) {
+                                               const CaShareOf& share, CaSmem<kKv>& sm) {
+  constexpr bool kFp8 = CaShape<kKv>::kFp8;
+  constexpr int kPlaces = CaShape<kKv>::kOnePlaces;
   const int lane = threadIdx.x & 31;
   DevError* err = a.err;
   uint8_t* places = &sm.kv[0][0];
@@ -409,17 +509,24 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
     if (share.u0 < share.u1) {
       int r = sm.start[1].r;
       const long long start = sm.start[1].unit;
-      CaReq q = sm.start[1].q;
+      CaReq<kShared> q{sm.start[1].q};
       int per = q.one_units();
       int g = (start >= per) + (start >= 2LL * per) + (start >= 3LL * per);
       int u = static_cast<int>(start - static_cast<long long>(g) * per);  // the unit in the item
       long long at = share.u0;
       while (true) {
-        const int blocks = (q.len - 1) / kBlock + 1, to = static_cast<int>(min(static_cast<long long>(per), u + share.u1 - at));
-        const int b = 2 * u;
-        CaItem it{q.t0 + q.n - 1, 1, g, q.len - 1, q.len, b, min(blocks, 2 * to) - b, 0};
-        it.slot = u == 0 && to == per ? -1 : static_cast<int>(2 * blockIdx.x + (u == 0));
-        if (u == 0 && to < per) cut = CaCut{it.t0, 1, g, static_cast<int>(((at + per) * share.ctas - 1) / share.total)};
+        const int blocks = (q.len - 1) / kBlock + 1 - (kShared ? q.skip : 0), to = static_cast<int>(min(static_cast<long long>(per), u + share.u1 - at));
+        const int b = 2 * u + (kShared ? q.skip : 0);  // (of the request's blocks)
+        CaItem it{q.t0 + q.n - 1, 1, g, q.len - 1, q.len, b, min(blocks, 2 * to) - 2 * u, 0, 0};
+        it.slot = u == 0 && to == per ? (q.joined() ? kCaOwn : -1) : static_cast<int>(2 * blockIdx.x + (u == 0));
+        if (kShared) {
+          if (u == 0 && lane == 0) {
+            const bool part = to < per;
+            a.own.at[static_cast<long long>(it.t0) * kKvHeads + g] =
+                CaPieces{part || q.joined(), q.joined(), part, true, static_cast<int>(blockIdx.x),
+                         part ? static_cast<int>(((at + per) * share.ctas - 1) / share.total) : 0, 0}.code();
+          }
+        } else if (u == 0 && to < per) cut = CaCut{it.t0, 1, g, static_cast<int>(((at + per) * share.ctas - 1) / share.total)};
         at += to - u;
         const int is = nitem % kCaInfo;
         if (!(ok = ca_wait(&sm.one_info_empty[is], ((nitem / kCaInfo) & 1) ^ 1, err, 840))) break;
@@ -428,7 +535,8 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
           mbar_arrive(&sm.one_info_full[is]);
         }
         ++nitem;
-        const int32_t* row = a.page_table + static_cast<long long>(r) * a.max_blocks + b;
+        const long long row0 = static_cast<long long>(kShared ? q.row : r) * a.max_blocks + b;
+        const int32_t* row = a.page_table + row0;
         int ids = 0, ids_next = lane < it.nb ? row[lane] : 0;
         for (int k = 0; k < it.nb && ok; ++k) {
           if ((k & 31) == 0) {
@@ -438,20 +546,26 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
           int page = __shfl_sync(0xffffffffu, ids, k & 31);
           const bool bad = page < 0 || page >= a.num_pages;
           if (bad) {
-            if (lane == 0) record_error(err, MSA_DEVERR_PAGE, static_cast<long long>(r) * a.max_blocks + b + k);
+            if (lane == 0) record_error(err, MSA_DEVERR_PAGE, row0 + k);
             page = 0;
           }
-          // E4M3: K and V to one place; bf16: to one each
+          // 8 bits: K and V to one place; bf16: to one each
 #pragma unroll
           for (int kv = 0; kv < (kFp8 ? 1 : 2); ++kv, ++nplace) {
-            const int s = nplace % kCaOnePlaces;
-            if (!(ok = ca_wait(&sm.one_empty[s], ((nplace / kCaOnePlaces) & 1) ^ 1, err, 841))) break;
+            const int s = nplace % kPlaces;
+            if (!(ok = ca_wait(&sm.one_empty[s], ((nplace / kPlaces) & 1) ^ 1, err, 841))) break;
             if (lane == 0) {
               sm.bad[s] = bad;
               uint8_t* st = places + s * kCaTile;
-              mbar_expect_tx(&sm.one_full[s], kCaTile);
+              mbar_expect_tx(&sm.one_full[s], kCaTile + (kKv == kCaI8 ? 4 * kBlock : 0));
               tma_load_3d(st, kv ? &vmap : &kmap, 0, g, page * kBlock, &sm.one_full[s]);
               tma_load_3d(st + kCaHalf, kFp8 || kv ? &vmap : &kmap, kFp8 ? 0 : 64, g, page * kBlock, &sm.one_full[s]);
+              if constexpr (kKv == kCaI8) {
+                uint8_t* sc = places + kPlaces * kCaTile + s * 4 * kBlock;
+                const long long from = (static_cast<long long>(page) * kKvHeads + g) * kBlock;
+                tma_bulk_g2s(sc, a.k_scales + from, 2 * kBlock, &sm.one_full[s]);
+                tma_bulk_g2s(sc + 2 * kBlock, a.v_scales + from, 2 * kBlock, &sm.one_full[s]);
+              }
             }
           }
         }
@@ -460,29 +574,31 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
         if (++g == kKvHeads) {
           g = 0;
           do {
-            q = ca_req(a, ++r, true);
+            q = ca_req<kShared>(a, ++r, true);
             per = q.one_units();
           } while (per == 0);
         }
       }
     }
-    if (lane == 0) (kFp8 ? a.cuts1 : a.cuts)[blockIdx.x] = cut;
+    if (!kShared && lane == 0) (kFp8 ? a.cuts1 : a.cuts)[blockIdx.x] = cut;
     if (ok && ca_wait(&sm.one_info_empty[nitem % kCaInfo], ((nitem / kCaInfo) & 1) ^ 1, err, 842) && lane == 0) {
-      sm.info[nitem % kCaInfo] = CaItem{0, 0, 0, 0, 0, 0, 0, 0};
+      sm.info[nitem % kCaInfo] = CaItem{0, 0, 0, 0, 0, 0, 0, 0, 0};
       mbar_arrive(&sm.one_info_full[nitem % kCaInfo]);
     }
     __syncwarp();
     if (lane == 0)  // no copy may still be landing when the CTA exits
-      for (int s = 0; s < kCaOnePlaces; ++s) {
-        const int fills = (nplace - s + kCaOnePlaces - 1) / kCaOnePlaces;
+      for (int s = 0; s < kPlaces; ++s) {
+        const int fills = (nplace - s + kPlaces - 1) / kPlaces;
         if (fills > 0) mbar_wait(&sm.one_full[s], (fills - 1) & 1, err, 843);
       }
   }
 }
 
 // The sums (warps 0 to 7).
-template <bool kFp8>
-__device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm, int warp) {
+template <int kKv, bool kShared>
+__device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kKv>& sm, int warp) {
+  constexpr bool kFp8 = CaShape<kKv>::kFp8, kI8 = kKv == kCaI8;
+  constexpr int kPlaces = CaShape<kKv>::kOnePlaces;
   const int lane = threadIdx.x & 31;
   DevError* err = a.err;
   uint8_t* places = &sm.kv[0][0];
@@ -499,7 +615,7 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm,
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.one_info_empty[is]);
       if (it.nb == 0) break;
-      // Q rows g8 and g8 + 8, the A operand.  bf16: k-step s holds dims 16 s + 2t, + 1, + 8, + 9.  E4M3 (as fp16): dims
+      // Q rows g8 and g8 + 8, the A operand.  bf16: k-step s holds dims 16 s + 2t, + 1, + 8, + 9.  E4M3 (as fp16), int8: dims
       // 16 s + 4 t .. + 3 in the same slots, which is where a lane's four bytes of K go.
       uint32_t qa[8][4];
       {
@@ -509,10 +625,13 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm,
         for (int s = 0; s < 8; ++s) {
           if constexpr (kFp8) {
             const uint2 x = reinterpret_cast<const uint2*>(q0 + 4 * t4)[4 * s], y = reinterpret_cast<const uint2*>(q1 + 4 * t4)[4 * s];
-            qa[s][0] = pack_f16(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u));
-            qa[s][1] = pack_f16(__uint_as_float(y.x << 16), __uint_as_float(y.x & 0xffff0000u));
-            qa[s][2] = pack_f16(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
-            qa[s][3] = pack_f16(__uint_as_float(y.y << 16), __uint_as_float(y.y & 0xffff0000u));
+            auto of = [](uint32_t w) {
+              return kI8 ? w : pack_f16(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            };
+            qa[s][0] = of(x.x);
+            qa[s][1] = of(y.x);
+            qa[s][2] = of(x.y);
+            qa[s][3] = of(y.y);
           } else {
             qa[s][0] = *reinterpret_cast<const uint32_t*>(q0 + 16 * s + 2 * t4);
             qa[s][1] = *reinterpret_cast<const uint32_t*>(q1 + 16 * s + 2 * t4);
@@ -521,16 +640,16 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm,
           }
         }
       }
-      constexpr float kLift = CaShape<kFp8>::kLift;
+      constexpr float kLift = CaShape<kKv>::kLift;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g8, g8 + 8; l: this lane's part
       // rows g8 (0, 1) and g8 + 8 (2, 3).  bf16: [n]: dims 8 n + 2t, + 1.  E4M3: [2 c + e]: dims 16 c + 4t + e, + 2 + e.
       float o[16][4];
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
       // The weights of a group of keys: x holds their scores, keys 8 i + 2t, + 1 of rows g8 (0, 1) and g8 + 8 (2, 3); the
-      // first `keys` count.  Raises the reference where a maximum passes it by kCaSlack, adds to l, and leaves P as the A
+      // first `keys` count; int8: vs[i] holds the scales of the two keys' values.  Raises the reference where a maximum passes it by kCaSlack, adds to l, and leaves P as the A
       // operand of k-steps of 16 keys.
-      auto weigh = [&](auto& x, auto& pa, int keys) {
+      auto weigh = [&](auto& x, auto& pa, int keys, const uint32_t* vs) {
         constexpr int kTiles = sizeof(x) / sizeof(x[0]);
         if (keys < 8 * kTiles)
 #pragma unroll
@@ -569,8 +688,15 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm,
 #pragma unroll
           for (int i = 0; i < kTiles; ++i) {
             const float p0 = ex2(fmaf(x[i][2 * h], a.scale_log2, -mu)), p1 = ex2(fmaf(x[i][2 * h + 1], a.scale_log2, -mu));
-            pa[i >> 1][2 * (i & 1) + h] = kFp8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
             l[h] += p0 + p1;
+            if constexpr (kI8) {
+              // the weights take the values' scales (behind the last key those may be anything: the weight stays zero)
+              const uint32_t w = vs[i];
+              pa[i >> 1][2 * (i & 1) + h] = pack_bf16(8 * i + 2 * t4 < keys ? p0 * __uint_as_float(w << 16) : 0.f,
+                                                      8 * i + 2 * t4 + 1 < keys ? p1 * __uint_as_float(w & 0xffff0000u) : 0.f);
+            } else {
+              pa[i >> 1][2 * (i & 1) + h] = kFp8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+            }
           }
         }
       };
@@ -588,10 +714,17 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm,
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.one_empty[s]);
       };
+      // four bytes of K, as the two 16-bit pairs that the products take
+      auto lo2 = [](uint32_t w) { return kI8 ? i8_lo2(w) : ca_widen2(w); };
+      auto hi2 = [](uint32_t w) { return kI8 ? i8_hi2(w) : ca_widen2(w >> 16); };
+      auto mma8 = [](float(&c)[4], const uint32_t(&x)[4], uint32_t b0, uint32_t b1) {
+        if constexpr (kI8) mma_bf16(c, x, b0, b1);
+        else mma_f16(c, x, b0, b1);
+      };
       bool ok = true;
       for (int k = 0; k < it.nb; ++k) {
-        const int s = nplace % kCaOnePlaces;
-        if (!(ok = ca_wait(&sm.one_full[s], (nplace / kCaOnePlaces) & 1, err, 845))) break;
+        const int s = nplace % kPlaces;
+        if (!(ok = ca_wait(&sm.one_full[s], (nplace / kPlaces) & 1, err, 845))) break;
         const int block_keys = sm.bad[s] ? 0 : min(kBlock, it.len - (it.b0 + k) * kBlock);
         const uint32_t kt = smem_u32(places + s * kCaTile);
         if constexpr (kFp8) {
@@ -607,26 +740,43 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm,
               for (int u = 0; u < 2; ++u) {
                 uint32_t kr[4];  // keys 16 u .. + 7 and .. + 15 of k-step c, then of k-step c + 1
                 ldsm_x4(kr, kt + sw128(mrow + 16 * u, c + (mi >> 1)));
-                mma_f16(x[2 * u], qa[c], ca_widen2(kr[0]), ca_widen2(kr[0] >> 16));
-                mma_f16(x[2 * u + 1], qa[c], ca_widen2(kr[1]), ca_widen2(kr[1] >> 16));
-                mma_f16(x[2 * u], qa[c + 1], ca_widen2(kr[2]), ca_widen2(kr[2] >> 16));
-                mma_f16(x[2 * u + 1], qa[c + 1], ca_widen2(kr[3]), ca_widen2(kr[3] >> 16));
+                mma8(x[2 * u], qa[c], lo2(kr[0]), hi2(kr[0]));
+                mma8(x[2 * u + 1], qa[c], lo2(kr[1]), hi2(kr[1]));
+                mma8(x[2 * u], qa[c + 1], lo2(kr[2]), hi2(kr[2]));
+                mma8(x[2 * u + 1], qa[c + 1], lo2(kr[3]), hi2(kr[3]));
               }
+            uint32_t vs[4] = {};
+            if constexpr (kI8) {
+              // scales of keys 8 i + 2t, + 1: K's go into the scores
+              const uint32_t* sc = reinterpret_cast<const uint32_t*>(places + kPlaces * kCaTile + s * 4 * kBlock) + 16 * (warp & 3) + t4;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t ks = sc[4 * i];
+                vs[i] = sc[kBlock / 2 + 4 * i];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i][e] *= __uint_as_float(e & 1 ? ks & 0xffff0000u : ks << 16);
+              }
+            }
             uint32_t pa[2][4];
-            weigh(x, pa, keys);
+            weigh(x, pa, keys, vs);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 uint32_t vr[4];  // keys 16 u .. + 7 and .. + 15 of dims 32 j .., then of dims 32 j + 16 ..
                 ldsm_x4_t(vr, vt + sw128(mrow + 16 * u, 2 * j + (mi >> 1)));
-                if (keys < 16 * (u + 1)) cut_v(vr, keys - 16 * u);
+                if (!kI8 && keys < 16 * (u + 1)) cut_v(vr, keys - 16 * u);  // (int8: always numbers)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                   // bytes of a register: key 2t dims 2n and 2n + 1, key 2t + 1 dims 2n and 2n + 1
-                  const uint32_t b0 = __byte_perm(vr[2 * c], 0, 0x3120), b1 = __byte_perm(vr[2 * c + 1], 0, 0x3120);
-                  mma_f16(o[4 * j + 2 * c], pa[u], ca_widen2(b0), ca_widen2(b1));
-                  mma_f16(o[4 * j + 2 * c + 1], pa[u], ca_widen2(b0 >> 16), ca_widen2(b1 >> 16));
+                  if constexpr (kI8) {
+                    mma_bf16(o[4 * j + 2 * c], pa[u], i8_even2(vr[2 * c]), i8_even2(vr[2 * c + 1]));
+                    mma_bf16(o[4 * j + 2 * c + 1], pa[u], i8_odd2(vr[2 * c]), i8_odd2(vr[2 * c + 1]));
+                  } else {
+                    const uint32_t b0 = __byte_perm(vr[2 * c], 0, 0x3120), b1 = __byte_perm(vr[2 * c + 1], 0, 0x3120);
+                    mma_f16(o[4 * j + 2 * c], pa[u], ca_widen2(b0), ca_widen2(b1));
+                    mma_f16(o[4 * j + 2 * c + 1], pa[u], ca_widen2(b0 >> 16), ca_widen2(b1 >> 16));
+                  }
                 }
               }
           }
@@ -650,13 +800,13 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm,
 #pragma unroll
               for (int e = 0; e < 4; ++e) y[i][e] = x[i][e] + x[i + 2][e];
             release(s);
-            weigh(y, pa, keys);
+            weigh(y, pa, keys, nullptr);
           } else {
             release(s);
           }
           ++nplace;
-          const int sv = nplace % kCaOnePlaces;
-          if (!(ok = ca_wait(&sm.one_full[sv], (nplace / kCaOnePlaces) & 1, err, 848))) break;
+          const int sv = nplace % kPlaces;
+          if (!(ok = ca_wait(&sm.one_full[sv], (nplace / kPlaces) & 1, err, 848))) break;
           ++nplace;
           if (keys > 0) {
             const uint32_t vt = smem_u32(places + sv * kCaTile);
@@ -716,9 +866,14 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm,
           v.w = fmaf(f, x.w, v.w);
         }
         if (it.slot >= 0) {
-          const long long rows = kFp8 ? kGroup : a.rows;
-          (kFp8 ? a.part1_o : a.part_o)[(static_cast<long long>(it.slot) * (kDim / 4) + lane) * rows + row] = v;
-          if (lane == 0) (kFp8 ? a.part1_ml : a.part_ml)[it.slot * rows + row] = make_float2(top, sum);
+          constexpr bool kApart = kFp8 || kShared;  // pieces of their own
+          const long long rows = kApart ? kGroup : a.rows;
+          (kApart ? a.part1_o : a.part_o)[(static_cast<long long>(it.slot) * (kDim / 4) + lane) * rows + row] = v;
+          if (lane == 0) (kApart ? a.part1_ml : a.part_ml)[it.slot * rows + row] = make_float2(top, sum);
+        } else if (kShared && it.slot == kCaOwn) {
+          const long long at = static_cast<long long>(it.t0) * kKvHeads + it.g;
+          a.own.o[(at * (kDim / 4) + lane) * kGroup + row] = v;
+          if (lane == 0) a.own.ml[at * kGroup + row] = make_float2(top, sum);
         } else {
           const long long orow = static_cast<long long>(it.t0) * kHeads + it.g * kGroup + row;
           const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
@@ -736,15 +891,18 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kFp8>& sm,
 }
 
 // kOne: one-token items may be computed apart (over an E4M3 cache always)
-template <bool kFp8, bool kOne>
-__global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kernel(
+// kShared: the requests' entries begin with those of the groups, and sums that belong together are joined by
+// shared_join_kernel
+template <int kKv, bool kOne, bool kShared>
+__global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel(
     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CaArgs a) {
-  using Shape = CaShape<kFp8>;
+  using Shape = CaShape<kKv>;
+  constexpr bool kFp8 = Shape::kFp8, kI8 = kKv == kCaI8;
   constexpr int kTiles = Shape::kTiles, kThreads = Shape::kThreads;
   constexpr int kRing = kFp8 ? Shape::kRaw : kTiles;  // places that tiles are copied into
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  CaSmem<kFp8>& sm = *reinterpret_cast<CaSmem<kFp8>*>(smem_raw);
+  CaSmem<kKv>& sm = *reinterpret_cast<CaSmem<kKv>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   DevError* err = a.err;
 
@@ -752,7 +910,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) {
       record_error(err, MSA_DEVERR_TIMEOUT, 899);
-      a.cuts[blockIdx.x] = a.cuts1[blockIdx.x] = CaCut{0, 0, 0, 0};
+      if (!kShared) a.cuts[blockIdx.x] = a.cuts1[blockIdx.x] = CaCut{0, 0, 0, 0};
     }
     return;
   }
@@ -805,7 +963,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  ca_find_shares<kFp8, kOne>(a, sm);
+  ca_find_shares<kKv, kOne, kShared>(a, sm);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -817,7 +975,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
   auto roles_done = [&] {
     if (!tiles) return;
     tc::fence_before();
-    if (kFp8) fence_proxy_async_smem();  // (bf16: either there are other items, or one-token items)
+    if (kFp8 || kShared) fence_proxy_async_smem();  // (bf16 else: either there are other items, or one-token items)
     __syncwarp();
     asm volatile("barrier.sync 1, %0;" ::"n"(kThreads) : "memory");
   };
@@ -833,7 +991,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     if (u0 < u1) {
       const int extra = sm.extra;
       int r = sm.start[0].r;
-      CaReq rq = sm.start[0].q;
+      CaReq<kShared> rq{sm.start[0].q};
       long long per = rq.per_head();
       int g = (sm.start[0].unit >= per) + (sm.start[0].unit >= 2 * per) + (sm.start[0].unit >= 3 * per);
       const long long rem = sm.start[0].unit - g * per;
@@ -863,11 +1021,15 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         it.g = g;
         it.pos0 = rq.len - rq.n + kCaTok * i;
         it.len = rq.len;
+        it.row = kShared ? rq.row : r;
+        if (kShared && rq.whole) it.pos0 = rq.len - 1;  // (all tokens see all keys)
         it.b0 = begun(at - item0);
         it.nb = begun(min(end, u1) - item0) - it.b0;
         const int b = it.b0;
         const bool to_end = b + it.nb == blocks;
-        it.slot = b == 0 && to_end ? -1 : static_cast<int>(2 * blockIdx.x + (b == 0));
+        it.slot = b == 0 && to_end ? (!rq.joined() ? -1 : rq.whole ? kCaShared : kCaOwn)
+                                   : static_cast<int>(2 * blockIdx.x + (b == 0));
+        if (kShared && !rq.whole) it.b0 += rq.skip;  // (of the request's blocks)
         at = end;
         item0 = end;
         if (it.nb > 0) {
@@ -880,8 +1042,9 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         }
         ++nitem;
         const int tiles = it.ntok > 8 ? 2 : 1;
-        const int32_t* row = a.page_table + static_cast<long long>(r) * a.max_blocks;
-        int ids = 0, ids_next = lane < it.nb ? row[b + lane] : 0;  // 32 page ids, and the next 32
+        const long long row0 = static_cast<long long>(it.row) * a.max_blocks + it.b0;
+        const int32_t* row = a.page_table + row0;
+        int ids = 0, ids_next = lane < it.nb ? row[lane] : 0;  // 32 page ids, and the next 32
         int last = 0, before = 0;  // pages of the last block that K was loaded of, and of the one before
         for (int j = 0; j < 2 * it.nb && ok; ++j) {  // tile j: K of block (j + 1) / 2 and V in turn
           const bool is_v = ca_is_v(j, it.nb);
@@ -890,12 +1053,12 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
             const int k = (j + 1) >> 1;
             if ((k & 31) == 0) {
               ids = ids_next;
-              ids_next = k + 32 + lane < it.nb ? row[b + k + 32 + lane] : 0;
+              ids_next = k + 32 + lane < it.nb ? row[k + 32 + lane] : 0;
             }
             page = __shfl_sync(0xffffffffu, ids, k & 31);
             const bool bad = page < 0 || page >= a.num_pages;
             if (bad) {
-              if (lane == 0) record_error(err, MSA_DEVERR_PAGE, static_cast<long long>(r) * a.max_blocks + b + k);
+              if (lane == 0) record_error(err, MSA_DEVERR_PAGE, row0 + k);
               page = 0;
             }
             if (lane == 0) sm.bad[nblk % kCaBad] = bad;
@@ -937,7 +1100,14 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         }
         }
         // (here, not before the copies: a division) the share that holds the item's last unit
-        if (b == 0 && !to_end) cut = CaCut{it.t0, it.ntok, g, static_cast<int>((end * ctas - 1) / total)};
+        if (kShared) {
+          if (b == 0 && lane < it.ntok)
+            (rq.whole ? a.shared : a.own).at[(static_cast<long long>(it.t0) + lane) * kKvHeads + g] =
+                CaPieces{!to_end || rq.joined(), rq.joined(), !to_end, false, static_cast<int>(blockIdx.x),
+                         to_end ? 0 : static_cast<int>((end * ctas - 1) / total), lane}.code();
+        } else if (b == 0 && !to_end) {
+          cut = CaCut{it.t0, it.ntok, g, static_cast<int>((end * ctas - 1) / total)};
+        }
         if (!ok || at >= u1) break;
         // the next item (the share goes on, so there is one)
         if (++i == rq.items()) {
@@ -945,15 +1115,15 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           if (++g == kKvHeads) {
             g = 0;
             do {
-              rq = ca_req(a, ++r, kOne && sm.apart, extra);
+              rq = ca_req<kShared>(a, ++r, kOne && sm.apart, extra);
             } while (rq.items() == 0);
           }
         }
       }
     }
-    if (lane == 0) a.cuts[blockIdx.x] = cut;
+    if (!kShared && lane == 0) a.cuts[blockIdx.x] = cut;
     if (tiles && ok && ca_wait(&sm.info_empty[nitem % kCaInfo], ((nitem / kCaInfo) & 1) ^ 1, err, 804) && lane == 0) {
-      sm.info[nitem % kCaInfo] = CaItem{0, 0, 0, 0, 0, 0, 0, 0};
+      sm.info[nitem % kCaInfo] = CaItem{0, 0, 0, 0, 0, 0, 0, 0, 0};
       mbar_arrive(&sm.info_full[nitem % kCaInfo]);
     }
     // no copy may still be landing when the CTA exits: wait for the last fill of every place
@@ -971,7 +1141,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     __syncwarp();
     roles_done();
     if constexpr (kOne)
-      if (sm.apart) ca_one_produce<kFp8>(kmap, vmap, a, sm.share[1], sm);
+      if (sm.apart) ca_one_produce<kKv, kShared>(kmap, vmap, a, sm.share[1], sm);
   } else if (warp == kCaMmaWarp) {
     // ---------------- S and O products ----------------
     // One thread issues them all, and they execute in the order in which they are issued: an S product that overwrites P
@@ -979,7 +1149,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     // the other's products.  (With a thread for each warpgroup's they fell into step, both softmaxes and then both
     // products at once: 1.59 ms instead of 1.34 ms for 2048 tokens over 32k keys.)  The thread holds few products
     // ahead of the tensor cores, so it looks for what the next ones need before it issues a group, not between groups.
-    constexpr uint32_t idesc_s = ca_idesc(kFp8), idesc_o = ca_idesc(kFp8) | (1u << 16);
+    constexpr uint32_t idesc_s = ca_idesc(Shape::kF16), idesc_o = ca_idesc(Shape::kF16) | (1u << 16);
     const bool leader = ca_elect();
     int base = 0, nq = 0;         // blocks and Q tiles of the items before
     uint32_t pcount[2] = {0, 0};  // P tiles taken
@@ -1050,7 +1220,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         // everything but the O products of the last block
         for (int q = 0; q < (dual ? 2 : 1) && ok; ++q) {
           const int t = nq + q;
-          ok = mbar_wait(kFp8 ? &sm.q_ready[t & 1] : &sm.q_full[t & 1], (t >> 1) & 1, err, 811);
+          ok = mbar_wait(Shape::kF16 ? &sm.q_ready[t & 1] : &sm.q_full[t & 1], (t >> 1) & 1, err, 811);
         }
         tc::fence_after();
         if (dual) {
@@ -1095,7 +1265,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     __syncwarp();
   } else if (warp == kCaMmaWarp + 1) {
     // ---------------- requests with bad lengths ----------------
-    ca_refuse_bad(a, lane);
+    ca_refuse_bad<kShared>(a, lane);
   } else if (warp < 8) {
     // ---------------- softmax, one row per thread; the end of an item ----------------
     ca_regs_up<Shape::kRegsSoftmax>();
@@ -1186,7 +1356,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
                   if (kLoad) top[q & 3] = fmax3(top[q & 3], xa, xb);
                   const float2 y = fma2(xa, xb, a.scale_log2, a.scale_log2, -mu, -mu);
                   const float pa = ex2(y.x), pb = ex2(y.y);
-                  pk[q] = kFp8 ? pack_f16(pa, pb) : pack_bf16(pa, pb);
+                  pk[q] = Shape::kF16 ? pack_f16(pa, pb) : pack_bf16(pa, pb);
                   add[q & 1] = add2(add[q & 1].x, add[q & 1].y, pa, pb);
                 }
                 tc::st_32x32b_x16(scol + ch * 16, pk);
@@ -1252,7 +1422,19 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       __syncwarp();
       tc::fence_after();
       if (active && (steps > 0 || shared)) {
-        const float inv = it.slot >= 0 ? 1.f : l == 0.f ? 0.f : a.v_scale / l;
+        const bool part = kShared ? it.slot != -1 : it.slot >= 0;
+        // where the sums go: a piece's place, or the token's
+        float4* po = a.part_o + static_cast<long long>(it.slot) * (kDim / 4) * a.rows + prow;
+        float2* pml = a.part_ml + static_cast<long long>(it.slot) * a.rows + prow;
+        int rows = a.rows;
+        if (kShared && it.slot < 0) {
+          const CaTokens& to = it.slot == kCaOwn ? a.own : a.shared;
+          const long long at = (static_cast<long long>(it.t0) + tok) * kKvHeads + it.g;
+          rows = kGroup;
+          po = to.o + at * (kDim / 4) * kGroup + (row & 15);
+          pml = to.ml + at * kGroup + (row & 15);
+        }
+        const float inv = part ? 1.f : l == 0.f ? 0.f : a.v_scale / l;
         f0 *= inv;
         f1 *= inv;
 #pragma unroll 1
@@ -1268,10 +1450,10 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
             o[q] = f0 != 0.f ? __uint_as_float(u[q]) * f0 : 0.f;
             if (shared && f1 != 0.f) o[q] = fmaf(__uint_as_float(v[q]), f1, o[q]);
           }
-          if (valid && it.slot >= 0) {
-            float4* p = a.part_o + (static_cast<long long>(it.slot) * (kDim / 4) + d / 4) * a.rows + prow;
+          if (valid && part) {
+            float4* p = po + static_cast<long long>(d / 4) * rows;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) p[q * a.rows] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) p[q * rows] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           } else if (valid) {
             uint32_t y[8];
 #pragma unroll
@@ -1281,7 +1463,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           __syncwarp();
         }
         if (valid && d0 == 0) {
-          if (it.slot >= 0) a.part_ml[static_cast<long long>(it.slot) * a.rows + prow] = make_float2(m, l);
+          if (part) *pml = make_float2(m, l);
           else if (a.lse) a.lse[orow] = l == 0.f ? -INFINITY : m + log2f(l);
         }
       }
@@ -1296,9 +1478,9 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
     }
     roles_done();
     if constexpr (kOne)
-      if (sm.apart) ca_one_attend<kFp8>(a, sm, warp);
+      if (sm.apart) ca_one_attend<kKv, kShared>(a, sm, warp);
   } else if (kFp8 && warp >= kCaWidenWarp) {
-    // ---------------- E4M3 pages and bf16 queries to fp16 ----------------
+    // ---------------- E4M3 pages and bf16 queries to fp16; int8 pages, with their rows' scales, to bf16 ----------------
     ca_regs_down<Shape::kRegsWiden>();
     constexpr int kLanes = 128, kStep = kLanes / 8;  // kStep: rows at once
     const int wt = tid - 32 * kCaWidenWarp;
@@ -1331,12 +1513,39 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
       const int is = n % kCaInfo;
       if (!(ok = ca_wait(&sm.info_full[is], (n / kCaInfo) & 1, err, 830))) break;
       const int nb = sm.info[is].nb, b0 = sm.info[is].b0, len = sm.info[is].len, ntok = sm.info[is].ntok;
+      // int8: each lane has the scale of one of the warp's 32 rows, asked for a tile ahead, from the pages as the producer
+      // finds them
+      const int i_row = 4 * (warp - kCaWidenWarp) + (lane & 3) + 16 * (lane >> 2);
+      const int32_t* table = a.page_table + static_cast<long long>(sm.info[is].row) * a.max_blocks + b0;
+      const int at_g = sm.info[is].g * kBlock + i_row;
+      int ids = 0, ids_next = 0, last = 0, before = 0;
+      uint32_t next_scale = 0;
+      if (kI8 && nb > 0) ids_next = lane < nb ? table[lane] : 0;
+      auto ask = [&](int j) {
+        if (j >= 2 * nb) return;
+        const bool is_v = ca_is_v(j, nb);
+        if (!is_v) {
+          const int k = (j + 1) >> 1;
+          if ((k & 31) == 0) {
+            ids = ids_next;
+            ids_next = k + 32 + lane < nb ? table[k + 32 + lane] : 0;
+          }
+          const int page = __shfl_sync(0xffffffffu, ids, k & 31);
+          before = last;
+          last = page < 0 || page >= a.num_pages ? 0 : page;
+        }
+        const int from = is_v && j < 2 * nb - 1 ? before : last;
+        next_scale = reinterpret_cast<const uint16_t*>(is_v ? a.v_scales : a.k_scales)[static_cast<long long>(from) * (kKvHeads * kBlock) + at_g];
+      };
+      if constexpr (kI8) ask(0);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.info_empty[is]);
       if (nb == 0) break;
       for (int j = 0; j < 2 * nb && ok; ++j) {
         const int load = 2 * base + j, rs = load % Shape::kRaw, st = load % kTiles;
         const bool is_v = ca_is_v(j, nb);
+        uint32_t scale = next_scale;
+        if constexpr (kI8) ask(j + 1);
         if (!(ok = ca_wait(&sm.raw_full[rs], (load / Shape::kRaw) & 1, err, 831))) break;
         // V rows behind the last key become zero: their weight is zero, but they may hold anything
         int keys = kBlock;
@@ -1344,6 +1553,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           const int k = ca_block_v(j, nb);
           keys = sm.bad[(base + k) % kCaBad] ? 0 : min(kBlock, len - (b0 + k) * kBlock);
         }
+        if (kI8) scale = i_row < keys ? scale * 0x10001u : 0u;  // (rows of zeros there, whatever the scales)
         const uint32_t src = smem_u32(sm.raw[kFp8 ? rs : 0]) + sw128(row0, piece);
         const uint32_t dst = smem_u32(sm.kv[st]) + (piece >> 2) * kCaHalf;
         const uint32_t dst0 = dst + sw128(row0, 2 * (piece & 3)), dst1 = dst + sw128(row0, 2 * (piece & 3) + 1);
@@ -1362,13 +1572,14 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
           for (int q = 0; q < 2; ++q) {
             const int down = (2 * n + q) * kStep;  // rows below row0, a multiple of the swizzle's eight
             uint4 v = x[n & 1][q];
-            if (keys < kBlock && row0 + down >= keys) v = make_uint4(0u, 0u, 0u, 0u);
+            if (!kI8 && keys < kBlock && row0 + down >= keys) v = make_uint4(0u, 0u, 0u, 0u);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t ss = kI8 ? __shfl_sync(0xffffffffu, scale, (row0 & 3) + 4 * (2 * n + q)) : 0u;
             uint32_t y[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              y[2 * i] = ca_widen2(w[i]);
-              y[2 * i + 1] = ca_widen2(w[i] >> 16);
+              y[2 * i] = kI8 ? mul_bf16x2(i8_lo2(w[i]), ss) : ca_widen2(w[i]);
+              y[2 * i + 1] = kI8 ? mul_bf16x2(i8_hi2(w[i]), ss) : ca_widen2(w[i] >> 16);
             }
             sts128(dst0 + down * 128, y[0], y[1], y[2], y[3]);
             sts128(dst1 + down * 128, y[4], y[5], y[6], y[7]);
@@ -1381,7 +1592,7 @@ __global__ void __launch_bounds__(CaShape<kFp8>::kThreads, 1) chunk_attend_kerne
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.kv_full[st]);
-        if (j == 0) widen_q(ntok);
+        if (!kI8 && j == 0) widen_q(ntok);
       }
       base += nb;
     }
@@ -1460,6 +1671,91 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_join_kernel(const __grid
     reinterpret_cast<uint4*>(a.out + row0 * kDim)[tid] = reinterpret_cast<const uint4*>(&out[0][0])[tid];
 }
 
+// The same where prefixes are shared: a CTA takes (token, KV head) pairs in turn, and joins the pieces of the token's own item
+// with those of its group's.  It asks for many pairs' codes at once, since most of a long batch's have nothing to join.
+__global__ void __launch_bounds__(kCaJoinThreads) shared_join_kernel(const __grid_constant__ CaArgs a) {
+  __shared__ float2 ml[2 * kNumSMs][kGroup];  // then .x: the piece's factor
+  __shared__ float inv[kGroup];
+  __shared__ __align__(16) uint2 out[kGroup][kDim / 4];
+  __shared__ long long todo[kCaJoinThreads];
+  __shared__ int count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long from = static_cast<long long>(max(a.cu[0], 0)) * kKvHeads;
+  const long long to = min(a.tokens, static_cast<long long>(a.cu[a.batch])) * kKvHeads;
+  const long long step = static_cast<long long>(gridDim.x) * kCaJoinThreads;
+  for (long long base = blockIdx.x; base < to; base += step) {
+    if (tid == 0) count = 0;
+    __syncthreads();
+    const long long p = base + static_cast<long long>(tid) * gridDim.x;
+    if (p >= from && p < to && CaPieces::of(a.own.at[p]).join) todo[atomicAdd(&count, 1)] = p;
+    __syncthreads();
+    const int pairs = count;
+    for (int k = 0; k < pairs; ++k) {
+      const long long at = todo[k];
+      const int32_t c0 = a.own.at[at], c1 = a.shared.at[at];
+      const CaPieces own = CaPieces::of(c0), with = CaPieces::of(c1);
+      const int n0 = own.cut ? max(own.last - own.first, 0) + 1 : 1;
+      const int n = n0 + (!own.shared ? 0 : with.cut ? max(with.last - with.first, 0) + 1 : 1);
+      // a piece's (m, l) and sums: of row 0, dims 0 .. 3, and the distance between rows of four dims
+      struct Piece {
+        const float2* ml;
+        const float4* o;
+        int rows;
+      };
+      auto piece = [&](int s) {
+        const bool mine = s < n0;
+        const CaPieces& c = mine ? own : with;
+        const CaTokens& t = mine ? a.own : a.shared;
+        if (!c.cut) return Piece{t.ml + at * kGroup, t.o + at * (kDim / 4) * kGroup, kGroup};
+        const int q = mine ? s : s - n0, rows = c.one ? kGroup : a.rows;
+        const long long slot = q == 0 ? 2 * c.first + 1 : 2 * (c.first + q), e0 = c.one ? 0 : c.e * kGroup;
+        return Piece{(c.one ? a.part1_ml : a.part_ml) + slot * rows + e0,
+                     (c.one ? a.part1_o : a.part_o) + slot * (kDim / 4) * rows + e0, rows};
+      };
+      for (int i = tid; i < n * kGroup; i += kCaJoinThreads) ml[i / kGroup][i % kGroup] = piece(i / kGroup).ml[i % kGroup];
+      __syncthreads();
+      const long long row0 = at / kKvHeads * kHeads + at % kKvHeads * kGroup;  // the token's first row
+      float m = -INFINITY, l = 0.f;  // of row `warp`
+      for (int s = lane; s < n; s += 32) m = fmaxf(m, ml[s][warp].x);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      for (int s = lane; s < n; s += 32) {
+        const float f = ml[s][warp].x == -INFINITY ? 0.f : ex2(ml[s][warp].x - m);
+        ml[s][warp].x = f;
+        l = fmaf(f, ml[s][warp].y, l);
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      if (lane == 0) {
+        inv[warp] = l == 0.f ? 0.f : a.v_scale / l;
+        if (a.lse) a.lse[row0 + warp] = l == 0.f ? -INFINITY : m + log2f(l);
+      }
+      __syncthreads();
+      const int row = tid % kGroup, d4 = tid / kGroup;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int s = 0; s < n; ++s) {
+        const Piece x = piece(s);
+        const float4 v = x.o[static_cast<long long>(d4) * x.rows + row];
+        const float f = ml[s][row].x;
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+      }
+      const float r = inv[row];
+      out[row][d4] = make_uint2(pack_bf16(o.x * r, o.y * r), pack_bf16(o.z * r, o.w * r));
+      __syncthreads();
+      if (tid < kGroup * kDim / 8)
+        reinterpret_cast<uint4*>(a.out + row0 * kDim)[tid] = reinterpret_cast<const uint4*>(&out[0][0])[tid];
+      __syncthreads();
+    }
+    __syncthreads();
+  }
+}
+
 // ---- host side ----------------------------------------------------------------------
 
 static size_t ca_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -1472,6 +1768,14 @@ size_t attend_chunk_bytes(long long tokens, int) {
   return ca_up(2 * kNumSMs * sizeof(CaCut)) + ca_up(rows * sizeof(float2)) + rows * kDim * sizeof(float) +
          ca_up(kCaRows1 * sizeof(float2)) + kCaRows1 * kDim * sizeof(float);
 }
+
+// With shared prefixes behind that: the sums of whole items and the codes of their pieces, of the tokens' own items and of
+// their groups'.
+static size_t ca_tokens_bytes(long long tokens) {
+  const size_t pairs = static_cast<size_t>(tokens) * kKvHeads;
+  return ca_up(pairs * sizeof(int32_t)) + ca_up(pairs * kGroup * sizeof(float2)) + pairs * kGroup * kDim * sizeof(float);
+}
+size_t attend_shared_bytes(long long tokens) { return attend_chunk_bytes(tokens, 0) + 2 * ca_tokens_bytes(tokens); }
 
 // q [T, 64, 128] bf16 as (dims 0-63, head % 8, dims / 64, head / 8, token): a token's 16 heads of a KV head in one box of
 // four 8-row swizzle atoms.
@@ -1501,24 +1805,24 @@ static bool ca_encode_kv(CUtensorMap* map, const void* base, cuuint64_t slots, b
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kFp8, bool kOne>
+template <int kKv, bool kOne, bool kShared>
 static cudaError_t ca_launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, const CaArgs& a,
                              cudaStream_t stream) {
-  constexpr size_t bytes = sizeof(CaSmem<kFp8>);
+  constexpr size_t bytes = sizeof(CaSmem<kKv>);
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-  if (const cudaError_t e = cudaFuncSetAttribute(chunk_attend_kernel<kFp8, kOne>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(bytes));
+  if (const cudaError_t e = cudaFuncSetAttribute(chunk_attend_kernel<kKv, kOne, kShared>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
       e != cudaSuccess)
     return e;
-  return launch_dependent(chunk_attend_kernel<kFp8, kOne>, dim3(kNumSMs), CaShape<kFp8>::kThreads, bytes, stream, qmap, kmap,
-                             vmap, a);
+  return launch_dependent(chunk_attend_kernel<kKv, kOne, kShared>, dim3(kNumSMs), CaShape<kKv>::kThreads, bytes, stream, qmap,
+                          kmap, vmap, a);
 }
 
 cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream) {
   if (const cudaError_t e0 = launch_prologue(); e0 != cudaSuccess) return e0;
   CUtensorMap qmap, kmap, vmap;
-  if (!ca_encode_q(&qmap, L.q, L.tokens) || !ca_encode_kv(&kmap, L.k, L.num_slots, L.kv_fp8) ||
-      !ca_encode_kv(&vmap, L.v, L.num_slots, L.kv_fp8))
+  if (!ca_encode_q(&qmap, L.q, L.tokens) || !ca_encode_kv(&kmap, L.k, L.num_slots, L.kv != kCaBf16) ||
+      !ca_encode_kv(&vmap, L.v, L.num_slots, L.kv != kCaBf16))
     return cudaErrorInvalidValue;
   CaArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(L.q);
@@ -1546,15 +1850,41 @@ cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream) {
   a.part1_ml = reinterpret_cast<float2*>(p);
   p += ca_up(kCaRows1 * sizeof(float2));
   a.part1_o = reinterpret_cast<float4*>(p);
+  p += kCaRows1 * kDim * sizeof(float);
   a.err = L.err;
+  a.k_scales = static_cast<const __nv_bfloat16*>(L.k_scales);
+  a.v_scales = static_cast<const __nv_bfloat16*>(L.v_scales);
+  if (L.groups > 0) {
+    a.group_offsets = L.group_offsets;
+    a.shared_lens = L.shared_lens;
+    a.groups = L.groups;
+    const size_t pairs = static_cast<size_t>(L.tokens) * kKvHeads;
+    for (CaTokens* t : {&a.own, &a.shared}) {
+      t->at = reinterpret_cast<int32_t*>(p);
+      p += ca_up(pairs * sizeof(int32_t));
+      t->ml = reinterpret_cast<float2*>(p);
+      p += ca_up(pairs * kGroup * sizeof(float2));
+      t->o = reinterpret_cast<float4*>(p);
+      p += pairs * kGroup * kDim * sizeof(float);
+    }
+    if (const cudaError_t e = L.kv == kCaBf16   ? ca_launch<kCaBf16, true, true>(qmap, kmap, vmap, a, stream)
+                              : L.kv == kCaE4m3 ? ca_launch<kCaE4m3, true, true>(qmap, kmap, vmap, a, stream)
+                                                : ca_launch<kCaI8, true, true>(qmap, kmap, vmap, a, stream);
+        e != cudaSuccess)
+      return e;
+    // (two CTAs an SM; a batch of single tokens has a CTA for each of its pairs)
+    const int ctas = static_cast<int>(std::min(static_cast<long long>(pairs), 2LL * kNumSMs));
+    return launch_dependent(shared_join_kernel, dim3(ctas), kCaJoinThreads, 0, stream, a);
+  }
   // A batch of single tokens has no more of them than requests.  (The code for such batches cost others 0.4 us a call, and
   // 16 tokens over 32k keys 3.)
-  if (const cudaError_t e = L.kv_fp8 ? ca_launch<true, true>(qmap, kmap, vmap, a, stream)
-                            : L.tokens <= L.batch ? ca_launch<false, true>(qmap, kmap, vmap, a, stream)
-                                                  : ca_launch<false, false>(qmap, kmap, vmap, a, stream);
+  if (const cudaError_t e = L.kv == kCaI8     ? ca_launch<kCaI8, true, false>(qmap, kmap, vmap, a, stream)
+                            : L.kv == kCaE4m3 ? ca_launch<kCaE4m3, true, false>(qmap, kmap, vmap, a, stream)
+                            : L.tokens <= L.batch ? ca_launch<kCaBf16, true, false>(qmap, kmap, vmap, a, stream)
+                                                  : ca_launch<kCaBf16, false, false>(qmap, kmap, vmap, a, stream);
       e != cudaSuccess)
     return e;
-  return launch_dependent(chunk_join_kernel, dim3(kNumSMs * (a.rows / kGroup + (L.kv_fp8 ? 1 : 0))), kCaJoinThreads, 0,
+  return launch_dependent(chunk_join_kernel, dim3(kNumSMs * (a.rows / kGroup + (L.kv != kCaBf16 ? 1 : 0))), kCaJoinThreads, 0,
                              stream, a);
 }
 

@@ -138,12 +138,16 @@ cudaError_t launch_dequantize(const DequantizeLaunch& L, cudaStream_t stream);
 // One chunk attention call.
 struct ChunkLaunch {
   const void *q, *k, *v;
-  int kv_fp8;
-  float k_scale, v_scale;
+  int kv;                            // the caches hold bf16 (0), E4M3 (1) or int8 (2)
+  float k_scale, v_scale;            // E4M3
+  const void *k_scales, *v_scales;   // int8
   const int32_t* seq_lens;
   const int32_t* page_table;
   const int32_t* cu;
   int batch, max_blocks;
+  const int32_t* group_offsets;      // shared prefixes; groups = 0: none
+  const int32_t* shared_lens;
+  int groups;
   long long tokens, num_slots;
   float scale;
   void* out;
@@ -155,6 +159,7 @@ cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream);
 // What it multiplies the products of q and the cache's values by: the score in base 2.
 inline float chunk_scale_log2(float scale, float k_scale) { return scale * 1.4426950408889634f * k_scale; }
 size_t attend_chunk_bytes(long long tokens, int max_blocks);
+size_t attend_shared_bytes(long long tokens);
 // First step of every launcher.  Clears the calling thread's last CUDA error
 // (the launches are checked with cudaGetLastError, which reports the calling
 // thread's error) and makes the current device's primary context current on

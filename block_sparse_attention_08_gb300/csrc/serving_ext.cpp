@@ -454,61 +454,6 @@ PyObject* rotary_insert(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// fp8, q, k_cache, v_cache, seq_lens, page_table, cu_seqlens_q, k_scale, v_scale, scale, out, lse, workspace
-PyObject* attend_chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return entry("attend_chunk", n, 13, [&]() -> PyObject* {
-    const bool fp8 = truth(a[0]);
-    const at::Tensor& q = tensor_of(a[1], "q", 3);
-    const c10::DeviceIndex d = device_of(q, "q");
-    const at::Tensor &k = tensor_of(a[2], "k_cache", 3), &v = tensor(a[3], "v_cache"), &lens = tensor(a[4], "seq_lens"),
-                     &table = tensor_of(a[5], "page_table", 2), &cu = tensor(a[6], "cu_seqlens_q");
-    const float k_scale = static_cast<float>(number(a[7])), v_scale = static_cast<float>(number(a[8]));
-    const float scale = a[9] == Py_None ? 0.088388347648318447f : static_cast<float>(number(a[9]));  // 1 / sqrt(128)
-    const int64_t tokens = q.size(0), batch = table.size(0), width = table.size(1);
-    fit(q, "q", at::kBFloat16, {tokens, kH, kD}, d);
-    if (fit_caches(k, v, d) != fp8)
-      throw Raise{PyExc_ValueError, std::string(fp8 ? "msa_attend_chunk_fp8kv takes float8_e4m3fn or uint8 caches, got "
-                                                    : "msa_attend_chunk takes bf16 caches, got ") +
-                                        c10::toString(k.scalar_type())};
-    fit(table, "page_table", at::kInt, {batch, width}, d);
-    fit(lens, "seq_lens", at::kInt, {batch}, d);
-    fit(cu, "cu_seqlens_q", at::kInt, {batch + 1}, d);
-    if (tokens < 1 || batch < 1 || batch > INT32_MAX || width < 1 || width > INT32_MAX)
-      return PyLong_FromLong(MSA_ERR_SHAPE);
-    const at::Tensor out = output(a[10], "out", at::kBFloat16, q.sizes(), d);
-    at::Tensor lse;
-    if (a[11] != Py_None) lse = output(a[11], "lse", at::kFloat, {tokens, kH}, d);
-    msa_config cfg;
-    msa_config_default(&cfg);
-    Space ws;
-    if (a[12] == Py_None) {
-      size_t bytes = 0;
-      const msa_status st = msa_workspace_size(&cfg, MSA_MODE_CHUNK, tokens, static_cast<int>(width), &bytes);
-      if (st != MSA_OK) return PyLong_FromLong(st);
-      ws.keep = at::empty({static_cast<int64_t>(bytes)},
-                          at::TensorOptions().dtype(at::kByte).device(c10::Device(c10::kCUDA, d)));
-      ws.at = ws.keep.data_ptr();
-      ws.bytes = bytes;
-    } else {
-      ws = error_word(a[12], d);
-    }
-    const msa_status st = run(d, [&](void* stream) {
-      const int32_t *lp = lens.const_data_ptr<int32_t>(), *tp = table.const_data_ptr<int32_t>(),
-                    *cp = cu.const_data_ptr<int32_t>();
-      float* sp = lse.defined() ? lse.data_ptr<float>() : nullptr;
-      const int b = static_cast<int>(batch), w = static_cast<int>(width);
-      return fp8 ? msa_attend_chunk_fp8kv(&cfg, q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), k_scale, v_scale,
-                                          lp, tp, cp, b, w, tokens, k.size(0), scale, out.data_ptr(), sp, ws.at, ws.bytes,
-                                          stream)
-                 : msa_attend_chunk(&cfg, q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), lp, tp, cp, b, w, tokens,
-                                    k.size(0), scale, out.data_ptr(), sp, ws.at, ws.bytes, stream);
-    });
-    if (st != MSA_OK) return PyLong_FromLong(st);
-    changed({out, lse});
-    return wrap(out);
-  });
-}
-
 // An int8 cache: its caches [slots, 4, 128], and its scales by page, KV head and slot.
 void fit_int8(const at::Tensor& k, const at::Tensor& v, const at::Tensor& ks, const at::Tensor& vs, c10::DeviceIndex d) {
   const int64_t slots = k.size(0);
@@ -518,6 +463,94 @@ void fit_int8(const at::Tensor& k, const at::Tensor& v, const at::Tensor& ks, co
     throw Raise{PyExc_ValueError, "k_cache has " + std::to_string(slots) + " slots, expected a multiple of 128"};
   fit(ks, "k_scales", at::kBFloat16, {slots / kD, kG, kD}, d);
   fit(vs, "v_scales", at::kBFloat16, {slots / kD, kG, kD}, d);
+}
+
+// kind, q, k_cache, v_cache, k_scale, v_scale, seq_lens, page_table, cu_seqlens_q, group_offsets, shared_lens, scale, out, lse,
+// workspace.  kind: 0 bf16, 1 E4M3 (one number each for k_scale and v_scale), 2 int8 (the rows' scales); group_offsets and
+// shared_lens None: msa_attend_chunk
+PyObject* attend_chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("attend_chunk", n, 15, [&]() -> PyObject* {
+    const int64_t kind = whole(a[0]);
+    const bool shared = a[9] != Py_None || a[10] != Py_None;
+    const at::Tensor& q = tensor_of(a[1], "q", 3);
+    const c10::DeviceIndex d = device_of(q, "q");
+    const at::Tensor &k = tensor_of(a[2], "k_cache", 3), &v = tensor(a[3], "v_cache"), &lens = tensor(a[6], "seq_lens"),
+                     &table = tensor_of(a[7], "page_table", 2), &cu = tensor(a[8], "cu_seqlens_q");
+    const float scale = a[11] == Py_None ? 0.088388347648318447f : static_cast<float>(number(a[11]));  // 1 / sqrt(128)
+    const int64_t tokens = q.size(0), batch = table.size(0), width = table.size(1);
+    fit(q, "q", at::kBFloat16, {tokens, kH, kD}, d);
+    float k_scale = 1.f, v_scale = 1.f;
+    at::Tensor k_scales, v_scales, offsets, lengths;
+    if (kind == 2) {
+      k_scales = tensor(a[4], "k_scales");
+      v_scales = tensor(a[5], "v_scales");
+      fit_int8(k, v, k_scales, v_scales, d);
+    } else {
+      k_scale = static_cast<float>(number(a[4]));
+      v_scale = static_cast<float>(number(a[5]));
+      if (fit_caches(k, v, d) != (kind == 1))
+        throw Raise{PyExc_ValueError, std::string(shared ? "msa_attend_shared" : "msa_attend_chunk") +
+                                          (kind == 1 ? "_fp8kv takes float8_e4m3fn or uint8 caches, got "
+                                                     : " takes bf16 caches, got ") +
+                                          c10::toString(k.scalar_type())};
+    }
+    fit(table, "page_table", at::kInt, {batch, width}, d);
+    fit(lens, "seq_lens", at::kInt, {batch}, d);
+    fit(cu, "cu_seqlens_q", at::kInt, {batch + 1}, d);
+    int groups = 0;
+    if (shared) {
+      lengths = tensor_of(a[10], "shared_lens", 1);
+      offsets = tensor(a[9], "group_offsets");
+      const int64_t g = lengths.size(0);
+      fit(lengths, "shared_lens", at::kInt, {g}, d);
+      fit(offsets, "group_offsets", at::kInt, {g + 1}, d);
+      if (g > batch)
+        throw Raise{PyExc_ValueError, "shared_lens has " + std::to_string(g) + " groups, the batch " + std::to_string(batch) +
+                                          " requests"};
+      groups = static_cast<int>(g);
+    }
+    if (tokens < 1 || batch < 1 || batch > INT32_MAX || width < 1 || width > INT32_MAX)
+      return PyLong_FromLong(MSA_ERR_SHAPE);
+    const at::Tensor out = output(a[12], "out", at::kBFloat16, q.sizes(), d);
+    at::Tensor lse;
+    if (a[13] != Py_None) lse = output(a[13], "lse", at::kFloat, {tokens, kH}, d);
+    msa_config cfg;
+    msa_config_default(&cfg);
+    Space ws;
+    if (a[14] == Py_None) {
+      size_t bytes = 0;
+      const msa_status st = msa_workspace_size(&cfg, groups ? MSA_MODE_SHARED : MSA_MODE_CHUNK, tokens, static_cast<int>(width),
+                                               &bytes);
+      if (st != MSA_OK) return PyLong_FromLong(st);
+      ws.keep = at::empty({static_cast<int64_t>(bytes)},
+                          at::TensorOptions().dtype(at::kByte).device(c10::Device(c10::kCUDA, d)));
+      ws.at = ws.keep.data_ptr();
+      ws.bytes = bytes;
+    } else {
+      ws = error_word(a[14], d);
+    }
+    const msa_status st = run(d, [&](void* stream) {
+      const void *qp = q.const_data_ptr(), *kp = k.const_data_ptr(), *vp = v.const_data_ptr();
+      const int32_t *lp = lens.const_data_ptr<int32_t>(), *tp = table.const_data_ptr<int32_t>(),
+                    *cp = cu.const_data_ptr<int32_t>(), *gp = groups ? offsets.const_data_ptr<int32_t>() : nullptr,
+                    *sl = groups ? lengths.const_data_ptr<int32_t>() : nullptr;
+      const void *ks = kind == 2 ? k_scales.const_data_ptr() : nullptr, *vs = kind == 2 ? v_scales.const_data_ptr() : nullptr;
+      float* sp = lse.defined() ? lse.data_ptr<float>() : nullptr;
+      const int b = static_cast<int>(batch), w = static_cast<int>(width);
+      void* op = out.data_ptr();
+      if (kind == 2)
+        return msa_attend_shared_int8kv(&cfg, qp, kp, vp, ks, vs, lp, tp, cp, b, w, gp, sl, groups, tokens, k.size(0), scale, op,
+                                        sp, ws.at, ws.bytes, stream);
+      if (kind == 1)
+        return msa_attend_shared_fp8kv(&cfg, qp, kp, vp, k_scale, v_scale, lp, tp, cp, b, w, gp, sl, groups, tokens, k.size(0),
+                                       scale, op, sp, ws.at, ws.bytes, stream);
+      return msa_attend_shared(&cfg, qp, kp, vp, lp, tp, cp, b, w, gp, sl, groups, tokens, k.size(0), scale, op, sp, ws.at,
+                               ws.bytes, stream);
+    });
+    if (st != MSA_OK) return PyLong_FromLong(st);
+    changed({out, lse});
+    return wrap(out);
+  });
 }
 
 // k, v, slots, k_cache, v_cache, k_scales, v_scales, workspace

@@ -70,7 +70,8 @@ enum {
   MSA_MODE_PREFILL = 1,
   MSA_MODE_PACK = 2,
   MSA_MODE_PREFILL_BWD = 3,
-  MSA_MODE_CHUNK = 4
+  MSA_MODE_CHUNK = 4,
+  MSA_MODE_SHARED = 5
 };
 
 /* Device error codes reported by msa_read_device_error. */
@@ -120,6 +121,7 @@ msa_status msa_config_check(const msa_config* cfg);
  *   MSA_MODE_PREFILL_BWD: as MSA_MODE_PREFILL, for msa_sparse_attend_prefill_backward.
  *   MSA_MODE_CHUNK  : n = total new tokens, max_blocks = blocks per row of the page table,
  *                     for msa_attend_chunk (alone, it needs its first 256 bytes zero-filled).
+ *   MSA_MODE_SHARED : as MSA_MODE_CHUNK, for msa_attend_shared with groups (67 KB a token more).
  * The workspace must be zero-filled once before its first use (see
  * msa_workspace_init), which clears the device error word and the decode
  * scorer's page-claim counter in its first 256 bytes, and the completion
@@ -672,6 +674,60 @@ msa_status msa_sparse_attend_decode_int8kv(const msa_config* cfg, const void* q,
                                            const int32_t* seq_lens, const int32_t* page_table, int batch,
                                            int max_blocks, int64_t num_slots, float scale, void* out,
                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* msa_attend_chunk over an int8 cache.  The int8 values enter the bf16 products with their rows'
+ * scales, exactly where those are powers of two (else n * s is rounded to bf16 for the items of
+ * two and more tokens).  Other arguments, the output and the errors as msa_attend_chunk. */
+msa_status msa_attend_chunk_int8kv(const msa_config* cfg, const void* q, const void* k_cache,
+                                   const void* v_cache, const void* k_scales, const void* v_scales,
+                                   const int32_t* seq_lens, const int32_t* page_table,
+                                   const int32_t* cu_seqlens_q, int batch, int max_blocks,
+                                   int64_t total_tokens, int64_t num_slots, float scale, void* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- attention of a batch that shares prefixes ----------------------------------
+ * msa_attend_chunk for requests whose contexts begin with the same tokens (instructions, a
+ * document, several samples of one prompt) in the same pages of the cache: group g is the requests
+ * group_offsets[g] .. group_offsets[g + 1] - 1, and the first floor(shared_lens[g] / 128) entries of
+ * their page-table rows are the same.  Those pages are read for 16 tokens of the group at once instead of
+ * for each request, and the parts over the shared and over each request's own keys are joined by
+ * their maxima and sums.  out, lse and every other argument are those of msa_attend_chunk on the
+ * same tables (which the sums' order may round differently).
+ *   group_offsets dev int32 [groups + 1], not decreasing, in [0, batch]; requests outside all groups share
+ *                 nothing
+ *   shared_lens   dev int32 [groups]: tokens that the group's requests share, context all of them: at
+ *                 most seq_lens[r] - new of each request r that brings new tokens (one that has fewer gets
+ *                 out 0 and lse -inf, MSA_DEVERR_LENGTH, detail r)
+ *   groups        0 to batch; 0: msa_attend_chunk (the arrays may be NULL)
+ *   workspace     >= msa_workspace_size(cfg, MSA_MODE_SHARED, total_tokens, max_blocks), with groups 0
+ *                 of MSA_MODE_CHUNK
+ * The shared pages are read through the row of the group's first request, whether or not that
+ * brings tokens.  A group whose requests bring 16 tokens or more each on average, or with a single
+ * request, gains nothing and is computed as if it shared nothing (so a request with a long chunk is best left
+ * outside its group); so is one whose offsets are no range in the batch. */
+msa_status msa_attend_shared(const msa_config* cfg, const void* q, const void* k_cache,
+                             const void* v_cache, const int32_t* seq_lens, const int32_t* page_table,
+                             const int32_t* cu_seqlens_q, int batch, int max_blocks,
+                             const int32_t* group_offsets, const int32_t* shared_lens, int groups,
+                             int64_t total_tokens, int64_t num_slots, float scale, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same over an FP8 cache (as msa_attend_chunk_fp8kv) and over an int8 cache (as
+ * msa_attend_chunk_int8kv). */
+msa_status msa_attend_shared_fp8kv(const msa_config* cfg, const void* q, const void* k_cache,
+                                   const void* v_cache, float k_scale, float v_scale,
+                                   const int32_t* seq_lens, const int32_t* page_table,
+                                   const int32_t* cu_seqlens_q, int batch, int max_blocks,
+                                   const int32_t* group_offsets, const int32_t* shared_lens, int groups,
+                                   int64_t total_tokens, int64_t num_slots, float scale, void* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, void* stream);
+msa_status msa_attend_shared_int8kv(const msa_config* cfg, const void* q, const void* k_cache,
+                                    const void* v_cache, const void* k_scales, const void* v_scales,
+                                    const int32_t* seq_lens, const int32_t* page_table,
+                                    const int32_t* cu_seqlens_q, int batch, int max_blocks,
+                                    const int32_t* group_offsets, const int32_t* shared_lens, int groups,
+                                    int64_t total_tokens, int64_t num_slots, float scale, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

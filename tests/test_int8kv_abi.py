@@ -56,6 +56,37 @@ def test_sparse_attend(lib):
         (15, size.value - 1, WORKSPACE)])
 
 
+def test_attend_chunk_and_shared(lib):
+    cfg, size, more = msa_config(), ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.msa_config_default(ctypes.byref(cfg)) == OK
+    assert lib.msa_workspace_size(ctypes.byref(cfg), 4, 100, 9, ctypes.byref(size)) == OK
+    assert lib.msa_workspace_size(ctypes.byref(cfg), 5, 100, 9, ctypes.byref(more)) == OK and more.value > size.value
+    bad = msa_config()
+    lib.msa_config_default(ctypes.byref(bad))
+    bad.head_dim = 64
+    c = ctypes.byref(cfg)
+    # cfg, q, caches, (scales,) seq_lens, page_table, cu, batch, max_blocks, (groups,) tokens, slots, scale, out, lse, workspace
+    for f, head, group in ((lib.msa_attend_chunk_int8kv, [FAKE] * 2, False), (lib.msa_attend_shared, [], True),
+                           (lib.msa_attend_shared_fp8kv, [1.0, 1.0], True), (lib.msa_attend_shared_int8kv, [FAKE] * 2, True)):
+        groups = [FAKE, FAKE, 2] if group else []
+        need = more.value if group else size.value
+        good = [c, FAKE, FAKE, FAKE] + head + [FAKE, FAKE, FAKE, 4, 9] + groups + [100, 1280, 0.1, FAKE, None, FAKE, need, None]
+        a = 4 + len(head)       # seq_lens
+        b = a + 5 + len(groups)  # tokens
+        cases = _tensors(1, 2, 3, b + 3) + [
+            (0, None, NULL), (0, ctypes.byref(bad), SHAPE), (a, None, NULL), (a + 1, None, NULL), (a + 2, None, NULL), (a + 3, 0, SHAPE),
+            (a + 4, 0, SHAPE), (a + 4, 1 << 24, SHAPE), (b, 0, SHAPE), (b, 1 << 31, SHAPE), (b + 1, 0, SHAPE), (b + 1, 1000, SHAPE),
+            (b + 1, 1 << 31, SHAPE), (b + 2, 0.0, SHAPE), (b + 2, math.nan, SHAPE), (b + 2, math.inf, SHAPE), (b + 2, -1.0, SHAPE),
+            (b + 5, None, WORKSPACE), (b + 5, FAKE + 16, WORKSPACE), (b + 6, need - 1, WORKSPACE)]
+        if group:
+            cases += [(a + 5, None, NULL), (a + 6, None, NULL), (a + 7, -1, SHAPE), (a + 7, 5, SHAPE)]
+        if head == [FAKE] * 2:
+            cases += _tensors(4, 5)
+        elif head:
+            cases += [(4, 0.0, SHAPE), (4, math.nan, SHAPE), (5, -1.0, SHAPE), (5, math.inf, SHAPE), (5, 2.0 ** -81, SHAPE)]
+        _refuses(f, good, cases)
+
+
 def test_the_binding_refuses_other_tensors():
     x = torch.zeros(4, 4, 128, dtype=torch.bfloat16)
     c = torch.zeros(128, 4, 128, dtype=torch.int8)
@@ -71,3 +102,11 @@ def test_the_binding_refuses_other_tensors():
         msa.msa_dequantize_gather(c, c, s, s, i[None], i, 4)
     with pytest.raises(ValueError, match="q must be a CUDA tensor"):
         msa.msa_sparse_attend_decode_int8kv(x, c, c, s, s, i[None, None], i, i[None])
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        msa.msa_attend_shared(x, c, c, i, i[None], i, i, i)
+    with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+        msa.msa_attend_shared_fp8kv(None, c, c, i, i[None], i, i, i)
+    with pytest.raises(ValueError, match="q has shape .4,., expected 3 dimensions"):
+        msa.msa_attend_shared_int8kv(i, c, c, s, s, i, i[None], i, i, i)
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        msa.msa_attend_chunk_int8kv(x, c, c, s, s, i, i[None], i)
