@@ -320,11 +320,9 @@ __device__ __forceinline__ uint32_t i8_pair(uint32_t t) {
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(t & 0xff7fff7fu), "r"(t & 0xff80ff80u));
   return d;
 }
-// Bytes 0 and 1 / 2 and 3 / 0 and 2 / 1 and 3 of a word.
+// Bytes 0 and 1 / 2 and 3 of a word.
 __device__ __forceinline__ uint32_t i8_lo2(uint32_t w) { return i8_pair(__byte_perm(w, 0x43434343u, 0x4140)); }
 __device__ __forceinline__ uint32_t i8_hi2(uint32_t w) { return i8_pair(__byte_perm(w, 0x43434343u, 0x4342)); }
-__device__ __forceinline__ uint32_t i8_even2(uint32_t w) { return i8_pair(__byte_perm(w, 0x43434343u, 0x4240)); }
-__device__ __forceinline__ uint32_t i8_odd2(uint32_t w) { return i8_pair(__byte_perm(w, 0x43434343u, 0x4341)); }
 
 // (a, b) -> bf16x2 hi = round(a, b) and lo = round(residuals): hi + lo holds
 // a and b to about 16 significant bits.

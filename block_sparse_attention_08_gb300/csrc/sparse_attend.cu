@@ -50,6 +50,7 @@
 // v_scale into the normalisation.
 #include <mutex>
 
+#include "int8_attend.cuh"
 #include "launch.h"
 
 namespace msa {
@@ -63,8 +64,6 @@ constexpr int kBoxBytes = kChunkKeys * 128;        // 64 rows x 128 bytes (64 bf
 constexpr int kAttStageBytes = 4 * kBoxBytes;      // K lo/hi + V lo/hi
 constexpr int kAttStage8Bytes = 2 * kBoxBytes;     // FP8 K/V: K + V, one box each
 constexpr int kConsumerWarps = 3;
-constexpr int kConsumerThreads = kConsumerWarps * 32;
-constexpr int kAttThreads = kConsumerThreads + 32;
 constexpr int kSegSlots = 2;
 constexpr int kQBoxBytes = kGroup * 128;            // 16 rows x 128 bytes (64 dims)
 constexpr int kCombStride = kDim + 8;               // padded fp32 row of the merge buffer
@@ -128,6 +127,11 @@ struct AttShape {
   static constexpr int kCtasPerSm = kKv ? 2 : 1;
   static constexpr int kQSlots = kKv ? 1 : kSegSlots;             // Q tiles in the segment ring
   static constexpr int kCombSlots = kKv ? 1 : kConsumerWarps - 1;  // stream-K: where states meet
+  // int8: two warps share a chunk, 32 keys each, so that its stage is soon refilled, and two take the next (with a chunk to each
+  // of six warps, 64 requests of 2048 selected keys took 71 us, and 78 with three)
+  static constexpr int kSharers = kKv == kKvI8 ? 2 : 1;
+  static constexpr int kConsumers = kKv == kKvI8 ? 4 : kConsumerWarps;
+  static constexpr int kThreads = 32 * (kConsumers + 1);
 };
 
 // Where the consumer warps' states meet (stream-K only).
@@ -178,7 +182,10 @@ __device__ __forceinline__ CombRef comb_ref(AttSmem<kKv, kSplit>& sm, int who) {
 }
 static_assert((kGroup * kCombStride + 2 * kGroup) * sizeof(float) <= kAttStage8Bytes, "a warp state fits in a stage");
 
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
+template <int kConsumers>
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+}
 
 __device__ __forceinline__ long long seg_begin(long long c, long long N, long long G) { return c * N / G; }
 __device__ __forceinline__ long long cta_of(long long i, long long N, long long G) {
@@ -264,9 +271,6 @@ __device__ __forceinline__ void merge_from_smem(WarpState& st, const CombRef& c,
   }
 }
 
-// The low (e = 0) or high value of a bf16 pair.
-__device__ __forceinline__ float bf16_of(uint32_t w, int e) { return __uint_as_float(e ? w & 0xffff0000u : w << 16); }
-
 // Two E4M3 values, rounded to nearest (ties to even) and saturated at +-448;
 // `lo` in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -342,21 +346,6 @@ __device__ __forceinline__ uint32_t e4m3_lo2(uint32_t w) { return e4m3_hb_to_f16
 __device__ __forceinline__ uint32_t e4m3_hi2(uint32_t w) { return e4m3_hb_to_f16x2_s8(__byte_perm(w, 0u, 0x3424)); }
 __device__ __forceinline__ uint32_t e4m3_even2(uint32_t w) { return e4m3_hb_to_f16x2_s8(__byte_perm(w, 0u, 0x2404)); }
 __device__ __forceinline__ uint32_t e4m3_odd2(uint32_t w) { return e4m3_hb_to_f16x2_s8(__byte_perm(w, 0u, 0x3414)); }
-
-// The same of an 8-bit cache's words, in the type that its products take.
-template <int kKv>
-__device__ __forceinline__ uint32_t lo2(uint32_t w) { return kKv == kKvI8 ? i8_lo2(w) : e4m3_lo2(w); }
-template <int kKv>
-__device__ __forceinline__ uint32_t hi2(uint32_t w) { return kKv == kKvI8 ? i8_hi2(w) : e4m3_hi2(w); }
-template <int kKv>
-__device__ __forceinline__ uint32_t even2(uint32_t w) { return kKv == kKvI8 ? i8_even2(w) : e4m3_even2(w); }
-template <int kKv>
-__device__ __forceinline__ uint32_t odd2(uint32_t w) { return kKv == kKvI8 ? i8_odd2(w) : e4m3_odd2(w); }
-template <int kKv>
-__device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (kKv == kKvI8) mma_bf16(c, a, b0, b1);
-  else mma_f16(c, a, b0, b1);
-}
 
 constexpr int kMaxCluster = 8;
 
@@ -462,7 +451,7 @@ __device__ __forceinline__ void split_finish(Smem& sm, int csize, int warp, int 
 // the units are split evenly over the grid and cut segments are merged
 // through fp32 partials in global memory and a ticket per segment.
 template <int kKv, int kSplit>
-__global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm) sparse_attend_kernel(
+__global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv, kSplit>::kCtasPerSm) sparse_attend_kernel(
     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
     const __grid_constant__ CUtensorMap qmap, const int32_t* __restrict__ q2k, AttnGeom geo, int topk,
     float scale_log2, float v_scale, const __nv_bfloat16* __restrict__ k_scales,
@@ -475,6 +464,7 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kStg = AttShape<kKv, kSplit>::kStages;
   constexpr int kQS = AttShape<kKv, kSplit>::kQSlots;
+  constexpr int kConsumers = AttShape<kKv, kSplit>::kConsumers;
   const long long N = static_cast<long long>(geo.nq) * kKvHeads * topk;
   const long long G = gridDim.x;
   long long lo, hi;
@@ -490,15 +480,15 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
   if (tid == 0) {
     for (int s = 0; s < kStg; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.empty[s], AttShape<kKv, kSplit>::kSharers);
     }
     for (int s = 0; s < kQS; ++s) {
       mbar_init(&sm.seg_full[s], 1);
-      mbar_init(&sm.seg_empty[s], kConsumerWarps);
+      mbar_init(&sm.seg_empty[s], kConsumers);
     }
     fence_mbar_init();
   }
-  if (warp == kConsumerWarps && lo < hi) {
+  if (warp == kConsumers && lo < hi) {
     if (lane == 0) {
       prefetch_tmap(&kmap);
       prefetch_tmap(&vmap);
@@ -533,7 +523,7 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
     return;
   }
 
-  if (warp == kConsumerWarps) {
+  if (warp == kConsumers) {
     // ---------------- producer warp ----------------
     long long sc = 0;
     int nseg = 0;
@@ -646,18 +636,22 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
     {
       const uint32_t qt = smem_u32(sm.qtile[ss]);
       if constexpr (kKv != 0) {
-        // (E4M3: as fp16) k slots permuted as the K fragments are (S = Q K^T below):
-        // slots 2t, 2t+1, 2t+8, 2t+9 of k-step s hold dims 16s + 4t .. + 3
+        // fp16 (int8: bf16, i8_queries), k slots permuted as the K fragments are
+        // (S = Q K^T below): slots 2t, 2t+1, 2t+8, 2t+9 of k-step s hold dims 16s + 4t .. + 3
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const int chunk = 2 * (kk & 3) + (t4 >> 1);  // 16-byte chunk of 8 dims in the box of 64
           const uint32_t off = (kk >> 2) * kQBoxBytes + 8 * (t4 & 1);
           const uint2 a = lds64(qt + off + sw128(g8, chunk));
           const uint2 b = lds64(qt + off + sw128(g8 + 8, chunk));
-          qa[kk][0] = kKv == kKvE4m3 ? bf16x2_to_f16x2(a.x) : a.x;
-          qa[kk][1] = kKv == kKvE4m3 ? bf16x2_to_f16x2(b.x) : b.x;
-          qa[kk][2] = kKv == kKvE4m3 ? bf16x2_to_f16x2(a.y) : a.y;
-          qa[kk][3] = kKv == kKvE4m3 ? bf16x2_to_f16x2(b.y) : b.y;
+          if constexpr (kKv == kKvI8) {
+            i8_queries(qa[kk], a, b);
+            continue;
+          }
+          qa[kk][0] = bf16x2_to_f16x2(a.x);
+          qa[kk][1] = bf16x2_to_f16x2(b.x);
+          qa[kk][2] = bf16x2_to_f16x2(a.y);
+          qa[kk][3] = bf16x2_to_f16x2(b.y);
         }
       } else {
         const int qrow = (lane & 7) + 8 * ((lane >> 3) & 1);
@@ -679,6 +673,10 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
     const bool pf = kSplit == 0 && warp == 0 && seg_end == range0 + topk && seg_lo > range0;
     const int pf_k = jn > 2 ? jn - 2 : 0;
 
+    I8State st8;  // (an int8 cache's sums, until the merge)
+    uint32_t at8[4];
+    if constexpr (kKv == kKvI8) i8_offsets(at8, 32 * (warp % 2), lane);
+    if constexpr (kKv == kKvI8) i8_clear(st8);
     WarpState st;
     st.m0 = st.m1 = -INFINITY;
     st.l0 = st.l1 = 0.f;
@@ -699,17 +697,27 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
       }
       for (int ch = 0; ch < nch; ++ch, ++sc) {
         const int s = static_cast<int>(sc % kStg);
-        if (s % kConsumerWarps != warp) continue;
+        constexpr int kSharers = AttShape<kKv, kSplit>::kSharers;
+        if (s % (kConsumers / kSharers) != warp / kSharers) continue;
         const int valid = min(kChunkKeys, nk - ch * kChunkKeys);  // keys of this chunk
         mbar_wait(&sm.full[s], static_cast<uint32_t>((sc / kStg) & 1), err, 300);
         const uint32_t stg = smem_u32(sm.stage[s]);
+        if constexpr (kKv == kKvI8) {
+          const int k0 = 32 * (warp % 2);
+          if (k0 < valid)
+            i8_attend32(st8, qa, stg, stg + kBoxBytes, at8, &sm.scales[s][k0 / 2 + t4],
+                        &sm.scales[s][(kChunkKeys + k0) / 2 + t4], valid - k0, scale_log2, t4);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.empty[s]);
+          continue;
+        }
         const int mi = lane >> 3;
         // ---- S = Q K^T over the chunk's keys (n-tiles of 8 keys, in pairs) ----
         float sacc[8][4];
 #pragma unroll
         for (int p = 0; p < 8; ++p) sacc[p][0] = sacc[p][1] = sacc[p][2] = sacc[p][3] = 0.f;
         if constexpr (kKv != 0) {
-          // E4M3 (or int8) K rows are 128 bytes: a 16-byte chunk is one k-step of 16 dims.
+          // E4M3 K rows are 128 bytes: a 16-byte chunk is one k-step of 16 dims.
           // ldmatrix (16-bit view) gives a lane 4 consecutive bytes, dims
           // 16s + 4t .. + 3 of one key, converted in registers into the B
           // fragment whose slots the Q fragments above were permuted to match.
@@ -721,10 +729,10 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
             for (int kk = 0; kk < 8; kk += 2) {
               uint32_t kr[4];  // keys lo / hi of k-step kk, then of k-step kk + 1
               ldsm_x4(kr, stg + sw128(krow, kk + (mi >> 1)));
-              mma8<kKv>(sacc[2 * kp], qa[kk], lo2<kKv>(kr[0]), hi2<kKv>(kr[0]));
-              mma8<kKv>(sacc[2 * kp + 1], qa[kk], lo2<kKv>(kr[1]), hi2<kKv>(kr[1]));
-              mma8<kKv>(sacc[2 * kp], qa[kk + 1], lo2<kKv>(kr[2]), hi2<kKv>(kr[2]));
-              mma8<kKv>(sacc[2 * kp + 1], qa[kk + 1], lo2<kKv>(kr[3]), hi2<kKv>(kr[3]));
+              mma_f16(sacc[2 * kp], qa[kk], e4m3_lo2(kr[0]), e4m3_hi2(kr[0]));
+              mma_f16(sacc[2 * kp + 1], qa[kk], e4m3_lo2(kr[1]), e4m3_hi2(kr[1]));
+              mma_f16(sacc[2 * kp], qa[kk + 1], e4m3_lo2(kr[2]), e4m3_hi2(kr[2]));
+              mma_f16(sacc[2 * kp + 1], qa[kk + 1], e4m3_lo2(kr[3]), e4m3_hi2(kr[3]));
             }
           }
         } else {
@@ -749,10 +757,8 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const bool ok = 8 * p + 2 * t4 + e < valid;
-            // (int8: with the key's own scale)
-            const float f = kKv == kKvI8 ? scale_log2 * bf16_of(sm.scales[s][kKv == kKvI8 ? 4 * p + t4 : 0], e) : scale_log2;
-            sacc[p][e] = ok ? sacc[p][e] * f : -INFINITY;
-            sacc[p][2 + e] = ok ? sacc[p][2 + e] * f : -INFINITY;
+            sacc[p][e] = ok ? sacc[p][e] * scale_log2 : -INFINITY;
+            sacc[p][2 + e] = ok ? sacc[p][2 + e] * scale_log2 : -INFINITY;
             mx0 = fmaxf(mx0, sacc[p][e]);
             mx1 = fmaxf(mx1, sacc[p][2 + e]);
           }
@@ -787,20 +793,7 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
           st.o[nd][2] *= al1;
           st.o[nd][3] *= al1;
         }
-        if constexpr (kKv == kKvI8) {
-          // the values' scales go into the weights that multiply them (a masked key's may be anything: its weight stays zero)
-#pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const uint32_t vs = sm.scales[s][kChunkKeys / 2 + 4 * p + t4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float f = 8 * p + 2 * t4 + e < valid ? bf16_of(vs, e) : 0.f;
-              sacc[p][e] *= f;
-              sacc[p][2 + e] *= f;
-            }
-          }
-        }
-        // ---- O += P V, one k-step per 16 keys (P exact in 16 bits after the rounding above; int8: with a power of two) ----
+        // ---- O += P V, one k-step per 16 keys (P exact in 16 bits after the rounding above) ----
 #pragma unroll
         for (int kp = 0; kp < 4; ++kp) {
           if (16 * kp >= valid) break;
@@ -810,7 +803,7 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
                                   pack16<kKv>(sacc[2 * kp + 1][2], sacc[2 * kp + 1][3])};
           const int vrow = 16 * kp + 8 * (mi & 1) + (lane & 7);
           if constexpr (kKv != 0) {
-            // The transposing ldmatrix (16-bit view) of 8-bit V gives a lane
+            // The transposing ldmatrix (16-bit view) of E4M3 V gives a lane
             // keys 2t, 2t+1 of dims 2g, 2g+1 of a 16-dim block: bytes 0 / 2 are
             // the pair of the even dim, 1 / 3 that of the odd one, so the block
             // feeds two n-tiles, its even and its odd dims (st.o[2c], [2c+1]).
@@ -818,10 +811,10 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
             for (int c = 0; c < 8; c += 2) {
               uint32_t vr[4];  // keys lo / hi of block c, then of block c + 1
               ldsm_x4_t(vr, stg + kBoxBytes + sw128(vrow, c + (mi >> 1)));
-              mma8<kKv>(st.o[2 * c], pa, even2<kKv>(vr[0]), even2<kKv>(vr[1]));
-              mma8<kKv>(st.o[2 * c + 1], pa, odd2<kKv>(vr[0]), odd2<kKv>(vr[1]));
-              mma8<kKv>(st.o[2 * c + 2], pa, even2<kKv>(vr[2]), even2<kKv>(vr[3]));
-              mma8<kKv>(st.o[2 * c + 3], pa, odd2<kKv>(vr[2]), odd2<kKv>(vr[3]));
+              mma_f16(st.o[2 * c], pa, e4m3_even2(vr[0]), e4m3_even2(vr[1]));
+              mma_f16(st.o[2 * c + 1], pa, e4m3_odd2(vr[0]), e4m3_odd2(vr[1]));
+              mma_f16(st.o[2 * c + 2], pa, e4m3_even2(vr[2]), e4m3_even2(vr[3]));
+              mma_f16(st.o[2 * c + 3], pa, e4m3_odd2(vr[2]), e4m3_odd2(vr[3]));
             }
           } else {
 #pragma unroll
@@ -840,31 +833,44 @@ __global__ void __launch_bounds__(kAttThreads, AttShape<kKv, kSplit>::kCtasPerSm
     }
     it = seg_end;
 
-    // ---- merge the three warps' states into warp 0 ----
+    // ---- merge the warps' states into warp 0 ----
+    if constexpr (kKv == kKvI8) {
+      st.m0 = st8.m[0];
+      st.m1 = st8.m[1];
+      st.l0 = st8.l[0];
+      st.l1 = st8.l[1];
+#pragma unroll
+      for (int nd = 0; nd < 16; ++nd)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[nd][e] = st8.o[nd][e];
+    }
     st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, 1);
     st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, 2);
     st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, 1);
     st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, 2);
     if constexpr (kSplit == 0 && AttShape<kKv, kSplit>::kCombSlots == 1) {
-      // one slot: warp 2, then warp 1, hands its state to warp 0 (warp 0 has
-      // read it before it reaches the next segment's first meeting, the only
-      // place the slot is written again)
-      consumer_sync();
-      if (warp == 2) state_to_smem<kKv>(st, comb_ref(sm, 1), g8, t4);
-      consumer_sync();
-      if (warp == 0) merge_from_smem<kKv>(st, comb_ref(sm, 1), g8, t4);
-      consumer_sync();
+      // one slot: the last warp, then the one before it and so on, hands its
+      // state to warp 0 (which has read the last before it reaches the next
+      // segment's first meeting, the only place the slot is written again)
+#pragma unroll 1
+      for (int w = kConsumers - 1; w > 1; --w) {
+        consumer_sync<kConsumers>();
+        if (warp == w) state_to_smem<kKv>(st, comb_ref(sm, 1), g8, t4);
+        consumer_sync<kConsumers>();
+        if (warp == 0) merge_from_smem<kKv>(st, comb_ref(sm, 1), g8, t4);
+      }
+      consumer_sync<kConsumers>();
       if (warp == 1) state_to_smem<kKv>(st, comb_ref(sm, 1), g8, t4);
-      consumer_sync();
-      if (warp > 0) continue;  // warps 1 and 2 go on to the next segment
+      consumer_sync<kConsumers>();
+      if (warp > 0) continue;  // the others go on to the next segment
       merge_from_smem<kKv>(st, comb_ref(sm, 1), g8, t4);
     } else {
-      consumer_sync();
+      consumer_sync<kConsumers>();
       if (warp > 0) state_to_smem<kKv>(st, comb_ref(sm, warp), g8, t4);
-      consumer_sync();
+      consumer_sync<kConsumers>();
       if (warp > 0) continue;  // warps 1 and 2 go on to the next segment
 #pragma unroll
-      for (int w = 1; w < kConsumerWarps; ++w) merge_from_smem<kKv>(st, comb_ref(sm, w), g8, t4);
+      for (int w = 1; w < kConsumers; ++w) merge_from_smem<kKv>(st, comb_ref(sm, w), g8, t4);
     }
     __syncwarp();
     state_to_smem<kKv>(st, comb_ref(sm, 0), g8, t4);  // staging for coalesced stores (read only by warp 0)
@@ -1002,7 +1008,8 @@ static bool make_kv_map(CUtensorMap* map, const void* base, long long rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D map over a [rows, 4, 128] E4M3 array; box = 128 dims (128 bytes) x 1 head x 64 rows, 128-byte swizzle.
+// 3-D map over a [rows, 4, 128] array of 8-bit values; box = 128 dims (128 bytes) x 1 head x 64 rows, 128-byte swizzle.  A
+// head's row is 128 bytes: with promotion to 256, L2 would fetch the neighbouring head's with it, which another selection reads.
 static bool make_kv_map8(CUtensorMap* map, const void* base, long long rows) {
   EncodeTiledFn enc = get_encode_tiled();
   if (!enc) return false;
@@ -1012,7 +1019,7 @@ static bool make_kv_map8(CUtensorMap* map, const void* base, long long rows) {
   cuuint32_t box[3] = {128, 1, kChunkKeys};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1046,9 +1053,12 @@ using AttKernel = decltype(&sparse_attend_kernel<kKvBf16, 0>);
 struct AttForm {
   AttKernel kernel;
   size_t smem;
+  int threads;
 };
 template <int kKv, int kSplit>
-constexpr AttForm att_form_of() { return AttForm{sparse_attend_kernel<kKv, kSplit>, att_smem<kKv, kSplit>()}; }
+constexpr AttForm att_form_of() {
+  return AttForm{sparse_attend_kernel<kKv, kSplit>, att_smem<kKv, kSplit>(), AttShape<kKv, kSplit>::kThreads};
+}
 static AttForm att_form(int kv, bool split) {
   if (kv == kKvI8) return split ? att_form_of<kKvI8, 1>() : att_form_of<kKvI8, 0>();
   if (kv == kKvE4m3) return split ? att_form_of<kKvE4m3, 1>() : att_form_of<kKvE4m3, 0>();
@@ -1066,11 +1076,11 @@ static int max_active_clusters(int kv, int c) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
   if (done[dev][kv][c]) return cache[dev][kv][c];
-  const auto [kern, smem] = att_form(kv, true);
+  const auto [kern, smem, threads] = att_form(kv, true);
   int n = 0;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>(c * 16));
-  lc.blockDim = dim3(kAttThreads);
+  lc.blockDim = dim3(threads);
   lc.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1115,13 +1125,13 @@ cudaError_t launch_sparse_attend(const AttnGeom& geo, const void* q, const void*
     const int fit = max_active_clusters(kv, c);
     if (fit > 0 && S <= fit) C = c;
   }
-  const auto [kern, smem] = att_form(kv, C > 0);
+  const auto [kern, smem, threads] = att_form(kv, C > 0);
   const auto *ks = static_cast<const __nv_bfloat16*>(k_scales), *vss = static_cast<const __nv_bfloat16*>(v_scales);
   // a programmatic dependent of the previous kernel in the stream (the kernel
   // waits for that grid before touching memory), so its launch and prologue
   // overlap the decode top-k
   cudaLaunchConfig_t lc = {};
-  lc.blockDim = dim3(kAttThreads);
+  lc.blockDim = dim3(threads);
   lc.dynamicSmemBytes = smem;
   lc.stream = stream;
   cudaLaunchAttribute attr[2];

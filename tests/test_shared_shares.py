@@ -146,7 +146,8 @@ def walk(work, c, extra, total, emit, mistake):
                         break
 
 
-def walk_one(work, c, total, emit, mistake):
+def walk_one(work, cta, total, emit, mistake):
+    c = CTAS - 1 - cta
     ctas, u0, u1 = split(total, c, 0)
     if u0 >= u1:
         return
