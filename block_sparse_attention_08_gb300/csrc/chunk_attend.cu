@@ -1590,7 +1590,7 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
             sts128(dst0 + down * 128, y[0], y[1], y[2], y[3]);
             sts128(dst1 + down * 128, y[4], y[5], y[6], y[7]);
           }
-          if (n + 2 == kBatches) {
+          if (n + 1 == kBatches) {  // (once the last rows have been stored: a load that is only asked for may still read the place)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.raw_empty[rs]);
           }

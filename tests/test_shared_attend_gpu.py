@@ -250,3 +250,16 @@ def test_calls_on_two_streams_and_a_replayed_graph():
         graph.replay()
         expect = b.call(b.q, *b.cache, lens, b.table, b.cu, off, shared)
         assert torch.equal(out, expect)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("name,plain", [("16 tokens", False), ("9 tokens, long", False), ("drafted tokens", False), ("chunks and single tokens", True),
+                                        ("drafted tokens", True)])
+def test_calls_behind_one_another_give_the_same_bits(name, plain, kind):
+    """Many calls with nothing between them: a tile that is given back before it has been read shows in some of them."""
+    b = Batch(SHAPES[name], kind)
+    lens, off, shared = ints(b.lens), ints(b.off), ints(b.shared)
+    args = (b.q, *b.cache, lens, b.table, b.cu) + (() if plain else (off, shared))
+    call = b.plain if plain else b.call
+    outs = [call(*args, **b.more({})) for _ in range(60)]
+    assert all(torch.equal(outs[0], x) for x in outs)
