@@ -184,6 +184,10 @@ __device__ __forceinline__ void i8_attend32(I8State& st, const uint32_t (&qa)[8]
         mma_bf16(st.o[2 * (2 * c + i) + 1], pa[u], o0, o1);
       }
   }
+  // the caller gives the tiles back next: no load of them may be put off until then
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    asm volatile("" ::"r"(r[1][u][0]), "r"(r[1][u][1]), "r"(r[1][u][2]), "r"(r[1][u][3]) : "memory");
 }
 
 }  // namespace msa

@@ -22,8 +22,8 @@ def eighths(x):
 
 
 class Entry:
-    def __init__(self, t0=0, n=0, length=0, skip=0, whole=False, extra=0):
-        self.t0, self.n, self.len, self.skip, self.whole, self.extra = t0, n, length, skip, whole, extra
+    def __init__(self, t0=0, n=0, length=0, skip=0, whole=False):
+        self.t0, self.n, self.len, self.skip, self.whole, self.extra, self.extra1 = t0, n, length, skip, whole, 0, 0
 
     def one(self):
         return not self.whole and self.n % TOK == 1
@@ -52,8 +52,14 @@ class Entry:
         i = self.items() - 1
         return 0 if i < 0 else self.before(i) + self.units(i)
 
+    def one_blocks(self):
+        return (self.len - 1) // BLOCK + 1 - self.skip
+
     def one_units(self):
-        return ((self.len - 1) // BLOCK + 2 - self.skip) // 2 if self.one() else 0
+        return (self.one_blocks() + 1) // 2 + self.extra1 if self.one() else 0
+
+    def one_begun(self, x):
+        return min(self.one_blocks(), 0 if x <= 0 else 2 * (1 + max(0, x - 1 - self.extra1)))
 
     def joined(self):
         return self.whole or self.skip > 0
@@ -146,9 +152,9 @@ def walk(work, c, extra, total, emit, mistake):
                         break
 
 
-def walk_one(work, cta, total, emit, mistake):
+def walk_one(work, cta, extra1, total, emit, mistake):
     c = CTAS - 1 - cta
-    ctas, u0, u1 = split(total, c, 0)
+    ctas, u0, u1 = split(total, c, extra1)
     if u0 >= u1:
         return
     base = 0
@@ -159,13 +165,14 @@ def walk_one(work, cta, total, emit, mistake):
     per = q.one_units()
     g, u, at = (u0 - base) // per, (u0 - base) % per, u0
     while True:
-        blocks = (q.len - 1) // BLOCK + 1 - q.skip
         to = min(per, u + u1 - at)
-        nb = min(blocks, 2 * to) - 2 * u
-        whole = u == 0 and to == per
-        slot = ("token", False) if whole and q.joined() else ("out",) if whole else ("one", 2 * c + (u == 0))
+        nb = q.one_begun(to) - q.one_begun(u)
+        begins, whole = u == 0, u == 0 and nb == q.one_blocks()
+        slot = ("token", False) if whole and q.joined() else ("out",) if whole else ("one", 2 * c + begins)
         skip = 0 if mistake == "skip" else q.skip
-        emit(q, q.t0 + q.n - 1, 1, g, 2 * u + skip, nb, slot, True, u == 0 and (to < per, ((at + per) * ctas - 1) // total), c)
+        if nb > 0:
+            emit(q, q.t0 + q.n - 1, 1, g, q.one_begun(u) + skip, nb, slot, True,
+                 begins and (not whole, ((at + per) * ctas - 1) // total), c)
         at += to - u
         if at >= u1:
             return
@@ -186,11 +193,12 @@ def check(lens, news, offsets, shared, mistake=None):
     tokens, max_blocks, bad = cu[-1], max(-(-n // BLOCK) for n in lens), set()
     work = entries(lens, cu, offsets, shared, tokens, max_blocks, bad)
     total = 4 * sum(q.per_head() for q in work)
-    items = 4 * sum(q.items() for q in work)
     extra = 2 if total >= 16 * CTAS else 1 if total >= 4 * CTAS else 0
-    total += extra * items
+    ones = 4 * sum(q.one_units() for q in work)
+    extra1 = 1 if ones >= 4 * CTAS else 0
     for q in work:
-        q.extra = extra
+        q.extra, q.extra1 = extra, extra1
+    total = 4 * sum(q.per_head() for q in work)
     ones = 4 * sum(q.one_units() for q in work)
     seen, places, own, with_, direct = {}, {}, {}, {}, {}
 
@@ -213,7 +221,7 @@ def check(lens, news, offsets, shared, mistake=None):
                 at[t0 + e, g] = (begin[0] or q.joined(), q.joined(), begin[0], one, c, begin[1], e)
     for c in range(CTAS):
         walk(work, c, extra, total, emit, mistake)
-        walk_one(work, c, ones, emit, mistake)
+        walk_one(work, c, extra1, ones, emit, mistake)
     # each good token's keys, once; each of its pieces where the join looks for it
     request = [r for r, n in enumerate(news) for _ in range(n)]
     read = set()
