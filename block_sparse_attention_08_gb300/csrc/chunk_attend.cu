@@ -163,15 +163,15 @@ struct CaShape {
   static constexpr float kLift = kF16 ? 7.f : 0.f;
 };
 
-// Which share of kind k (1: of one-token items) this CTA takes.  Where prefixes are shared the one-token items are dealt out
-// from the last CTA on: small batches have both kinds, in different CTAs.
-template <bool kShared>
-__device__ __forceinline__ int ca_share_index(int k) {
-  return kShared && k ? static_cast<int>(gridDim.x - 1 - blockIdx.x) : static_cast<int>(blockIdx.x);
-}
-// A CTA's part [u0, u1) of all units.
+// A CTA's part [u0, u1) of all units of a kind.  The shares are equal parts of `total`, to which a unit of this kind adds
+// `weight`, behind the `before` of the other (shared prefixes: both kinds are shared out in one row, else each by itself).
 struct CaShareOf {
-  long long total, ctas, u0, u1;
+  long long total, ctas, u0, u1, before;
+  int weight;
+  // the share that holds the last unit before unit x
+  __device__ __forceinline__ int holder(long long x) const {
+    return static_cast<int>(((before + weight * x) * ctas - 1) / total);
+  }
 };
 // ---- the units of a request --------------------------------------------------------
 
@@ -226,35 +226,46 @@ struct CaReq : CaReqOf {
 __device__ __forceinline__ bool ca_good(const CaArgs& a, long long c0, long long c1, int len) {
   return c0 >= 0 && c0 <= c1 && c1 <= a.tokens && c1 - c0 <= len && (len + kBlock - 1LL) / kBlock <= a.max_blocks;
 }
-// The requests of group g, the blocks that they share (0: none) and their tokens.  A group whose requests bring 16 tokens
-// or more on average fills its items without sharing, so it shares nothing; neither does one with offsets that are no range.
+// The requests of group g, the blocks that they share, the blocks that are attended to once for all of them (all or none), and
+// their tokens.  Nothing is shared by a group with offsets that are no range, and nothing attended to once where that does not pay: for
+// requests that bring 16 tokens or more on average, which fill their items by themselves; for two tokens (26 us instead of 21
+// over 16k shared keys, 64 instead of 68 over 128k, and over E4M3 59 instead of 51); and for less than 8 over few pages (4 over 8k 20 us
+// instead of 19, over 32k 35 and 34, over 64k 42 instead of 55; 5 over 16k 27 instead of 29; 8 over 1k 15 instead of 17).
+constexpr int kCaFewTokens = 8, kCaFewBlocks = 400;
 struct CaGroup {
-  int r0, r1, blocks, t0, n;
+  int r0, blocks, once, t0, n;
 };
 __device__ __forceinline__ CaGroup ca_group(const CaArgs& a, int g) {
   const int r0 = a.group_offsets[g], r1 = a.group_offsets[g + 1], blocks = a.shared_lens[g] / kBlock;
-  if (r0 < 0 || r1 > a.batch || r1 <= r0 || r1 - r0 < 2 || blocks < 1) return CaGroup{r0, r1, 0, 0, 0};
-  const long long c0 = a.cu[r0], c1 = a.cu[r1];
-  if (c0 < 0 || c1 < c0 || c1 > a.tokens || c1 - c0 >= static_cast<long long>(kCaTok) * (r1 - r0)) return CaGroup{r0, r1, 0, 0, 0};
-  return CaGroup{r0, r1, min(blocks, a.max_blocks), static_cast<int>(c0), static_cast<int>(c1 - c0)};
+  if (r0 < 0 || r1 > a.batch || r1 <= r0 || blocks < 1) return CaGroup{r0, 0, 0, 0, 0};
+  const int some = min(blocks, a.max_blocks);
+  const long long c0 = a.cu[r0], c1 = a.cu[r1], n = c1 - c0;
+  if (c0 < 0 || n < 3 || c1 > a.tokens || r1 - r0 < 2 || n >= static_cast<long long>(kCaTok) * (r1 - r0) ||
+      (n < kCaFewTokens && (n - 1) * some < kCaFewBlocks))
+    return CaGroup{r0, some, 0, 0, 0};
+  return CaGroup{r0, some, some, static_cast<int>(c0), static_cast<int>(n)};
 }
-// The blocks that request r shares with its group.
-__device__ __forceinline__ int ca_skip(const CaArgs& a, int r) {
+// The group of request r (no blocks: none).
+__device__ __forceinline__ CaGroup ca_group_of(const CaArgs& a, int r) {
   int lo = 0, hi = a.groups;  // the first group that ends behind r
   while (lo < hi) {
     const int mid = lo + (hi - lo) / 2;
     if (a.group_offsets[mid + 1] > r) hi = mid;
     else lo = mid + 1;
   }
-  if (lo == a.groups) return 0;
+  if (lo == a.groups) return CaGroup{0, 0, 0, 0, 0};
   const CaGroup g = ca_group(a, lo);
-  return g.r0 <= r ? g.blocks : 0;
+  return g.r0 <= r ? g : CaGroup{0, 0, 0, 0, 0};
 }
-// Whether request r is good, and the blocks that it shares.
+// Whether request r is good, and the blocks that its group attends to for it.
 template <bool kShared>
 __device__ __forceinline__ bool ca_good_request(const CaArgs& a, int r, int c0, int c1, int len, int& skip) {
-  skip = kShared ? ca_skip(a, r) : 0;
-  return ca_good(a, c0, c1, len) && (!kShared || c0 == c1 || len - (c1 - c0) >= skip * kBlock);
+  skip = 0;
+  if (!ca_good(a, c0, c1, len)) return false;
+  if (!kShared) return true;
+  const CaGroup g = ca_group_of(a, r);
+  skip = g.once;
+  return c0 == c1 || len - (c1 - c0) >= g.blocks * kBlock;
 }
 // Entry r of the list of work: a request, with shared prefixes the groups before them; one with bad lengths has no tokens.
 template <bool kShared>
@@ -263,7 +274,7 @@ __device__ __forceinline__ CaReq<kShared> ca_req(const CaArgs& a, int r, bool ap
   if (kShared) {
     if (r < a.groups) {
       const CaGroup g = ca_group(a, r);
-      if (g.blocks) q.t0 = g.t0, q.n = g.n, q.len = g.blocks * kBlock, q.row = g.r0, q.whole = true;
+      if (g.once) q.t0 = g.t0, q.n = g.n, q.len = g.once * kBlock, q.row = g.r0, q.whole = true;
       return q;
     }
     r -= a.groups;
@@ -394,18 +405,40 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kKv>& sm)
   auto split = [&](const long long (&total)[kN]) {
     apart = kOne && (kFp8 || kShared || total[0] == 0);  // (bf16: only where there are no others)
     extra = 0;
-    extra = ca_item_units(units(total, 0));
-    // (an end of an item is worth two blocks: 256 requests over 32k shared keys 0.264 ms without, 0.249 with)
-    if (kShared && total[2] >= 4LL * gridDim.x) extra1 = 1;
+    // (a share is long enough to hold some block's beginning)
+    auto ctas = [&](long long n, int e) { return min(static_cast<long long>(gridDim.x), max(n / (1 + e), 1LL)); };
+    bool row = false;
+    if constexpr (kShared) {
+      // The end of a one-token item is worth a unit (256 requests over 32k shared keys 0.264 ms without, 0.249 with).
+      extra = ca_item_units(total[0] + total[2]);
+      extra1 = min(extra, 1);
+      // Both kinds in one row, so that all but one CTA have items of one kind, and the one's start, end and waits for HBM pass
+      // beside the other's products: 64 requests over 16k keys, bf16, 63 us instead of 76, four over 2k 15 instead of 17.  In time a unit
+      // of one-token items (two blocks) is 1.2 units of tiles over a bf16 cache.  Over 8-bit ones, long shares of
+      // both kinds beside one another slow some SMs down (256 requests, int8: 0.38 ms instead of 0.29), so there each CTA takes
+      // the one after the other.
+      row = !kFp8 || extra < 2;
+    }
+    if (row) {
+      const int tile = kFp8 || extra == 0 ? 1 : 5, token = kFp8 || extra == 0 ? 1 : 6;
+      const long long n0 = units(total, 0), n1 = units(total, 1), sum = tile * n0 + token * n1;
+      const long long c = ctas(sum / token, extra);
+      const long long p0 = sum * min(static_cast<long long>(blockIdx.x), c) / c, p1 = sum * min(blockIdx.x + 1LL, c) / c;
+      auto part = [&](long long p) { return max(p - tile * n0, 0LL) / token; };
+      share[0] = CaShareOf{sum, c, min(p0 / tile, n0), min(p1 / tile, n0), 0, tile};
+      share[kKinds - 1] = CaShareOf{sum, c, part(p0), part(p1), tile * n0, token};
+      return;
+    }
+    if (!kShared) extra = ca_item_units(units(total, 0));
 #pragma unroll
     for (int k = 0; k < kKinds; ++k) {
       CaShareOf& s = share[k];
       s.total = units(total, k);
-      // (a share is long enough to hold some block's beginning)
-      s.ctas = min(static_cast<long long>(gridDim.x), max(s.total / (1 + (k ? extra1 : extra)), 1LL));
-      const int c = ca_share_index<kShared>(k);
-      s.u0 = min(s.total, s.total * c / s.ctas);
-      s.u1 = min(s.total, s.total * (c + 1) / s.ctas);
+      s.ctas = ctas(s.total, k ? extra1 : extra);
+      s.u0 = min(s.total, s.total * blockIdx.x / s.ctas);
+      s.u1 = min(s.total, s.total * (blockIdx.x + 1) / s.ctas);
+      s.before = 0;
+      s.weight = 1;
     }
   };
   const bool once = entries <= kThreads;
@@ -551,7 +584,7 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
                                                const CaShareOf& share, CaSmem<kKv>& sm) {
   constexpr bool kFp8 = CaShape<kKv>::kFp8;
   constexpr int kPlaces = CaShape<kKv>::kOnePlaces;
-  const int lane = threadIdx.x & 31, c = ca_share_index<kShared>(1);
+  const int lane = threadIdx.x & 31, c = static_cast<int>(blockIdx.x);
   DevError* err = a.err;
   uint8_t* places = &sm.kv[0][0];
   static_assert(sizeof(sm.kv) + sizeof(sm.raw) >= kCaOnePlaces * kCaTile, "the places lie over kv and raw");
@@ -568,8 +601,7 @@ __device__ __forceinline__ void ca_one_produce(const CUtensorMap& kmap, const CU
         const bool begins = w.u == 0, whole = begins && it.nb == q.one_blocks();
         it.slot = whole ? (q.joined() ? kCaOwn : -1) : 2 * c + begins;
         if (begins) {
-          // the share that holds the item's last unit
-          const int last = whole ? 0 : static_cast<int>(((w.at + w.per) * share.ctas - 1) / share.total);
+          const int last = whole ? 0 : share.holder(w.at + w.per);  // the share that holds the item's last unit
           if (kShared) {
             if (lane == 0)
               a.own.at[static_cast<long long>(it.t0) * kKvHeads + g] =
@@ -1026,7 +1058,7 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
   if (warp >= 8 && warp < kCaWidenWarp) ca_regs_down<Shape::kRegsIssue>();
   if (warp == kCaProducerWarp) {
     // ---------------- the share's items, and their copies ----------------
-    const long long total = sm.share[0].total, ctas = sm.share[0].ctas, u0 = sm.share[0].u0, u1 = sm.share[0].u1;
+    const long long u0 = sm.share[0].u0, u1 = sm.share[0].u1;
     CaCut cut{0, 0, 0, 0};
     int nitem = 0, nq = 0, nload = 0, nblk = 0;  // descriptors, Q tiles, K / V tiles and blocks issued
     bool ok = true;
@@ -1146,9 +1178,9 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
           if (b == 0 && lane < it.ntok)
             (rq.whole ? a.shared : a.own).at[(static_cast<long long>(it.t0) + lane) * kKvHeads + g] =
                 CaPieces{!to_end || rq.joined(), rq.joined(), !to_end, false, static_cast<int>(blockIdx.x),
-                         to_end ? 0 : static_cast<int>((end * ctas - 1) / total), lane}.code();
+                         to_end ? 0 : sm.share[0].holder(end), lane}.code();
         } else if (b == 0 && !to_end) {
-          cut = CaCut{it.t0, it.ntok, g, static_cast<int>((end * ctas - 1) / total)};
+          cut = CaCut{it.t0, it.ntok, g, sm.share[0].holder(end)};
         }
         if (!ok || at >= u1) break;
         // the next item (the share goes on, so there is one)
@@ -1714,12 +1746,20 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_join_kernel(const __grid
 }
 
 // The same where prefixes are shared: a CTA takes (token, KV head) pairs, and joins the pieces of the token's own item with
-// those of its group's.  A thread has four dims of a row, and reads the row's (m, l) of each piece beside its sums: the warps
-// need no meeting, and the only loads that follow each other are a pair's code and its pieces.  (With the factors worked out
-// once per row in shared memory, as above, the call took 11.6 us longer than without the join for four tokens, 26 for 330.)
-constexpr int kCaJoinBatch = 4;  // pieces in flight per thread
+// those of its group's.  A thread has four dims of a row, and reads the row's (m, l) of each piece beside its sums, so the only
+// loads that follow each other are a pair's code and its pieces, kCaJoinBatch of them at a time.  (With the factors
+// worked out once per row in shared memory, as above, four tokens took 28 us instead of 17.)  Few tokens over a long
+// prefix have many pieces, one from each CTA that had a part of their group's item, and leave most SMs idle: kSplit > 1 gives a
+// pair to kSplit CTAs, a part of the dims each, whose threads share out the pieces (4 tokens over 16k keys: 36 us without).
+constexpr int kCaJoinBatch = 4, kCaJoinSplit = 4;
+template <int kSplit>
 __global__ void __launch_bounds__(kCaJoinThreads, 2) shared_join_kernel(const __grid_constant__ CaArgs a) {
-  const int tid = threadIdx.x, lane = tid & 31, row = tid % kGroup, d4 = tid / kGroup;
+  constexpr int kLanes = kCaJoinThreads / kSplit;  // threads that share out nothing: 16 rows, and dims in fours
+  __shared__ float2 part_ml[kSplit][kGroup];
+  __shared__ float4 part_o[kSplit][kSplit > 1 ? kLanes : 1];
+  const int tid = threadIdx.x, lane = tid & 31, share = tid / kLanes, row = tid % kGroup;
+  const int d4 = static_cast<int>(blockIdx.x % kSplit) * (kLanes / kGroup) + tid % kLanes / kGroup;
+  const int cta = blockIdx.x / kSplit, ctas = gridDim.x / kSplit;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long from = static_cast<long long>(max(a.cu[0], 0)) * kKvHeads;
@@ -1745,25 +1785,34 @@ __global__ void __launch_bounds__(kCaJoinThreads, 2) shared_join_kernel(const __
                   max(c.last - c.first, 0) + 1};
   };
   // 32 pairs' codes at once: most of a long batch's have nothing to join
-  for (long long base = blockIdx.x; base < to; base += 32LL * gridDim.x) {
-    const long long mine = base + static_cast<long long>(lane) * gridDim.x;
+  for (long long base = cta; base < to; base += 32LL * ctas) {
+    const long long mine = base + static_cast<long long>(lane) * ctas;
     const bool in = mine >= from && mine < to;
     const int32_t own_code = in ? a.own.at[mine] : 0, with_code = in ? a.shared.at[mine] : 0;  // (the second may be anything)
     for (unsigned left = __ballot_sync(0xffffffffu, CaPieces::of(own_code).join); left; left &= left - 1) {
       const int k = __ffs(left) - 1;
-      const long long at = base + static_cast<long long>(k) * gridDim.x;
+      const long long at = base + static_cast<long long>(k) * ctas;
       const CaPieces own = CaPieces::of(__shfl_sync(0xffffffffu, own_code, k));
       const CaPieces with = CaPieces::of(__shfl_sync(0xffffffffu, with_code, k));
       const Source x = source(own, a.own, at), y = source(with, a.shared, at);
       const int n = x.n + (own.shared ? y.n : 0);
       float m = -INFINITY, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s0 = 0; s0 < n; s0 += kCaJoinBatch) {
+      auto add = [&](float2 ml, float4 v) {  // (m is at least the piece's)
+        if (ml.x == -INFINITY) return;
+        const float g = ex2(ml.x - m);
+        l = fmaf(g, ml.y, l);
+        o.x = fmaf(g, v.x, o.x);
+        o.y = fmaf(g, v.y, o.y);
+        o.z = fmaf(g, v.z, o.z);
+        o.w = fmaf(g, v.w, o.w);
+      };
+      for (int s0 = share; s0 < n; s0 += kSplit * kCaJoinBatch) {
         float4 v[kCaJoinBatch];
         float2 ml[kCaJoinBatch];
 #pragma unroll
         for (int i = 0; i < kCaJoinBatch; ++i) {
-          const int s = min(s0 + i, n - 1);
+          const int s = min(s0 + kSplit * i, n - 1);
           const bool first = s < x.n;
           const int q = first ? s : s - x.n;
           const float4* o0 = first ? x.o0 : y.o0;
@@ -1777,29 +1826,42 @@ __global__ void __launch_bounds__(kCaJoinThreads, 2) shared_join_kernel(const __
         float top = m;
 #pragma unroll
         for (int i = 0; i < kCaJoinBatch; ++i)
-          if (s0 + i < n) top = fmaxf(top, ml[i].x);
+          if (s0 + kSplit * i < n) top = fmaxf(top, ml[i].x);
         const float f = m == -INFINITY ? 0.f : ex2(m - top);
         m = top;
         l *= f;
         o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll
-        for (int i = 0; i < kCaJoinBatch; ++i) {
-          if (s0 + i >= n || ml[i].x == -INFINITY) continue;
-          const float g = ex2(ml[i].x - top);
-          l = fmaf(g, ml[i].y, l);
-          o.x = fmaf(g, v[i].x, o.x);
-          o.y = fmaf(g, v[i].y, o.y);
-          o.z = fmaf(g, v[i].z, o.z);
-          o.w = fmaf(g, v[i].w, o.w);
+        for (int i = 0; i < kCaJoinBatch; ++i)
+          if (s0 + kSplit * i < n) add(ml[i], v[i]);
+      }
+      if constexpr (kSplit > 1) {
+        part_o[share][tid % kLanes] = o;
+        if (tid % kLanes < kGroup) part_ml[share][row] = make_float2(m, l);
+        __syncthreads();
+        if (share == 0) {
+          const float mine_m = m;
+          float top = m;
+#pragma unroll
+          for (int i = 1; i < kSplit; ++i) top = fmaxf(top, part_ml[i][row].x);
+          const float f = mine_m == -INFINITY ? 0.f : ex2(mine_m - top);
+          m = top;
+          l *= f;
+          o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+          for (int i = 1; i < kSplit; ++i) add(part_ml[i][row], part_o[i][tid % kLanes]);
         }
       }
-      const long long orow = at / kKvHeads * kHeads + at % kKvHeads * kGroup + row;
-      const float inv = l == 0.f ? 0.f : a.v_scale / l;
-      if (a.lse && d4 == 0) a.lse[orow] = l == 0.f ? -INFINITY : m + log2f(l);
-      // the lanes of 16 rows have dims 4 d4 .. and, in the warp's other half, the next four: one 16-byte store for both
-      const uint2 mine2 = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-      const uint2 next = make_uint2(__shfl_xor_sync(0xffffffffu, mine2.x, 16), __shfl_xor_sync(0xffffffffu, mine2.y, 16));
-      if (lane < 16) stg128(a.out + orow * kDim + 4 * d4, mine2.x, mine2.y, next.x, next.y);
+      if (share == 0) {
+        const long long orow = at / kKvHeads * kHeads + at % kKvHeads * kGroup + row;
+        const float inv = l == 0.f ? 0.f : a.v_scale / l;
+        if (a.lse && d4 == 0) a.lse[orow] = l == 0.f ? -INFINITY : m + log2f(l);
+        // the lanes of 16 rows have dims 4 d4 .. and, in the warp's other half, the next four: one 16-byte store for both
+        const uint2 lo = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        const uint2 hi = make_uint2(__shfl_xor_sync(0xffffffffu, lo.x, 16), __shfl_xor_sync(0xffffffffu, lo.y, 16));
+        if (lane < 16) stg128(a.out + orow * kDim + 4 * d4, lo.x, lo.y, hi.x, hi.y);
+      }
+      if (kSplit > 1) __syncthreads();
     }
   }
 }
@@ -1921,8 +1983,12 @@ cudaError_t launch_attend_chunk(const ChunkLaunch& L, cudaStream_t stream) {
         e != cudaSuccess)
       return e;
     // as many CTAs as are resident at once: two an SM
-    const int ctas = static_cast<int>(std::min(static_cast<long long>(pairs), 2LL * kNumSMs));
-    return launch_dependent(shared_join_kernel, dim3(ctas), kCaJoinThreads, 0, stream, a);
+    constexpr size_t kCtas = 2 * kNumSMs;
+    if (pairs * kCaJoinSplit <= 2 * kCtas)
+      return launch_dependent(shared_join_kernel<kCaJoinSplit>, dim3(static_cast<unsigned>(pairs * kCaJoinSplit)),
+                              kCaJoinThreads, 0, stream, a);
+    return launch_dependent(shared_join_kernel<1>, dim3(static_cast<unsigned>(std::min(pairs, kCtas))), kCaJoinThreads, 0,
+                            stream, a);
   }
   // A batch of single tokens has no more of them than requests.  (The code for such batches cost others 0.4 us a call, and
   // 16 tokens over 32k keys 3.)

@@ -701,10 +701,11 @@ msa_status msa_attend_chunk_int8kv(const msa_config* cfg, const void* q, const v
  *   groups        0 to batch; 0: msa_attend_chunk (the arrays may be NULL)
  *   workspace     >= msa_workspace_size(cfg, MSA_MODE_SHARED, total_tokens, max_blocks), with groups 0
  *                 of MSA_MODE_CHUNK
- * The shared pages are read through the row of the group's first request, whether or not that
- * brings tokens.  A group whose requests bring 16 tokens or more each on average, or with a single
- * request, gains nothing and is computed as if it shared nothing (so a request with a long chunk is best left
- * outside its group); so is one whose offsets are no range in the batch. */
+ * Where that pays, the shared pages are read through the row of the group's first request, whether or
+ * not that brings tokens; else each request's through its own row.  It does not pay for two tokens, for
+ * fewer than 8 over few pages, and for a group whose requests bring 16 tokens or more each on
+ * average (so a request with a long chunk is best left outside its group).  A group whose offsets are no
+ * range in the batch shares nothing. */
 msa_status msa_attend_shared(const msa_config* cfg, const void* q, const void* k_cache,
                              const void* v_cache, const int32_t* seq_lens, const int32_t* page_table,
                              const int32_t* cu_seqlens_q, int batch, int max_blocks,

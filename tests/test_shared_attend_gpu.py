@@ -179,7 +179,7 @@ def test_what_lies_behind_the_last_key_does_not_matter(kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_bad_lengths_and_pages(kind):
-    b = Batch([(600, [(100, 1), (100, 2), (100, 1)]), (300, [(5, 1), (6, 1)])], kind)
+    b = Batch([(600, [(100, 1), (100, 2), (100, 1)] + [(20, 2)] * 3), (300, [(5, 5), (6, 5)])], kind)
     ws = msa.Workspace(msa.workspace_size(msa.make_config(), 5, b.q.shape[0], b.table.shape[1]))
     ref = b.want()
     lens = list(b.lens)
@@ -188,7 +188,7 @@ def test_bad_lengths_and_pages(kind):
     out = b.run(lse=lse, workspace=ws)
     assert ws.read_device_error() == (3, 1)
     assert bool((out[1:3] == 0).all()) and bool((lse[1:3] == -math.inf).all())
-    good = [0, 3, 4, 5]
+    good = [0] + list(range(3, len(out)))
     b.check(out[good], lse[good], tuple(x[good] for x in ref))
     b.lens = lens
     table = b.table.clone()
@@ -196,16 +196,33 @@ def test_bad_lengths_and_pages(kind):
         b.table[0, 2] = page                      # a shared page: its keys are missing for the whole group
         out = b.run(lse=lse, workspace=ws)
         assert ws.read_device_error() == (1, 2)
-        b.check(out, lse, b.want(skip=[(0, 2), (1, 2), (2, 2)]))
+        b.check(out, lse, b.want(skip=[(r, 2) for r in range(6)]))
         b.table.copy_(table)
-        b.table[4, 2] = page                      # one of a request's own
+        b.table[7, 2] = page                      # one of a request's own
         out = b.run(lse=lse, workspace=ws)
-        assert ws.read_device_error() == (1, 4 * table.shape[1] + 2)
-        b.check(out, lse, b.want(skip=[(4, 2)]))
+        assert ws.read_device_error() == (1, 7 * table.shape[1] + 2)
+        b.check(out, lse, b.want(skip=[(7, 2)]))
         b.table.copy_(table)
 
 
-@pytest.mark.parametrize("off,shared", [([-1, 3], [256]), ([1, 9], [256]), ([4, 2], [256]), ([2, 3], [256]), ([0, 5], [-7]),
+def test_small_groups_have_the_same_lengths_to_keep():
+    """A group whose pages are read for each request (few tokens) refuses the requests that the others would."""
+    for requests in ([(100, 1), (50, 1), (60, 1)], [(10, 1)], [(10, 40), (20, 50)]):
+        b = Batch([(600, requests)], "bf16")
+        ws = msa.Workspace(msa.workspace_size(msa.make_config(), 5, b.q.shape[0], b.table.shape[1]))
+        ref = b.want()
+        b.check(b.run(workspace=ws), None, ref)
+        assert ws.read_device_error() == (0, 0)
+        b.lens[0] = 512 + requests[0][1] - 1      # 511 tokens before the new ones, four whole pages are shared
+        out = b.run(workspace=ws)
+        assert ws.read_device_error() == (3, 0)
+        n = requests[0][1]
+        assert bool((out[:n] == 0).all())
+        if len(requests) > 1:
+            b.check(out[n:], None, tuple(x[n:] for x in ref))
+
+
+@pytest.mark.parametrize("off,shared", [([-1, 3], [256]), ([1, 9], [256]), ([4, 2], [256]), ([3, 4], [256]), ([0, 5], [-7]),
                                         ([0, 0, 0, 5], [256, 256, 0]), ([5, 5], [128])])
 def test_groups_that_share_nothing(off, shared):
     b = Batch([(None, [(600, 1), (300, 3), (5, 1), (700, 1), (900, 2)])], "bf16")

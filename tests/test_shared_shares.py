@@ -6,14 +6,19 @@ be attended to exactly once, no two pieces may leave their sums in the same plac
 have to be those that hold its sums.  Planted mistakes have to be found.  No GPU is involved.
 """
 import random
+import re
 
 import pytest
 
-from _kernel_consts import kconst
+from _kernel_consts import _source, kconst
 
 FILE = "chunk_attend.cu"
+FEW_TOKENS = kconst("kCaFewTokens", FILE)
+FEW_BLOCKS = int(re.search(r"kCaFewBlocks = (\d+);", _source(FILE))[1])
 TOK, CTAS = kconst("kCaTok", FILE), kconst("kNumSMs", FILE)
 BLOCK = 128
+_w = re.search(r"tile = kFp8 \|\| extra == 0 \? 1 : (\d+), token = kFp8 \|\| extra == 0 \? 1 : (\d+);", _source(FILE))
+WEIGHTS = int(_w[1]), int(_w[2])  # of a unit of either kind
 
 
 def eighths(x):
@@ -66,20 +71,22 @@ class Entry:
 
 
 def group(g, offsets, shared, cu, batch, tokens, max_blocks):
+    """(first request, blocks that its requests share, blocks attended to once, first token, tokens)."""
     r0, r1, blocks = offsets[g], offsets[g + 1], int(shared[g] / BLOCK)
-    if r0 < 0 or r1 > batch or r1 <= r0 or r1 - r0 < 2 or blocks < 1:
-        return r0, r1, 0, 0, 0
-    c0, c1 = cu[r0], cu[r1]
-    if c0 < 0 or c1 < c0 or c1 > tokens or c1 - c0 >= TOK * (r1 - r0):
-        return r0, r1, 0, 0, 0
-    return r0, r1, min(blocks, max_blocks), c0, c1 - c0
+    if r0 < 0 or r1 > batch or r1 <= r0 or blocks < 1:
+        return r0, 0, 0, 0, 0
+    some, c0, c1 = min(blocks, max_blocks), cu[r0], cu[r1]
+    n = c1 - c0
+    if c0 < 0 or n < 3 or c1 > tokens or r1 - r0 < 2 or n >= TOK * (r1 - r0) or (n < FEW_TOKENS and (n - 1) * some < FEW_BLOCKS):
+        return r0, some, 0, 0, 0
+    return r0, some, some, c0, n
 
 
 def entries(lens, cu, offsets, shared, tokens, max_blocks, bad):
     batch, groups, out = len(lens), len(shared), []
     for g in range(groups):
-        r0, r1, blocks, t0, n = group(g, offsets, shared, cu, batch, tokens, max_blocks)
-        out.append(Entry(t0, n, blocks * BLOCK, 0, True) if blocks else Entry())
+        _, _, once, t0, n = group(g, offsets, shared, cu, batch, tokens, max_blocks)
+        out.append(Entry(t0, n, once * BLOCK, 0, True) if once else Entry())
     for r in range(batch):
         lo, hi = 0, groups
         while lo < hi:
@@ -88,13 +95,14 @@ def entries(lens, cu, offsets, shared, tokens, max_blocks, bad):
                 hi = mid
             else:
                 lo = mid + 1
-        skip = 0
+        blocks = skip = 0
         if lo < groups:
-            r0, _, blocks, _, _ = group(lo, offsets, shared, cu, batch, tokens, max_blocks)
-            skip = blocks if r0 <= r else 0
+            r0, blocks, skip, _, _ = group(lo, offsets, shared, cu, batch, tokens, max_blocks)
+            if r0 > r:
+                blocks = skip = 0
         c0, c1 = cu[r], cu[r + 1]
         good = 0 <= c0 <= c1 <= tokens and c1 - c0 <= lens[r] and -(-lens[r] // BLOCK) <= max_blocks
-        if good and (c0 == c1 or lens[r] - (c1 - c0) >= skip * BLOCK):
+        if good and (c0 == c1 or lens[r] - (c1 - c0) >= blocks * BLOCK):
             out.append(Entry(c0, c1 - c0, lens[r], skip))
         else:
             bad.update(range(max(0, c0), min(tokens, c1)))
@@ -102,14 +110,25 @@ def entries(lens, cu, offsets, shared, tokens, max_blocks, bad):
     return out
 
 
-def split(total, c, extra):
-    ctas = min(CTAS, max(total // (1 + extra), 1))
-    return ctas, min(total, total * c // ctas), min(total, total * (c + 1) // ctas)
+def split(n0, n1, c, extra, fp8):
+    """For the tiles' items and for the one-token items: (units from .. to, what all shares are parts of, CTAs, before, weight)."""
+    if fp8 and extra == 2:  # each kind by itself
+        out = []
+        for n, e in ((n0, extra), (n1, min(extra, 1))):
+            ctas = min(CTAS, max(n // (1 + e), 1))
+            out.append((min(n, n * c // ctas), min(n, n * (c + 1) // ctas), n, ctas, 0, 1))
+        return out
+    tile, token = (1, 1) if fp8 or extra == 0 else WEIGHTS
+    total = tile * n0 + token * n1
+    ctas = min(CTAS, max(total // token // (1 + extra), 1))
+    p0, p1 = total * min(c, ctas) // ctas, total * min(c + 1, ctas) // ctas
+    return [(min(p0 // tile, n0), min(p1 // tile, n0), total, ctas, 0, tile),
+            (max(p0 - tile * n0, 0) // token, max(p1 - tile * n0, 0) // token, total, ctas, tile * n0, token)]
 
 
-def walk(work, c, extra, total, emit, mistake):
+def walk(work, c, share, emit, mistake):
     """The items of two and more tokens of CTA c."""
-    ctas, u0, u1 = split(total, c, extra)
+    u0, u1, total, ctas, before, weight = share
     if u0 >= u1:
         return
     base = 0
@@ -133,9 +152,9 @@ def walk(work, c, extra, total, emit, mistake):
         if nb > 0:
             t0, ntok = q.t0 + TOK * i, min(TOK, q.n - TOK * i)
             slot = ("token", q.whole) if b0 == 0 and to_end and q.joined() else ("out",) if b0 == 0 and to_end else ("cta", 2 * c + (b0 == 0))
-            last = (end * ctas - 1) // total
+            last = ((before + weight * end) * ctas - 1) // total
             if mistake == "last":
-                last = (end * ctas) // total
+                last = ((before + weight * (end - 1)) * ctas - 1) // total
             emit(q, t0, ntok, g, b0 + q.skip, nb, slot, False, b0 == 0 and (not to_end, last), c)
         at = item0 = end
         if at >= u1:
@@ -152,9 +171,8 @@ def walk(work, c, extra, total, emit, mistake):
                         break
 
 
-def walk_one(work, cta, extra1, total, emit, mistake):
-    c = CTAS - 1 - cta
-    ctas, u0, u1 = split(total, c, extra1)
+def walk_one(work, c, share, emit, mistake):
+    u0, u1, total, ctas, before, weight = share
     if u0 >= u1:
         return
     base = 0
@@ -172,7 +190,7 @@ def walk_one(work, cta, extra1, total, emit, mistake):
         skip = 0 if mistake == "skip" else q.skip
         if nb > 0:
             emit(q, q.t0 + q.n - 1, 1, g, q.one_begun(u) + skip, nb, slot, True,
-                 begins and (not whole, ((at + per) * ctas - 1) // total), c)
+                 begins and (not whole, ((before + weight * (at + per)) * ctas - 1) // total), c)
         at += to - u
         if at >= u1:
             return
@@ -186,20 +204,17 @@ def walk_one(work, cta, extra1, total, emit, mistake):
                     break
 
 
-def check(lens, news, offsets, shared, mistake=None):
+def check(lens, news, offsets, shared, mistake=None, fp8=False):
     cu = [0]
     for n in news:
         cu.append(cu[-1] + n)
     tokens, max_blocks, bad = cu[-1], max(-(-n // BLOCK) for n in lens), set()
     work = entries(lens, cu, offsets, shared, tokens, max_blocks, bad)
-    total = 4 * sum(q.per_head() for q in work)
-    extra = 2 if total >= 16 * CTAS else 1 if total >= 4 * CTAS else 0
-    ones = 4 * sum(q.one_units() for q in work)
-    extra1 = 1 if ones >= 4 * CTAS else 0
+    both = 4 * sum(q.per_head() + q.one_units() for q in work)
+    extra = 2 if both >= 16 * CTAS else 1 if both >= 4 * CTAS else 0
     for q in work:
-        q.extra, q.extra1 = extra, extra1
-    total = 4 * sum(q.per_head() for q in work)
-    ones = 4 * sum(q.one_units() for q in work)
+        q.extra, q.extra1 = extra, min(extra, 1)
+    n0, n1 = 4 * sum(q.per_head() for q in work), 4 * sum(q.one_units() for q in work)
     seen, places, own, with_, direct = {}, {}, {}, {}, {}
 
     def emit(q, t0, ntok, g, b0, nb, slot, one, begin, c):
@@ -220,8 +235,9 @@ def check(lens, news, offsets, shared, mistake=None):
                 assert (t0 + e, g) not in at
                 at[t0 + e, g] = (begin[0] or q.joined(), q.joined(), begin[0], one, c, begin[1], e)
     for c in range(CTAS):
-        walk(work, c, extra, total, emit, mistake)
-        walk_one(work, c, extra1, ones, emit, mistake)
+        shares = split(n0, n1, c, extra, fp8)
+        walk(work, c, shares[0], emit, mistake)
+        walk_one(work, c, shares[1], emit, mistake)
     # each good token's keys, once; each of its pieces where the join looks for it
     request = [r for r, n in enumerate(news) for _ in range(n)]
     read = set()
@@ -282,7 +298,7 @@ def batch(rng):
 
 @pytest.mark.parametrize("seed", range(60))
 def test_every_key_once_and_every_piece_found(seed):
-    check(*batch(random.Random(seed)))
+    check(*batch(random.Random(seed)), fp8=seed % 2 == 1)
 
 
 @pytest.mark.parametrize("mistake", ["last", "skip"])
@@ -297,7 +313,9 @@ def test_planted_mistakes_are_found(mistake):
 
 
 @pytest.mark.parametrize("offsets,shared", [([-1, 3], [256]), ([2, 9], [256]), ([4, 2], [256]), ([2, 2], [256]), ([0, 1], [256]),
-                                            ([0, 6], [0]), ([0, 6], [-500]), ([0, 6], [127]), ([0, 6], [599]), ([0, 6], [600])])
-def test_odd_groups(offsets, shared):
+                                            ([0, 6], [0]), ([0, 6], [-500]), ([0, 6], [127]), ([0, 6], [599]), ([0, 6], [600]),
+                                            ([0, 6], [639]), ([0, 6], [640]), ([0, 6], [2 ** 31 - 1])])
+@pytest.mark.parametrize("each", [1, 2])
+def test_odd_groups(offsets, shared, each):
     """Offsets that are no range, a single request, nothing shared, and as much as there is or more."""
-    check([600] * 6, [1] * 6, offsets, shared)
+    check([640] * 6, [each] * 6, offsets, shared)
