@@ -664,9 +664,8 @@ def msa_dequantize_gather(k_cache, v_cache, k_scales, v_scales, page_table, cu_s
 
 def msa_sparse_attend_decode_int8kv(q, k_cache, v_cache, k_scales, v_scales, q2k, seq_lens, page_table, *, scale=None,
                                     out=None, workspace=None):
-    """bf16 out [batch, 64, 128] over the blocks of ``q2k`` of an int8 cache (C: msa_sparse_attend_decode_int8kv).  Without
-    ``workspace`` each stream has scratch of its own, and each captured graph; a ``Workspace`` (of
-    ``workspace_size(cfg, 0, batch, page_table.shape[1])`` bytes) also tells bad lengths, blocks and pages."""
+    """bf16 out [batch, 64, 128] over the blocks of ``q2k`` of an int8 cache (C: msa_sparse_attend_decode_int8kv).  Bad lengths,
+    blocks and pages are told to ``workspace``, a ``Workspace`` of 256 bytes or more."""
     r = (_ext or _serving()).sparse_attend_int8(q, k_cache, v_cache, k_scales, v_scales, q2k, seq_lens, page_table, scale,
                                                 out, _buf(workspace))
     return r if type(r) is not int else _fail("msa_sparse_attend_decode_int8kv", r)

@@ -219,7 +219,8 @@ static msa_status attend_decode(const msa_config* cfg, const void* q, const void
       (out_q && !aligned16(out_q)))
     return MSA_ERR_ALIGN;
   const Layout L = layout(MSA_MODE_DECODE, batch, max_blocks, cfg->topk);
-  if ((st = check_ws(workspace, workspace_bytes, L.total)) != MSA_OK) return st;
+  // (an int8 cache's segments are whole, or merged on chip: the call has only the error word to write)
+  if ((st = check_ws(workspace, workspace_bytes, kv == 2 ? kHeaderBytes : L.total)) != MSA_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // the merge tickets start at zero: the workspace was zero-filled once and

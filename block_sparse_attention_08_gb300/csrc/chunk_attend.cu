@@ -787,6 +787,10 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kKv>& sm, 
         // (int8: four warps have read the place, and arrive for the other four)
         if (lane < (kI8 ? 2 : 1)) mbar_arrive(&sm.one_empty[s]);
       };
+      auto q_of = [&](int c, uint32_t(&x)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = qa[c][i];
+      };
       I8State st;  // (an int8 cache's sums, until the item's end)
       if constexpr (kI8) i8_clear(st);
       uint32_t at8[4];
@@ -805,7 +809,7 @@ __device__ __forceinline__ void ca_one_attend(const CaArgs& a, CaSmem<kKv>& sm, 
           ++nplace;
           const int row0 = 32 * (warp & 3), keys = block_keys - row0;  // of this warp's 32
           const uint32_t* sc = reinterpret_cast<const uint32_t*>(places + kPlaces * kCaTile + s * 4 * kBlock) + row0 / 2 + t4;
-          if (keys > 0) i8_attend32(st, qa, kt, kt + kCaHalf, at8, sc, sc + kBlock / 2, keys, a.scale_log2, t4);
+          if (keys > 0) i8_attend32(st, q_of, kt, kt + kCaHalf, at8, sc, sc + kBlock / 2, keys, a.scale_log2, t4);
           release(s);
         } else if constexpr (kFp8) {
           ++nplace;

@@ -131,8 +131,9 @@ __device__ __forceinline__ void i8_offsets(uint32_t (&at)[4], int row, int lane)
 }
 
 // 32 keys, from the rows at `at` of the K and V tiles (i8_offsets) on, of which the first `keys` count (at least one).  ks, vs:
-// the scales of keys 2 t, + 1 (at [0]), 8 + 2 t, + 1 (at [4]) and so on.
-__device__ __forceinline__ void i8_attend32(I8State& st, const uint32_t (&qa)[8][4], uint32_t kt, uint32_t vt,
+// the scales of keys 2 t, + 1 (at [0]), 8 + 2 t, + 1 (at [4]) and so on.  qa(c, a) puts Q's fragments of k-step c into a.
+template <class Queries>
+__device__ __forceinline__ void i8_attend32(I8State& st, const Queries& qa, uint32_t kt, uint32_t vt,
                                             const uint32_t (&at)[4], const uint32_t* ks, const uint32_t* vs, int keys,
                                             float scale_log2, int t4) {
   constexpr uint32_t kNext = 16 * 128;
@@ -156,14 +157,19 @@ __device__ __forceinline__ void i8_attend32(I8State& st, const uint32_t (&qa)[8]
 #pragma unroll
       for (int u = 0; u < 2; ++u) ldsm_x4_t(r[0][u], vt + at[0] + u * kNext);  // dims 32 c .., then 32 c + 16 ..
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int h = 0; h < 2; ++h) {
+      uint32_t q[4];
+      qa(2 * c + h, q);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t e, o;
-        i8_pairs(r[c & 1][u][i], e, o, magic);
-        if (c == 0 && i < 2) i8_mma_first(x[2 * u + i], qa[0], e, o);
-        else mma_bf16(x[2 * u + (i & 1)], qa[2 * c + (i >> 1)], e, o);
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t e, o;
+          i8_pairs(r[c & 1][u][2 * h + i], e, o, magic);
+          if (c == 0 && h == 0) i8_mma_first(x[2 * u + i], q, e, o);
+          else mma_bf16(x[2 * u + i], q, e, o);
+        }
+    }
   }
   uint32_t pa[2][4];
   if (keys >= 32) i8_weigh<true>(st, x, pa, kw, vw, keys, scale_log2, t4);

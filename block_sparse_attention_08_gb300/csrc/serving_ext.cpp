@@ -21,8 +21,6 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
-#include <map>
-#include <mutex>
 #include <stdexcept>
 #include <sstream>
 #include <string>
@@ -611,30 +609,6 @@ PyObject* dequantize_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// Scratch of the decode attention, zero-filled before its first use: one buffer for each device and stream, kept for the
-// process and replaced by a larger one where a call needs that.  A capture gets one of its own (with the memset), which belongs
-// to the graph.
-Space decode_scratch(c10::DeviceIndex index, size_t bytes) {
-  const c10::cuda::CUDAGuard guard(index);
-  const c10::cuda::CUDAStream stream = c10::cuda::getCurrentCUDAStream(index);
-  auto fresh = [&] {
-    at::Tensor t = at::empty({static_cast<int64_t>(bytes)},
-                             at::TensorOptions().dtype(at::kByte).device(c10::Device(c10::kCUDA, index)));
-    if (const msa_status st = msa_workspace_init(t.data_ptr(), bytes, stream.stream()); st != MSA_OK) throw Refused(st);
-    return t;
-  };
-  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
-    at::Tensor t = fresh();
-    return {t.data_ptr(), bytes, t};
-  }
-  static std::mutex mu;
-  static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>;
-  const std::lock_guard<std::mutex> lock(mu);
-  at::Tensor& t = (*kept)[{index, stream.stream()}];
-  if (!t.defined() || static_cast<size_t>(t.nbytes()) < bytes) t = fresh();
-  return {t.data_ptr(), static_cast<size_t>(t.nbytes()), t};
-}
-
 // q, k_cache, v_cache, k_scales, v_scales, q2k, seq_lens, page_table, scale, out, workspace
 PyObject* sparse_attend_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return entry("sparse_attend_int8", n, 11, [&]() -> PyObject* {
@@ -657,15 +631,7 @@ PyObject* sparse_attend_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     msa_config_default(&cfg);
     cfg.topk = static_cast<int>(topk);
     cfg.local_blocks = 0;
-    Space ws;
-    if (a[10] == Py_None) {
-      size_t bytes = 0;
-      const msa_status st = msa_workspace_size(&cfg, MSA_MODE_DECODE, batch, static_cast<int>(width), &bytes);
-      if (st != MSA_OK) return PyLong_FromLong(st);
-      ws = decode_scratch(d, bytes);
-    } else {
-      ws = error_word(a[10], d);
-    }
+    const Space ws = error_word(a[10], d);
     const msa_status st = run(d, [&](void* stream) {
       return msa_sparse_attend_decode_int8kv(&cfg, q.const_data_ptr(), kc.const_data_ptr(), vc.const_data_ptr(),
                                              ks.const_data_ptr(), vs.const_data_ptr(), q2k.const_data_ptr<int32_t>(),

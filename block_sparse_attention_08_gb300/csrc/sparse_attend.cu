@@ -120,18 +120,30 @@ struct SegInfo {
 // 31.4 -> 27.2 us.  A bf16 ring of 96 KB would leave each warp a single stage,
 // nothing landing while it computes: slower (18.4 -> 20.9 us on the 4-request
 // workload), so bf16 stays at one CTA per SM.
+//
+// An int8 cache is converted by ordinary instructions, whose latency bounds it, so
+// three CTAs share an SM, with Q's fragments in shared memory (128 registers a
+// thread).  Two warps share a chunk, 32 keys each, so that its stage is soon
+// refilled.  It takes the cluster form alone, or a CTA for each whole segment:
+// cutting segments and merging them through memory cost 7 us.  (64 requests
+// of 2048 selected keys: 78 us with a chunk to each of three warps, two CTAs; 46
+// in pairs of warps; 39 with whole segments; 41 with three CTAs, where 48 requests take 34 us instead of 38 and
+// 256 take 120 instead of 128.)
 template <int kKv, int kSplit>
 struct AttShape {
+  static constexpr bool kI8 = kKv == kKvI8;
   static constexpr int kStageBytes = kKv ? kAttStage8Bytes : kAttStageBytes;
-  static constexpr int kStages = kAttStages;
-  static constexpr int kCtasPerSm = kKv ? 2 : 1;
-  static constexpr int kQSlots = kKv ? 1 : kSegSlots;             // Q tiles in the segment ring
+  static constexpr int kStages = kI8 ? 4 : kAttStages;
+  static constexpr int kCtasPerSm = kI8 ? 3 : kKv ? 2 : 1;
+  static constexpr int kQSlots = kKv ? 1 : kSegSlots;              // Q tiles in the segment ring
   static constexpr int kCombSlots = kKv ? 1 : kConsumerWarps - 1;  // stream-K: where states meet
-  // int8: two warps share a chunk, 32 keys each, so that its stage is soon refilled, and two take the next (with a chunk to each
-  // of six warps, 64 requests of 2048 selected keys took 71 us, and 78 with three)
-  static constexpr int kSharers = kKv == kKvI8 ? 2 : 1;
-  static constexpr int kConsumers = kKv == kKvI8 ? 4 : kConsumerWarps;
+  static constexpr int kSharers = kI8 ? 2 : 1;                     // warps that share a chunk
+  static constexpr int kConsumers = kI8 ? 4 : kConsumerWarps;
   static constexpr int kThreads = 32 * (kConsumers + 1);
+  // stage s is always consumed by the warps of group s % kGroups, so a warp never waits on a stage more than one mbarrier
+  // phase ahead
+  static constexpr int kGroups = kConsumers / kSharers;
+  static_assert(kStages % kGroups == 0, "stages must be a multiple of the groups");
 };
 
 // Where the consumer warps' states meet (stream-K only).
@@ -149,7 +161,9 @@ struct AttSmem {
   using Shape = AttShape<kKv, kSplit>;
   alignas(1024) uint8_t stage[Shape::kStages][Shape::kStageBytes];
   alignas(1024) uint8_t qtile[Shape::kQSlots][2 * kQBoxBytes];
-  uint32_t scales[kKv == kKvI8 ? Shape::kStages : 1][kKv == kKvI8 ? kChunkKeys : 4];  // int8: K's, then V's, bf16
+  // int8: Q's fragments by k-step and lane, and the scales of a chunk's keys, K's, then V's (bf16)
+  uint4 queries[kKv == kKvI8 ? 8 : 1][32];
+  uint32_t scales[kKv == kKvI8 ? Shape::kStages : 1][kKv == kKvI8 ? kChunkKeys : 4];
   AttComb<kSplit, Shape::kCombSlots> c;
   SegInfo seg[Shape::kQSlots];
   uint64_t full[Shape::kStages];
@@ -348,6 +362,8 @@ __device__ __forceinline__ uint32_t e4m3_even2(uint32_t w) { return e4m3_hb_to_f
 __device__ __forceinline__ uint32_t e4m3_odd2(uint32_t w) { return e4m3_hb_to_f16x2_s8(__byte_perm(w, 0u, 0x3414)); }
 
 constexpr int kMaxCluster = 8;
+// CTAs of a cluster, at most (int8: its smaller ring has room for three states).
+__host__ __device__ constexpr int largest_cluster(int kv) { return kv == kKvI8 ? 4 : kMaxCluster; }
 
 // Cluster split (kSplit): the CTAs of one cluster each hold their share of a
 // (query, KV head) segment as an unnormalised state (m, l, O) in comb slot 0
@@ -368,7 +384,7 @@ __device__ __forceinline__ void split_finish(Smem& sm, int csize, int warp, int 
                                              __nv_bfloat16* __restrict__ out, uint8_t* __restrict__ out_q,
                                              uint8_t* __restrict__ out_scale) {
   // the slots start at stage 1: stage 0 holds this CTA's merged state
-  static_assert(sizeof(sm.stage) - sizeof(sm.stage[0]) >= (kMaxCluster - 1) * kPushFloats * sizeof(float),
+  static_assert(sizeof(sm.stage) - sizeof(sm.stage[0]) >= (largest_cluster(kKv) - 1) * kPushFloats * sizeof(float),
                 "push slots");
   const int rank = blockIdx.x % csize;
   const int row = lane >> 1, d0 = (lane & 1) * 64;
@@ -484,7 +500,7 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
     }
     for (int s = 0; s < kQS; ++s) {
       mbar_init(&sm.seg_full[s], 1);
-      mbar_init(&sm.seg_empty[s], kConsumers);
+      mbar_init(&sm.seg_empty[s], kConsumerWarps);
     }
     fence_mbar_init();
   }
@@ -525,8 +541,7 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
 
   if (warp == kConsumers) {
     // ---------------- producer warp ----------------
-    long long sc = 0;
-    int nseg = 0;
+    int sc = 0, nseg = 0;  // chunks and segments so far
     long long it = lo;
     while (it < hi) {
       const int qi = static_cast<int>(it / (kKvHeads * topk));
@@ -571,7 +586,7 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
         const int nch = (nk + kChunkKeys - 1) / kChunkKeys;
         for (int ch = 0; ch < nch; ++ch, ++sc) {
           if (lane == 0) {
-            const int s = static_cast<int>(sc % kStg);
+            const int s = sc % kStg;
             mbar_wait(&sm.empty[s], static_cast<uint32_t>(((sc / kStg) & 1) ^ 1), err, 200);
             const int row = static_cast<int>(r0 + ch * kChunkKeys);
             uint8_t* st = sm.stage[s];
@@ -603,7 +618,7 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
     // been passed.
     if (lane == 0) {
       for (int s = 0; s < kStg; ++s) {
-        const long long f = (sc - s + kStg - 1) / kStg;  // fills of stage s
+        const int f = (sc - s + kStg - 1) / kStg;  // fills of stage s
         if (f > 0) mbar_wait(&sm.full[s], static_cast<uint32_t>((f - 1) & 1), err, 220);
       }
       for (int s = 0; s < kQS; ++s) {
@@ -618,7 +633,7 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
 
   // ---------------- consumer warps: whole 64-key chunks, stage s -> warp s % 3 ----------------
   const int g8 = lane >> 2, t4 = lane & 3;
-  long long sc = 0;  // chunk counter, identical in every consumer warp and the producer
+  int sc = 0;  // chunk counter, identical in every consumer warp and the producer
   int nseg = 0;
   long long it = lo;
   while (it < hi) {
@@ -645,7 +660,11 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
           const uint2 a = lds64(qt + off + sw128(g8, chunk));
           const uint2 b = lds64(qt + off + sw128(g8 + 8, chunk));
           if constexpr (kKv == kKvI8) {
-            i8_queries(qa[kk], a, b);
+            // (each warp two k-steps, for all)
+            if (kk / 2 == warp) {
+              i8_queries(qa[0], a, b);
+              sm.queries[kk][lane] = make_uint4(qa[0][0], qa[0][1], qa[0][2], qa[0][3]);
+            }
             continue;
           }
           qa[kk][0] = bf16x2_to_f16x2(a.x);
@@ -662,8 +681,9 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
         }
       }
     }
+    if constexpr (kKv == kKvI8) consumer_sync<kConsumers>();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.seg_empty[ss]);  // the slot may be refilled
+    if (lane == 0 && warp < kConsumerWarps) mbar_arrive(&sm.seg_empty[ss]);  // the slot may be refilled
     ++nseg;
 
     // This CTA holds the end of a segment whose start lies in earlier CTAs: it
@@ -674,6 +694,14 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
     const int pf_k = jn > 2 ? jn - 2 : 0;
 
     I8State st8;  // (an int8 cache's sums, until the merge)
+    const uint32_t queries = smem_u32(&sm.queries[0][lane]);
+    auto q_of = [&](int c, uint32_t(&x)[4]) {
+      const uint4 v = lds128(queries + c * 512);
+      x[0] = v.x;
+      x[1] = v.y;
+      x[2] = v.z;
+      x[3] = v.w;
+    };
     uint32_t at8[4];
     if constexpr (kKv == kKvI8) i8_offsets(at8, 32 * (warp % 2), lane);
     if constexpr (kKv == kKvI8) i8_clear(st8);
@@ -696,16 +724,16 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
         }
       }
       for (int ch = 0; ch < nch; ++ch, ++sc) {
-        const int s = static_cast<int>(sc % kStg);
-        constexpr int kSharers = AttShape<kKv, kSplit>::kSharers;
-        if (s % (kConsumers / kSharers) != warp / kSharers) continue;
+        const int s = sc % kStg;
+        using Shape = AttShape<kKv, kSplit>;
+        if (s % Shape::kGroups != warp / Shape::kSharers) continue;
         const int valid = min(kChunkKeys, nk - ch * kChunkKeys);  // keys of this chunk
         mbar_wait(&sm.full[s], static_cast<uint32_t>((sc / kStg) & 1), err, 300);
         const uint32_t stg = smem_u32(sm.stage[s]);
         if constexpr (kKv == kKvI8) {
           const int k0 = 32 * (warp % 2);
           if (k0 < valid)
-            i8_attend32(st8, qa, stg, stg + kBoxBytes, at8, &sm.scales[s][k0 / 2 + t4],
+            i8_attend32(st8, q_of, stg, stg + kBoxBytes, at8, &sm.scales[s][k0 / 2 + t4],
                         &sm.scales[s][(kChunkKeys + k0) / 2 + t4], valid - k0, scale_log2, t4);
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.empty[s]);
@@ -1039,9 +1067,10 @@ static bool make_q_map(CUtensorMap* map, const void* base, long long nq) {
 template <int kKv, int kSplit>
 constexpr size_t att_smem() { return sizeof(AttSmem<kKv, kSplit>) + 1024; }
 static_assert(att_smem<0, 0>() <= 227 * 1024 && att_smem<0, 1>() <= 227 * 1024, "shared memory of the decode attention");
-// two CTAs of the 8-bit forms per SM (int8 needs the most) (228 KB of shared memory per SM, 1 KB of it per CTA reserved)
-static_assert(2 * (att_smem<kKvI8, 0>() + 1024) <= 228 * 1024 && 2 * (att_smem<kKvI8, 1>() + 1024) <= 228 * 1024,
-              "shared memory of the decode attention, 8-bit K/V");
+// two CTAs of the FP8 forms per SM (228 KB of shared memory per SM, 1 KB of it per CTA reserved)
+static_assert(2 * (att_smem<kKvE4m3, 0>() + 1024) <= 228 * 1024 && 2 * (att_smem<kKvE4m3, 1>() + 1024) <= 228 * 1024,
+              "shared memory of the decode attention, FP8 K/V");
+static_assert(3 * (att_smem<kKvI8, 1>() + 1024) <= 228 * 1024, "shared memory of the decode attention, int8 K/V");
 
 // The stream-K grid: at most kCtasPerSm CTAs per SM (2 with an FP8 cache).
 constexpr int kMaxStreamKCtas = 2 * kNumSMs;
@@ -1059,24 +1088,32 @@ template <int kKv, int kSplit>
 constexpr AttForm att_form_of() {
   return AttForm{sparse_attend_kernel<kKv, kSplit>, att_smem<kKv, kSplit>(), AttShape<kKv, kSplit>::kThreads};
 }
-static AttForm att_form(int kv, bool split) {
-  if (kv == kKvI8) return split ? att_form_of<kKvI8, 1>() : att_form_of<kKvI8, 0>();
+// alone: with so much shared memory that no two CTAs share an SM.
+constexpr size_t kAloneSmem = 120 * 1024;
+constexpr int kAloneSegments = 36;
+static AttForm att_form(int kv, bool split, bool alone = false) {
+  if (kv == kKvI8) {
+    AttForm f = att_form_of<kKvI8, 1>();
+    if (alone && f.smem < kAloneSmem) f.smem = kAloneSmem;
+    return f;
+  }
   if (kv == kKvE4m3) return split ? att_form_of<kKvE4m3, 1>() : att_form_of<kKvE4m3, 0>();
   return split ? att_form_of<kKvBf16, 1>() : att_form_of<kKvBf16, 0>();
 }
 
 // How many clusters of c CTAs of the split kernel can be resident at once
-// (cudaOccupancyMaxActiveClusters, asked once per device, K/V type and c; 0
+// (cudaOccupancyMaxActiveClusters, asked once per device, form and c; 0
 // when the query fails, which keeps the stream-K kernel for that call).
-static int max_active_clusters(int kv, int c) {
+static int max_active_clusters(int kv, int c, bool alone) {
   static std::mutex mu;
-  static int cache[64][3][kMaxCluster + 1];
-  static bool done[64][3][kMaxCluster + 1];
+  static int cache[64][6][kMaxCluster + 1];
+  static bool done[64][6][kMaxCluster + 1];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
-  if (done[dev][kv][c]) return cache[dev][kv][c];
-  const auto [kern, smem, threads] = att_form(kv, true);
+  const int form = kv + (alone ? 3 : 0);
+  if (done[dev][form][c]) return cache[dev][form][c];
+  const auto [kern, smem, threads] = att_form(kv, true, alone);
   int n = 0;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>(c * 16));
@@ -1094,8 +1131,8 @@ static int max_active_clusters(int kv, int c) {
     cudaGetLastError();  // a failed query leaves no error behind for the launch that follows
     return 0;            // and is asked again next time (it is not kept)
   }
-  cache[dev][kv][c] = n;
-  done[dev][kv][c] = true;
+  cache[dev][form][c] = n;
+  done[dev][form][c] = true;
   return n;
 }
 
@@ -1116,16 +1153,22 @@ cudaError_t launch_sparse_attend(const AttnGeom& geo, const void* q, const void*
   const long long N = S * topk;
   // Few segments (small batches): one cluster of C CTAs per segment, merged
   // on chip -- the largest C in {8, 4, 2} with C <= topk (every CTA gets a
-  // unit), at most one CTA per SM (two with an 8-bit cache), and every cluster
+  // unit), at most one CTA per SM (two with an FP8 cache, three with an int8 one), and every cluster
   // resident at once.  Otherwise stream-K over the whole grid, one CTA per SM.
-  const long long per_sm = kv ? AttShape<kKvE4m3, 1>::kCtasPerSm : AttShape<kKvBf16, 1>::kCtasPerSm;
+  const long long per_sm = kv == kKvI8     ? AttShape<kKvI8, 1>::kCtasPerSm
+                           : kv == kKvE4m3 ? AttShape<kKvE4m3, 1>::kCtasPerSm
+                                           : AttShape<kKvBf16, 1>::kCtasPerSm;
   int C = 0;
-  for (int c = kMaxCluster; c >= 2 && !C; c >>= 1) {
-    if (c > topk || S * c > per_sm * kNumSMs) continue;
-    const int fit = max_active_clusters(kv, c);
+  // int8, few segments: one CTA per SM (four requests 14.9 us instead of 17 with CTAs that share one)
+  const bool alone = kv == kKvI8 && S <= kAloneSegments;
+  for (int c = largest_cluster(kv); c >= 2 && !C; c >>= 1) {
+    if (c > topk || S * c > (alone ? 1 : per_sm) * kNumSMs) continue;
+    const int fit = max_active_clusters(kv, c, alone);
     if (fit > 0 && S <= fit) C = c;
   }
-  const auto [kern, smem, threads] = att_form(kv, C > 0);
+  // int8: else a CTA for each segment
+  if (kv == kKvI8 && !C) C = 1;
+  const auto [kern, smem, threads] = att_form(kv, C > 0, alone && C > 0);
   const auto *ks = static_cast<const __nv_bfloat16*>(k_scales), *vss = static_cast<const __nv_bfloat16*>(v_scales);
   // a programmatic dependent of the previous kernel in the stream (the kernel
   // waits for that grid before touching memory), so its launch and prologue

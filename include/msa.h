@@ -666,7 +666,8 @@ msa_status msa_dequantize_gather(const void* k_cache, const void* v_cache, const
  * int8 values enter the bf16 products exactly; a key's scale multiplies its score in fp32, a
  * value's scale its softmax weight (rounded to bf16 before; their sum is fp32 over the unrounded ones).
  * What lies behind a request's last key does not reach its rows, whatever it holds.
- *   scale finite and > 0, scale * log2(e) a normal fp32 number (else MSA_ERR_SHAPE)
+ *   scale     finite and > 0, scale * log2(e) a normal fp32 number (else MSA_ERR_SHAPE)
+ *   workspace >= 256 bytes (only its device error word is used)
  * Other arguments, the output and the errors as msa_sparse_attend_decode. */
 msa_status msa_sparse_attend_decode_int8kv(const msa_config* cfg, const void* q, const void* k_cache,
                                            const void* v_cache, const void* k_scales,

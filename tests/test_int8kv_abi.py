@@ -45,15 +45,14 @@ def test_dequantize_gather(lib):
 
 
 def test_sparse_attend(lib):
-    cfg, size = msa_config(), ctypes.c_size_t()
+    cfg = msa_config()
     assert lib.msa_config_default(ctypes.byref(cfg)) == OK
-    assert lib.msa_workspace_size(ctypes.byref(cfg), 0, 4, 9, ctypes.byref(size)) == OK
-    good = [ctypes.byref(cfg), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 9, 1280, 0.1, FAKE, FAKE, size.value, None]
+    good = [ctypes.byref(cfg), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 9, 1280, 0.1, FAKE, FAKE, 256, None]
     _refuses(lib.msa_sparse_attend_decode_int8kv, good, _tensors(1, 2, 3, 4, 5, 13) + [
         (0, None, NULL), (6, None, NULL), (7, None, NULL), (8, None, NULL), (9, 0, SHAPE), (10, 0, SHAPE), (11, 0, SHAPE),
         (11, 1000, SHAPE), (11, 1 << 31, SHAPE), (12, 0.0, SHAPE), (12, -1.0, SHAPE), (12, math.nan, SHAPE),
         (12, math.inf, SHAPE), (12, 5e-39, SHAPE), (14, None, WORKSPACE), (14, FAKE + 8, WORKSPACE),
-        (15, size.value - 1, WORKSPACE)])
+        (15, 255, WORKSPACE)])
 
 
 def test_attend_chunk_and_shared(lib):

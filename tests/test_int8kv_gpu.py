@@ -176,7 +176,7 @@ def test_sparse_attend(lens, topk, powers):
                 s[int(table[r, n // PAGE]), :, n % PAGE:] = math.nan if r % 2 else math.inf
     q = torch.randn(len(lens), H, D, generator=gen).bfloat16().cuda()
     q2k = _selection(lens, topk, gen)
-    ws = msa.Workspace(msa.workspace_size(msa.make_config(), 0, len(lens), table.shape[1]))
+    ws = msa.Workspace(256)
     want = ref.sparse(q, ref.values(k, ks), ref.values(v, vs), q2k, lens, table, SCALE)
     for workspace in (None, ws):
         got = msa.msa_sparse_attend_decode_int8kv(q, k, v, ks, vs, q2k, ints(lens), table, workspace=workspace)
@@ -192,7 +192,7 @@ def test_sparse_attend_bad_blocks_and_pages():
     q2k = _selection(lens, 16, gen)
     q2k[:, 1] = -1                                # a row without a block
     table[0, 3] = pages                           # and a page outside the pool
-    ws = msa.Workspace(msa.workspace_size(msa.make_config(), 0, 2, table.shape[1]))
+    ws = msa.Workspace(256)
     got = msa.msa_sparse_attend_decode_int8kv(q, k, k, ks, ks, q2k, ints(lens), table, workspace=ws)
     assert ws.read_device_error()[0] == 1
     assert bool((got[1] == 0).all())
