@@ -604,6 +604,7 @@ msa_status msa_sparse_attend_decode_int8kv(const msa_config* cfg, const void* q,
   msa_status st = msa_config_check(cfg);
   if (st != MSA_OK) return st;
   if (!out || !page_table) return MSA_ERR_NULL;
+  if (batch > 0x7fffffff / kKvHeads) return MSA_ERR_SHAPE;  // (a CTA for each request and KV head)
   if ((st = check_int8(k_cache, v_cache, k_scales, v_scales, num_slots)) != MSA_OK) return st;
   // (as the chunk attention: a factor that is no normal number would make NaN of a score of zero or of a masked key)
   if (!(scale > 0.f) || !std::isnormal(chunk_scale_log2(scale, 1.f))) return MSA_ERR_SHAPE;
@@ -618,7 +619,7 @@ static msa_status attend_chunk(const msa_config* cfg, ChunkLaunch L, void* works
   if (L.batch < 1 || L.max_blocks < 1 || L.max_blocks > 0x7fffffff / kBlock || L.tokens < 1 || L.tokens >= (1LL << 31) ||
       L.num_slots < 1 || L.num_slots >= (1LL << 31) || L.num_slots % kBlock)
     return MSA_ERR_SHAPE;
-  if (L.groups < 0 || L.groups > L.batch) return MSA_ERR_SHAPE;
+  if (L.groups < 0 || L.groups > L.batch || L.groups > 0x3fffffff || L.batch > 0x7fffffff - 1024 - L.groups) return MSA_ERR_SHAPE;
   if (L.groups && (!L.group_offsets || !L.shared_lens)) return MSA_ERR_NULL;
   if (L.kv == 2)
     if ((st = check_int8(L.k, L.v, L.k_scales, L.v_scales, L.num_slots)) != MSA_OK) return st;

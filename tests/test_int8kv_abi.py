@@ -49,7 +49,7 @@ def test_sparse_attend(lib):
     assert lib.msa_config_default(ctypes.byref(cfg)) == OK
     good = [ctypes.byref(cfg), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 9, 1280, 0.1, FAKE, FAKE, 256, None]
     _refuses(lib.msa_sparse_attend_decode_int8kv, good, _tensors(1, 2, 3, 4, 5, 13) + [
-        (0, None, NULL), (6, None, NULL), (7, None, NULL), (8, None, NULL), (9, 0, SHAPE), (10, 0, SHAPE), (11, 0, SHAPE),
+        (0, None, NULL), (6, None, NULL), (7, None, NULL), (8, None, NULL), (9, 0, SHAPE), (9, 1 << 30, SHAPE), (10, 0, SHAPE), (11, 0, SHAPE),
         (11, 1000, SHAPE), (11, 1 << 31, SHAPE), (12, 0.0, SHAPE), (12, -1.0, SHAPE), (12, math.nan, SHAPE),
         (12, math.inf, SHAPE), (12, 5e-39, SHAPE), (14, None, WORKSPACE), (14, FAKE + 8, WORKSPACE),
         (15, 255, WORKSPACE)])
@@ -78,7 +78,7 @@ def test_attend_chunk_and_shared(lib):
             (b + 1, 1 << 31, SHAPE), (b + 2, 0.0, SHAPE), (b + 2, math.nan, SHAPE), (b + 2, math.inf, SHAPE), (b + 2, -1.0, SHAPE),
             (b + 5, None, WORKSPACE), (b + 5, FAKE + 16, WORKSPACE), (b + 6, need - 1, WORKSPACE)]
         if group:
-            cases += [(a + 5, None, NULL), (a + 6, None, NULL), (a + 7, -1, SHAPE), (a + 7, 5, SHAPE)]
+            cases += [(a + 5, None, NULL), (a + 6, None, NULL), (a + 7, -1, SHAPE), (a + 7, 5, SHAPE), (a + 3, 0x7fffffff, SHAPE)]
         if head == [FAKE] * 2:
             cases += _tensors(4, 5)
         elif head:
