@@ -1,5 +1,6 @@
 // chunk_attend.cu -- causal attention of each request's new tokens over all its
-// keys in the paged cache (bf16 or E4M3).
+// keys in the paged cache (bf16, E4M3 or int8), and the same where requests share
+// the first pages of their contexts.
 //
 // out[t, h] = sum_j p_j v_j / sum_j p_j, p_j = 2^(x_j - m), x_j = scale log2(e)
 // <q, k_j>, over the keys j <= the token's position.  One pass over the keys, a
@@ -25,7 +26,9 @@
 // all blocks pass both; with 8 or fewer there is one tile, and the warpgroups
 // take its blocks in turn, each into sums of its own, joined at the end: the
 // tensor cores work on one block while the other's softmax runs.  An E4M3 cache
-// has a third warpgroup that widens each page to fp16 (exactly) in shared memory.
+// has a third warpgroup that widens each page to fp16 (exactly) in shared memory;
+// an int8 one has it write n s as bf16, each row by its scale (exactly, where
+// scales are powers of two), so that Q and P stay bf16.
 //
 // That widening writes and reads every tile once more, and shared memory's rate
 // then bounds an item of one new token, which needs only 16 of a tile's 128 rows
@@ -49,6 +52,19 @@
 // 1.38 ms.  Single tokens over long contexts are bound by HBM (64 requests,
 // 4.0 GB: 0.58 ms, 6.9 TB/s), short ones by latency: 4.6 us without any work,
 // 8.2 with one block.
+// int8: 2548 tokens in chunks over 4k to 12k keys take 0.61 ms (E4M3 0.51, bf16
+// 0.475: its widening is 9 instructions for four values where E4M3's is 2, of one
+// warp per scheduler beside two softmax warps), 16 single tokens over 128k keys
+// (2.18 GB) 0.335 ms, 6.5 TB/s.
+//
+// Shared prefixes: sum_j p_j v_j and sum_j p_j over all keys are those over the
+// shared and over a request's own keys, brought to one m.  The groups' shared blocks
+// are items of their own, 16 tokens of any of the group's requests without a mask,
+// listed before the requests', whose items leave these blocks out: pages that n
+// requests share are read n / 16 times instead of n.  The pieces of both are
+// joined by shared_join_kernel.  64 tokens over 16k shared keys, bf16: 64 us
+// (194 unshared; 168 MB, 26 us); 256 over 32k, E4M3: 254 us (1200; 145), two thirds of it
+// the shared items' tiles; four over 2k: 14 us, computed per request.
 #include <cuda_fp16.h>
 
 #include <algorithm>
