@@ -557,6 +557,24 @@ __device__ __forceinline__ uint32_t ca_widen2(uint32_t x) {
   return y;
 }
 
+// Two int8 values (bytes 0 and 1 of w, or 2 and 3) times a power of two s, as bf16, exactly.  at: the bits of 128 s in both halves,
+// step: the bits in which those of 256 s differ.  With its low seven bits m a byte makes (128 + m) s, with its sign 128 s, or
+// 256 s for a negative one (the byte permutation has the sign in all the upper bits); their difference is n s.
+template <bool kUpper>
+__device__ __forceinline__ uint32_t ca_i8_scaled(uint32_t w, uint32_t at, uint32_t step) {
+  uint32_t t, d;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(t) : "r"(w), "n"(kUpper ? 0xb3a2 : 0x9180));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"((t & 0x007f007fu) | at), "r"((t & step) ^ at));
+  return d;
+}
+// at (upper half) and step (lower) for the scale with bits s; ok: it is a power of two for which 128 s and 256 s are normal numbers.
+__device__ __forceinline__ uint32_t ca_i8_code(uint32_t s, bool& ok) {
+  const uint32_t field = s >> 7;  // (with the sign)
+  ok = field ? (s & 0x7fu) == 0 && field <= 246 : __popc(s) == 1;
+  const uint32_t at = field ? s + 0x380 : (32 - __clz(s)) << 7;
+  return at << 16 | ((at ^ (at + 0x80)) & 0xffff);
+}
+
 // Products of m16n8k16, the 16 query heads their rows, from the copied pages.  E4M3: warps 0 to 3 take the even blocks, 32
 // keys each, warps 4 to 7 the odd ones.  S = Q K^T: a 16-bit ldmatrix of K gives a lane four consecutive bytes of one key,
 // dims 16 s + 4 t .. + 3 of k-step s, so Q's fragments hold those dims in the same slots.  O += P V: a transposing ldmatrix
@@ -1647,7 +1665,15 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
           const int k = ca_block_v(j, nb);
           keys = sm.bad[(base + k) % kCaBad] ? 0 : min(kBlock, len - (b0 + k) * kBlock);
         }
-        if (kI8) scale = i_row < keys ? scale * 0x10001u : 0u;  // (rows of zeros there, whatever the scales)
+        // int8: rows of powers of two, as they are written, take no multiplication
+        bool powers = true;
+        uint32_t code = 0;
+        if constexpr (kI8) {
+          if (i_row >= keys) scale = 0x3f80u;
+          code = ca_i8_code(scale, powers);
+          powers = __all_sync(0xffffffffu, powers);
+          if (!powers) code = scale * 0x10001u;
+        }
         const uint32_t src = smem_u32(sm.raw[kFp8 ? rs : 0]) + sw128(row0, piece);
         const uint32_t dst = smem_u32(sm.kv[st]) + (piece >> 2) * kCaHalf;
         const uint32_t dst0 = dst + sw128(row0, 2 * (piece & 3)), dst1 = dst + sw128(row0, 2 * (piece & 3) + 1);
@@ -1657,32 +1683,45 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
 #pragma unroll
         for (int q = 0; q < 2; ++q) x[0][q] = lds128(src + q * kStep * 128);
         if (!(ok = ca_wait(&sm.kv_empty[st], ((load / kTiles) & 1) ^ 1, err, 832))) break;
+        auto widen = [&](auto fast) {
 #pragma unroll
-        for (int n = 0; n < kBatches; ++n) {
-          if (n + 1 < kBatches)
+          for (int n = 0; n < kBatches; ++n) {
+            if (n + 1 < kBatches)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) x[(n + 1) & 1][q] = lds128(src + (2 * n + 2 + q) * kStep * 128);
+              for (int q = 0; q < 2; ++q) x[(n + 1) & 1][q] = lds128(src + (2 * n + 2 + q) * kStep * 128);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int down = (2 * n + q) * kStep;  // rows below row0, a multiple of the swizzle's eight
-            uint4 v = x[n & 1][q];
-            if (!kI8 && keys < kBlock && row0 + down >= keys) v = make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            const uint32_t ss = kI8 ? __shfl_sync(0xffffffffu, scale, (row0 & 3) + 4 * (2 * n + q)) : 0u;
-            uint32_t y[8];
+            for (int q = 0; q < 2; ++q) {
+              const int down = (2 * n + q) * kStep;  // rows below row0, a multiple of the swizzle's eight
+              uint4 v = x[n & 1][q];
+              if (keys < kBlock && row0 + down >= keys) v = make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              const uint32_t ss = kI8 ? __shfl_sync(0xffffffffu, code, (row0 & 3) + 4 * (2 * n + q)) : 0u;
+              const uint32_t at = __byte_perm(ss, 0, 0x3232), step = __byte_perm(ss, 0, 0x1010);
+              uint32_t y[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              y[2 * i] = kI8 ? mul_bf16x2(i8_lo2(w[i]), ss) : ca_widen2(w[i]);
-              y[2 * i + 1] = kI8 ? mul_bf16x2(i8_hi2(w[i]), ss) : ca_widen2(w[i] >> 16);
+              for (int i = 0; i < 4; ++i) {
+                if constexpr (!kI8) {
+                  y[2 * i] = ca_widen2(w[i]);
+                  y[2 * i + 1] = ca_widen2(w[i] >> 16);
+                } else if constexpr (decltype(fast)::value) {
+                  y[2 * i] = ca_i8_scaled<false>(w[i], at, step);
+                  y[2 * i + 1] = ca_i8_scaled<true>(w[i], at, step);
+                } else {
+                  y[2 * i] = mul_bf16x2(i8_lo2(w[i]), ss);
+                  y[2 * i + 1] = mul_bf16x2(i8_hi2(w[i]), ss);
+                }
+              }
+              sts128(dst0 + down * 128, y[0], y[1], y[2], y[3]);
+              sts128(dst1 + down * 128, y[4], y[5], y[6], y[7]);
             }
-            sts128(dst0 + down * 128, y[0], y[1], y[2], y[3]);
-            sts128(dst1 + down * 128, y[4], y[5], y[6], y[7]);
+            if (n + 1 == kBatches) {  // (once the last rows have been stored: a load that is only asked for may still read the place)
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.raw_empty[rs]);
+            }
           }
-          if (n + 1 == kBatches) {  // (once the last rows have been stored: a load that is only asked for may still read the place)
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.raw_empty[rs]);
-          }
-        }
+        };
+        if (!kI8 || powers) widen(std::true_type{});
+        else widen(std::false_type{});
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.kv_full[st]);
