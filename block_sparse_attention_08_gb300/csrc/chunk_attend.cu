@@ -52,9 +52,9 @@
 // 1.38 ms.  Single tokens over long contexts are bound by HBM (64 requests,
 // 4.0 GB: 0.58 ms, 6.9 TB/s), short ones by latency: 4.6 us without any work,
 // 8.2 with one block.
-// int8: 2548 tokens in chunks over 4k to 12k keys take 0.61 ms (E4M3 0.51, bf16
-// 0.475: its widening is 9 instructions for four values where E4M3's is 2, of one
-// warp per scheduler beside two softmax warps), 16 single tokens over 128k keys
+// int8: 2548 tokens in chunks over 4k to 12k keys take 0.587 ms (E4M3 0.51, bf16
+// 0.475: its widening is 8 instructions for four values where E4M3's is 2; with one
+// instead of four for a pair of values it would be 0.49), 16 single tokens over 128k keys
 // (2.18 GB) 0.335 ms, 6.5 TB/s.
 //
 // Shared prefixes: sum_j p_j v_j and sum_j p_j over all keys are those over the
@@ -166,12 +166,16 @@ struct CaShape {
   static constexpr int kTiles = kFp8 ? 4 : 5;
   static constexpr int kRaw = kFp8 ? 2 : 1;    // E4M3 tiles as copied
   static constexpr int kWiden = kFp8 ? 4 : 0;  // widening warps
+  // and beside the issuing warps: an int8 tile takes a widening warp longer than the softmax of its scores (2548 tokens in chunks
+  // over 4k to 12k keys 631 us without, 587 with them)
+  static constexpr int kHelp = kKv == kCaI8 ? 2 : 0;
   static constexpr int kThreads = 32 * (kCaWidenWarp + kWiden);
   // registers per thread of the roles, out of the launch's 168 (384 threads) or 128 (512 threads) a thread:
   // 256 * 216 + 128 * 72 = 384 * 168, and 256 * 208 + 128 * 56 + 128 * 40 = 512 * 128.  (With 184 for the softmax, E4M3
   // chunks took 6% more.
   // Two widening warps in the issuing warps' group leave it 216: chunks 1% faster, but items of few tokens, bound by the
-  // widening, made 17 mixed requests 126 us instead of 115.)
+  // widening, made 17 mixed requests 126 us instead of 115.  int8: 256 * 200 + 256 * 56; the widening in 40 registers 688 us,
+  // in 48 599, in 64, which leave the softmax 192, 580, but 3 groups of 40 requests 138 instead of 137.)
   static constexpr int kRegsSoftmax = kKv == kCaI8 ? 200 : kFp8 ? 208 : 216, kRegsIssue = kFp8 ? 56 : 72;
   static constexpr int kRegsWiden = kKv == kCaI8 ? 56 : 40;
   // fp16 weights are kept near the top of their range (at most 2^(kLift + kCaSlack) = 2^15), so that small ones
@@ -559,7 +563,8 @@ __device__ __forceinline__ uint32_t ca_widen2(uint32_t x) {
 
 // Two int8 values (bytes 0 and 1 of w, or 2 and 3) times a power of two s, as bf16, exactly.  at: the bits of 128 s in both halves,
 // step: the bits in which those of 256 s differ.  With its low seven bits m a byte makes (128 + m) s, with its sign 128 s, or
-// 256 s for a negative one (the byte permutation has the sign in all the upper bits); their difference is n s.
+// 256 s for a negative one (the byte permutation has the sign in all the upper bits); their difference is n s.  (Decoded
+// first and multiplied then, one more instruction of four: 648 us instead of 625 for 2548 tokens in chunks.)
 template <bool kUpper>
 __device__ __forceinline__ uint32_t ca_i8_scaled(uint32_t w, uint32_t at, uint32_t step) {
   uint32_t t, d;
@@ -567,12 +572,13 @@ __device__ __forceinline__ uint32_t ca_i8_scaled(uint32_t w, uint32_t at, uint32
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"((t & 0x007f007fu) | at), "r"((t & step) ^ at));
   return d;
 }
-// at (upper half) and step (lower) for the scale with bits s; ok: it is a power of two for which 128 s and 256 s are normal numbers.
+// at (upper half) and step (lower) for the scale with bits s; not ok: it is no power of two for which 128 s and 256 s are normal
+// numbers (and its code is that of 1).
 __device__ __forceinline__ uint32_t ca_i8_code(uint32_t s, bool& ok) {
   const uint32_t field = s >> 7;  // (with the sign)
-  ok = field ? (s & 0x7fu) == 0 && field <= 246 : __popc(s) == 1;
-  const uint32_t at = field ? s + 0x380 : (32 - __clz(s)) << 7;
-  return at << 16 | ((at ^ (at + 0x80)) & 0xffff);
+  ok = field ? (s & 0x7fu) == 0 && field <= 246 : s != 0 && (s & (s - 1)) == 0;
+  const uint32_t at = !ok ? 0x4300u : field ? s + 0x380 : (32 - __clz(s)) << 7;
+  return at << 16 | (at ^ (at + 0x80));
 }
 
 // Products of m16n8k16, the 16 query heads their rows, from the copied pages.  E4M3: warps 0 to 3 take the even blocks, 32
@@ -1036,19 +1042,22 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
       mbar_init(&sm.o_full[i], 1);
     }
     for (int i = 0; i < kTiles; ++i) {
-      mbar_init(&sm.kv_full[i], kFp8 ? 4 : 1);
+      if (!Shape::kHelp) mbar_init(&sm.kv_full[i], kFp8 ? 4 : 1);
+      else mbar_init(&sm.kv_full[i], 4 + Shape::kHelp);
       mbar_init(&sm.kv_empty[i], 1);
     }
     for (int i = 0; i < Shape::kRaw; ++i) {
       mbar_init(&sm.raw_full[i], 1);
-      mbar_init(&sm.raw_empty[i], 4);
+      if (!Shape::kHelp) mbar_init(&sm.raw_empty[i], 4);
+      else mbar_init(&sm.raw_empty[i], 4 + Shape::kHelp);
     }
     mbar_init(&sm.x_full, 8);
     mbar_init(&sm.x_done, 8);
     mbar_init(&sm.done, 1);
     for (int i = 0; i < kCaInfo; ++i) {
       mbar_init(&sm.info_full[i], 1);
-      mbar_init(&sm.info_empty[i], 9 + Shape::kWiden);  // the softmax, MMA and widening warps
+      if (!Shape::kHelp) mbar_init(&sm.info_empty[i], 9 + Shape::kWiden);  // the softmax, MMA and widening warps
+      else mbar_init(&sm.info_empty[i], 9 + Shape::kWiden + Shape::kHelp);
     }
     for (int i = 0; i < kCaOnePlaces; ++i) {
       mbar_init(&sm.one_full[i], 1);
@@ -1094,6 +1103,7 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
   // A wait that gives up (recorded in the error word) ends its role, so a broken pipeline ends after one bounded wait
   // per role.
   if (warp >= 8 && warp < kCaWidenWarp) ca_regs_down<Shape::kRegsIssue>();
+  if (Shape::kHelp && warp >= kCaWidenWarp) ca_regs_down<Shape::kRegsWiden>();
   if (warp == kCaProducerWarp) {
     // ---------------- the share's items, and their copies ----------------
     const long long u0 = sm.share[0].u0, u1 = sm.share[0].u1;
@@ -1375,7 +1385,7 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
       mbar_wait(&sm.done, 0, err, 815);
     }
     __syncwarp();
-  } else if (warp == kCaMmaWarp + 1) {
+  } else if (!Shape::kHelp && warp == kCaMmaWarp + 1) {
     // ---------------- requests with bad lengths ----------------
     ca_refuse_bad<kShared>(a, lane);
   } else if (warp < 8) {
@@ -1591,11 +1601,13 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
     roles_done();
     if constexpr (kOne)
       if (sm.apart) ca_one_attend<kKv, kShared>(a, sm, warp);
-  } else if (kFp8 && warp >= kCaWidenWarp) {
+  } else if (kFp8 && (Shape::kHelp || warp >= kCaWidenWarp)) {
     // ---------------- E4M3 pages and bf16 queries to fp16; int8 pages, with their rows' scales, to bf16 ----------------
-    ca_regs_down<Shape::kRegsWiden>();
-    constexpr int kLanes = 128, kStep = kLanes / 8;  // kStep: rows at once
-    const int wt = tid - 32 * kCaWidenWarp;
+    if (!Shape::kHelp) ca_regs_down<Shape::kRegsWiden>();
+    constexpr int kLanes = 32 * (kFp8 ? Shape::kWiden + Shape::kHelp : 4), kStep = kLanes / 8;  // kStep: rows at once
+    constexpr int kSteps = (kBlock + kStep - 1) / kStep;                            // the last one by some warps alone
+    const int ww = warp >= kCaWidenWarp ? warp - kCaWidenWarp : warp - (kCaWidenWarp - Shape::kHelp) + Shape::kWiden, wt = 32 * ww + lane;
+    const bool all_steps = kBlock % kStep == 0 || 4 * ww + (kSteps - 1) * kStep < kBlock;
     // Eight lanes take 16-byte pieces of two neighbouring rows, the odd row's from the other half: they read and write
     // eight different 16-byte banks of the swizzled tiles.
     const int i8 = wt & 7, odd = i8 >> 2, piece = (i8 & 3) + 4 * (((wt >> 3) & 1) ^ odd), row0 = 2 * (wt >> 4) + odd;
@@ -1627,9 +1639,9 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
       const int nb = sm.info[is].nb, b0 = sm.info[is].b0, len = sm.info[is].len, ntok = sm.info[is].ntok;
       // int8: each lane has the scale of one of the warp's 32 rows, asked for a tile ahead, from the pages as the producer
       // finds them
-      const int i_row = 4 * (warp - kCaWidenWarp) + (lane & 3) + 16 * (lane >> 2);
+      const int i_row = 4 * ww + (lane & 3) + kStep * (lane >> 2);
       const int32_t* table = a.page_table + static_cast<long long>(sm.info[is].row) * a.max_blocks + b0;
-      const int at_g = sm.info[is].g * kBlock + i_row;
+      const int at_g = sm.info[is].g * kBlock + min(i_row, kBlock - 1);
       int ids = 0, ids_next = 0, last = 0, before = 0;
       uint32_t next_scale = 0;
       if (kI8 && nb > 0) ids_next = lane < nb ? table[lane] : 0;
@@ -1656,8 +1668,13 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
       for (int j = 0; j < 2 * nb && ok; ++j) {
         const int load = 2 * base + j, rs = load % Shape::kRaw, st = load % kTiles;
         const bool is_v = ca_is_v(j, nb);
-        uint32_t scale = next_scale;
-        if constexpr (kI8) ask(j + 1);
+        const uint32_t scale = next_scale;
+        bool powers = true;
+        uint32_t code = 0;
+        if constexpr (kI8) {
+          code = ca_i8_code(scale, powers);
+          ask(j + 1);
+        }
         if (!(ok = ca_wait(&sm.raw_full[rs], (load / Shape::kRaw) & 1, err, 831))) break;
         // V rows behind the last key become zero: their weight is zero, but they may hold anything
         int keys = kBlock;
@@ -1665,20 +1682,14 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
           const int k = ca_block_v(j, nb);
           keys = sm.bad[(base + k) % kCaBad] ? 0 : min(kBlock, len - (b0 + k) * kBlock);
         }
-        // int8: rows of powers of two, as they are written, take no multiplication
-        bool powers = true;
-        uint32_t code = 0;
-        if constexpr (kI8) {
-          if (i_row >= keys) scale = 0x3f80u;
-          code = ca_i8_code(scale, powers);
-          powers = __all_sync(0xffffffffu, powers);
-          if (!powers) code = scale * 0x10001u;
-        }
+        // int8: tiles of powers of two, as rows are written, take no multiplication
+        if constexpr (kI8)
+          if (!(powers = __all_sync(0xffffffffu, powers || i_row >= keys))) code = (i_row < keys ? scale : 0x3f80u) * 0x10001u;
         const uint32_t src = smem_u32(sm.raw[kFp8 ? rs : 0]) + sw128(row0, piece);
         const uint32_t dst = smem_u32(sm.kv[st]) + (piece >> 2) * kCaHalf;
         const uint32_t dst0 = dst + sw128(row0, 2 * (piece & 3)), dst1 = dst + sw128(row0, 2 * (piece & 3) + 1);
         // two rows at a time, the next two asked for before
-        constexpr int kBatches = kBlock / kStep / 2;
+        constexpr int kBatches = kSteps / 2;
         uint4 x[2][2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) x[0][q] = lds128(src + q * kStep * 128);
@@ -1688,9 +1699,11 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
           for (int n = 0; n < kBatches; ++n) {
             if (n + 1 < kBatches)
 #pragma unroll
-              for (int q = 0; q < 2; ++q) x[(n + 1) & 1][q] = lds128(src + (2 * n + 2 + q) * kStep * 128);
+              for (int q = 0; q < 2; ++q)
+                if (2 * n + 3 + q < kSteps || all_steps) x[(n + 1) & 1][q] = lds128(src + (2 * n + 2 + q) * kStep * 128);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
+              if (2 * n + q + 1 == kSteps && !all_steps) break;
               const int down = (2 * n + q) * kStep;  // rows below row0, a multiple of the swizzle's eight
               uint4 v = x[n & 1][q];
               if (keys < kBlock && row0 + down >= keys) v = make_uint4(0u, 0u, 0u, 0u);
@@ -1729,6 +1742,7 @@ __global__ void __launch_bounds__(CaShape<kKv>::kThreads, 1) chunk_attend_kernel
       }
       base += nb;
     }
+    if (Shape::kHelp && warp == kCaMmaWarp + 1) ca_refuse_bad<kShared>(a, lane);
   }
   // (the roles' register counts end with their branches, so the one-token items are taken inside them)
   if (warp >= 8 && warp != kCaProducerWarp) roles_done();
