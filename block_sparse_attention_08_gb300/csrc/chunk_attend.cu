@@ -1823,7 +1823,8 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_join_kernel(const __grid
 // loads that follow each other are a pair's code and its pieces, kCaJoinBatch of them at a time.  (With the factors
 // worked out once per row in shared memory, as above, four tokens took 28 us instead of 17.)  Few tokens over a long
 // prefix have many pieces, one from each CTA that had a part of their group's item, and leave most SMs idle: kSplit > 1 gives a
-// pair to kSplit CTAs, a part of the dims each, whose threads share out the pieces (4 tokens over 16k keys: 36 us without).
+// pair to kSplit CTAs, a part of the dims each, whose threads share out the pieces (4 tokens over 16k keys: 36 us without; two
+// CTAs each for 64 tokens over 16k: 66.6 us instead of 64.1).
 constexpr int kCaJoinBatch = 4, kCaJoinSplit = 4;
 template <int kSplit>
 __global__ void __launch_bounds__(kCaJoinThreads, 2) shared_join_kernel(const __grid_constant__ CaArgs a) {
@@ -1835,8 +1836,9 @@ __global__ void __launch_bounds__(kCaJoinThreads, 2) shared_join_kernel(const __
   const int cta = blockIdx.x / kSplit, ctas = gridDim.x / kSplit;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long from = static_cast<long long>(max(a.cu[0], 0)) * kKvHeads;
-  const long long to = min(a.tokens, static_cast<long long>(a.cu[a.batch])) * kKvHeads;
+  // (read beside the first codes, not before them)
+  const long long from = static_cast<long long>(max(a.cu[0], 0)) * kKvHeads, all = a.tokens * kKvHeads;
+  const long long to = min(all, static_cast<long long>(a.cu[a.batch]) * kKvHeads);
   // one source of pieces: the first, and the second with the distance of those that follow it
   struct Source {
     const float4 *o0, *o1;
@@ -1858,11 +1860,12 @@ __global__ void __launch_bounds__(kCaJoinThreads, 2) shared_join_kernel(const __
                   max(c.last - c.first, 0) + 1};
   };
   // 32 pairs' codes at once: most of a long batch's have nothing to join
-  for (long long base = cta; base < to; base += 32LL * ctas) {
+  for (long long base = cta; base < all; base += 32LL * ctas) {
     const long long mine = base + static_cast<long long>(lane) * ctas;
+    const int32_t own_code = mine < all ? a.own.at[mine] : 0, with_code = mine < all ? a.shared.at[mine] : 0;  // (may be anything)
+    if (base >= to) break;
     const bool in = mine >= from && mine < to;
-    const int32_t own_code = in ? a.own.at[mine] : 0, with_code = in ? a.shared.at[mine] : 0;  // (the second may be anything)
-    for (unsigned left = __ballot_sync(0xffffffffu, CaPieces::of(own_code).join); left; left &= left - 1) {
+    for (unsigned left = __ballot_sync(0xffffffffu, in && CaPieces::of(own_code).join); left; left &= left - 1) {
       const int k = __ffs(left) - 1;
       const long long at = base + static_cast<long long>(k) * ctas;
       const CaPieces own = CaPieces::of(__shfl_sync(0xffffffffu, own_code, k));
