@@ -1839,25 +1839,18 @@ __global__ void __launch_bounds__(kCaJoinThreads, 2) shared_join_kernel(const __
   // (read beside the first codes, not before them)
   const long long from = static_cast<long long>(max(a.cu[0], 0)) * kKvHeads, all = a.tokens * kKvHeads;
   const long long to = min(all, static_cast<long long>(a.cu[a.batch]) * kKvHeads);
-  // one source of pieces: the first, and the second with the distance of those that follow it
+  // one source of n pieces, of which piece 0 lies one slot behind the pointers and piece q > 0 2 q slots (a slot has as many rows; a
+  // token's place none)
   struct Source {
-    const float4 *o0, *o1;
-    const float2 *ml0, *ml1;
-    long long step;  // between pieces, in rows of four dims
-    int n;
+    const float4* o;
+    const float2* ml;
+    int rows, n;
   };
   auto source = [&](const CaPieces& c, const CaTokens& t, long long at) {
-    if (!c.cut) {
-      const float4* o = t.o + (at * (kDim / 4) + d4) * kGroup + row;
-      const float2* ml = t.ml + at * kGroup + row;
-      return Source{o, o, ml, ml, 0, 1};
-    }
-    const int rows = c.one ? kGroup : a.rows, in = (c.one ? 0 : c.e * kGroup) + row;
-    const float4* o = (c.one ? a.part1_o : a.part_o) + static_cast<long long>(d4) * rows + in;
-    const float2* ml = (c.one ? a.part1_ml : a.part_ml) + in;
-    const long long s0 = 2LL * c.first + 1, s1 = 2LL * c.first + 2;
-    return Source{o + s0 * (kDim / 4) * rows, o + s1 * (kDim / 4) * rows, ml + s0 * rows, ml + s1 * rows, 2LL * rows,
-                  max(c.last - c.first, 0) + 1};
+    if (!c.cut) return Source{t.o + (at * (kDim / 4) + d4) * kGroup + row, t.ml + at * kGroup + row, 0, 1};
+    const int rows = c.one ? kGroup : a.rows, in = (c.one ? 0 : c.e * kGroup) + row, from = 2 * c.first * rows;
+    return Source{(c.one ? a.part1_o : a.part_o) + (from * (kDim / 4) + d4 * rows + in),
+                  (c.one ? a.part1_ml : a.part_ml) + (from + in), rows, max(c.last - c.first, 0) + 1};
   };
   // 32 pairs' codes at once: most of a long batch's have nothing to join
   for (long long base = cta; base < all; base += 32LL * ctas) {
@@ -1890,14 +1883,9 @@ __global__ void __launch_bounds__(kCaJoinThreads, 2) shared_join_kernel(const __
         for (int i = 0; i < kCaJoinBatch; ++i) {
           const int s = min(s0 + kSplit * i, n - 1);
           const bool first = s < x.n;
-          const int q = first ? s : s - x.n;
-          const float4* o0 = first ? x.o0 : y.o0;
-          const float4* o1 = first ? x.o1 : y.o1;
-          const float2* ml0 = first ? x.ml0 : y.ml0;
-          const float2* ml1 = first ? x.ml1 : y.ml1;
-          const long long off = (first ? x.step : y.step) * (q - 1);
-          ml[i] = *(q == 0 ? ml0 : ml1 + off);
-          v[i] = *(q == 0 ? o0 : o1 + off * (kDim / 4));
+          const int q = first ? s : s - x.n, off = (2 * q + (q == 0)) * (first ? x.rows : y.rows);
+          ml[i] = (first ? x.ml : y.ml)[off];
+          v[i] = (first ? x.o : y.o)[off * (kDim / 4)];
         }
         float top = m;
 #pragma unroll
