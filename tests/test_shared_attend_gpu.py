@@ -94,6 +94,8 @@ SHAPES = {
     "requests without new tokens": [(900, [(0, 0), (5, 1), (6, 0), (7, 2), (0, 0)])],
     "a group without tokens": [(900, [(10, 0), (5, 0)]), (300, [(5, 1), (8, 1)])],
     "more tokens than fill the items": [(600, [(0, 20), (3, 50)])],
+    "48 groups": [(128 + 3 * g, [(g, 1)] * (2 + 7 * (g % 2))) for g in range(48)],
+    "49 groups and others": [(256, [(g + i, 1) for i in range(2 + g % 9)]) for g in range(49)] + [(None, [(40, 1), (600, 3)])],
     "700 requests": [(256, [(i % 90, 1) for i in range(350)]), (384, [(i % 70, 1) for i in range(350)])],
 }
 
