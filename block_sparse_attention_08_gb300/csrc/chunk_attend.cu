@@ -62,8 +62,8 @@
 // are items of their own, 16 tokens of any of the group's requests without a mask,
 // listed before the requests', whose items leave these blocks out: pages that n
 // requests share are read n / 16 times instead of n.  The pieces of both are
-// joined by shared_join_kernel.  64 tokens over 16k shared keys, bf16: 64 us
-// (194 unshared; 168 MB, 26 us); 256 over 32k, E4M3: 254 us (1200; 145), two thirds of it
+// joined by shared_join_kernel.  64 tokens over 16k shared keys, bf16: 63 us
+// (194 unshared; 168 MB, 26 us); 256 over 32k, E4M3: 249 us (1200; 145), two thirds of it
 // the shared items' tiles; four over 2k: 14 us, computed per request.
 #include <cuda_fp16.h>
 

@@ -13,7 +13,9 @@
 //
 // Bound by the instructions that it issues: seven for the four values of a word, five of them
 // on the half-rate integer pipe.  So no lane masks, tests or counts what a full group of keys does
-// not need, and a warp takes 32 keys for each wait on a barrier.
+// not need, and a warp takes 32 keys for each wait on a barrier.  (Three of them on that pipe and six on
+// the other, with the sign taken off by a fused operation that ends at zero: 364 us instead of 339 for 16 tokens over 128k
+// keys.)
 #pragma once
 
 #include "common.cuh"

@@ -128,7 +128,7 @@ struct SegInfo {
 // cutting segments and merging them through memory cost 7 us.  (64 requests
 // of 2048 selected keys: 78 us with a chunk to each of three warps, two CTAs; 46
 // in pairs of warps; 39 with whole segments; 41 with three CTAs, where 48 requests take 34 us instead of 38 and
-// 256 take 120 instead of 128.)
+// 256 take 120 instead of 128; 43 with six warps in each of two CTAs.)
 template <int kKv, int kSplit>
 struct AttShape {
   static constexpr bool kI8 = kKv == kKvI8;
@@ -1070,7 +1070,7 @@ static_assert(att_smem<0, 0>() <= 227 * 1024 && att_smem<0, 1>() <= 227 * 1024, 
 // two CTAs of the FP8 forms per SM (228 KB of shared memory per SM, 1 KB of it per CTA reserved)
 static_assert(2 * (att_smem<kKvE4m3, 0>() + 1024) <= 228 * 1024 && 2 * (att_smem<kKvE4m3, 1>() + 1024) <= 228 * 1024,
               "shared memory of the decode attention, FP8 K/V");
-static_assert(3 * (att_smem<kKvI8, 1>() + 1024) <= 228 * 1024, "shared memory of the decode attention, int8 K/V");
+static_assert(AttShape<kKvI8, 1>::kCtasPerSm * (att_smem<kKvI8, 1>() + 1024) <= 228 * 1024, "shared memory of the decode attention, int8 K/V");
 
 // The stream-K grid: at most kCtasPerSm CTAs per SM (2 with an FP8 cache).
 constexpr int kMaxStreamKCtas = 2 * kNumSMs;
