@@ -625,7 +625,9 @@ msa_status msa_attend_chunk_fp8kv(const msa_config* cfg, const void* q, const vo
  * The scales need no calibration, and 7 bits of magnitude are 8 to 16 times E4M3's steps near a
  * row's largest value.  msa_quantize_insert writes powers of two, with which n * s is a bf16
  * number; the readers take any finite bf16 scale (n * s is then rounded to bf16 once where
- * it is read back or enters a product). */
+ * it is read back or enters a product).  As over the other caches, a row's weighted values are summed up
+ * in fp32 before they are divided by the weights' sum, with weights of up to 2^8: values near the end of
+ * fp32's range do not fit. */
 
 /* Quantises K and V rows as they are written at their slots.  Per row of 128 values x:
  * s = 2^(e - 6), 2^e the power of two at or below max |x| (e >= -127; a row of zeros: s = 2^-133),
