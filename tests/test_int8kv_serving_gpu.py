@@ -260,3 +260,35 @@ def test_offsets_beyond_32_bits():
     assert ws.read_device_error()[0] == 0
     slot = to[look]
     assert torch.equal(ko[look].double(), value(k, ks)) and torch.equal(vo[look].double(), value(v, vs))
+
+
+@pytest.mark.parametrize("requests", [1, 7, 20, 45, 150])
+def test_a_captured_sparse_step_with_lengths_that_change(requests):
+    """Split over clusters, and with a CTA for each of few or many segments; requests of no keys at all among them."""
+    gen = torch.Generator().manual_seed(requests)
+    lens = [1500 + 11 * i % 700 for i in range(requests)]
+    table, pool = S.page_table(lens, seed=requests)
+    (k, ks), (v, vs) = i8.cache(pool, 1), i8.cache(pool, 2)
+    q = torch.randn(requests, 64, 128, generator=gen).bfloat16().cuda()
+    q2k = torch.randint(0, 11, (4, requests, 1), generator=gen, dtype=torch.int32).cuda() + torch.arange(6, dtype=torch.int32, device="cuda")
+    q2k = torch.where(q2k < 11, q2k, -1).contiguous()
+    seq, ws, out = S.ints(lens), msa.Workspace(256), torch.empty_like(q)
+    values = i8.values(k, ks), i8.values(v, vs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        msa.msa_sparse_attend_decode_int8kv(q, k, v, ks, vs, q2k, seq, table, out=out, workspace=ws)
+    for turn in range(3):
+        now = [n if turn == 0 else 1408 + n % 90 if (r + turn) % 3 else 0 for r, n in enumerate(lens)]
+        seq.copy_(S.ints(now))
+        out.fill_(9)
+        # (blocks behind a request's last are an error: none is asked for but by those without keys)
+        live = torch.where((torch.tensor(now) > 0)[None, :, None].cuda(), q2k, -1)
+        kept = q2k.clone()
+        q2k.copy_(live)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ws.read_device_error()[0] == 0
+        i8.check_sparse(out, i8.sparse(q, *values, q2k, now, table, SCALE))
+        assert all(bool((out[r] == 0).all()) for r, n in enumerate(now) if n == 0)
+        q2k.copy_(kept)
