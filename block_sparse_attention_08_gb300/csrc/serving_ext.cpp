@@ -103,20 +103,21 @@ void changed(std::initializer_list<at::Tensor> written) {
     if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
-// New outputs of one call as parts of one allocation (four of them took 3 us more): next(type, n) gives the next.
+// New outputs of one call as parts of one allocation (four of them took 3 us more): next(type, shape) gives the next.
 class Parts {
  public:
   Parts(c10::DeviceIndex index, int64_t bytes)
       : buf_(at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(c10::Device(c10::kCUDA, index)))) {}
   static int64_t room(int64_t bytes) { return (bytes + 255) / 256 * 256; }
-  at::Tensor next(at::ScalarType type, int64_t n) {
+  at::Tensor next(at::ScalarType type, int64_t n) { return next(type, at::IntArrayRef{n}); }
+  at::Tensor next(at::ScalarType type, at::IntArrayRef shape) {
     const int64_t size = static_cast<int64_t>(c10::elementSize(type));
     at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf_.storage()),
                                                             c10::DispatchKeySet(c10::DispatchKey::CUDA),
                                                             c10::scalarTypeToTypeMeta(type));
     t.unsafeGetTensorImpl()->set_storage_offset((buf_.storage_offset() + at_) / size);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
-    at_ += room(n * size);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    at_ += room(t.numel() * size);
     return t;
   }
 
@@ -593,8 +594,17 @@ PyObject* dequantize_gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (tokens < 1 || tokens > INT32_MAX || batch < 1 || batch > INT32_MAX || width < 1 || width > INT32_MAX)
       return PyLong_FromLong(MSA_ERR_SHAPE);
-    const at::Tensor ko = output(a[8], "k_out", at::kBFloat16, {tokens, kG, kD}, d),
-                     vo = output(a[9], "v_out", at::kBFloat16, {tokens, kG, kD}, d);
+    at::Tensor ko, vo;
+    // (one allocation for both of a short read, which waits for the host; long ones may be freed by themselves)
+    if (a[8] == Py_None && a[9] == Py_None && tokens <= 4096) {
+      const Sizes shape{tokens, kG, kD};
+      Parts parts(d, 2 * Parts::room(tokens * kG * kD * 2));
+      ko = parts.next(at::kBFloat16, shape);
+      vo = parts.next(at::kBFloat16, shape);
+    } else {
+      ko = output(a[8], "k_out", at::kBFloat16, {tokens, kG, kD}, d);
+      vo = output(a[9], "v_out", at::kBFloat16, {tokens, kG, kD}, d);
+    }
     const Space ws = error_word(a[10], d);
     const msa_status st = run(d, [&](void* stream) {
       return msa_dequantize_gather(kc.const_data_ptr(), vc.const_data_ptr(), ks.const_data_ptr(), vs.const_data_ptr(),

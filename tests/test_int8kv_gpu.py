@@ -216,3 +216,19 @@ def test_sparse_attend_equals_the_bf16_call_on_the_values():
     # each rounds its weights by 2^-8 in the values' sum and in theirs, and the output by 2^-8
     spread = ref.sparse(q, kb, vb, q2k, lens, table, SCALE)[1]
     assert bool(((got.double() - want.double()).abs() <= 2.0 ** -7 * want.double().abs() + 4 * 2.0 ** -8 * 1.01 * spread).all())
+
+
+@pytest.mark.parametrize("tokens", [1, 4096, 4097])
+def test_new_outputs_are_apart(tokens):
+    (k, ks), (v, vs) = ref.cache(2, 1), ref.cache(2, 2)
+    table, cu = ints([[i % 2 for i in range(33)]]), ints([0, tokens])
+    ko, vo = msa.msa_dequantize_gather(k, v, ks, vs, table, cu, tokens)
+    want = vo.clone()
+    assert ko.shape == vo.shape == (tokens, G, D) and ko.is_contiguous() and vo.is_contiguous()
+    assert ko.data_ptr() % 256 == vo.data_ptr() % 256 == 0
+    ko.fill_(3)
+    assert torch.equal(vo, want) and bool((ko == 3).all())
+    del ko
+    torch.cuda.synchronize()
+    torch.full((tokens, G, D), 5.0, device="cuda")
+    assert torch.equal(vo, want)
