@@ -232,3 +232,18 @@ def test_new_outputs_are_apart(tokens):
     torch.cuda.synchronize()
     torch.full((tokens, G, D), 5.0, device="cuda")
     assert torch.equal(vo, want)
+
+
+def test_new_outputs_are_ordinary_tensors():
+    (k, ks), (v, vs) = ref.cache(2, 1), ref.cache(2, 2)
+    args = (k, v, ks, vs, ints([[0, 1]]), ints([0, 200]), 200)
+    ko, vo = msa.msa_dequantize_gather(*args)
+    ko.requires_grad_()
+    (ko.float() * vo.float()).sum().backward()
+    assert torch.equal(ko.grad, vo) and not vo.requires_grad
+    with torch.inference_mode():
+        a, b = msa.msa_dequantize_gather(*args)
+        assert a.is_inference() and torch.equal(a, ko.detach()) and torch.equal(b, vo)
+    rows = vo[3:9].clone()
+    vo[3:9].zero_()
+    assert bool((vo[3:9] == 0).all()) and bool((rows != 0).any())
