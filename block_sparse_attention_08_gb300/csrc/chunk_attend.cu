@@ -434,13 +434,16 @@ __device__ __forceinline__ void ca_find_shares(const CaArgs& a, CaSmem<kKv>& sm)
       extra1 = min(extra, 1);
       // Both kinds in one row, so that all but one CTA have items of one kind, and the one's start, end and waits for HBM pass
       // beside the other's products: 64 requests over 16k keys, bf16, 63 us instead of 76, four over 2k 15 instead of 17.  In time a unit
-      // of one-token items (two blocks) is 1.2 units of tiles over a bf16 cache.  Over 8-bit ones, long shares of
-      // both kinds beside one another slow some SMs down (256 requests, int8: 0.38 ms instead of 0.29), so there each CTA takes
-      // the one after the other.
+      // of one-token items (two blocks) is 1.2 units of tiles over a bf16 cache, and 1.4 in shares of 32 units on (256 requests
+      // over 32k 233 us instead of 244, 128 over 16k 86.6 instead of 89.2, but 64 over 16k 65 instead of 63).  Over 8-bit ones a unit
+      // of either kind keeps an SM busy, and the one-token items' ends fall to few of them: in long shares the kinds take no less
+      // side by side, whatever a unit counts (256 requests over 32k, E4M3, 0.29 ms instead of 0.25), so there each CTA takes the one
+      // after the other.
       row = !kFp8 || extra < 2;
     }
     if (row) {
-      const int tile = kFp8 || extra == 0 ? 1 : 5, token = kFp8 || extra == 0 ? 1 : 6;
+      const bool far = total[0] + total[2] >= 32LL * gridDim.x;
+      const int tile = kFp8 || extra == 0 ? 1 : 5, token = kFp8 || extra == 0 ? 1 : far ? 7 : 6;
       const long long n0 = units(total, 0), n1 = units(total, 1), sum = tile * n0 + token * n1;
       const long long c = ctas(sum / token, extra);
       const long long p0 = sum * min(static_cast<long long>(blockIdx.x), c) / c, p1 = sum * min(blockIdx.x + 1LL, c) / c;

@@ -17,8 +17,9 @@ FEW_TOKENS = kconst("kCaFewTokens", FILE)
 FEW_BLOCKS = int(re.search(r"kCaFewBlocks = (\d+);", _source(FILE))[1])
 TOK, CTAS = kconst("kCaTok", FILE), kconst("kNumSMs", FILE)
 BLOCK = 128
-_w = re.search(r"tile = kFp8 \|\| extra == 0 \? 1 : (\d+), token = kFp8 \|\| extra == 0 \? 1 : (\d+);", _source(FILE))
-WEIGHTS = int(_w[1]), int(_w[2])  # of a unit of either kind
+_w = re.search(r"tile = kFp8 \|\| extra == 0 \? 1 : (\d+), token = kFp8 \|\| extra == 0 \? 1 : far \? (\d+) : (\d+);", _source(FILE))
+WEIGHTS = {True: (int(_w[1]), int(_w[2])), False: (int(_w[1]), int(_w[3]))}  # of a unit of either kind, in long and short shares
+FAR = int(re.search(r"far = total\[0\] \+ total\[2\] >= (\d+)LL", _source(FILE))[1])
 
 
 def eighths(x):
@@ -110,7 +111,7 @@ def entries(lens, cu, offsets, shared, tokens, max_blocks, bad):
     return out
 
 
-def split(n0, n1, c, extra, fp8):
+def split(n0, n1, c, extra, fp8, far):
     """For the tiles' items and for the one-token items: (units from .. to, what all shares are parts of, CTAs, before, weight)."""
     if fp8 and extra == 2:  # each kind by itself
         out = []
@@ -118,7 +119,7 @@ def split(n0, n1, c, extra, fp8):
             ctas = min(CTAS, max(n // (1 + e), 1))
             out.append((min(n, n * c // ctas), min(n, n * (c + 1) // ctas), n, ctas, 0, 1))
         return out
-    tile, token = (1, 1) if fp8 or extra == 0 else WEIGHTS
+    tile, token = (1, 1) if fp8 or extra == 0 else WEIGHTS[far]
     total = tile * n0 + token * n1
     ctas = min(CTAS, max(total // token // (1 + extra), 1))
     p0, p1 = total * min(c, ctas) // ctas, total * min(c + 1, ctas) // ctas
@@ -235,7 +236,7 @@ def check(lens, news, offsets, shared, mistake=None, fp8=False):
                 assert (t0 + e, g) not in at
                 at[t0 + e, g] = (begin[0] or q.joined(), q.joined(), begin[0], one, c, begin[1], e)
     for c in range(CTAS):
-        shares = split(n0, n1, c, extra, fp8)
+        shares = split(n0, n1, c, extra, fp8, both >= FAR * CTAS)
         walk(work, c, shares[0], emit, mistake)
         walk_one(work, c, shares[1], emit, mistake)
     # each good token's keys, once; each of its pieces where the join looks for it
