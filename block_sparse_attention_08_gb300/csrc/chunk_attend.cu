@@ -55,7 +55,7 @@
 // int8: 2548 tokens in chunks over 4k to 12k keys take 0.587 ms (E4M3 0.51, bf16
 // 0.475: its widening is 8 instructions for four values where E4M3's is 2; with one
 // instead of four for a pair of values it would be 0.49), 16 single tokens over 128k keys
-// (2.18 GB) 0.335 ms, 6.5 TB/s.
+// (2.18 GB) 0.339 ms, 6.4 TB/s.
 //
 // Shared prefixes: sum_j p_j v_j and sum_j p_j over all keys are those over the
 // shared and over a request's own keys, brought to one m.  The groups' shared blocks
@@ -82,7 +82,7 @@ constexpr int kCaQEntry = 4096;       // one token's 16 heads x 128 dims
 constexpr int kCaInfo = 4;            // item descriptors in flight
 constexpr int kCaOnePlaces = 5;       // blocks in flight of one-token items (32 KB each)
 constexpr int kCaBad = 8;             // block flags in flight (at most 5 blocks are)
-// warps 0-7 softmax, 8 producer, 9 MMA, 10 bad requests (11 fills their warpgroup), 12-15 widening
+// warps 0-7 softmax, 8 producer, 9 MMA, 10 bad requests (11 fills their warpgroup; int8: both widen too), 12-15 widening
 constexpr int kCaProducerWarp = 8, kCaMmaWarp = 9, kCaWidenWarp = 12;
 constexpr float kCaSlack = 8.f;
 // Units that an item counts besides its blocks, for its start and its end: none where shares are short, since a share is
@@ -164,10 +164,10 @@ struct CaShape {
   // 16-bit K / V tiles.  (E4M3: with 3 of them and 4 copied ones, the places of widened tiles came free too late: 0.63 ms
   // instead of 0.60 for 2548 tokens in chunks over 4k to 12k keys.)
   static constexpr int kTiles = kFp8 ? 4 : 5;
-  static constexpr int kRaw = kFp8 ? 2 : 1;    // E4M3 tiles as copied
+  static constexpr int kRaw = kFp8 ? 2 : 1;    // 8-bit tiles as copied
   static constexpr int kWiden = kFp8 ? 4 : 0;  // widening warps
-  // and beside the issuing warps: an int8 tile takes a widening warp longer than the softmax of its scores (2548 tokens in chunks
-  // over 4k to 12k keys 631 us without, 587 with them)
+  // and beside the issuing warps: int8 tiles wait for their widening (2548 tokens in chunks over 4k to 12k keys 631 us without,
+  // 587 with them; E4M3 511 either way)
   static constexpr int kHelp = kKv == kCaI8 ? 2 : 0;
   static constexpr int kThreads = 32 * (kCaWidenWarp + kWiden);
   // registers per thread of the roles, out of the launch's 168 (384 threads) or 128 (512 threads) a thread:
