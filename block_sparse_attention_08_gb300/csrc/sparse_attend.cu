@@ -1079,22 +1079,31 @@ size_t attend_partials_bytes() { return 2ull * kMaxStreamKCtas * kPartialFloats 
 size_t attend_tickets_bytes() { return static_cast<size_t>(kMaxStreamKCtas) * sizeof(int); }
 
 using AttKernel = decltype(&sparse_attend_kernel<kKvBf16, 0>);
+// A kernel, what a call launches it with, and the most that any call does.
 struct AttForm {
   AttKernel kernel;
-  size_t smem;
+  size_t smem, limit;
   int threads;
+  // A kernel has one limit for all threads of the process, so every call sets the same: a smaller one, set between another
+  // thread's setting and its launch, would refuse that launch.
+  cudaError_t set_limit() const {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(limit));
+  }
 };
 template <int kKv, int kSplit>
 constexpr AttForm att_form_of() {
-  return AttForm{sparse_attend_kernel<kKv, kSplit>, att_smem<kKv, kSplit>(), AttShape<kKv, kSplit>::kThreads};
+  constexpr size_t smem = att_smem<kKv, kSplit>();
+  return AttForm{sparse_attend_kernel<kKv, kSplit>, smem, smem, AttShape<kKv, kSplit>::kThreads};
 }
 // alone: with so much shared memory that no two CTAs share an SM.
 constexpr size_t kAloneSmem = 120 * 1024;
+static_assert(att_smem<kKvI8, 1>() <= kAloneSmem, "the limit of the int8 kernel");
 constexpr int kAloneSegments = 36;
 static AttForm att_form(int kv, bool split, bool alone = false) {
   if (kv == kKvI8) {
     AttForm f = att_form_of<kKvI8, 1>();
-    if (alone && f.smem < kAloneSmem) f.smem = kAloneSmem;
+    f.limit = kAloneSmem;
+    if (alone) f.smem = kAloneSmem;
     return f;
   }
   if (kv == kKvE4m3) return split ? att_form_of<kKvE4m3, 1>() : att_form_of<kKvE4m3, 0>();
@@ -1113,12 +1122,12 @@ static int max_active_clusters(int kv, int c, bool alone) {
   std::lock_guard<std::mutex> lock(mu);
   const int form = kv + (alone ? 3 : 0);
   if (done[dev][form][c]) return cache[dev][form][c];
-  const auto [kern, smem, threads] = att_form(kv, true, alone);
+  const AttForm shape = att_form(kv, true, alone);
   int n = 0;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>(c * 16));
-  lc.blockDim = dim3(threads);
-  lc.dynamicSmemBytes = smem;
+  lc.blockDim = dim3(shape.threads);
+  lc.dynamicSmemBytes = shape.smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;
@@ -1126,8 +1135,7 @@ static int max_active_clusters(int kv, int c, bool alone) {
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kern, &lc) != cudaSuccess) {
+  if (shape.set_limit() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, shape.kernel, &lc) != cudaSuccess) {
     cudaGetLastError();  // a failed query leaves no error behind for the launch that follows
     return 0;            // and is asked again next time (it is not kept)
   }
@@ -1168,14 +1176,15 @@ cudaError_t launch_sparse_attend(const AttnGeom& geo, const void* q, const void*
   }
   // int8: else a CTA for each segment
   if (kv == kKvI8 && !C) C = 1;
-  const auto [kern, smem, threads] = att_form(kv, C > 0, alone && C > 0);
+  const AttForm form = att_form(kv, C > 0, alone);
+  if (const cudaError_t e = form.set_limit(); e != cudaSuccess) return e;
   const auto *ks = static_cast<const __nv_bfloat16*>(k_scales), *vss = static_cast<const __nv_bfloat16*>(v_scales);
   // a programmatic dependent of the previous kernel in the stream (the kernel
   // waits for that grid before touching memory), so its launch and prologue
   // overlap the decode top-k
   cudaLaunchConfig_t lc = {};
-  lc.blockDim = dim3(threads);
-  lc.dynamicSmemBytes = smem;
+  lc.blockDim = dim3(form.threads);
+  lc.dynamicSmemBytes = form.smem;
   lc.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1191,8 +1200,7 @@ cudaError_t launch_sparse_attend(const AttnGeom& geo, const void* q, const void*
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     lc.numAttrs = 2;
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    return cudaLaunchKernelEx(&lc, kern, kmap, vmap, qmap, q2k, geo, topk, scale_log2, vs, ks, vss, o, out_q, out_scale,
+    return cudaLaunchKernelEx(&lc, form.kernel, kmap, vmap, qmap, q2k, geo, topk, scale_log2, vs, ks, vss, o, out_q, out_scale,
                               static_cast<float*>(nullptr), static_cast<int*>(nullptr), C, err);
   }
   // At least 4 units per CTA: a segment is then shared by at most ~topk/4 + 1
@@ -1202,8 +1210,7 @@ cudaError_t launch_sparse_attend(const AttnGeom& geo, const void* q, const void*
   if (grid_l > max_ctas) grid_l = max_ctas;
   if (grid_l < 1) grid_l = 1;
   lc.gridDim = dim3(static_cast<unsigned>(grid_l));
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  return cudaLaunchKernelEx(&lc, kern, kmap, vmap, qmap, q2k, geo, topk, scale_log2, vs, ks, vss, o, out_q, out_scale,
+  return cudaLaunchKernelEx(&lc, form.kernel, kmap, vmap, qmap, q2k, geo, topk, scale_log2, vs, ks, vss, o, out_q, out_scale,
                             partials, tickets, 1, err);
 }
 
