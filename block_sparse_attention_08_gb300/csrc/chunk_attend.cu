@@ -1870,9 +1870,10 @@ __global__ void __launch_bounds__(kCaJoinThreads, 2) shared_join_kernel(const __
       const int n = x.n + (own.shared ? y.n : 0);
       float m = -INFINITY, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](float2 ml, float4 v) {  // (m is at least the piece's)
-        if (ml.x == -INFINITY) return;
-        const float g = ex2(ml.x - m);
+      // (m is at least the piece's.  A maximum passes over what is no number, so a piece without one may still have a sum that is
+      // none: it is added, by a factor that keeps it so.)
+      auto add = [&](float2 ml, float4 v) {
+        const float g = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
         l = fmaf(g, ml.y, l);
         o.x = fmaf(g, v.x, o.x);
         o.y = fmaf(g, v.y, o.y);

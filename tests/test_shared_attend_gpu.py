@@ -282,3 +282,53 @@ def test_calls_behind_one_another_give_the_same_bits(name, plain, kind):
     call = b.plain if plain else b.call
     outs = [call(*args, **b.more({})) for _ in range(60)]
     assert all(torch.equal(outs[0], x) for x in outs)
+
+
+def _poison(b, name, slot, g):
+    """A key ("k") or a value ("v") that is not finite."""
+    i = "kv".index(name)
+    if b.kind == "int8":
+        b.cache[2 + i][slot // PAGE, g, slot % PAGE] = math.nan
+    elif b.kind == "bf16":
+        b.cache[i][slot, g, 5] = math.nan
+    else:
+        b.cache[i].view(torch.uint8)[slot, g, 5] = 0x7F
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("where", ["query", "only own key", "only own value", "shared key", "one of the own keys"])
+@pytest.mark.parametrize("tokens", [9, 20, 60])
+def test_what_is_not_finite_stays_so_where_pieces_are_joined(tokens, where, kind):
+    """Requests that bring one token each (every third one two) behind a whole number of shared pages; a group's items are cut
+    into pieces for few tokens and for many.  As in the chunk attention, what a number is missing for is NaN, and
+    nothing else changes."""
+    b = Batch([(20 * PAGE, [(0 if i % 2 else 200, 2 if i % 3 == 2 else 1) for i in range(tokens)])], kind)
+    r, g = 7, 2                                    # (a request with one new token and no other own key)
+    t, heads = sum(b.news[:r]), slice(16 * g, 16 * g + 16)
+    lse = torch.empty(b.q.shape[:2], dtype=torch.float32, device="cuda")
+    clean = b.run(lse=lse)
+    clean_lse = lse.clone()
+    bad = torch.zeros(b.q.shape[:2], dtype=torch.bool, device="cuda")
+    if where == "query":
+        b.q[t, 16 * g + 3] = math.nan
+        bad[t, 16 * g + 3] = True
+    elif where == "shared key":
+        _poison(b, "k", int(b.table[0, 3]) * PAGE + 17, g)
+        bad[:, heads] = True
+    elif where == "one of the own keys":           # its only page: 201 keys
+        r, t = 6, sum(b.news[:6])
+        _poison(b, "k", int(b.table[r, 20]) * PAGE + 40, g)
+        bad[t:t + b.news[r], heads] = True
+    else:
+        _poison(b, "k" if where == "only own key" else "v", int(b.table[r, 20]) * PAGE, g)
+        bad[t, heads] = True
+    assert b.news[7] == 1 and b.lens[7] == 20 * PAGE + 1
+    plain_lse = torch.empty_like(lse)
+    plain = b.run_plain(lse=plain_lse)
+    out = b.run(lse=lse)
+    nan = out.isnan()
+    assert torch.equal(nan.all(-1), bad) or where == "only own value"
+    assert torch.equal(nan, plain.isnan()) and torch.equal(lse.isnan(), plain_lse.isnan())
+    assert torch.equal(out[~bad], clean[~bad]) and torch.equal(lse[~bad], clean_lse[~bad])
+    if where != "only own value":
+        assert torch.equal(lse.isnan(), bad)
