@@ -247,3 +247,21 @@ def test_new_outputs_are_ordinary_tensors():
     rows = vo[3:9].clone()
     vo[3:9].zero_()
     assert bool((vo[3:9] == 0).all()) and bool((rows != 0).any())
+
+
+@pytest.mark.parametrize("requests", [2, 12, 60])
+def test_sparse_attend_names_a_block_behind_the_context(requests):
+    """In each launch form, where nothing else is wrong: the block is told, with its place in q2k, and adds no key."""
+    lens, gen = [1500 + r for r in range(requests)], torch.Generator().manual_seed(6)
+    table, pages = page_table(lens, width=20)      # (entries behind a request's pages name page 0: what is there must not count)
+    k, ks = ref.cache(pages, 1)
+    v, vs = ref.cache(pages, 2)
+    q = torch.randn(requests, H, D, generator=gen).bfloat16().cuda()
+    ws = msa.Workspace(256)
+    for r, g, j, block in ((requests - 1, 2, 15, 12 + (requests > 36)), (0, 0, 5, 19), (1, 3, 0, 2 ** 31 - 1)):
+        q2k = _selection(lens, 16, gen)
+        q2k[g, r, j] = block
+        got = msa.msa_sparse_attend_decode_int8kv(q, k, v, ks, vs, q2k, ints(lens), table, workspace=ws)
+        # detail: the entry's number, request by request
+        assert ws.read_device_error() == (2, (r * G + g) * 16 + j)
+        ref.check_sparse(got, ref.sparse(q, ref.values(k, ks), ref.values(v, vs), q2k, lens, table, SCALE))
