@@ -11,7 +11,8 @@
 // GB300 design.  The 16 query heads that share a KV head form exactly one
 // 16-row MMA tile, so one (query, KV head, selected block) triple is the unit
 // of work and a (query, KV head) pair is a segment of up to topk units.  All
-// units are split evenly over a persistent grid of one CTA per SM (stream-K).
+// units are split evenly over a persistent grid of one CTA per SM (stream-K;
+// an int8 cache: at the end).
 //
 // A producer warp walks the CTA's segments.  Per segment its lanes resolve the
 // selected blocks in parallel (q2k entry, then page id); it puts the segment's
@@ -48,6 +49,12 @@
 // block feeding an even-dim and an odd-dim n-tile.  q is rounded to fp16 once
 // per segment, P to fp16.  k_scale is folded into the softmax scale and
 // v_scale into the normalisation.
+//
+// int8 K/V cache, a scale per row: chunks as over an FP8 cache, with their
+// keys' scales beside them, in a 4-stage ring.  Four consumer warps form two
+// groups; both warps of a group take 32 keys of every chunk of its stages
+// (stage s: group s % 2).  Never stream-K: a CTA takes a whole segment or, where
+// there are few, a cluster of 4 or 2 CTAs does.
 #include <mutex>
 
 #include "int8_attend.cuh"
@@ -183,7 +190,7 @@ struct CombRef {
 // who = 0: the CTA's merged state; who = w in 1, 2: the state of consumer warp w.
 // Stream-K: the shared buffer (the merged state over warp 1's slot, which warp
 // 0 has read by then; with one slot the warps take turns); cluster form: stage
-// `who`, which belongs to warp `who`.
+// `who` (the warps have met: every stage has been read).
 template <int kKv, int kSplit>
 __device__ __forceinline__ CombRef comb_ref(AttSmem<kKv, kSplit>& sm, int who) {
   if constexpr (kSplit != 0) {
@@ -631,7 +638,7 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
     return;
   }
 
-  // ---------------- consumer warps: whole 64-key chunks, stage s -> warp s % 3 ----------------
+  // ---------------- consumer warps: 64-key chunks, stage s -> group s % kGroups (one warp; int8: two, 32 keys each) ----------
   const int g8 = lane >> 2, t4 = lane & 3;
   int sc = 0;  // chunk counter, identical in every consumer warp and the producer
   int nseg = 0;
@@ -896,7 +903,7 @@ __global__ void __launch_bounds__(AttShape<kKv, kSplit>::kThreads, AttShape<kKv,
       consumer_sync<kConsumers>();
       if (warp > 0) state_to_smem<kKv>(st, comb_ref(sm, warp), g8, t4);
       consumer_sync<kConsumers>();
-      if (warp > 0) continue;  // warps 1 and 2 go on to the next segment
+      if (warp > 0) continue;  // the others go on to the next segment
 #pragma unroll
       for (int w = 1; w < kConsumers; ++w) merge_from_smem<kKv>(st, comb_ref(sm, w), g8, t4);
     }
@@ -1038,6 +1045,8 @@ static bool make_kv_map(CUtensorMap* map, const void* base, long long rows) {
 
 // 3-D map over a [rows, 4, 128] array of 8-bit values; box = 128 dims (128 bytes) x 1 head x 64 rows, 128-byte swizzle.  A
 // head's row is 128 bytes: with promotion to 256, L2 would fetch the neighbouring head's with it, which another selection reads.
+// (E4M3, promotion to 128 and to 256: 16 requests over 128k keys 20.2 and 21.9 us, 64 over 4k to 64k 60.7 and 61.6, 256 over 4k to
+// 32k 176.6 and 178.2; with one selection for all heads 20.2 and 20.3, 60.7 and 61.7, 176.6 and 178.3.)
 static bool make_kv_map8(CUtensorMap* map, const void* base, long long rows) {
   EncodeTiledFn enc = get_encode_tiled();
   if (!enc) return false;
@@ -1095,10 +1104,11 @@ constexpr AttForm att_form_of() {
   constexpr size_t smem = att_smem<kKv, kSplit>();
   return AttForm{sparse_attend_kernel<kKv, kSplit>, smem, smem, AttShape<kKv, kSplit>::kThreads};
 }
-// alone: with so much shared memory that no two CTAs share an SM.
+// alone: with so much shared memory that no two CTAs share an SM, up to as many segments as leave an SM to each CTA of the
+// largest clusters (nine requests).
 constexpr size_t kAloneSmem = 120 * 1024;
 static_assert(att_smem<kKvI8, 1>() <= kAloneSmem, "the limit of the int8 kernel");
-constexpr int kAloneSegments = 36;
+constexpr int kAloneSegments = kNumSMs / largest_cluster(kKvI8);
 static AttForm att_form(int kv, bool split, bool alone = false) {
   if (kv == kKvI8) {
     AttForm f = att_form_of<kKvI8, 1>();
@@ -1112,7 +1122,7 @@ static AttForm att_form(int kv, bool split, bool alone = false) {
 
 // How many clusters of c CTAs of the split kernel can be resident at once
 // (cudaOccupancyMaxActiveClusters, asked once per device, form and c; 0
-// when the query fails, which keeps the stream-K kernel for that call).
+// when the query fails, which leaves that call without clusters).
 static int max_active_clusters(int kv, int c, bool alone) {
   static std::mutex mu;
   static int cache[64][6][kMaxCluster + 1];
@@ -1160,9 +1170,10 @@ cudaError_t launch_sparse_attend(const AttnGeom& geo, const void* q, const void*
   const long long S = static_cast<long long>(geo.nq) * kKvHeads;  // (query, KV head) segments
   const long long N = S * topk;
   // Few segments (small batches): one cluster of C CTAs per segment, merged
-  // on chip -- the largest C in {8, 4, 2} with C <= topk (every CTA gets a
-  // unit), at most one CTA per SM (two with an FP8 cache, three with an int8 one), and every cluster
-  // resident at once.  Otherwise stream-K over the whole grid, one CTA per SM.
+  // on chip -- the largest C in {8, 4, 2} (int8: {4, 2}) with C <= topk (every
+  // CTA gets a unit), at most one CTA per SM (FP8: two; int8: one up to
+  // kAloneSegments, then three), and every cluster resident at once.  Otherwise
+  // stream-K over the whole grid, one CTA per SM (FP8: two); int8: a CTA per segment.
   const long long per_sm = kv == kKvI8     ? AttShape<kKvI8, 1>::kCtasPerSm
                            : kv == kKvE4m3 ? AttShape<kKvE4m3, 1>::kCtasPerSm
                                            : AttShape<kKvBf16, 1>::kCtasPerSm;
