@@ -52,7 +52,7 @@
 // 1.38 ms.  Single tokens over long contexts are bound by HBM (64 requests,
 // 4.0 GB: 0.58 ms, 6.9 TB/s), short ones by latency: 4.6 us without any work,
 // 8.2 with one block.
-// int8: 2548 tokens in chunks over 4k to 12k keys take 0.587 ms (E4M3 0.51, bf16
+// int8: 2682 tokens in chunks over 3k to 13k keys take 0.587 ms (E4M3 0.51, bf16
 // 0.475: its widening is 8 instructions for four values where E4M3's is 2; with one
 // instead of four for a pair of values it would be 0.49), 16 single tokens over 128k keys
 // (2.18 GB) 0.339 ms, 6.4 TB/s.
@@ -166,7 +166,7 @@ struct CaShape {
   static constexpr int kTiles = kFp8 ? 4 : 5;
   static constexpr int kRaw = kFp8 ? 2 : 1;    // 8-bit tiles as copied
   static constexpr int kWiden = kFp8 ? 4 : 0;  // widening warps
-  // and beside the issuing warps: int8 tiles wait for their widening (2548 tokens in chunks over 4k to 12k keys 631 us without,
+  // and beside the issuing warps: int8 tiles wait for their widening (2682 tokens in chunks over 3k to 13k keys 631 us without,
   // 587 with them; E4M3 511 either way)
   static constexpr int kHelp = kKv == kCaI8 ? 2 : 0;
   static constexpr int kThreads = 32 * (kCaWidenWarp + kWiden);
@@ -567,7 +567,7 @@ __device__ __forceinline__ uint32_t ca_widen2(uint32_t x) {
 // Two int8 values (bytes 0 and 1 of w, or 2 and 3) times a power of two s, as bf16, exactly.  at: the bits of 128 s in both halves,
 // step: the bits in which those of 256 s differ.  With its low seven bits m a byte makes (128 + m) s, with its sign 128 s, or
 // 256 s for a negative one (the byte permutation has the sign in all the upper bits); their difference is n s.  (Decoded
-// first and multiplied then, one more instruction of four: 648 us instead of 625 for 2548 tokens in chunks.)
+// first and multiplied then, one more instruction of four: 648 us instead of 625 for 2682 tokens in chunks.)
 template <bool kUpper>
 __device__ __forceinline__ uint32_t ca_i8_scaled(uint32_t w, uint32_t at, uint32_t step) {
   uint32_t t, d;

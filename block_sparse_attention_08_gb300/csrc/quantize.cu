@@ -67,7 +67,7 @@ __device__ __forceinline__ void qz_row(const uint32_t (&w)[4], uint32_t field, u
 }
 
 // Bound by the instructions of a row, so the offsets are counted in 32 bits where they fit, and rows that need care go another way.
-// (16560 tokens, 51 MB: 10.8 us, 4.7 TB/s, the integer pipe 71% busy; 16.2 with a division, a
+// (17416 tokens, 54 MB: 10.8 us, 5.0 TB/s, the integer pipe 71% busy; 16.2 with a division, a
 // conversion and a comparison per value.)
 __global__ void __launch_bounds__(kQzThreads) quantize_kernel(const __grid_constant__ QzArgs a) {
   const uint32_t lane16 = threadIdx.x & 15, part = (threadIdx.x / 16) % kQzParts, g = part % kKvHeads;
