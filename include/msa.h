@@ -682,7 +682,8 @@ msa_status msa_sparse_attend_decode_int8kv(const msa_config* cfg, const void* q,
  * scales, exactly where those are powers of two (else n * s is rounded to bf16 for the items of
  * two and more tokens).  Each 16 tokens of a chunk widen the keys that they read; for long chunks
  * msa_dequantize_gather and msa_attend_chunk over its rows take less time (five chunks of 333 to 700
- * tokens over 3k to 13k keys 0.48 ms instead of 0.59), where there is memory for them.  Other arguments, the output and the errors as msa_attend_chunk. */
+ * tokens over 3k to 13k keys 0.48 ms instead of 0.59), where there is memory for them.  Other
+ * arguments, the output and the errors as msa_attend_chunk. */
 msa_status msa_attend_chunk_int8kv(const msa_config* cfg, const void* q, const void* k_cache,
                                    const void* v_cache, const void* k_scales, const void* v_scales,
                                    const int32_t* seq_lens, const int32_t* page_table,
